@@ -1,6 +1,7 @@
-"""GB300 (sm_103a) W8A8 mixture-of-experts expert layer.
+"""GB300 (sm_103a) W8A8 mixture-of-experts expert layer, its router and its MXFP4 form.
 
-Thin Python binding over the C ABI in ``include/moe_layer.h`` (library
+Thin Python binding over the C ABI in ``include/moe_layer.h`` and
+``include/moe_mxfp4.h`` (library
 ``_build/libmoe_layer.so``, built by ``moe_expert_layer_gb300.build``).  The
 functions below carry the ABI's names and only marshal arguments: torch
 tensors (device memory) become raw pointers, the stream defaults to torch's
@@ -19,7 +20,7 @@ STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SHAPE", -3: "MOE_ERR_ALI
           -4: "MOE_ERR_ARCH", -5: "MOE_ERR_WORKSPACE", -6: "MOE_ERR_LAUNCH",
           -8: "MOE_ERR_TIMEOUT"}
 
-# every entry point declared in include/moe_layer.h
+# every entry point declared in include/moe_layer.h and include/moe_mxfp4.h
 EXPORTS = [
     "moe_status_string", "moe_layer_workspace_size", "moe_layer_fwd",
     "moe_layer_host_workspace_size", "moe_layer_fwd_host", "moe_workspace_status",
@@ -31,6 +32,9 @@ EXPORTS = [
     "moe_layer_pipeline_workspace_size", "moe_layer_pipeline_create", "moe_layer_pipeline_submit",
     "moe_layer_pipeline_wait", "moe_layer_pipeline_destroy",
     "moe_weight_tiles_bytes", "moe_pack_weight_tiles",
+    "moe_route_topk", "moe_mxfp4_scale_words", "moe_mxfp4_quant", "moe_mxfp4_dequant", "moe_mxfp4_weights_bytes",
+    "moe_mxfp4_quant_weights", "moe_mxfp4_pack_weights", "moe_mxfp4_gmm_workspace_size", "moe_mxfp4_gmm",
+    "moe_mxfp4_gmm_swiglu", "moe_mxfp4_layer_workspace_size", "moe_mxfp4_layer_fwd",
 ]
 
 # weight layouts (moe_dims_t.weight_layout)
@@ -100,6 +104,18 @@ def load_library(path=None):
         "moe_selftest_count_timeout": ([vp, vp, ctypes.c_uint32, vp], i32),
         "moe_weight_tiles_bytes": ([D, i32], sz),
         "moe_pack_weight_tiles": ([D, i32, vp, vp, vp], i32),
+        "moe_route_topk": ([i32] * 3 + [vp, i32, ctypes.c_int64, vp, i32, i32, ctypes.c_float] + [vp] * 3, i32),
+        "moe_mxfp4_scale_words": ([ctypes.c_int64, i32], sz),
+        "moe_mxfp4_quant": ([i32, i32, vp, i32, ctypes.c_int64, vp, i32, i32] + [vp] * 3, i32),
+        "moe_mxfp4_dequant": ([i32, i32, vp, vp, vp, i32, vp], i32),
+        "moe_mxfp4_weights_bytes": ([i32] * 3, sz),
+        "moe_mxfp4_quant_weights": ([i32] * 4 + [vp, i32, vp, vp], i32),
+        "moe_mxfp4_pack_weights": ([i32] * 4 + [vp] * 4, i32),
+        "moe_mxfp4_gmm_workspace_size": ([i32] * 4, sz),
+        "moe_mxfp4_gmm": ([i32] * 4 + [vp] * 6 + [sz, vp], i32),
+        "moe_mxfp4_gmm_swiglu": ([i32] * 4 + [vp] * 7 + [sz, vp], i32),
+        "moe_mxfp4_layer_workspace_size": ([D], sz),
+        "moe_mxfp4_layer_fwd": ([D] + [vp] * 7 + [sz, vp], i32),
     }
     for name, (args, res) in sigs.items():
         f = getattr(lib, name)
@@ -334,3 +350,130 @@ def moe_route_sort_noalloc(d, expert_idx, sorted_src_route, expanded_row_idx, to
     _check("moe_route_sort_noalloc", load_library().moe_route_sort_noalloc(
         ctypes.byref(d), _p(expert_idx), _p(sorted_src_route), _p(expanded_row_idx),
         _p(tokens_per_expert), _p(cumsum), _stream(stream)))
+
+
+# ------------------------------------------------------------------- include/moe_mxfp4.h
+# Element types and router scores (MOE_TYPE_*, MOE_SCORE_*).
+TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+_TYPES = {"torch.float32": TYPE_F32, "torch.float16": TYPE_F16, "torch.bfloat16": TYPE_BF16}
+
+
+def _type(t):
+    try:
+        return _TYPES[str(t.dtype)]
+    except KeyError:
+        raise ValueError("float32, float16 or bfloat16 wanted; got %s" % t.dtype) from None
+
+
+def _rows(t):
+    """Pointer and row stride (elements) of a 2-D tensor whose rows are dense."""
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("a 2-D tensor with dense rows wanted; got shape %s, strides %s"
+                         % (tuple(t.shape), tuple(t.stride())))
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _sized(t, n, size, what):
+    """Pointer of a dense array that has to hold n elements of `size` bytes."""
+    if t.numel() < n or t.element_size() != size:
+        raise ValueError("%s: %d elements of %d bytes wanted; got %d of %d"
+                         % (what, n, size, t.numel(), t.element_size()))
+    return _p(t)
+
+
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
+def moe_route_topk(logits, expert_idx, probs, bias=None, scoring=SCORE_SOFTMAX, renormalise=True, scale=1.0,
+                   stream=None):
+    """Routes of logits [M][E] (any row stride) into expert_idx, probs [M][topK]."""
+    M, E = logits.shape
+    topK = expert_idx.shape[1]
+    p, stride = _rows(logits)
+    _check("moe_route_topk", load_library().moe_route_topk(
+        M, E, topK, p, _type(logits), stride, None if bias is None else _sized(bias, E, 4, "bias"), scoring,
+        1 if renormalise else 0, scale, _sized(expert_idx, M * topK, 4, "expert_idx"),
+        _sized(probs, M * topK, 4, "probs"), _stream(stream)))
+
+
+def moe_mxfp4_scale_words(rows, D):
+    return load_library().moe_mxfp4_scale_words(rows, D)
+
+
+def _scales(t, rows, D):
+    return _sized(t, (D + 127) // 128 * ((rows + 3) // 4 * 4), 4, "scales")
+
+
+def moe_mxfp4_quant(x, codes, scales, row_map=None, copies=1, stream=None):
+    """MXFP4 rows of x [M][D] (any row stride): codes [rows][D / 2], scales of moe_mxfp4_scale_words(rows, D) words."""
+    M, D = x.shape
+    rows = codes.shape[0]
+    p, stride = _rows(x)
+    _check("moe_mxfp4_quant", load_library().moe_mxfp4_quant(
+        M, D, p, _type(x), stride, None if row_map is None else _sized(row_map, M * copies, 4, "row_map"), copies,
+        rows, _sized(codes, rows * D // 2, 1, "codes"), _scales(scales, rows, D), _stream(stream)))
+
+
+def moe_mxfp4_dequant(codes, scales, out, stream=None):
+    rows, D = out.shape
+    _check("moe_mxfp4_dequant", load_library().moe_mxfp4_dequant(
+        rows, D, _sized(codes, rows * D // 2, 1, "codes"), _scales(scales, rows, D), _p(out), _type(out),
+        _stream(stream)))
+
+
+def moe_mxfp4_weights_bytes(E, N, D):
+    return load_library().moe_mxfp4_weights_bytes(E, N, D)
+
+
+def _blocks(t, E, N, D):
+    return _sized(t, max(1, moe_mxfp4_weights_bytes(E, N, D)), 1, "blocks")
+
+
+def moe_mxfp4_quant_weights(w, blocks, gate_up=False, stream=None):
+    """Weight blocks of w [E][N][D]."""
+    E, N, D = w.shape
+    _check("moe_mxfp4_quant_weights", load_library().moe_mxfp4_quant_weights(
+        E, N, D, 1 if gate_up else 0, _p(w), _type(w), _blocks(blocks, E, N, D), _stream(stream)))
+
+
+def moe_mxfp4_pack_weights(codes, scales, blocks, gate_up=False, stream=None):
+    """Weight blocks of MXFP4 rows: codes [E][N][D / 2], scale bytes [E][N][D / 32]."""
+    E, N, half = codes.shape
+    _check("moe_mxfp4_pack_weights", load_library().moe_mxfp4_pack_weights(
+        E, N, 2 * half, 1 if gate_up else 0, _sized(codes, E * N * half, 1, "codes"),
+        _sized(scales, E * N * half // 16, 1, "scales"), _blocks(blocks, E, N, 2 * half), _stream(stream)))
+
+
+def moe_mxfp4_gmm_workspace_size(R, E, N, D):
+    return load_library().moe_mxfp4_gmm_workspace_size(R, E, N, D)
+
+
+def moe_mxfp4_gmm(codes, scales, cumsum, w, c, workspace, stream=None):
+    """c [R][N] (binary16) = rows of codes [R][D / 2] times their experts' blocks w."""
+    R, N = c.shape
+    E, D = cumsum.shape[0], 2 * codes.shape[1]
+    _check("moe_mxfp4_gmm", load_library().moe_mxfp4_gmm(
+        R, E, N, D, _sized(codes, R * D // 2, 1, "codes"), _scales(scales, R, D), _sized(cumsum, E, 4, "cumsum"),
+        _blocks(w, E, N, D), _sized(c, R * N, 2, "c"), _p(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def moe_mxfp4_gmm_swiglu(codes, scales, cumsum, w, h_codes, h_scales, workspace, stream=None):
+    """SwiGLU of the product with gate_up blocks w, as MXFP4 rows h_codes [R][I / 2], h_scales."""
+    R, I = h_codes.shape[0], 2 * h_codes.shape[1]
+    E, D = cumsum.shape[0], 2 * codes.shape[1]
+    _check("moe_mxfp4_gmm_swiglu", load_library().moe_mxfp4_gmm_swiglu(
+        R, E, I, D, _sized(codes, R * D // 2, 1, "codes"), _scales(scales, R, D), _sized(cumsum, E, 4, "cumsum"),
+        _blocks(w, E, 2 * I, D), _sized(h_codes, R * I // 2, 1, "h_codes"), _scales(h_scales, R, I),
+        _p(workspace), _nbytes(workspace), _stream(stream)))
+
+
+def moe_mxfp4_layer_workspace_size(d):
+    return load_library().moe_mxfp4_layer_workspace_size(ctypes.byref(d))
+
+
+def moe_mxfp4_layer_fwd(d, x, expert_idx, probs, w1, w2, out, workspace, stream=None):
+    _check("moe_mxfp4_layer_fwd", load_library().moe_mxfp4_layer_fwd(
+        ctypes.byref(d), _p(x), _p(expert_idx), _p(probs), _p(w1), _p(w2), _p(out), _p(workspace),
+        _nbytes(workspace), _stream(stream)))

@@ -12,8 +12,9 @@ CSRC = os.path.join(HERE, "csrc")
 OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libmoe_layer.so")
 SOURCES = ["route_sort.cu", "elementwise.cu", "gemm_hmma.cu", "gemm_tc.cu", "gemm_dispatch.cu", "moe_layer.cu",
-           "route_sort_noalloc.cu", "selftest.cu", "weight_tiles.cu"]
-HEADERS = ["abi_checks.h", "common.cuh", "kernels.h", "swiglu.cuh", "tensor_map.h"]
+           "route_sort_noalloc.cu", "selftest.cu", "weight_tiles.cu",
+           "route_topk.cu", "mxfp4_quant.cu", "mxfp4_gmm.cu", "mxfp4_abi.cu"]
+HEADERS = ["abi_checks.h", "common.cuh", "kernels.h", "mxfp4.cuh", "mxfp4.h", "swiglu.cuh", "tensor_map.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
               "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall"]
@@ -22,7 +23,7 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", 
 def _inputs():
     root = os.path.dirname(HERE)
     return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-            + [os.path.join(root, "include", "moe_layer.h"), os.path.abspath(__file__)])
+            + [os.path.join(root, "include", h) for h in ("moe_layer.h", "moe_mxfp4.h")] + [os.path.abspath(__file__)])
 
 
 def up_to_date():

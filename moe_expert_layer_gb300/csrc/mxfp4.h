@@ -1,0 +1,56 @@
+// Internal launch interface of the router and the MXFP4 kernels (host side).
+#pragma once
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace moe {
+
+// Weight blocks (include/moe_mxfp4.h): 128 channels x 256 reduction steps.
+constexpr int kMxCodeBytes = 128 * 128;
+constexpr int kMxBlockBytes = kMxCodeBytes + 2 * 512;
+constexpr int kMxMaxDepth = 16384, kMxMaxN = 65536, kMxMaxE = 1023;
+inline int mx_depth_blocks(int D) { return (D + 255) / 256; }
+inline size_t mx_weights_bytes(int E, int N, int D) {
+  return (size_t)E * (size_t)(N / 128) * (size_t)mx_depth_blocks(D) * kMxBlockBytes;
+}
+// Words per plane of the scales of `rows` MXFP4 rows, and planes of depth D.
+inline int mx_scale_pitch(int rows) { return (rows + 3) & ~3; }
+inline int mx_scale_planes(int D) { return (D + 127) / 128; }
+
+// route_topk.cu
+cudaError_t launch_route_topk(int M, int E, int topK, const void* logits, int type, int64_t stride, const float* bias,
+                              int score, bool renormalise, float scale, int32_t* expert_idx, float* probs,
+                              cudaStream_t stream);
+
+// mxfp4_quant.cu
+cudaError_t launch_mx_quant(int M, int D, const void* x, int type, int64_t stride, const int32_t* row_map, int copies,
+                            int rows, uint8_t* codes, uint32_t* scales, cudaStream_t stream);
+cudaError_t launch_mx_dequant(int rows, int D, const uint8_t* codes, const uint32_t* scales, void* out, int type,
+                              cudaStream_t stream);
+cudaError_t launch_mx_quant_weights(int E, int N, int D, bool gate_up, const void* w, int type, uint8_t* blocks,
+                                    cudaStream_t stream);
+cudaError_t launch_mx_pack_weights(int E, int N, int D, bool gate_up, const uint8_t* codes, const uint8_t* scales,
+                                   uint8_t* blocks, cudaStream_t stream);
+
+// Grouped product over expert-major MXFP4 rows (mxfp4_gmm.cu).  h_codes null: c gets the
+// binary16 sums; else N = 2 I channels in gate_up order, and the SwiGLU of the sums is
+// written as MXFP4 rows of depth N / 2.
+struct MxGemmProblem {
+  int R, E, N, D;
+  const uint8_t* codes;    // [R][D / 2]
+  const uint32_t* scales;  // [planes(D)][pitch(R)]
+  const int32_t* cumsum;   // [E]
+  const uint8_t* w;        // blocks
+  uint16_t* c;             // [R][N] or null
+  uint8_t* h_codes;        // [R][N / 4] or null
+  uint32_t* h_scales;      // [planes(N / 2)][pitch(R)]
+  int32_t* status;
+};
+cudaError_t launch_mx_gmm(const MxGemmProblem& p, cudaStream_t stream);
+
+// out[t] = sum over j of probs[t][j] * c2[expanded[t * topK + j]] (entries < 0 skipped)
+cudaError_t launch_mx_combine(const uint16_t* c2, const int32_t* expanded, const float* probs, int M, int K, int topK,
+                              uint16_t* out, cudaStream_t stream);
+
+}  // namespace moe
