@@ -70,6 +70,7 @@
 #include "common.cuh"
 #include "kernels.h"
 #include "swiglu.cuh"
+#include "tc_common.cuh"
 #include "tensor_map.h"
 
 namespace moe {
@@ -337,21 +338,6 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 template <uint32_t kRegs>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
-// Shared-memory matrix descriptor, K-major operand in the 128-byte swizzle layout:
-// rows 128 B apart, groups of 8 rows 1024 B apart.
-__device__ __forceinline__ uint64_t sw128_desc(uint32_t saddr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);     // start address
-  d |= (uint64_t)1 << 16;                        // leading byte offset (unused for this layout)
-  d |= (uint64_t)(1024 >> 4) << 32;              // stride byte offset: 8-row groups
-  d |= (uint64_t)1 << 46;                        // descriptor version
-  d |= (uint64_t)2 << 61;                        // swizzle: 128 B
-  return d;
-}
-
 // D[256 x N] (+)= A[256 x 16] * B[N x 16]^T over the pair: A rows 0-127 from this
 // CTA's tensor memory, 128-255 from the peer's; B rows split N/2 + N/2 likewise.
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
@@ -386,17 +372,6 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
       "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
       : "memory");
 }
-
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-      : "r"(taddr)
-      : "memory");
-}
-__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   uint4 v;
@@ -531,42 +506,6 @@ __device__ __forceinline__ Item decode_item(int j, const WorkList& wl, int& e_hi
   it.n_mma = wl.pow2_n ? (it.rows <= 32 ? 32 : 1 << (32 - __clz(it.rows - 1)))  // 32, 64, 128 or 256
                       : (it.rows + 31) & ~31;                                  // N in steps of 32
   return it;
-}
-
-// try_wait that lets the warp sleep in hardware until the phase completes (up to
-// `hint_ns`), instead of re-issuing probes that take issue slots from the MMA warp.
-__device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t* bar, uint32_t parity, uint32_t hint_ns) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
-      : "memory");
-  return ok != 0;
-}
-
-// Bounded wait: false after about two seconds of %globaltimer.
-__device__ __forceinline__ bool mbar_wait_sleep_bounded(uint64_t* bar, uint32_t parity) {
-  constexpr uint32_t kHintNs = 100000;
-  if (mbar_try_wait_sleep(bar, parity, kHintNs)) return true;
-  const uint64_t t0 = globaltimer_ns();
-  for (;;) {
-    for (int i = 0; i < 16; ++i)
-      if (mbar_try_wait_sleep(bar, parity, kHintNs)) return true;
-    if (globaltimer_ns() - t0 > kWaitLimitNs) return false;
-  }
-}
-
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
-                                              int32_t* status) {
-  if (mbar_try_wait(bar, parity)) return true;  // fast path: one probe of a completed phase
-  if (*abort_flag) return false;
-  if (mbar_wait_sleep_bounded(bar, parity)) return true;
-  *abort_flag = 1;
-  record_status(status, MOE_ERR_TIMEOUT);
-  return false;
 }
 
 // GATHER: token rows gathered by index (args.gather_route) instead of tiled boxes of

@@ -38,6 +38,20 @@ inline bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, size_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same of 32-bit words without a swizzle: rows of box_inner words land one after another.
+inline bool encode_tensor_map_words(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
+                                    uint32_t box_inner, uint32_t box_outer) {
+  PFN_encodeTiled fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, outer};
+  cuuint64_t strides[1] = {inner * 4};
+  cuuint32_t box[2] = {box_inner, box_outer};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Per-device, once-only host state (kernel attributes, SM counts): devices 0..63.
 constexpr int kMaxDevices = 64;
 inline int current_device() {
