@@ -175,6 +175,14 @@ __device__ __forceinline__ void bulk_store(void* gdst, const void* smem_src, uin
                "r"(smem_u32(smem_src)), "r"(bytes)
                : "memory");
 }
+// Tiled store of a 2-D tensor map's box at coordinates (x, y) (neither negative) from this
+// CTA's shared memory, with the same requirements on the source.
+__device__ __forceinline__ void tma_store_2d(const void* tmap, int32_t x, int32_t y, const void* smem_src) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(smem_u32(smem_src))
+               : "memory");
+}
 __device__ __forceinline__ void bulk_commit_group() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 // Waits until this thread's committed bulk stores have read their shared source.
 __device__ __forceinline__ void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }

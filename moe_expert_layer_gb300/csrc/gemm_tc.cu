@@ -309,30 +309,6 @@ __device__ __forceinline__ void swiglu_row_warp(const Args& a, int d, int e, int
 #endif
 
 // ------------------------------------------------------------------ cluster / tcgen05 helpers
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_sync_all() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// shared::cluster address of the same shared variable in CTA `rank` of the cluster
-__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
-  uint32_t r;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-  return r;
-}
-// Arrive on a barrier given by its shared::cluster address (either CTA of the pair).
-// Default semantics: an arrive with cluster-scope release costs ~320 cycles on
-// GB300, this one ~6; the data it publishes is tensor memory (ordered by
-// tcgen05.wait + tcgen05.fence) or TMA-written shared memory whose barrier the
-// signalling thread has already seen complete.
-__device__ __forceinline__ void mbar_arrive_remote(uint32_t caddr) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
-}
-
 template <uint32_t kRegs>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <uint32_t kRegs>

@@ -7,79 +7,211 @@
 // (256 elements, four MMAs deep) in the 128-byte swizzle.  Their scales lie in tensor
 // memory: for 128 elements of depth, the four scale bytes of row r as one 32-bit word in
 // lane r % 32, column r / 32, the same in all four 32-lane groups; an MMA uses the low or
-// the high half of the words, which its instruction descriptor selects.  Warps write them
-// there from registers (tcgen05.st): the words then need no particular order in global or
-// shared memory beyond one row after the other.
+// the high half of the words, which its instruction descriptor selects.  In global memory
+// and as copied the words stand one row after the other; a warp puts the 512 bytes of 128
+// rows into the order of the lanes in place (mx_arrange_scales), and tcgen05.cp, issued
+// before the MMAs that use them by the same thread, copies them on.
 #pragma once
 #include "mxfp4.cuh"
 #include "tc_common.cuh"
 
 namespace moe {
 
-// Instruction descriptor of kind::mxf4: A and B e2m1, e8m0 scales, M = 128, N in steps of 8.
-__device__ __forceinline__ uint32_t mx_idesc(int n) {
-  return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | (1u << 27);
+// Instruction descriptor of kind::mxf4: A and B e2m1, e8m0 scales, M = 128 (a CTA; N in steps
+// of 16) or 256 (a pair; N in steps of 32).
+__device__ __forceinline__ uint32_t mx_idesc(int m, int n) {
+  return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(m >> 7) << 27);
 }
-// The scale halves (0: elements 0-63 of the 128, 1: 64-127) an MMA uses.
+// The scale half (0: elements 0-63 of the 128, 1: 64-127) an MMA uses.
 __device__ __forceinline__ uint32_t mx_idesc_half(uint32_t half) { return (half * 2u) << 4 | (half * 2u) << 29; }
 
-__device__ __forceinline__ void mx_mma(uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
-                                       uint32_t sfb, uint32_t accumulate) {
+// The warp's number in its CTA, in a form the compiler knows to be the same in all lanes:
+// branches on it are uniform.
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
+
+// One lane of a converged warp: nonzero there, zero in the others.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.u32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+      "{\n\t.reg .pred e;\n\t"
+      "elect.sync _|e, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, e;\n\t}"
+      : "=r"(r));
+  return r;
+}
+
+// MMAs, commits and copies are issued by a whole warp in uniform control flow, each
+// instruction predicated on the elected lane, and not by one lane in a branch of its own: the
+// operands then stay in uniform registers.  An MMA of 256 x 64 x 64 cost 123 cycles issued by
+// a lone lane and 55 this way, one of 256 x 224 x 64 its 112 cycles of tensor-core time
+// instead of 147.
+//
+// PAIR: the MMA of a CTA pair.  Each CTA holds its 128 rows of A and their scales, half of
+// B's rows, the scales of all of them, and gets its 128 rows of D.
+template <bool PAIR>
+__device__ __forceinline__ void mx_mma(uint32_t elected, uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                       uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.u32 p, %6, 0;\n\t"
+        "setp.ne.u32 e, %7, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.u32 p, %6, 0;\n\t"
+        "setp.ne.u32 e, %7, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+// Arrive on `bar` (of both CTAs of a pair) once the MMAs issued so far by this thread have
+// completed.
+template <bool PAIR>
+__device__ __forceinline__ void mx_commit(uint32_t elected, uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.u32 e, %2, 0;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+            bar),
+        "h"((uint16_t)3), "r"(elected)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.u32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(elected)
+        : "memory");
+}
+
+// The same on a barrier of this CTA alone.
+template <bool PAIR>
+__device__ __forceinline__ void mx_commit_local(uint32_t elected, uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.u32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+        "r"(elected)
+        : "memory");
+  else
+    mx_commit<false>(elected, bar);
+}
+
+// The copies of common.cuh and the expectation of their bytes, predicated the same way;
+// shared-memory operands as addresses.
+__device__ __forceinline__ void expect_tx_elect(uint32_t elected, uint32_t bar, uint32_t bytes) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.u32 e, %2, 0;\n\t"
+      "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+      "r"(bytes), "r"(elected)
       : "memory");
 }
-// Arrive on `bar` once the MMAs issued so far by this thread have completed.
-__device__ __forceinline__ void mx_commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void bulk_load_elect(uint32_t elected, uint32_t dst, const void* src, uint32_t bytes,
+                                                uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.u32 e, %4, 0;\n\t"
+      "@e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(bar), "r"(elected)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_2d_elect(uint32_t elected, uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                                  uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.u32 e, %5, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "r"(elected)
+      : "memory");
 }
 
-template <int kCols>
+// A ring of n slots: the current one and the parity of its current use.
+struct RingPos {
+  uint32_t slot = 0, phase = 0;
+  __device__ __forceinline__ void next(uint32_t n) {
+    if (++slot == n) {
+      slot = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
+template <bool PAIR, int kCols>
 __device__ __forceinline__ void tmem_alloc(uint32_t* where) {
-  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "n"(kCols)
-               : "memory");
-  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  if (PAIR) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "n"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  } else {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(where)), "n"(kCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
 }
-template <int kCols>
+template <bool PAIR, int kCols>
 __device__ __forceinline__ void tmem_dealloc(uint32_t tmem) {
-  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols) : "memory");
+  if (PAIR)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols) : "memory");
+  else
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols) : "memory");
 }
 
-// Columns from the calling warp's 32 lanes (taddr names them): one register per column.
-__device__ __forceinline__ void tmem_st1(uint32_t t, uint32_t a) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};" ::"r"(t), "r"(a) : "memory");
+// The words of 128 rows at `tile`, read by all lanes (rows 4 l .. 4 l + 3 to lane l), and
+// written back as row r's word at byte (r % 32) * 16 + (r / 32) * 4.  Between the two the
+// warp synchronises.
+__device__ __forceinline__ uint4 mx_scale_words(const uint8_t* tile, int lane) {
+  return reinterpret_cast<const uint4*>(tile)[lane];
 }
-__device__ __forceinline__ void tmem_st4(uint32_t t, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1, %2, %3, %4};" ::"r"(t), "r"(v[0]), "r"(v[1]),
-               "r"(v[2]), "r"(v[3])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_st8(uint32_t t, const uint32_t* v) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(t), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-               : "memory");
+__device__ __forceinline__ void mx_put_scale_words(uint8_t* tile, uint4 w, int lane) {
+  uint32_t* p = reinterpret_cast<uint32_t*>(tile) + (lane & 7) * 16 + (lane >> 3);
+  p[0] = w.x;
+  p[4] = w.y;
+  p[8] = w.z;
+  p[12] = w.w;
 }
 
-// The MMAs of one 256-deep stage: `steps` (1..4) of 64 elements.  sfa and sfb are the first
-// columns of the stage's scales, a plane of 128 elements every sfa_plane / sfb_plane columns.
-__device__ __forceinline__ void mx_mma_stage(uint32_t d, uint32_t a_smem, uint32_t b_smem, uint32_t idesc, uint32_t sfa,
-                                             uint32_t sfa_plane, uint32_t sfb, uint32_t sfb_plane, int steps,
-                                             uint32_t accumulate) {
-  const uint64_t a = sw128_desc(a_smem), b = sw128_desc(b_smem);
-#pragma unroll
-  for (int k = 0; k < 4; ++k)
-    if (k < steps)
-      mx_mma(d, a + 2 * k, b + 2 * k, idesc | mx_idesc_half(k & 1), sfa + (k >> 1) * sfa_plane,
-             sfb + (k >> 1) * sfb_plane, k ? 1u : accumulate);
+// 512 bytes of arranged scale words -> four tensor-memory columns, in each of the four lane
+// groups (and, PAIR, in both CTAs from their own shared memory).
+template <bool PAIR>
+__device__ __forceinline__ void mx_copy_scales(uint32_t elected, uint32_t taddr, uint32_t saddr) {
+  // unswizzled: groups of 8 rows of 16 bytes, 128 bytes apart
+  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.u32 e, %2, 0;\n\t"
+        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc), "r"(elected)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.u32 e, %2, 0;\n\t"
+        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+        "l"(desc), "r"(elected)
+        : "memory");
+}
+
+// Two MMAs: 128 elements of depth, `half` (0, 1) of a 256-deep stage.
+template <bool PAIR>
+__device__ __forceinline__ void mx_mma2(uint32_t elected, uint32_t d, uint64_t a, uint64_t b, int half, uint32_t idesc,
+                                        uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+  mx_mma<PAIR>(elected, d, a + 4 * half, b + 4 * half, idesc, sfa, sfb, accumulate);
+  mx_mma<PAIR>(elected, d, a + 4 * half + 2, b + 4 * half + 2, idesc | mx_idesc_half(1), sfa, sfb, 1u);
 }
 
 // wait_or_abort by a whole warp: every lane gets the same answer, so that no lane leaves a
 // sequence of warp-wide instructions alone.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int32_t* status) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, status));
 }
 

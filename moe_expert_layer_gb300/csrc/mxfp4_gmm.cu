@@ -2,51 +2,59 @@
 // (tcgen05.mma kind::mxf4), with SwiGLU and requantisation behind it where asked, and the
 // probability-weighted sum of a token's rows (include/moe_mxfp4.h).
 //
-// A work item is (expert, 128-channel block, tile of up to NT rows).  The weight channels
-// are the MMA's 128 rows (operand A), the token rows its N columns (operand B), so the
-// ragged side is the one whose size the instruction takes in steps of 16: an expert of cnt
-// rows is cut into ceil(cnt / NT) tiles of equal size rounded up to 16.  One persistent CTA
-// per SM; items are dealt out expert-major, channel blocks innermost, so that CTAs working
-// at the same time share an expert's rows and its weights through L2.
+// A work item is (expert, channel block, tile of up to NT rows).  The weight channels are the
+// MMA's rows (operand A), the token rows its N columns (operand B), so the ragged side is the
+// one whose size the instruction takes in steps of 16 (32 for a pair): an expert of cnt rows is
+// cut into ceil(cnt / NT) tiles of equal size rounded up to that step.  Items are dealt out expert-major,
+// channel blocks innermost, so that CTAs working at the same time share an expert's rows and
+// its weights through L2.  Persistent CTAs, one per SM, in two forms:
+//   - few rows per expert: single CTAs, 128 channels, tiles of up to 32 rows: the weights
+//     stream past;
+//   - more: CTA pairs (cta_group::2), 256 channels, tiles of up to 192 rows.  Each CTA loads
+//     half of the rows: the copies through shared memory, which bound a single CTA's 128 x 208
+//     (325 us at 49152 rows, N = 2816, D = 4096, 64 experts), are fewer for each MMA.
+// A tile starts on a multiple of four rows (a 16-byte boundary of the scale words), so an
+// expert's first one may begin with up to three rows of the expert before, not stored.
 //
 // Roles: warp 0 loads, per 256-deep stage, one 17408-byte copy of a weight block with its
 // scales and the rows' words of the two scale planes; warp 2 loads the rows' codes, in tensor
-// copies of 128, 64 and 32 rows; warp 1 issues the MMAs; warps 4-7 move the stage's scales from
-// shared into tensor memory; warps 8-15 are two epilogue groups, each owning one of the two
-// accumulators.  A copy instruction holds its thread 65-90 cycles, a stage's MMAs take 600 at
-// 208 rows: few copies, from two threads.  (Product of 49152 rows, N = 2816, D = 4096, 64
-// experts: all copies from one warp in boxes of 32 rows 402 us; scale words read from global
-// memory by the scale warps 1754 us.)
-// Every wait is bounded:
-// one that gives up records MOE_ERR_TIMEOUT and the CTA winds down.
+// copies of 64, 32 and 16 rows; warps 4-7 in turn put a stage's scale words in tensor-memory order;
+// warp 1 issues the copies of the scales and the MMAs; warps 8-23 are four epilogue groups, two
+// for each of the two accumulators, taking its columns in turn, 16 at a time.  Every wait is bounded: one that gives up records
+// MOE_ERR_TIMEOUT and the CTA winds down.
 #include "mx_tc.cuh"
 #include "tensor_map.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 768;
 constexpr int kWeightWarp = 0, kMmaWarp = 1, kTokenWarp = 2, kScaleWarp0 = 4, kEpiWarp0 = 8;
 constexpr int kMaxExperts = 1024;
-constexpr int kXchgBytes = 4 * 4 * 2 * 8 * 32 * 4 / 2;  // 4 warp pairs x 2 buffers x 2 directions of [8][32] fp32
+constexpr int kEpiGroups = 4, kEpiBytes = 4096;  // an epilogue group's shared memory
 
-template <int NT>
+template <int NT, bool PAIR>
 struct Cfg {
-  // words of a scale plane: NT rows from a row rounded down to 4 (a 16-byte boundary)
-  static constexpr int kPlaneWords = (NT + 31) / 32 * 32 + 4;
-  static constexpr int kScales = kMxBlockBytes + NT * 128;  // of a stage: the planes' words
-  static constexpr int kStageBytes = kScales + (2 * kPlaneWords * 4 + 1023) / 1024 * 1024;
-  static constexpr int kStages = NT <= 32 ? 8 : 4;
-  static constexpr int kSfbPlane = NT > 128 ? 8 : 4;     // columns per 128 elements of depth
-  static constexpr int kSfCols = 8 + 2 * kSfbPlane;      // tensor-memory columns of a stage's scales
-  // stages whose scales are in tensor memory at once: a stage's commit arrives ~500 cycles
-  // after its last MMA is issued, and putting the next scales there takes ~250 more
-  static constexpr int kSfStages = 4;
+  static constexpr int kStep = PAIR ? 32 : 16;         // of the MMA's columns
+  static constexpr int kCtaRows = PAIR ? NT / 2 : NT;  // token rows in a CTA's shared memory
+  static constexpr int kRowTiles = (NT + 127) / 128;      // 128-row tiles of the rows' scale words
+  static constexpr int kPlaneWords = 128 * kRowTiles;
+  static constexpr int kScales = kMxBlockBytes + kCtaRows * 128;  // of a stage: the rows' scale words
+  static constexpr int kStageBytes = kScales + 2 * kPlaneWords * 4;
+  static constexpr int kStages = PAIR ? 6 : 8;
+  static constexpr int kSfbPlane = 4 * kRowTiles;        // tensor-memory columns per 128 elements of depth
+  static constexpr int kSfCols = 8 + 2 * kSfbPlane;      // and of a stage's scales
+  // Stages whose scales are in tensor memory.  Copies are executed before the MMAs that
+  // follow them, but not after the MMAs that precede them: a slot is written again only when
+  // the MMAs of the stage that used it have completed.
+  static constexpr int kSfStages = 5;
   static constexpr int kSf0 = 2 * NT;                    // accumulators in columns [0, 2 NT)
   static constexpr int kTmemCols = (kSf0 + kSfStages * kSfCols) <= 128 ? 128 : (kSf0 + kSfStages * kSfCols) <= 256 ? 256 : 512;
-  static constexpr int kSmem = kStages * kStageBytes + kXchgBytes + 1024;
-  static_assert(NT % 16 == 0 && kSf0 + kSfStages * kSfCols <= 512, "tensor memory");
-  static_assert(kStageBytes % 1024 == 0 && kSmem + 10 * 1024 <= 227 * 1024, "shared memory");
+  static constexpr int kSmem = kStages * kStageBytes + kEpiGroups * kEpiBytes + 1024;
+  static_assert(kSfStages < kStages, "a stage's scale columns are waited for after its slot's last use");
+  static_assert(NT % kStep == 0 && kSf0 + kSfStages * kSfCols <= 512, "tensor memory");
+  static_assert(kMxBlockBytes % 1024 == 0 && kScales % 128 == 0 && kStageBytes % 1024 == 0, "swizzled rows");
+  static_assert(kSmem + 8704 <= 227 * 1024, "shared memory, with ~8.5 KB static");
 };
 
 struct GmmArgs {
@@ -60,28 +68,33 @@ struct GmmArgs {
   int32_t* status;
 };
 
-// Tensor maps of the codes, 256 elements x 128, 64, 32 and 16 rows (a tile's rows, a multiple
-// of 16, are copied as a sum of them), and of the scale words, 2 planes x kPlaneWords rows.
-constexpr int kBoxes = 4;
+// Tensor maps of the codes, 256 elements x 64, 32 and 16 rows (a CTA's rows of a tile, a
+// multiple of 16, are copied as a sum of them), of the scale words, 2 planes x kPlaneWords rows,
+// and of the output.
+constexpr int kBoxes = 3, kBoxRows = 64;
 struct Maps {
-  CUtensorMap box[kBoxes], scales;
+  CUtensorMap box[kBoxes], scales, c;  // c: the output, 128 channels x 16 rows
 };
 
 struct Item {
-  int e, nb, row0, rows, n;  // n: MMA columns, rows rounded up to 16
+  int e, cb, row0, rows, skip, n;  // the first `skip` rows are another expert's; n: MMA columns
 };
 
 struct WorkList {
   const int* pref;  // first item of each expert; pref[E] = their number
   const int* end;   // last row of each expert + 1
-  int NB, E;
+  int CB, E;        // channel blocks (of a CTA or a pair), experts
 };
 
-// Row tiles of an expert of cnt rows, and their size.  (t - 1) * size < cnt: none is empty.
+// Row tiles of an expert with rows [start, end), from start rounded down to 4.  With t tiles
+// of `size` rows (a multiple of the step, at most NT), (t - 1) * size is less than their number:
+// none is empty.
 template <int NT>
-__device__ __forceinline__ int tiles_of(int cnt) { return (cnt + NT - 1) / NT; }
+__device__ __forceinline__ int tiles_of(int start, int end) {
+  return end > start ? (end - (start & ~3) + NT - 1) / NT : 0;
+}
 
-template <int NT>
+template <int NT, int STEP>
 __device__ __forceinline__ Item decode_item(int j, const WorkList& wl, int& e_hint) {
   int lo = e_hint, hi = wl.E;  // pref[lo] <= j < pref[hi]
   while (hi - lo > 1) {
@@ -89,15 +102,16 @@ __device__ __forceinline__ Item decode_item(int j, const WorkList& wl, int& e_hi
     if (wl.pref[mid] <= j) lo = mid; else hi = mid;
   }
   e_hint = lo;
-  const int start = lo ? wl.end[lo - 1] : 0, cnt = wl.end[lo] - start;
-  const int t = tiles_of<NT>(cnt), size = ((cnt + t - 1) / t + 15) & ~15;
-  const int local = j - wl.pref[lo], rt = local / wl.NB;
+  const int start = lo ? wl.end[lo - 1] : 0, end = wl.end[lo], start4 = start & ~3;
+  const int t = tiles_of<NT>(start, end), size = ((end - start4 + t - 1) / t + STEP - 1) & -STEP;
+  const int local = j - wl.pref[lo], rt = local / wl.CB;
   Item it;
   it.e = lo;
-  it.nb = local - rt * wl.NB;
-  it.row0 = start + rt * size;
-  it.rows = min(size, cnt - rt * size);
-  it.n = (it.rows + 15) & ~15;
+  it.cb = local - rt * wl.CB;
+  it.row0 = start4 + rt * size;
+  it.rows = min(size, end - it.row0);
+  it.skip = max(start - it.row0, 0);
+  it.n = (it.rows + STEP - 1) & -STEP;
   return it;
 }
 
@@ -115,18 +129,20 @@ __device__ __forceinline__ bool group_all(int id, bool ok) {
   return r != 0;
 }
 
-template <int NT, bool SWIGLU>
+template <int NT, bool SWIGLU, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gmm_kernel(const __grid_constant__ Maps maps, const GmmArgs a) {
-  using C = Cfg<NT>;
-  constexpr int S = C::kStages, SF = C::kSfStages;
+  using C = Cfg<NT, PAIR>;
+  constexpr int S = C::kStages;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], sf_bar[SF], accfull_bar[2], accempty_bar[2], final_bar;
+  __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], sf_bar[S], accfull_bar[2], accempty_bar[2], final_bar;
   __shared__ int s_pref[kMaxExperts + 1], s_end[kMaxExperts], s_wsum[kThreads / 32];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_issued[2];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int E = a.E, NB = a.N / 128, KB = a.KB;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int E = a.E, NB = a.N / 128, KB = a.KB, CB = PAIR ? (NB + 1) / 2 : NB;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
   volatile int* abort_flag = &s_abort;
 
   // ---- work list, barriers, tensor memory
@@ -138,7 +154,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hi = min(max(__ldg(a.cumsum + e), 0), a.R);
       const int lo = e ? min(max(__ldg(a.cumsum + e - 1), 0), a.R) : 0;
       s_end[e] = hi;
-      local += tiles_of<NT>(max(hi - lo, 0)) * NB;
+      local += tiles_of<NT>(lo, hi) * CB;
     }
     int incl = local;
 #pragma unroll
@@ -152,18 +168,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       s_issued[0] = s_issued[1] = 0;
     }
     if (warp == kMmaWarp) {
-      tmem_alloc<C::kTmemCols>(&s_tmem);
+      tmem_alloc<PAIR, C::kTmemCols>(&s_tmem);
       if (lane == 0) {
         for (int b = 0; b < kBoxes; ++b) prefetch_tmap(&maps.box[b]);
         prefetch_tmap(&maps.scales);
+        if (!SWIGLU) prefetch_tmap(&maps.c);
         for (int s = 0; s < S; ++s) {
           mbar_init(&full_bar[s], 2);
           mbar_init(&empty_bar[s], 1);
         }
-        for (int s = 0; s < SF; ++s) mbar_init(&sf_bar[s], 4);
+        for (int s = 0; s < S; ++s) mbar_init(&sf_bar[s], PAIR ? 2 : 1);
         for (int s = 0; s < 2; ++s) {
           mbar_init(&accfull_bar[s], 1);
-          mbar_init(&accempty_bar[s], 4);
+          mbar_init(&accempty_bar[s], PAIR ? 16 : 8);
         }
         mbar_init(&final_bar, 1);
         fence_barrier_init();
@@ -175,16 +192,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int w = 0; w < warp; ++w) run += s_wsum[w];
     for (int e = e0; e < e1; ++e) {
       s_pref[e] = run;
-      run += tiles_of<NT>(max(s_end[e] - (e ? s_end[e - 1] : 0), 0)) * NB;
+      run += tiles_of<NT>(e ? s_end[e - 1] : 0, s_end[e]) * CB;
     }
     if (e0 < E && e1 == E) s_pref[E] = run;
   }
   __syncthreads();
+  __syncwarp();
+  if (PAIR) cluster_sync_all();  // the peer's barriers and tensor memory are ready
   tc_fence_after();
   WorkList wl;
   wl.pref = s_pref;
   wl.end = s_end;
-  wl.NB = NB;
+  wl.CB = CB;
   wl.E = E;
   const int total = s_pref[E];
   const uint32_t tmem = s_tmem;
@@ -194,167 +213,206 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int planes = (a.D + 127) / 128;
 
   if (warp == kWeightWarp || warp == kTokenWarp) {
-    if (lane == 0) {
-      int n = 0, e_hint = 0;
-      bool ok = true;
-      for (int j = blockIdx.x; ok && j < total; j += gridDim.x) {
-        const Item it = decode_item<NT>(j, wl, e_hint);
-        const uint8_t* wb = a.w + ((size_t)it.e * NB + it.nb) * (size_t)KB * kMxBlockBytes;
-        for (int kb = 0; kb < KB; ++kb, ++n) {
-          const int slot = n % S;
-          if (!(ok = wait_or_abort(&empty_bar[slot], ((n / S) & 1) ^ 1, abort_flag, a.status))) break;
-          uint8_t* st = ring_g + slot * C::kStageBytes;
-          uint64_t* bar = &full_bar[slot];
-          if (warp == kWeightWarp) {
-            mbar_arrive_expect_tx(bar, kMxBlockBytes + 2 * C::kPlaneWords * 4);
-            bulk_load(st, wb + (size_t)kb * kMxBlockBytes, kMxBlockBytes, bar);
-            tma_load_2d(st + C::kScales, &maps.scales, it.row0 & ~3, 2 * kb, bar);
-          } else {
-            mbar_arrive_expect_tx(bar, (uint32_t)it.n * 128);
-            int r = 0;
-#pragma unroll
-            for (int b = 0; b < kBoxes; ++b) {
-              const int rows = 128 >> b;
-              for (; it.n - r >= rows; r += rows)
-                tma_load_2d(st + kMxBlockBytes + r * 128, &maps.box[b], kb * 128, it.row0 + r, bar);
-            }
-          }
-        }
-      }
-      s_issued[warp == kTokenWarp] = n;
-    }
-  } else if (warp == kMmaWarp) {
-    if (lane == 0) {
-      int n = 0, e_hint = 0, u = 0;
-      bool ok = true;
-      for (int j = blockIdx.x; ok && j < total; j += gridDim.x, ++u) {
-        const Item it = decode_item<NT>(j, wl, e_hint);
-        const int buf = u & 1;
-        if (!(ok = wait_or_abort(&accempty_bar[buf], ((u >> 1) & 1) ^ 1, abort_flag, a.status))) break;
-        tc_fence_after();
-        const uint32_t idesc = mx_idesc(it.n), d = tmem + buf * NT;
-        for (int kb = 0; kb < KB; ++kb, ++n) {
-          const int slot = n % S, sf = n % SF;
-          // the scale warps arrive after they have seen the stage's copies complete
-          if (!(ok = wait_or_abort(&sf_bar[sf], (n / SF) & 1, abort_flag, a.status))) break;
-          tc_fence_after();
-          const uint32_t st = ring + slot * C::kStageBytes, t_sf = tmem + C::kSf0 + sf * C::kSfCols;
-          mx_mma_stage(d, st, st + kMxBlockBytes, idesc, t_sf, 4, t_sf + 8, C::kSfbPlane,
-                       min(4, (a.D - kb * 256 + 63) >> 6), kb ? 1u : 0u);
-          mx_commit(&empty_bar[slot]);
-        }
-        if (ok) mx_commit(&accfull_bar[buf]);
-      }
-      mx_commit(&final_bar);  // every MMA done before tensor memory is freed
-      mbar_wait_sleep_bounded(&final_bar, 0);
-    }
-  } else if (warp >= kScaleWarp0 && warp < kScaleWarp0 + 4) {
-    constexpr int J = (NT + 31) / 32;
-    const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // 32 * (warp % 4) in the lane field
-    const uint32_t last_mask = a.D % 128 ? (1u << (a.D % 128 / 4)) - 1u : 0xffffffffu;  // bytes past D are no scales
+    const uint32_t elected = elect_one();
+    RingPos at;
     int n = 0, e_hint = 0;
     bool ok = true;
-    for (int j = blockIdx.x; ok && j < total; j += gridDim.x) {
-      const Item it = decode_item<NT>(j, wl, e_hint);
-      const int skew = it.row0 & 3;
-      for (int kb = 0; kb < KB; ++kb, ++n) {
-        const int slot = n % S, sf = n % SF;
-        if (!(ok = warp_wait(&full_bar[slot], (n / S) & 1, abort_flag, a.status))) break;
-        const uint8_t* st = ring_g + slot * C::kStageBytes;
-        const uint32_t* ws = reinterpret_cast<const uint32_t*>(st + kMxCodeBytes) + lane;
-        const uint32_t* xs = reinterpret_cast<const uint32_t*>(st + C::kScales) + skew + lane;
-        uint32_t av[8], bv[2][C::kSfbPlane] = {};
+    for (int j = first; ok && j < total; j += stride) {
+      const Item it = decode_item<NT, C::kStep>(j, wl, e_hint);
+      // a pair's second block past the last channel reads the last one again (not stored)
+      const int nb = PAIR ? min(2 * it.cb + (int)rank, NB - 1) : it.cb;
+      const uint8_t* wb = a.w + ((size_t)it.e * NB + nb) * (size_t)KB * kMxBlockBytes;
+      const int cta_rows = PAIR ? it.n / 2 : it.n, row0 = it.row0 + (int)rank * cta_rows;
+      for (int kb = 0; kb < KB; ++kb, ++n, at.next(S)) {
+        if (!(ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status))) break;
+        const uint32_t st = ring + at.slot * C::kStageBytes, bar = smem_u32(&full_bar[at.slot]);
+        if (warp == kWeightWarp) {
+          expect_tx_elect(elected, bar, kMxBlockBytes + 2 * C::kPlaneWords * 4);
+          bulk_load_elect(elected, st, wb + (size_t)kb * kMxBlockBytes, kMxBlockBytes, bar);
+          tma_load_2d_elect(elected, st + C::kScales, &maps.scales, it.row0, 2 * kb, bar);
+        } else {
+          expect_tx_elect(elected, bar, (uint32_t)cta_rows * 128);
+          int r = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) av[i] = ws[32 * i];
-        // words past the item's rows scale columns whose sums are never read
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int i = 0; i < J; ++i) {
-            bv[q][i] = xs[q * C::kPlaneWords + 32 * i];
-            if (2 * kb + q == planes - 1) bv[q][i] &= last_mask;
+          for (int b = 0; b < kBoxes; ++b) {
+            const int rows = kBoxRows >> b;
+            for (; cta_rows - r >= rows; r += rows)
+              tma_load_2d_elect(elected, st + kMxBlockBytes + r * 128, &maps.box[b], kb * 128, row0 + r, bar);
           }
-        // the scale columns are free once the MMAs of stage n - SF are done
-        if (n >= SF) {
-          const int m = n - SF;
-          if (!(ok = warp_wait(&empty_bar[m % S], (m / S) & 1, abort_flag, a.status))) break;
+        }
+      }
+    }
+    // the last stages' releases: commits arrive in both CTAs of a pair, and neither may leave
+    // before an arrival that is still on its way to it
+    for (int s = 0; ok && s < S; ++s, at.next(S)) ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status);
+    if (lane == 0) s_issued[warp == kTokenWarp] = n;
+  } else if (warp == kMmaWarp) {
+    if (rank == 0) {
+      const uint32_t elected = elect_one(), t0 = __shfl_sync(0xffffffffu, tmem, 0);
+      RingPos at, sf;
+      int e_hint = 0, u = 0;
+      bool ok = true;
+      for (int j = first; ok && j < total; j += stride, ++u) {
+        const Item it = decode_item<NT, C::kStep>(j, wl, e_hint);
+        const int buf = u & 1;
+        if (!(ok = warp_wait(&accempty_bar[buf], ((u >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+        tc_fence_after();
+        const uint32_t idesc = mx_idesc(PAIR ? 256 : 128, it.n), d = t0 + buf * NT;
+        const int last = (a.D - (KB - 1) * 256 + 127) >> 7;  // 128-deep halves of the last stage
+        for (int kb = 0; kb < KB; ++kb, at.next(S), sf.next(C::kSfStages)) {
+          // the scale warps arrive after they have seen the stage's copies complete
+          if (!(ok = warp_wait(&sf_bar[at.slot], at.phase, abort_flag, a.status))) break;
           tc_fence_after();
-        }
-        const uint32_t t = tmem + lanes + C::kSf0 + sf * C::kSfCols;
-        tmem_st8(t, av);
+          const uint32_t st = ring + at.slot * C::kStageBytes, t_sf = t0 + C::kSf0 + sf.slot * C::kSfCols;
+          const uint64_t da = sw128_desc(st), db = sw128_desc(st + kMxBlockBytes);
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (C::kSfbPlane == 8) tmem_st8(t + 8 + q * C::kSfbPlane, bv[q]);
-          else if (J == 1) tmem_st1(t + 8 + q * C::kSfbPlane, bv[q][0]);
-          else tmem_st4(t + 8 + q * C::kSfbPlane, bv[q]);
+          for (int q = 0; q < 2; ++q) {
+            mx_copy_scales<PAIR>(elected, t_sf + 4 * q, st + kMxCodeBytes + 512 * q);
+#pragma unroll
+            for (int h = 0; h < C::kRowTiles; ++h)
+              mx_copy_scales<PAIR>(elected, t_sf + 8 + C::kSfbPlane * q + 4 * h,
+                                   st + C::kScales + (C::kRowTiles * q + h) * 512);
+          }
+          mx_mma2<PAIR>(elected, d, da, db, 0, idesc, t_sf, t_sf + 8, kb ? 1u : 0u);
+          if (kb < KB - 1 || last == 2)
+            mx_mma2<PAIR>(elected, d, da, db, 1, idesc, t_sf + 4, t_sf + 8 + C::kSfbPlane, 1u);
+          mx_commit<PAIR>(elected, smem_u32(&empty_bar[at.slot]));
         }
-        tmem_wait_st();
-        tc_fence_before();
-        if (lane == 0) mbar_arrive(&sf_bar[sf]);
+        if (ok) mx_commit<PAIR>(elected, smem_u32(&accfull_bar[buf]));
+      }
+      mx_commit_local<PAIR>(elected, smem_u32(&final_bar));  // every MMA done before tensor memory is freed
+      mbar_wait_sleep_bounded(&final_bar, 0);
+    }
+  } else if (warp >= kScaleWarp0 && warp < kEpiWarp0) {
+    // bytes of the last plane past D are no scales
+    const uint32_t last_mask = a.D % 128 ? (1u << (a.D % 128 / 4)) - 1u : 0xffffffffu;
+    RingPos at, old;  // old: the stage kSfStages before
+    int n = 0;
+    bool ok = true;
+    for (int j = first; ok && j < total; j += stride) {
+      for (int kb = 0; kb < KB; ++kb, ++n, at.next(S)) {
+        if (n > C::kSfStages) old.next(S);
+        if ((n & 3) != warp - kScaleWarp0) continue;
+        // The scale columns are free once the MMAs of the stage that used them are done.  This wait
+        // comes first for another reason too: a warp that takes every fourth stage has not itself
+        // seen the slot's previous copies complete, and copies complete in any order; only after
+        // that stage's MMAs is the barrier known to be in this use's phase.
+        if (n >= C::kSfStages && !(ok = warp_wait(&empty_bar[old.slot], old.phase, abort_flag, a.status))) break;
+        if (!(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status))) break;
+        uint8_t* st = ring_g + at.slot * C::kStageBytes;
+        uint4 w[2 + 2 * C::kRowTiles];
+#pragma unroll
+        for (int i = 0; i < 2 + 2 * C::kRowTiles; ++i) {
+          w[i] = mx_scale_words(i < 2 ? st + kMxCodeBytes + 512 * i : st + C::kScales + 512 * (i - 2), lane);
+          const int q = (i - 2) / C::kRowTiles;
+          if (i >= 2 && 2 * kb + q == planes - 1) {
+            w[i].x &= last_mask;
+            w[i].y &= last_mask;
+            w[i].z &= last_mask;
+            w[i].w &= last_mask;
+          }
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2 + 2 * C::kRowTiles; ++i)
+          mx_put_scale_words(i < 2 ? st + kMxCodeBytes + 512 * i : st + C::kScales + 512 * (i - 2), w[i], lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) mbar_arrive_remote(cluster_addr(&sf_bar[at.slot], 0)); else mbar_arrive(&sf_bar[at.slot]);
+        }
       }
     }
   } else if (warp >= kEpiWarp0) {
-    const int group = (warp - kEpiWarp0) >> 2, quarter = warp & 3;
-    const uint32_t lanes = (uint32_t)quarter << 21;
+    const int group = (warp - kEpiWarp0) >> 2, quarter = warp & 3, buf = group & 1;
+    const uint32_t lanes = (uint32_t)quarter << 21;  // 32 * quarter in the lane field
+    uint8_t* own = ring_g + S * C::kStageBytes + group * kEpiBytes;
     int e_hint = 0;
-    for (int u = group, j = blockIdx.x + group * gridDim.x; j < total; j += 2 * gridDim.x, u += 2) {
-      const Item it = decode_item<NT>(j, wl, e_hint);
-      bool ok = warp_wait(&accfull_bar[group], (u >> 1) & 1, abort_flag, a.status);
-      if (SWIGLU) ok = group_all(1 + group, ok);  // the group's warps wait for one another below
+    for (int u = buf, j = first + buf * stride; j < total; j += 2 * stride, u += 2) {
+      const Item it = decode_item<NT, C::kStep>(j, wl, e_hint);
+      bool ok = warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status);
+      ok = group_all(9 + group, ok);  // the group's warps wait for one another below
       if (!ok) break;
       tc_fence_after();
-      const uint32_t t = tmem + lanes + group * NT;
+      const uint32_t t = tmem + lanes + buf * NT;
+      const int nb = PAIR ? 2 * it.cb + (int)rank : it.cb;
+      const int rows = nb < NB ? it.rows : 0;  // a pair's block past the last channel stores nothing
+      const int skip = it.skip;
       if (!SWIGLU) {
-        __half* out = a.c + (size_t)it.row0 * a.N + it.nb * 128 + quarter * 32 + lane;
-        for (int c0 = 0; c0 < it.n; c0 += 16) {
+        // 16 rows x 128 channels of binary16 gathered in shared memory and stored from there by one
+        // tensor copy, or, where the tile's first or last rows are not its own, row by row
+        for (int c0 = 16 * (group >> 1); c0 < it.n; c0 += 32) {
           uint32_t v[16];
+          __syncwarp();
           tmem_ld16(t + c0, v);
+          if (quarter == 0) bulk_wait_read_all();
           tmem_wait_ld();
+          asm volatile("bar.sync %0, 128;" ::"r"(9 + group) : "memory");
+          __half* o = reinterpret_cast<__half*>(own) + quarter * 32 + lane;
 #pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (c0 + i < it.rows) out[(size_t)(c0 + i) * a.N] = from_f32<__half>(__uint_as_float(v[i]));
+          for (int i = 0; i < 16; i += 2) {
+            const __half2 h = f2h2_sat(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            o[i * 128] = __low2half(h);
+            o[i * 128 + 128] = __high2half(h);
+          }
+          fence_proxy_async_smem();
+          asm volatile("bar.sync %0, 128;" ::"r"(9 + group) : "memory");
+          if (quarter == 0) {
+            if (c0 >= skip && c0 + 16 <= rows) {
+              if (lane == 0) tma_store_2d(&maps.c, nb * 128, it.row0 + c0, own);
+            } else if (lane < 16 && c0 + lane >= skip && c0 + lane < rows) {
+              bulk_store(a.c + (size_t)(it.row0 + c0 + lane) * a.N + nb * 128, own + lane * 256, 256);
+            }
+            bulk_commit_group();
+          }
         }
       } else {
         // warps in pairs: the even one holds 32 gate channels, the odd one the up channels
         // that multiply them.  Of 16 rows each finishes 8, with the other's half through
-        // shared memory (double-buffered: one pair barrier per 16 rows).
+        // shared memory.
         const int pair = (warp - kEpiWarp0) >> 1, odd = warp & 1;
-        float* x = reinterpret_cast<float*>(ring_g + S * C::kStageBytes) + pair * (2 * 2 * 256);
-        const int k = it.nb * 2 + ((quarter >> 1) & 1), I = a.N / 2;  // scaled block of h
-        for (int c0 = 0, p = 0; c0 < it.n; c0 += 16, p ^= 1) {
+        float* x = reinterpret_cast<float*>(own) + (pair & 1) * 512;
+        float* give = x + odd * 256 + lane;
+        const float* take = x + (odd ^ 1) * 256 + lane;
+        const int k = nb * 2 + (quarter >> 1), I = a.N / 2;  // scaled block of h
+        uint8_t* sc = a.h_scales + ((size_t)(k >> 2) * a.pitch + it.row0) * 4;
+        uint8_t* co = a.h_codes + (size_t)it.row0 * (I / 2) + k * 16 + (lane >> 3) * 4;
+        const bool tail = k == I / 32 - 1 && (k & 3) != 3;  // bytes of the word past the last block: 0
+        for (int c0 = 16 * (group >> 1); c0 < it.n; c0 += 32) {
           uint32_t v[16];
+          __syncwarp();
           tmem_ld16(t + c0, v);
           tmem_wait_ld();
-          float* give = x + p * 512 + odd * 256;
-          const float* take = x + p * 512 + (odd ^ 1) * 256;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) give[i * 32 + lane] = __uint_as_float(odd ? v[i] : v[8 + i]);
-          asm volatile("bar.sync %0, 64;" ::"r"(3 + pair) : "memory");
+          for (int i = 0; i < 8; ++i) give[i * 32] = __uint_as_float(odd ? v[i] : v[8 + i]);
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
           float h[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
-            const float o = take[i * 32 + lane];
+            const float o = take[i * 32];
             h[i] = odd ? mx_swiglu(o, __uint_as_float(v[8 + i])) : mx_swiglu(__uint_as_float(v[i]), o);
           }
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");  // both have taken
           uint32_t byte;
           const uint32_t w = mx_quant_rows8(h, lane, byte);
           const int r = c0 + odd * 8 + (lane & 7);
-          if (r < it.rows) {
-            const size_t row = (size_t)it.row0 + r;
-            *reinterpret_cast<uint32_t*>(a.h_codes + row * (I / 2) + k * 16 + (lane >> 3) * 4) = w;
+          if (r >= skip && r < rows) {
+            *reinterpret_cast<uint32_t*>(co + (size_t)r * (I / 2)) = w;
             if (lane < 8) {
-              uint8_t* sc = a.h_scales + ((size_t)(k >> 2) * a.pitch + row) * 4;
-              sc[k & 3] = (uint8_t)byte;
-              if (k == I / 32 - 1)
-                for (int z = (k & 3) + 1; z < 4; ++z) sc[z] = 0;
+              if (tail)
+                for (int z = (k & 3) + 1; z < 4; ++z) sc[r * 4 + z] = 0;
+              sc[r * 4 + (k & 3)] = (uint8_t)byte;
             }
           }
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&accempty_bar[group]);
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_remote(cluster_addr(&accempty_bar[buf], 0)); else mbar_arrive(&accempty_bar[buf]);
+      }
     }
+    if (!SWIGLU && quarter == 0) bulk_wait_all();  // stores done before shared memory is released
   }
 
   __syncthreads();
@@ -365,28 +423,33 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  __syncwarp();
+  if (PAIR) cluster_sync_all();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc<C::kTmemCols>(tmem);
+    tmem_dealloc<PAIR, C::kTmemCols>(tmem);
   }
 }
 
-template <int NT, bool SWIGLU>
+template <int NT, bool SWIGLU, bool PAIR>
 cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
-  using C = Cfg<NT>;
+  using C = Cfg<NT, PAIR>;
   Maps maps;
   const uint64_t half = (uint64_t)p.D / 2, rows = (uint64_t)p.R;
   for (int b = 0; b < kBoxes; ++b)
-    if (!encode_tensor_map_2d(&maps.box[b], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.codes, half, rows, 128, 128u >> b))
+    if (!encode_tensor_map_2d(&maps.box[b], CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.codes, half, rows, 128, (uint32_t)kBoxRows >> b))
       return cudaErrorInvalidValue;
   if (!encode_tensor_map_words(&maps.scales, p.scales, (uint64_t)mx_scale_pitch(p.R), (uint64_t)mx_scale_planes(p.D),
                                C::kPlaneWords, 2))
+    return cudaErrorInvalidValue;
+  if (!SWIGLU && !encode_tensor_map_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p.c, (uint64_t)p.N, rows, 128, 16,
+                                       CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   static PerContextOnce set;
   const int dev = current_device();
   if (set.needed(dev)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(mx_gmm_kernel<NT, SWIGLU>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        cudaFuncSetAttribute(mx_gmm_kernel<NT, SWIGLU, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     set.done(dev);
   }
@@ -404,8 +467,18 @@ cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   a.h_codes = p.h_codes;
   a.h_scales = reinterpret_cast<uint8_t*>(p.h_scales);
   a.status = p.status;
-  mx_gmm_kernel<NT, SWIGLU><<<sm_count(), kThreads, C::kSmem, stream>>>(maps, a);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(PAIR ? sm_count() & ~1 : sm_count()));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute cluster;
+  cluster.id = cudaLaunchAttributeClusterDimension;
+  cluster.val.clusterDim.x = PAIR ? 2 : 1;
+  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
+  cfg.attrs = &cluster;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mx_gmm_kernel<NT, SWIGLU, PAIR>, maps, a);
 }
 
 __global__ void mx_combine_kernel(const __half* c2, const int32_t* expanded, const float* probs, int K, int topK,
@@ -425,8 +498,8 @@ __global__ void mx_combine_kernel(const __half* c2, const int32_t* expanded, con
 
 cudaError_t launch_mx_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   if ((double)p.R / p.E <= 32.0)
-    return p.h_codes ? launch_gmm<32, true>(p, stream) : launch_gmm<32, false>(p, stream);
-  return p.h_codes ? launch_gmm<208, true>(p, stream) : launch_gmm<208, false>(p, stream);
+    return p.h_codes ? launch_gmm<32, true, false>(p, stream) : launch_gmm<32, false, false>(p, stream);
+  return p.h_codes ? launch_gmm<192, true, true>(p, stream) : launch_gmm<192, false, true>(p, stream);
 }
 
 cudaError_t launch_mx_combine(const uint16_t* c2, const int32_t* expanded, const float* probs, int M, int K, int topK,

@@ -1,9 +1,33 @@
-// Device helpers shared by the tcgen05 kernels: tensor-memory loads, fences, operand
-// descriptors and the bounded mbarrier waits of their pipelines.
+// Device helpers shared by the tcgen05 kernels: cluster addresses and barriers, tensor-memory
+// loads, fences, operand descriptors and the bounded mbarrier waits of their pipelines.
 #pragma once
 #include "common.cuh"
 
 namespace moe {
+
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync_all() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// shared::cluster address of the same shared variable in CTA `rank` of the cluster
+__device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+// Arrive on a barrier given by its shared::cluster address (either CTA of the pair).
+// Default semantics: an arrive with cluster-scope release costs ~320 cycles on
+// GB300, this one ~6; the data it publishes is tensor memory (ordered by
+// tcgen05.wait + tcgen05.fence) or TMA-written shared memory whose barrier the
+// signalling thread has already seen complete.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
 
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }

@@ -24,9 +24,10 @@ inline PFN_encodeTiled tensor_map_encoder() {
 }
 
 // 2-D row-major tensor [outer][inner] of `elem`-byte elements, box {box_inner, box_outer},
-// 128-byte swizzle, 256-byte L2 promotion, zero fill out of bounds.
+// 128-byte swizzle (or another), 256-byte L2 promotion, zero fill out of bounds.
 inline bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, size_t elem, const void* base,
-                                 uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer) {
+                                 uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer,
+                                 CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
   PFN_encodeTiled fn = tensor_map_encoder();
   if (!fn) return false;
   cuuint64_t dims[2] = {inner, outer};
@@ -34,7 +35,7 @@ inline bool encode_tensor_map_2d(CUtensorMap* m, CUtensorMapDataType dt, size_t 
   cuuint32_t box[2] = {box_inner, box_outer};
   cuuint32_t estr[2] = {1, 1};
   return fn(m, dt, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
