@@ -13,7 +13,8 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(OUT_DIR, "libmoe_layer.so")
 SOURCES = ["route_sort.cu", "elementwise.cu", "gemm_hmma.cu", "gemm_tc.cu", "gemm_dispatch.cu", "moe_layer.cu",
            "route_sort_noalloc.cu", "selftest.cu", "weight_tiles.cu",
-           "route_topk.cu", "mxfp4_quant.cu", "mxfp4_gmm.cu", "mxfp4_abi.cu"]
+           "route_topk.cu", "mxfp4_quant.cu", "mxfp4_gmm.cu", "mxfp4_few.cu",
+           "mxfp4_abi.cu"]
 HEADERS = ["abi_checks.h", "common.cuh", "kernels.h", "mx_tc.cuh", "mxfp4.cuh", "mxfp4.h", "swiglu.cuh", "tc_common.cuh",
            "tensor_map.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")

@@ -34,11 +34,11 @@ size_t gmm_workspace_bytes() { return kAlign; }
 
 // The layer's workspace.
 struct Layout {
-  size_t status, sorted, expanded, tpe, cumsum, sort_ws, a_codes, a_scales, h_codes, h_scales, c2, total;
+  size_t status, sorted, expanded, tpe, cumsum, sort_ws, a_codes, a_scales, h_codes, h_scales, c2, part, counters, total;
 };
 Layout layout_of(const moe_dims_t* d) {
   const size_t M = d->M, K = d->K, I = d->I, E = d->E, R = M * d->topK;
-  Layout L;
+  Layout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) {
     const size_t at = off;
@@ -46,6 +46,14 @@ Layout layout_of(const moe_dims_t* d) {
     return at;
   };
   L.status = take(gmm_workspace_bytes());
+  if (moe::mx_few(d->M, d->topK)) {
+    L.h_codes = take(R * (I / 2));
+    L.h_scales = take(R * (size_t)moe::mx_scale_planes((int)I) * 4);
+    L.part = take(moe::mx_few_part_bytes((int)M, (int)K));
+    L.counters = take(K / 128 * 4);
+    L.total = off;
+    return L;
+  }
   L.sorted = take(R * 4);
   L.expanded = take(R * 4);
   L.tpe = take(E * 4);
@@ -68,9 +76,29 @@ P* at(void* base, size_t off) {
 int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_idx, const float* probs,
                   const uint8_t* w1, const uint8_t* w2, uint16_t* out, void* ws, const Layout& L, cudaStream_t st) {
   const int M = d->M, K = d->K, I = d->I, E = d->E, topK = d->topK, R = M * topK;
+  cudaError_t e;
+  if (moe::mx_few(M, topK)) {
+    moe::MxFewProblem p;
+    p.M = M;
+    p.K = K;
+    p.I = I;
+    p.E = E;
+    p.topK = topK;
+    p.x = x;
+    p.expert_idx = expert_idx;
+    p.probs = probs;
+    p.w1 = w1;
+    p.w2 = w2;
+    p.h_codes = at<uint8_t>(ws, L.h_codes);
+    p.h_scales = at<uint32_t>(ws, L.h_scales);
+    p.part = at<float>(ws, L.part);
+    p.counters = at<int32_t>(ws, L.counters);
+    p.out = out;
+    p.status = at<int32_t>(ws, L.status);
+    return launch_status(moe::launch_mx_few(p, st));
+  }
   int32_t* expanded = at<int32_t>(ws, L.expanded);
   int32_t* cumsum = at<int32_t>(ws, L.cumsum);
-  cudaError_t e;
   if ((e = cudaMemsetAsync(ws, 0, 16, st)) != cudaSuccess) return launch_status(e);
   if ((e = moe::launch_route_sort(expert_idx, R, E, at<int32_t>(ws, L.sorted), expanded, at<int32_t>(ws, L.tpe), cumsum,
                                   at<void>(ws, L.sort_ws), st)) != cudaSuccess)
