@@ -52,20 +52,24 @@ cudaError_t launch_mx_gmm(const MxGemmProblem& p, cudaStream_t stream);
 // The layer for a few tokens in two kernels (mxfp4_few.cu).
 constexpr int kMxFewTokens = 32, kMxFewRoutes = 256;
 inline bool mx_few(int M, int topK) { return M <= kMxFewTokens && M * topK <= kMxFewRoutes; }
+bool mx_few_resident();  // whether its second kernel's CTAs, which wait for one another, fit the device at once
 struct MxFewProblem {
   int M, K, I, E, topK;
   const uint16_t* x;
   const int32_t* expert_idx;
   const float* probs;
   const uint8_t *w1, *w2;
+  uint8_t* x_codes;    // [M][K / 2]
+  uint32_t* x_scales;  // [M][planes(K)]
   uint8_t* h_codes;    // [M * topK][I / 2]
   uint32_t* h_scales;  // [M * topK][planes(I)]
   float* part;         // mx_few_part_bytes
-  int32_t* counters;   // [K / 128]
+  int32_t* counters;   // mx_few_counter_bytes
   uint16_t* out;
   int32_t* status;
 };
-size_t mx_few_part_bytes(int M, int K);
+size_t mx_few_part_bytes(int M);
+size_t mx_few_counter_bytes(int M, int K, int I, int topK);
 cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream);
 
 // out[t] = sum over j of probs[t][j] * c2[expanded[t * topK + j]] (entries < 0 skipped)

@@ -34,6 +34,7 @@ size_t gmm_workspace_bytes() { return kAlign; }
 
 // The layer's workspace.
 struct Layout {
+  // a few tokens: status, a_* (x), h_*, part, counters; behind them what the other path uses
   size_t status, sorted, expanded, tpe, cumsum, sort_ws, a_codes, a_scales, h_codes, h_scales, c2, part, counters, total;
 };
 Layout layout_of(const moe_dims_t* d) {
@@ -46,13 +47,10 @@ Layout layout_of(const moe_dims_t* d) {
     return at;
   };
   L.status = take(gmm_workspace_bytes());
-  if (moe::mx_few(d->M, d->topK)) {
-    L.h_codes = take(R * (I / 2));
-    L.h_scales = take(R * (size_t)moe::mx_scale_planes((int)I) * 4);
-    L.part = take(moe::mx_few_part_bytes((int)M, (int)K));
-    L.counters = take(K / 128 * 4);
-    L.total = off;
-    return L;
+  const bool few = moe::mx_few(d->M, d->topK);
+  if (few) {
+    L.part = take(moe::mx_few_part_bytes((int)M));
+    L.counters = take(moe::mx_few_counter_bytes((int)M, (int)K, (int)I, d->topK));
   }
   L.sorted = take(R * 4);
   L.expanded = take(R * 4);
@@ -77,7 +75,7 @@ int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_
                   const uint8_t* w1, const uint8_t* w2, uint16_t* out, void* ws, const Layout& L, cudaStream_t st) {
   const int M = d->M, K = d->K, I = d->I, E = d->E, topK = d->topK, R = M * topK;
   cudaError_t e;
-  if (moe::mx_few(M, topK)) {
+  if (moe::mx_few(M, topK) && moe::mx_few_resident()) {
     moe::MxFewProblem p;
     p.M = M;
     p.K = K;
@@ -89,6 +87,8 @@ int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_
     p.probs = probs;
     p.w1 = w1;
     p.w2 = w2;
+    p.x_codes = at<uint8_t>(ws, L.a_codes);
+    p.x_scales = at<uint32_t>(ws, L.a_scales);
     p.h_codes = at<uint8_t>(ws, L.h_codes);
     p.h_scales = at<uint32_t>(ws, L.h_scales);
     p.part = at<float>(ws, L.part);

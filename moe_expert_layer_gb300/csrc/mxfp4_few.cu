@@ -1,24 +1,26 @@
 // The MXFP4 expert layer for a few tokens (include/moe_mxfp4.h) in two kernels:
-//   1. gate and up products of every route, SwiGLU, h as MXFP4 rows by route;
-//   2. the down products of every route, weighted and summed into the tokens' outputs.
+//   1. x as MXFP4 rows, and the counters of the second kernel cleared;
+//   2. everything else: gate and up products of every route, SwiGLU, h as MXFP4 rows by
+//      route, down products, weighted sums of the tokens' routes.
 // Up to 32 tokens and 256 routes the layer's time is that of the active experts' weights
 // streaming past (17408 bytes per 128 channels x 256 reduction steps), so everything else is
-// done beside that stream: each CTA makes the routes' tables itself, x is quantised (and h
-// gathered) a 256-deep stage at a time straight into the MMA's operand, and no row is
+// done beside that stream: each CTA makes the routes' tables itself, and no row is
 // dispatched or permuted in memory.
 //
-// Both kernels are persistent, one CTA per SM, on the same pipeline: warp 0 copies weight
-// blocks; warps 4-7 in turn put a stage's weight scales in order and write its token rows;
-// warp 1 copies the scales to tensor memory and issues the MMAs, weight channels as rows,
-// up to 16 routes of one expert as columns; warps 8-11 take the sums.
-//   - Kernel 1 deals out (expert tile, 128-channel block) units.
-//   - Kernel 2 cuts the sequence (output block, expert tile, stage) into equal runs of
-//     stages, one per CTA: a run's sums add up in shared memory over experts and stages
-//     alike.  Where several runs meet in an output block each leaves its sum in the
-//     workspace, and the CTA that finishes last adds them in order of the runs.
-// Kernel 2 is launched as a programmatic dependent of kernel 1: its CTAs fit beside kernel
-// 1's, and its weights are on their way while kernel 1 still runs.
-// Every wait is bounded, as in the grouped product.
+// Kernel 2 is persistent, one CTA per SM, with one pipeline for both products, so that the
+// down projection's weights are on their way while the last of h is made: warp 0 copies
+// weight blocks; warps 4-7 in turn put a stage's weight scales in order and gather its token
+// rows into the MMA's operand; warp 1 copies the scales to tensor memory and issues the MMAs,
+// weight channels as rows, up to 16 routes of one expert as columns; warps 8-11 take the sums.
+// The stages of each product are cut into equal runs, one per CTA:
+//   - of (expert tile, 128-channel block, stage): where runs meet in a block each leaves its
+//     sums in the workspace, and the CTA that finishes last adds them in order of the runs,
+//     does the SwiGLU and counts the block on its tile;
+//   - of (output block, expert tile, stage), a tile's stages after all its blocks of h: a run's
+//     sums add up in shared memory over experts and stages alike, and meet the same way.
+// It is launched as a programmatic dependent of kernel 1: tables and first weights come while
+// that still runs.  A CTA waits for others' h, so all of them have to be resident: one per SM,
+// which the host checks fit.  Every wait is bounded, as in the grouped product.
 #include "mx_tc.cuh"
 #include "tensor_map.h"
 
@@ -31,29 +33,28 @@ constexpr int kRows = 16;                                  // routes per tile: t
 constexpr int kTokens = kMxBlockBytes;                     // of a stage: the token rows' codes
 constexpr int kTokenScales = kTokens + kRows * 128;        // and their scale words, arranged
 constexpr int kStageBytes = kTokenScales + 2 * 512;
-constexpr int kStages = 5, kSfStages = 4;
-constexpr int kSfCols = 16, kSf0 = 2 * kRows, kTmemCols = 128;
+constexpr int kStages = 10, kSfStages = 8;
+constexpr int kSfCols = 16, kSf0 = 2 * kRows, kTmemCols = 256;
 static_assert(kStageBytes % 1024 == 0 && kTokens % 1024 == 0, "swizzled rows");
 static_assert(kSf0 + kSfStages * kSfCols <= kTmemCols && kSfStages < kStages, "tensor memory");
 static_assert(kMxFewRoutes <= 256 && kMxFewRoutes <= kThreads, "a route per thread");
 
-// Shared memory behind the ring: the experts' counts while the tables are made, then kernel
-// 1's exchange or kernel 2's output sums.
-constexpr int kScratchBytes = 4096;
-inline int scratch_bytes(bool down, int M) { return down && M * 512 > kScratchBytes ? M * 512 : kScratchBytes; }
-inline int smem_bytes(bool down, int M) { return kStages * kStageBytes + scratch_bytes(down, M) + 1024; }
+// Shared memory behind the ring: the experts' counts while the tables are made, then the gate
+// and up exchange, then the output sums.
+inline int scratch_bytes(int M) { return M * 512 > 4096 ? M * 512 : 4096; }
+inline int smem_bytes(int M) { return kStages * kStageBytes + scratch_bytes(M) + 1024; }
 
 struct FewArgs {
   int M, K, I, E, topK, R;
-  int N, D, KB, NB;            // this kernel's product: channels, depth, stages, blocks
-  const __half* x;
   const int32_t* expert_idx;
   const float* probs;
-  const uint8_t* w;
+  const uint8_t *w1, *w2;
+  const uint8_t* x_codes;      // [M][K / 2]
+  const uint8_t* x_scales;     // [M][4 * planes(K)]
   uint8_t* h_codes;            // [R][I / 2]
   uint8_t* h_scales;           // [R][4 * planes(I)]
-  float* part;                 // [CTA][2][M][128]
-  int32_t* counters;           // [K / 128]
+  float* part;                 // per CTA: [2][16][128] of h, [2][M][128] of out
+  int32_t* counters;           // [R][I / 64] runs of h blocks, [R] blocks of h, [K / 128] runs of out blocks
   __half* out;
   int32_t* status;
 };
@@ -71,45 +72,48 @@ struct Seg {
   int nb, tile, kb0, kb1;
 };
 
-// The runs of kernel 2 (one per CTA, none empty) and where one begins.
-__device__ __forceinline__ int runs_of(int64_t total) { return (int)min((int64_t)gridDim.x, total); }
-__device__ __forceinline__ int64_t run_begin(int c, int64_t total) { return total * c / max(runs_of(total), 1); }
+// One of the two products: its blocks of 128 channels, 256-deep stages, and runs.
+template <bool DOWN>
+struct Product {
+  int NB, KB, tiles, runs;
+  int64_t total;
+  __device__ __forceinline__ Product(const FewArgs& a, int tiles_) {
+    tiles = tiles_;
+    NB = DOWN ? a.K / 128 : a.I / 64;
+    KB = ((DOWN ? a.I : a.K) + 255) / 256;
+    total = (int64_t)NB * tiles * KB;
+    runs = (int)min((int64_t)gridDim.x, total);  // none empty
+  }
+  __device__ __forceinline__ int64_t begin_of(int run) const { return runs ? total * min(run, runs) / runs : 0; }
+  // The run that holds stage `at`.
+  __device__ __forceinline__ int run_of(int64_t at) const {
+    int c = (int)(at * runs / total);
+    while (begin_of(c + 1) <= at) ++c;
+    while (begin_of(c) > at) --c;
+    return c;
+  }
+  // Stages of a block whose sums belong together, and the block that holds stage `at`.
+  __device__ __forceinline__ int per() const { return DOWN ? tiles * KB : KB; }
+  __device__ __forceinline__ int block_of(int64_t at) const { return (int)(at / per()); }
+};
 
 // The segments of a CTA, in order.
 template <bool DOWN>
 struct Walk {
+  const Product<DOWN>& p;
   int64_t at, end;
-  int step, tiles, NB, KB;
-  __device__ __forceinline__ Walk(const FewArgs& a, int tiles_) : tiles(tiles_), NB(a.NB), KB(a.KB) {
-    if (DOWN) {
-      const int64_t total = (int64_t)NB * tiles * KB;
-      const int c = min((int)blockIdx.x, runs_of(total));
-      at = run_begin(c, total);
-      end = run_begin(min((int)blockIdx.x + 1, runs_of(total)), total);
-      step = 0;
-    } else {
-      at = blockIdx.x;
-      end = (int64_t)tiles * NB;
-      step = gridDim.x;
-    }
+  __device__ __forceinline__ Walk(const Product<DOWN>& p_) : p(p_) {
+    at = p.begin_of(blockIdx.x);
+    end = p.begin_of(blockIdx.x + 1);
   }
   __device__ __forceinline__ bool next(Seg& s) {
     if (at >= end) return false;
-    if (DOWN) {
-      const int per = tiles * KB;
-      s.nb = (int)(at / per);
-      const int rem = (int)(at - (int64_t)s.nb * per);
-      s.tile = rem / KB;
-      s.kb0 = rem - s.tile * KB;
-      s.kb1 = (int)min((int64_t)KB, s.kb0 + (end - at));
-      at += s.kb1 - s.kb0;
-    } else {
-      s.tile = (int)(at / NB);
-      s.nb = (int)(at - (int64_t)s.tile * NB);
-      s.kb0 = 0;
-      s.kb1 = KB;
-      at += step;
-    }
+    const int64_t unit = at / p.KB;
+    s.kb0 = (int)(at - unit * p.KB);
+    s.tile = (int)(DOWN ? unit % p.tiles : unit / p.NB);
+    s.nb = (int)(DOWN ? unit / p.tiles : unit % p.NB);
+    s.kb1 = (int)min((int64_t)p.KB, s.kb0 + (end - at));
+    at += s.kb1 - s.kb0;
     return true;
   }
 };
@@ -165,40 +169,6 @@ __device__ __forceinline__ void make_tables(const FewArgs& a, Tables& t, int* co
   __syncthreads();
 }
 
-// One 256-deep stage of a tile's rows, from x: eight elements to a lane, four lanes to a
-// scaled block, a row per pass.
-__device__ __forceinline__ void put_x_rows(const FewArgs& a, const Tables& t, uint8_t* st, int row0, int rows, int kb,
-                                           int lane, const uint4 (&pre)[4]) {
-  const int k = kb * 256 + lane * 8;
-  for (int c = 0; c < rows; ++c) {
-    uint4 raw = make_uint4(0, 0, 0, 0);
-    if (c < 4) {
-      raw = c == 0 ? pre[0] : c == 1 ? pre[1] : c == 2 ? pre[2] : pre[3];
-    } else if (k < a.K) {
-      raw = __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)(t.list[row0 + c] / a.topK) * a.K + k));
-    }
-    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
-    float v[8];
-    uint32_t amax = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-      v[2 * i] = f.x;
-      v[2 * i + 1] = f.y;
-      amax = max(amax, max(abs_bits(f.x), abs_bits(f.y)));
-    }
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const uint32_t b = mx_scale_byte(amax);
-    const float mult = mx_multiplier(b);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = mx_scaled(v[i], mult, b);
-    const int chunk = lane >> 2;
-    *reinterpret_cast<uint32_t*>(st + kTokens + mx_chunk_at(c, chunk) + (lane & 3) * 4) = mx_codes8(v);
-    if ((lane & 3) == 0) st[kTokenScales + (chunk >> 2) * 512 + c * 16 + (chunk & 3)] = (uint8_t)b;
-  }
-}
-
 // Whether `ok` holds in all four epilogue warps (named barrier 1).
 __device__ __forceinline__ bool epi_all(bool ok) {
   uint32_t r;
@@ -213,15 +183,299 @@ __device__ __forceinline__ bool epi_all(bool ok) {
   return r != 0;
 }
 
-// The CTA of kernel 2 whose run holds stage `at` of `total`.
-__device__ __forceinline__ int run_of(int64_t at, int64_t total) {
-  int c = (int)(at * runs_of(total) / total);
-  while (run_begin(c + 1, total) <= at) ++c;
-  while (run_begin(c, total) > at) --c;
-  return c;
+// Barriers and shared memory of kernel 2's pipeline, and what its roles keep from product to
+// product.
+struct Pipe {
+  uint64_t *full, *empty, *sf, *accfull, *accempty;
+  uint32_t ring;
+  uint8_t* ring_g;
+  uint32_t tmem;
+  volatile int* abort_flag;
+  int32_t* status;
+};
+
+template <bool DOWN>
+__device__ __forceinline__ bool load_weights(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<DOWN>& p,
+                                             uint32_t elected, RingPos& at, int& n) {
+  Walk<DOWN> walk(p);
+  Seg s;
+  while (walk.next(s)) {
+    const uint8_t* wb =
+        (DOWN ? a.w2 : a.w1) + ((size_t)t.tile_e[s.tile] * p.NB + s.nb) * (size_t)p.KB * kMxBlockBytes;
+    for (int kb = s.kb0; kb < s.kb1; ++kb, ++n, at.next(kStages)) {
+      if (!warp_wait(&pp.empty[at.slot], at.phase ^ 1u, pp.abort_flag, pp.status)) return false;
+      const uint32_t bar = smem_u32(&pp.full[at.slot]);
+      expect_tx_elect(elected, bar, kMxBlockBytes);
+      bulk_load_elect(elected, pp.ring + at.slot * kStageBytes, wb + (size_t)kb * kMxBlockBytes, kMxBlockBytes, bar);
+    }
+  }
+  return true;
 }
 
 template <bool DOWN>
+__device__ __forceinline__ bool issue_mmas(const FewArgs& a, const Pipe& pp, const Product<DOWN>& p, uint32_t elected,
+                                           RingPos& at, RingPos& sf, int& u) {
+  const uint32_t t0 = __shfl_sync(0xffffffffu, pp.tmem, 0), idesc = mx_idesc(128, kRows);
+  const int last = ((DOWN ? a.I : a.K) - (p.KB - 1) * 256 + 127) >> 7;  // 128-deep halves of the last stage
+  Walk<DOWN> walk(p);
+  Seg s;
+  while (walk.next(s)) {
+    const int buf = u & 1;
+    if (!warp_wait(&pp.accempty[buf], ((u >> 1) & 1) ^ 1, pp.abort_flag, pp.status)) return false;
+    tc_fence_after();
+    const uint32_t d = t0 + buf * kRows;
+    for (int kb = s.kb0; kb < s.kb1; ++kb, at.next(kStages), sf.next(kSfStages)) {
+      if (!warp_wait(&pp.sf[at.slot], at.phase, pp.abort_flag, pp.status)) return false;
+      tc_fence_after();
+      const uint32_t st = pp.ring + at.slot * kStageBytes, t_sf = t0 + kSf0 + sf.slot * kSfCols;
+      const uint64_t da = sw128_desc(st), db = sw128_desc(st + kTokens);
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        mx_copy_scales<false>(elected, t_sf + 4 * q, st + kMxCodeBytes + 512 * q);
+        mx_copy_scales<false>(elected, t_sf + 8 + 4 * q, st + kTokenScales + 512 * q);
+      }
+      mx_mma2<false>(elected, d, da, db, 0, idesc, t_sf, t_sf + 8, kb > s.kb0 ? 1u : 0u);
+      if (kb < p.KB - 1 || last == 2) mx_mma2<false>(elected, d, da, db, 1, idesc, t_sf + 4, t_sf + 12, 1u);
+      mx_commit<false>(elected, smem_u32(&pp.empty[at.slot]));
+    }
+    mx_commit<false>(elected, smem_u32(&pp.accfull[buf]));
+    ++u;
+  }
+  return true;
+}
+
+// A stage's token rows and scales: rows of x by token, or of h by route, 16 of 128 bytes and a
+// scale word for each half of the stage.
+template <bool DOWN>
+__device__ __forceinline__ bool prepare_stages(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<DOWN>& p,
+                                               int who, int lane, RingPos& at, RingPos& old, int& n) {
+  const int depth = DOWN ? a.I : a.K, planes = (depth + 127) / 128;
+  const uint8_t* codes = DOWN ? a.h_codes : a.x_codes;
+  const uint32_t* scales = reinterpret_cast<const uint32_t*>(DOWN ? a.h_scales : a.x_scales);
+  const int32_t* ready = a.counters + (size_t)a.R * (a.I / 64);
+  Walk<DOWN> walk(p);
+  Seg s;
+  while (walk.next(s)) {
+    const int row0 = t.tile_row[s.tile] & 0xffff, rows = t.tile_row[s.tile] >> 16;
+    bool waited = !DOWN;
+    for (int kb = s.kb0; kb < s.kb1; ++kb, ++n, at.next(kStages)) {
+      if (n > kSfStages) old.next(kStages);
+      if (n % kPrepWarps != who) continue;
+      if (!waited) {  // all blocks of the tile's h
+        const bool ok = *pp.abort_flag == 0 && (lane != 0 || count_wait_bounded(ready + s.tile, a.I / 64));
+        if (!__all_sync(0xffffffffu, ok)) {
+          if (*pp.abort_flag == 0 && lane == 0) record_status(pp.status, MOE_ERR_TIMEOUT);
+          *pp.abort_flag = 1;
+          return false;
+        }
+        waited = true;
+      }
+      // lane: rows lane / 8 + 4 i, 16-byte chunk lane % 8
+      uint4 row[4];
+      const int chunk = kb * 8 + (lane & 7);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = (lane >> 3) + 4 * i;
+        row[i] = make_uint4(0, 0, 0, 0);
+        if (c < rows && chunk * 32 < depth) {
+          const int r = t.list[row0 + c];
+          row[i] = __ldcg(reinterpret_cast<const uint4*>(codes + (size_t)(DOWN ? r : r / a.topK) * (depth / 2) + chunk * 16));
+        }
+      }
+      uint32_t word = 0;
+      const int c = lane & 15, plane = 2 * kb + (lane >> 4);
+      if (c < rows && plane < planes) {
+        const int r = t.list[row0 + c];
+        word = __ldcg(scales + (size_t)(DOWN ? r : r / a.topK) * planes + plane);
+      }
+      // The stage that used the scale columns is done, and with it the slot's previous use: only
+      // then is `full` known to be in this use's phase (copies complete in any order).
+      if (n >= kSfStages && !warp_wait(&pp.empty[old.slot], old.phase, pp.abort_flag, pp.status)) return false;
+      uint8_t* st = pp.ring_g + at.slot * kStageBytes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(st + kTokens + mx_chunk_at((lane >> 3) + 4 * i, lane & 7)) = row[i];
+      *reinterpret_cast<uint32_t*>(st + kTokenScales + (lane >> 4) * 512 + (lane & 15) * 16) = word;
+      if (!warp_wait(&pp.full[at.slot], at.phase, pp.abort_flag, pp.status)) return false;
+      const uint4 w0 = mx_scale_words(st + kMxCodeBytes, lane), w1 = mx_scale_words(st + kMxCodeBytes + 512, lane);
+      __syncwarp();
+      mx_put_scale_words(st + kMxCodeBytes, w0, lane);
+      mx_put_scale_words(st + kMxCodeBytes + 512, w1, lane);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pp.sf[at.slot]);
+    }
+  }
+  return true;
+}
+
+// The epilogue warps' barrier.
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// A run's sums of a block are in `mine` (global, visible to this thread's CTA only so far):
+// counts it, and returns whether all `runs` of the block's are there.
+__device__ __forceinline__ bool last_run(int32_t* counter, int runs, bool first_thread, int* s_last) {
+  __threadfence();
+  epi_sync();
+  if (first_thread) *s_last = atomicAdd(counter, 1) == runs - 1;
+  epi_sync();
+  const bool last = *s_last != 0;
+  if (last) __threadfence();
+  return last;
+}
+
+// The sums of segment u: 16 columns of this lane's channel.
+__device__ __forceinline__ bool take_sums(const Pipe& pp, int u, int quarter, int lane, uint32_t (&v)[16]) {
+  const int buf = u & 1;
+  if (!epi_all(warp_wait(&pp.accfull[buf], (u >> 1) & 1, pp.abort_flag, pp.status))) return false;
+  tc_fence_after();
+  __syncwarp();
+  tmem_ld16(pp.tmem + ((uint32_t)quarter << 21) + buf * kRows, v);
+  tmem_wait_ld();
+  tc_fence_before();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&pp.accempty[buf]);
+  return true;
+}
+
+__device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<false>& p,
+                                         float* xchg, int quarter, int lane, int& u, int* s_last) {
+  const int pair = quarter >> 1, odd = quarter & 1, ch = quarter * 32 + lane, planes = (a.I + 127) / 128;
+  float* give = xchg + pair * 512 + odd * 256 + lane;
+  const float* take = xchg + pair * 512 + (odd ^ 1) * 256 + lane;
+  int32_t* ready = a.counters + (size_t)a.R * (a.I / 64);
+  const size_t cta_part = (size_t)2 * (16 + a.M) * 128;
+  Walk<false> walk(p);
+  const int64_t begin = walk.at;
+  Seg s;
+  while (walk.next(s)) {
+    uint32_t v[16];
+    if (!take_sums(pp, u, quarter, lane, v)) return false;
+    ++u;
+    const int row0 = t.tile_row[s.tile] & 0xffff, rows = t.tile_row[s.tile] >> 16;
+    if (s.kb1 - s.kb0 < p.KB) {
+      const int block = s.tile * p.NB + s.nb;
+      const int64_t b0 = (int64_t)block * p.KB;
+      float* part = a.part + blockIdx.x * cta_part + (block != p.block_of(begin)) * 16 * 128;
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (i < rows) __stcg(part + i * 128 + ch, __uint_as_float(v[i]));
+      const int c0 = p.run_of(b0), c1 = p.run_of(b0 + p.KB - 1);
+      if (!last_run(a.counters + block, c1 - c0 + 1, quarter == 0 && lane == 0, s_last)) continue;
+      float acc[16] = {};
+      for (int c = c0; c <= c1; ++c) {
+        const float* q = a.part + c * cta_part + (block != p.block_of(p.begin_of(c))) * 16 * 128 + ch;
+        float o[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) o[i] = i < rows ? __ldcg(q + i * 128) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[i] += o[i];
+      }
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(acc[i]);
+    }
+    // warps in pairs, 32 gate channels and the 32 up channels that multiply them: of 16 rows
+    // each warp finishes 8, with the other's half through shared memory
+#pragma unroll
+    for (int i = 0; i < 8; ++i) give[i * 32] = __uint_as_float(odd ? v[i] : v[8 + i]);
+    epi_sync();
+    float h[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float o = take[i * 32];
+      h[i] = odd ? mx_swiglu(o, __uint_as_float(v[8 + i])) : mx_swiglu(__uint_as_float(v[i]), o);
+    }
+    uint32_t byte;
+    const uint32_t w = mx_quant_rows8(h, lane, byte);
+    const int c = odd * 8 + (lane & 7);
+    if (c < rows) {
+      const int r = t.list[row0 + c], k = s.nb * 2 + pair;
+      *reinterpret_cast<uint32_t*>(a.h_codes + (size_t)r * (a.I / 2) + k * 16 + (lane >> 3) * 4) = w;
+      if (lane < 8) {
+        uint8_t* sc = a.h_scales + (size_t)r * planes * 4 + k;
+        *sc = (uint8_t)byte;
+        if (k == a.I / 32 - 1)  // bytes of the word past the last block
+          for (int z = 1; (k + z) & 3; ++z) sc[z] = 0;
+      }
+    }
+    __threadfence();
+    epi_sync();  // h is written, and the exchange free
+    if (quarter == 0 && lane == 0) atomicAdd(ready + s.tile, 1);
+  }
+  return true;
+}
+
+__device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<true>& p,
+                                           float* sums, int quarter, int lane, int& u, int* s_last) {
+  const int ch = quarter * 32 + lane;
+  const size_t cta_part = (size_t)2 * (16 + a.M) * 128;
+  int32_t* counters = a.counters + (size_t)a.R * (a.I / 64) + a.R;
+  Walk<true> walk(p);
+  const int64_t begin = walk.at;
+  Seg s;
+  for (int i = 0; i < a.M; ++i) sums[i * 128 + ch] = 0.0f;
+  if (p.tiles == 0)  // no route at all
+    for (int nb = blockIdx.x; nb < p.NB; nb += gridDim.x)
+      for (int i = 0; i < a.M; ++i) a.out[(size_t)i * a.K + nb * 128 + ch] = __float2half(0.0f);
+  while (walk.next(s)) {
+    uint32_t v[16];
+    if (!take_sums(pp, u, quarter, lane, v)) return false;
+    ++u;
+    const int row0 = t.tile_row[s.tile] & 0xffff, rows = t.tile_row[s.tile] >> 16;
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      if (i < rows) {
+        const int r = t.list[row0 + i];
+        float* o = sums + (r / a.topK) * 128 + ch;
+        *o = fmaf(t.prob[r], __uint_as_float(v[i]), *o);
+      }
+    if (walk.at < walk.end && (s.tile < p.tiles - 1 || s.kb1 < p.KB)) continue;
+    // the run's share of this output block is complete
+    const int64_t b0 = (int64_t)s.nb * p.per(), b1 = b0 + p.per();
+    __half* out = a.out + s.nb * 128;
+    if (begin <= b0 && walk.end >= b1) {
+      for (int i = 0; i < a.M; ++i) {
+        out[(size_t)i * a.K + ch] = from_f32<__half>(sums[i * 128 + ch]);
+        sums[i * 128 + ch] = 0.0f;
+      }
+      continue;
+    }
+    float* part = a.part + blockIdx.x * cta_part + 2 * 16 * 128 + (s.nb != p.block_of(begin)) * a.M * 128;
+    for (int i = 0; i < a.M; ++i) {
+      __stcg(part + i * 128 + ch, sums[i * 128 + ch]);
+      sums[i * 128 + ch] = 0.0f;
+    }
+    const int c0 = p.run_of(b0), c1 = p.run_of(b1 - 1);
+    if (!last_run(counters + s.nb, c1 - c0 + 1, quarter == 0 && lane == 0, s_last)) continue;
+    // a token to a warp, four channels to a lane, the runs' sums four at a time
+    for (int i = quarter; i < a.M; i += 4) {
+      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int c = c0; c <= c1; c += 4) {
+        float4 o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          o[k] = c + k <= c1 ? __ldcg(reinterpret_cast<const float4*>(
+                                   a.part + (c + k) * cta_part + 2 * 16 * 128 +
+                                   (s.nb != p.block_of(p.begin_of(c + k))) * a.M * 128 + i * 128) + lane)
+                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          acc.x += o[k].x;
+          acc.y += o[k].y;
+          acc.z += o[k].z;
+          acc.w += o[k].w;
+        }
+      }
+      uint2 h;
+      const __half2 lo = f2h2_sat(acc.x, acc.y), hi = f2h2_sat(acc.z, acc.w);
+      h.x = *reinterpret_cast<const uint32_t*>(&lo);
+      h.y = *reinterpret_cast<const uint32_t*>(&hi);
+      *reinterpret_cast<uint2*>(out + (size_t)i * a.K + lane * 4) = h;
+    }
+  }
+  return true;
+}
+
 __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], sf_bar[kStages], accfull_bar[2],
@@ -231,19 +485,21 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const FewArgs a) {
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_issued, s_last;
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  volatile int* abort_flag = &s_abort;
-  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* ring_g = smem_raw + (ring - smem_u32(smem_raw));
-  uint8_t* scratch = ring_g + kStages * kStageBytes;
+  Pipe pp;
+  pp.full = full_bar;
+  pp.empty = empty_bar;
+  pp.sf = sf_bar;
+  pp.accfull = accfull_bar;
+  pp.accempty = accempty_bar;
+  pp.ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  pp.ring_g = smem_raw + (pp.ring - smem_u32(smem_raw));
+  pp.abort_flag = &s_abort;
+  pp.status = a.status;
+  uint8_t* scratch = pp.ring_g + kStages * kStageBytes;
 
-  if (!DOWN) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     s_abort = 0;
     s_issued = 0;
-  }
-  if (!DOWN && blockIdx.x == 0) {  // what kernel 2 counts with, and the status word
-    for (int i = threadIdx.x; i < a.K / 128; i += kThreads) a.counters[i] = 0;
-    if (threadIdx.x == 0) *a.status = 0;
   }
   if (warp == kMmaWarp) {
     tmem_alloc<false, kTmemCols>(&s_tmem);
@@ -265,211 +521,37 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const FewArgs a) {
   }
   make_tables(a, s_t, reinterpret_cast<int*>(scratch), s_wsum);
   tc_fence_after();
-  const uint32_t tmem = s_tmem;
-  const int tiles = s_t.tiles;
+  pp.tmem = s_tmem;
+  const Product<false> up(a, s_t.tiles);
+  const Product<true> down(a, s_t.tiles);
 
   if (warp == kWeightWarp) {
     const uint32_t elected = elect_one();
-    Walk<DOWN> walk(a, tiles);
-    Seg s;
     RingPos at;
     int n = 0;
-    bool ok = true;
-    while (ok && walk.next(s)) {
-      const uint8_t* wb = a.w + ((size_t)s_t.tile_e[s.tile] * a.NB + s.nb) * (size_t)a.KB * kMxBlockBytes;
-      for (int kb = s.kb0; kb < s.kb1; ++kb, ++n, at.next(kStages)) {
-        if (!(ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status))) break;
-        const uint32_t bar = smem_u32(&full_bar[at.slot]);
-        expect_tx_elect(elected, bar, kMxBlockBytes);
-        bulk_load_elect(elected, ring + at.slot * kStageBytes, wb + (size_t)kb * kMxBlockBytes, kMxBlockBytes, bar);
-      }
-    }
+    if (load_weights<false>(a, s_t, pp, up, elected, at, n)) load_weights<true>(a, s_t, pp, down, elected, at, n);
     if (lane == 0) s_issued = n;
   } else if (warp == kMmaWarp) {
-    const uint32_t elected = elect_one(), t0 = __shfl_sync(0xffffffffu, tmem, 0), idesc = mx_idesc(128, kRows);
-    Walk<DOWN> walk(a, tiles);
-    Seg s;
+    const uint32_t elected = elect_one();
     RingPos at, sf;
     int u = 0;
-    bool ok = true;
-    const int last = (a.D - (a.KB - 1) * 256 + 127) >> 7;  // 128-deep halves of the last stage
-    while (ok && walk.next(s)) {
-      const int buf = u & 1;
-      if (!(ok = warp_wait(&accempty_bar[buf], ((u >> 1) & 1) ^ 1, abort_flag, a.status))) break;
-      tc_fence_after();
-      const uint32_t d = t0 + buf * kRows;
-      for (int kb = s.kb0; kb < s.kb1; ++kb, at.next(kStages), sf.next(kSfStages)) {
-        if (!(ok = warp_wait(&sf_bar[at.slot], at.phase, abort_flag, a.status))) break;
-        tc_fence_after();
-        const uint32_t st = ring + at.slot * kStageBytes, t_sf = t0 + kSf0 + sf.slot * kSfCols;
-        const uint64_t da = sw128_desc(st), db = sw128_desc(st + kTokens);
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          mx_copy_scales<false>(elected, t_sf + 4 * q, st + kMxCodeBytes + 512 * q);
-          mx_copy_scales<false>(elected, t_sf + 8 + 4 * q, st + kTokenScales + 512 * q);
-        }
-        mx_mma2<false>(elected, d, da, db, 0, idesc, t_sf, t_sf + 8, kb > s.kb0 ? 1u : 0u);
-        if (kb < a.KB - 1 || last == 2) mx_mma2<false>(elected, d, da, db, 1, idesc, t_sf + 4, t_sf + 12, 1u);
-        mx_commit<false>(elected, smem_u32(&empty_bar[at.slot]));
-      }
-      if (ok) mx_commit<false>(elected, smem_u32(&accfull_bar[buf]));
-      ++u;
-    }
+    if (issue_mmas<false>(a, pp, up, elected, at, sf, u)) issue_mmas<true>(a, pp, down, elected, at, sf, u);
+    __syncwarp();
     mx_commit<false>(elected, smem_u32(&final_bar));  // every MMA done before tensor memory is freed
     mbar_wait_sleep_bounded(&final_bar, 0);
   } else if (warp >= kPrepWarp0 && warp < kPrepWarp0 + kPrepWarps) {
-    if (DOWN) asm volatile("griddepcontrol.wait;" ::: "memory");  // h is kernel 1's
-    Walk<DOWN> walk(a, tiles);
-    Seg s;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's x and counters
     RingPos at, old;  // old: the stage kSfStages before
     int n = 0;
-    bool ok = true;
-    while (ok && walk.next(s)) {
-      const int row0 = s_t.tile_row[s.tile] & 0xffff, rows = s_t.tile_row[s.tile] >> 16;
-      for (int kb = s.kb0; kb < s.kb1; ++kb, ++n, at.next(kStages)) {
-        if (n > kSfStages) old.next(kStages);
-        if (n % kPrepWarps != warp - kPrepWarp0) continue;
-        uint4 pre[4];
-        uint32_t words = 0;
-        if (DOWN) {  // lane: rows lane / 8 + 4 i, 16-byte chunk lane % 8; one scale word
-          const int chunk = kb * 8 + (lane & 7), planes = (a.I + 127) / 128;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int c = (lane >> 3) + 4 * i;
-            pre[i] = c < rows && chunk * 32 < a.I
-                         ? __ldcg(reinterpret_cast<const uint4*>(a.h_codes + (size_t)s_t.list[row0 + c] * (a.I / 2) +
-                                                                 chunk * 16))
-                         : make_uint4(0, 0, 0, 0);
-          }
-          const int c = lane & 15, plane = 2 * kb + (lane >> 4);
-          if (c < rows && plane < planes)
-            words = __ldcg(reinterpret_cast<const uint32_t*>(a.h_scales) + (size_t)s_t.list[row0 + c] * planes + plane);
-        } else {
-          const int k = kb * 256 + lane * 8;
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            pre[i] = i < rows && k < a.K
-                         ? __ldg(reinterpret_cast<const uint4*>(a.x + (size_t)(s_t.list[row0 + i] / a.topK) * a.K + k))
-                         : make_uint4(0, 0, 0, 0);
-        }
-        // The stage that used the scale columns is done, and with it the slot's previous use: only
-        // then is full_bar known to be in this use's phase (copies complete in any order).
-        if (n >= kSfStages && !(ok = warp_wait(&empty_bar[old.slot], old.phase, abort_flag, a.status))) break;
-        uint8_t* st = ring_g + at.slot * kStageBytes;
-        if (DOWN) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            *reinterpret_cast<uint4*>(st + kTokens + mx_chunk_at((lane >> 3) + 4 * i, lane & 7)) = pre[i];
-          *reinterpret_cast<uint32_t*>(st + kTokenScales + (lane >> 4) * 512 + (lane & 15) * 16) = words;
-        } else {
-          put_x_rows(a, s_t, st, row0, rows, kb, lane, pre);
-        }
-        if (!(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status))) break;
-        const uint4 w0 = mx_scale_words(st + kMxCodeBytes, lane), w1 = mx_scale_words(st + kMxCodeBytes + 512, lane);
-        __syncwarp();
-        mx_put_scale_words(st + kMxCodeBytes, w0, lane);
-        mx_put_scale_words(st + kMxCodeBytes + 512, w1, lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_bar[at.slot]);
-      }
-    }
+    if (prepare_stages<false>(a, s_t, pp, up, warp - kPrepWarp0, lane, at, old, n))
+      prepare_stages<true>(a, s_t, pp, down, warp - kPrepWarp0, lane, at, old, n);
   } else if (warp >= kEpiWarp0) {
-    const int quarter = warp & 3, ch = quarter * 32 + lane;
-    const uint32_t lanes = (uint32_t)quarter << 21;
-    Walk<DOWN> walk(a, tiles);
-    Seg s;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     int u = 0;
-    float* sums = reinterpret_cast<float*>(scratch);  // kernel 2: [M][128]
-    if (DOWN) {
-      for (int t = 0; t < a.M; ++t) sums[t * 128 + ch] = 0.0f;
-      if (tiles == 0)  // no route at all
-        for (int nb = blockIdx.x; nb < a.NB; nb += gridDim.x)
-          for (int t = 0; t < a.M; ++t) a.out[(size_t)t * a.K + nb * 128 + ch] = __float2half(0.0f);
-      asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters are kernel 1's
-    }
-    const int64_t begin = walk.at;
-    while (walk.next(s)) {
-      const int row0 = s_t.tile_row[s.tile] & 0xffff, rows = s_t.tile_row[s.tile] >> 16, buf = u & 1;
-      const bool ok = epi_all(warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status));
-      if (!ok) break;
-      tc_fence_after();
-      __syncwarp();
-      uint32_t v[16];
-      tmem_ld16(tmem + lanes + buf * kRows, v);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&accempty_bar[buf]);
-      ++u;
-      if (!DOWN) {
-        // warps in pairs, 32 gate channels and the 32 up channels that multiply them: of 16
-        // rows each warp finishes 8, with the other's half through shared memory
-        const int pair = quarter >> 1, odd = quarter & 1;
-        float* give = reinterpret_cast<float*>(scratch) + pair * 512 + odd * 256 + lane;
-        const float* take = reinterpret_cast<float*>(scratch) + pair * 512 + (odd ^ 1) * 256 + lane;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) give[i * 32] = __uint_as_float(odd ? v[i] : v[8 + i]);
-        asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");
-        float h[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float o = take[i * 32];
-          h[i] = odd ? mx_swiglu(o, __uint_as_float(v[8 + i])) : mx_swiglu(__uint_as_float(v[i]), o);
-        }
-        asm volatile("bar.sync %0, 64;" ::"r"(2 + pair) : "memory");  // both have taken
-        uint32_t byte;
-        const uint32_t w = mx_quant_rows8(h, lane, byte);
-        const int c = odd * 8 + (lane & 7);
-        if (c < rows) {
-          const int r = s_t.list[row0 + c], k = s.nb * 2 + pair, planes = (a.I + 127) / 128;
-          *reinterpret_cast<uint32_t*>(a.h_codes + (size_t)r * (a.I / 2) + k * 16 + (lane >> 3) * 4) = w;
-          if (lane < 8) {
-            uint8_t* sc = a.h_scales + (size_t)r * planes * 4 + k;
-            *sc = (uint8_t)byte;
-            if (k == a.I / 32 - 1)  // bytes of the word past the last block
-              for (int z = 1; (k + z) & 3; ++z) sc[z] = 0;
-          }
-        }
-        __syncwarp();
-      } else {
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          if (i < rows) {
-            const int r = s_t.list[row0 + i];
-            float* o = sums + (r / a.topK) * 128 + ch;
-            *o = fmaf(s_t.prob[r], __uint_as_float(v[i]), *o);
-          }
-        if (walk.at < walk.end && (s.tile < tiles - 1 || s.kb1 < a.KB)) continue;
-        // the run's share of this output block is complete
-        const int64_t per = (int64_t)tiles * a.KB, total = per * a.NB, b0 = s.nb * per, b1 = b0 + per;
-        const bool whole = begin <= b0 && walk.end >= b1;
-        bool write = whole;
-        int c0 = 0, c1 = 0;
-        if (!whole) {
-          float* part = a.part + ((size_t)blockIdx.x * 2 + (s.nb != (int)(begin / per))) * a.M * 128;
-          for (int t = 0; t < a.M; ++t) __stcg(part + t * 128 + ch, sums[t * 128 + ch]);
-          c0 = run_of(b0, total);
-          c1 = run_of(b1 - 1, total);
-          __threadfence();
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          if (warp == kEpiWarp0 && lane == 0) s_last = atomicAdd(a.counters + s.nb, 1) == c1 - c0;
-          asm volatile("bar.sync 1, 128;" ::: "memory");
-          write = s_last != 0;
-          if (write) __threadfence();
-        }
-        for (int t = 0; t < a.M; ++t) {
-          float acc = sums[t * 128 + ch];
-          if (!whole && write) {
-            acc = 0.0f;
-            for (int c = c0; c <= c1; ++c)
-              acc += __ldcg(a.part + ((size_t)c * 2 + (s.nb != (int)(run_begin(c, total) / per))) * a.M * 128 +
-                            t * 128 + ch);
-          }
-          if (write) a.out[(size_t)t * a.K + s.nb * 128 + ch] = from_f32<__half>(acc);
-          sums[t * 128 + ch] = 0.0f;
-        }
-      }
+    float* shared = reinterpret_cast<float*>(scratch);
+    if (finish_h(a, s_t, pp, up, shared, warp & 3, lane, u, &s_last)) {
+      epi_sync();  // the exchange becomes the sums
+      finish_out(a, s_t, pp, down, shared, warp & 3, lane, u, &s_last);
     }
   }
 
@@ -483,29 +565,76 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const FewArgs a) {
   __syncwarp();
   if (warp == kMmaWarp) {
     tc_fence_after();
-    tmem_dealloc<false, kTmemCols>(tmem);
+    tmem_dealloc<false, kTmemCols>(pp.tmem);
   }
 }
+
+// Kernel 1: a warp per 256 elements of a token, eight to a lane, four lanes to a scaled block.
+constexpr int kXThreads = 256;
+__global__ void __launch_bounds__(kXThreads) mx_few_x_kernel(const __half* x, int M, int K, uint8_t* codes, uint8_t* scales,
+                                                             int32_t* counters, int n_counters, int32_t* status) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int i = blockIdx.x * kXThreads + threadIdx.x;
+  for (int c = i; c < n_counters; c += gridDim.x * kXThreads) counters[c] = 0;
+  if (i == 0) *status = 0;
+  const int per = K / 8;  // lanes of a row; K is a multiple of 128, so four lanes stay together
+  const int t = i / per, k = (i - t * per) * 8;
+  if (t >= M) return;
+  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(x + (size_t)t * K + k));
+  const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+  float v[8];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+    v[2 * j] = f.x;
+    v[2 * j + 1] = f.y;
+    amax = max(amax, max(abs_bits(f.x), abs_bits(f.y)));
+  }
+  const uint32_t mask = 0xfu << (threadIdx.x & 28u);  // M * K / 8 is a multiple of 16: groups of four are whole
+  amax = max(amax, __shfl_xor_sync(mask, amax, 1));
+  amax = max(amax, __shfl_xor_sync(mask, amax, 2));
+  const uint32_t b = mx_scale_byte(amax);
+  const float mult = mx_multiplier(b);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = mx_scaled(v[j], mult, b);
+  *reinterpret_cast<uint32_t*>(codes + (size_t)t * (K / 2) + k / 2) = mx_codes8(v);
+  if ((threadIdx.x & 3) == 0) scales[(size_t)t * (K / 32) + k / 32] = (uint8_t)b;
+}
+
+int counters_of(int M, int K, int I, int topK) { return M * topK * (I / 64 + 1) + K / 128; }
 
 }  // namespace
 
-size_t mx_few_part_bytes(int M, int K) {
-  (void)K;
-  return (size_t)sm_count() * 2 * M * 128 * 4;
+size_t mx_few_part_bytes(int M) { return (size_t)sm_count() * 2 * (16 + M) * 128 * 4; }
+size_t mx_few_counter_bytes(int M, int K, int I, int topK) { return (size_t)counters_of(M, K, I, topK) * 4; }
+
+// Whether every CTA of kernel 2 can be resident at once: one per SM.
+bool mx_few_resident() {
+  static PerContextOnce queried;
+  static bool ok[kMaxDevices] = {};
+  const int dev = current_device();
+  if (queried.needed(dev)) {
+    int n = 0;
+    ok[dev] = cudaFuncSetAttribute(mx_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                   smem_bytes(kMxFewTokens)) == cudaSuccess &&
+              cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, mx_few_kernel, kThreads, smem_bytes(kMxFewTokens)) ==
+                  cudaSuccess &&
+              n >= 1;
+    if (!ok[dev]) cudaGetLastError();
+    queried.done(dev);
+  }
+  return ok[dev];
 }
 
 cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
-  static PerContextOnce set;
-  const int dev = current_device();
-  if (set.needed(dev)) {
-    cudaError_t e = cudaFuncSetAttribute(mx_few_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         smem_bytes(false, kMxFewTokens));
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(mx_few_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               smem_bytes(true, kMxFewTokens));
-    if (e != cudaSuccess) return e;
-    set.done(dev);
-  }
+  const int n_counters = counters_of(p.M, p.K, p.I, p.topK);
+  const int x_blocks = (int)(((size_t)p.M * p.K / 8 + kXThreads - 1) / kXThreads);
+  mx_few_x_kernel<<<x_blocks, kXThreads, 0, stream>>>(reinterpret_cast<const __half*>(p.x), p.M, p.K, p.x_codes,
+                                                      reinterpret_cast<uint8_t*>(p.x_scales), p.counters, n_counters,
+                                                      p.status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   FewArgs a;
   a.M = p.M;
   a.K = p.K;
@@ -513,14 +642,12 @@ cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
   a.E = p.E;
   a.topK = p.topK;
   a.R = p.M * p.topK;
-  a.N = 2 * p.I;
-  a.D = p.K;
-  a.KB = mx_depth_blocks(p.K);
-  a.NB = p.I / 64;
-  a.x = reinterpret_cast<const __half*>(p.x);
   a.expert_idx = p.expert_idx;
   a.probs = p.probs;
-  a.w = p.w1;
+  a.w1 = p.w1;
+  a.w2 = p.w2;
+  a.x_codes = p.x_codes;
+  a.x_scales = reinterpret_cast<const uint8_t*>(p.x_scales);
   a.h_codes = p.h_codes;
   a.h_scales = reinterpret_cast<uint8_t*>(p.h_scales);
   a.part = p.part;
@@ -530,22 +657,14 @@ cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)sm_count());
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(false, p.M);
+  cfg.dynamicSmemBytes = smem_bytes(p.M);
   cfg.stream = stream;
-  cudaError_t e = cudaLaunchKernelEx(&cfg, mx_few_kernel<false>, a);
-  if (e != cudaSuccess) return e;
-  a.N = p.K;
-  a.D = p.I;
-  a.KB = mx_depth_blocks(p.I);
-  a.NB = p.K / 128;
-  a.w = p.w2;
   cudaLaunchAttribute after;
   after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   after.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &after;
   cfg.numAttrs = 1;
-  cfg.dynamicSmemBytes = smem_bytes(true, p.M);
-  return cudaLaunchKernelEx(&cfg, mx_few_kernel<true>, a);
+  return cudaLaunchKernelEx(&cfg, mx_few_kernel, a);
 }
 
 }  // namespace moe
