@@ -133,6 +133,19 @@ __device__ __forceinline__ void tma_load_2d_elect(uint32_t elected, uint32_t dst
       : "memory");
 }
 
+__device__ __forceinline__ void tma_gather4_elect(uint32_t elected, uint32_t dst, const void* tmap, int32_t x, int4 y,
+                                                  uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.u32 e, %8, 0;\n\t"
+      "@e cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y.x), "r"(y.y), "r"(y.z), "r"(y.w), "r"(bar), "r"(elected)
+      : "memory");
+}
+// Orders generic accesses of global memory before and after this point with TMA's.
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+
 // A ring of n slots: the current one and the parity of its current use.
 struct RingPos {
   uint32_t slot = 0, phase = 0;

@@ -60,15 +60,16 @@ struct MxFewProblem {
   const float* probs;
   const uint8_t *w1, *w2;
   uint8_t* x_codes;    // [M][K / 2]
-  uint32_t* x_scales;  // [M][planes(K)]
+  uint8_t* x_scales;   // mx_few_scale_bytes(M, K)
   uint8_t* h_codes;    // [M * topK][I / 2]
-  uint32_t* h_scales;  // [M * topK][planes(I)]
+  uint8_t* h_scales;   // mx_few_scale_bytes(M * topK, I)
   float* part;         // mx_few_part_bytes
   int32_t* counters;   // mx_few_counter_bytes
   uint16_t* out;
   int32_t* status;
 };
 size_t mx_few_part_bytes(int M);
+size_t mx_few_scale_bytes(int rows, int D);
 size_t mx_few_counter_bytes(int M, int K, int I, int topK);
 cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream);
 

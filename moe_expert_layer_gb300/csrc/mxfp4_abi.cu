@@ -34,8 +34,8 @@ size_t gmm_workspace_bytes() { return kAlign; }
 
 // The layer's workspace.
 struct Layout {
-  // a few tokens: status, a_* (x), h_*, part, counters; behind them what the other path uses
-  size_t status, sorted, expanded, tpe, cumsum, sort_ws, a_codes, a_scales, h_codes, h_scales, c2, part, counters, total;
+  // a few tokens: status, part, counters, the scale records, a_codes (x) and h_codes; and what the other path uses
+  size_t status, sorted, expanded, tpe, cumsum, sort_ws, a_codes, a_scales, h_codes, h_scales, c2, part, counters, x_rec, h_rec, total;
 };
 Layout layout_of(const moe_dims_t* d) {
   const size_t M = d->M, K = d->K, I = d->I, E = d->E, R = M * d->topK;
@@ -51,6 +51,8 @@ Layout layout_of(const moe_dims_t* d) {
   if (few) {
     L.part = take(moe::mx_few_part_bytes((int)M));
     L.counters = take(moe::mx_few_counter_bytes((int)M, (int)K, (int)I, d->topK));
+    L.x_rec = take(moe::mx_few_scale_bytes((int)M, (int)K));
+    L.h_rec = take(moe::mx_few_scale_bytes((int)R, (int)I));
   }
   L.sorted = take(R * 4);
   L.expanded = take(R * 4);
@@ -88,9 +90,9 @@ int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_
     p.w1 = w1;
     p.w2 = w2;
     p.x_codes = at<uint8_t>(ws, L.a_codes);
-    p.x_scales = at<uint32_t>(ws, L.a_scales);
+    p.x_scales = at<uint8_t>(ws, L.x_rec);
     p.h_codes = at<uint8_t>(ws, L.h_codes);
-    p.h_scales = at<uint32_t>(ws, L.h_scales);
+    p.h_scales = at<uint8_t>(ws, L.h_rec);
     p.part = at<float>(ws, L.part);
     p.counters = at<int32_t>(ws, L.counters);
     p.out = out;

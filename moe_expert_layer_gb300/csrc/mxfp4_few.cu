@@ -9,15 +9,17 @@
 //
 // Kernel 2 is persistent, one CTA per SM, with one pipeline for both products, so that the
 // down projection's weights are on their way while the last of h is made: warp 0 copies
-// weight blocks; warps 4-7 in turn put a stage's weight scales in order and gather its token
-// rows into the MMA's operand; warp 1 copies the scales to tensor memory and issues the MMAs,
-// weight channels as rows, up to 16 routes of one expert as columns; warps 8-11 take the sums.
-// The stages of each product are cut into equal runs, one per CTA:
+// weight blocks; warps 4-11 in turn gather a stage's token rows into the MMA's operand, read a
+// turn ahead, and put its weight scales in order; warp 1 copies the scales to tensor memory and issues the MMAs,
+// weight channels as rows, up to 16 routes of one expert as columns; warps 8-11 take the
+// sums.  The stages of each product are cut into equal runs, one per CTA:
 //   - of (expert tile, 128-channel block, stage): where runs meet in a block each leaves its
 //     sums in the workspace, and the CTA that finishes last adds them in order of the runs,
 //     does the SwiGLU and counts the block on its tile;
 //   - of (output block, expert tile, stage), a tile's stages after all its blocks of h: a run's
-//     sums add up in shared memory over experts and stages alike, and meet the same way.
+//     sums add up in shared memory over experts and stages alike, and meet the same way.  A
+//     run that goes over the end of a block takes the block it ends in first: the tiles whose
+//     h was made last come last.
 // It is launched as a programmatic dependent of kernel 1: tables and first weights come while
 // that still runs.  A CTA waits for others' h, so all of them have to be resident: one per SM,
 // which the host checks fit.  Every wait is bounded, as in the grouped product.
@@ -28,10 +30,12 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kWeightWarp = 0, kMmaWarp = 1, kPrepWarp0 = 4, kPrepWarps = 4, kEpiWarp0 = 8;
+constexpr int kWeightWarp = 0, kMmaWarp = 1, kTokenWarp = 2, kScaleWarp0 = 4, kScaleWarps = 4, kEpiWarp0 = 8;
 constexpr int kRows = 16;                                  // routes per tile: the MMA's columns
 constexpr int kTokens = kMxBlockBytes;                     // of a stage: the token rows' codes
-constexpr int kTokenScales = kTokens + kRows * 128;        // and their scale words, arranged
+constexpr int kTokenScales = kTokens + kRows * 128;        // and their scales: 16 bytes a row, four rows
+                                                           // to 128, as copied; then arranged
+constexpr int kScaleRec = 16;                              // a row's scales of a stage: 8 bytes, padded
 constexpr int kStageBytes = kTokenScales + 2 * 512;
 constexpr int kStages = 10, kSfStages = 8;
 constexpr int kSfCols = 16, kSf0 = 2 * kRows, kTmemCols = 256;
@@ -49,18 +53,22 @@ struct FewArgs {
   const int32_t* expert_idx;
   const float* probs;
   const uint8_t *w1, *w2;
-  const uint8_t* x_codes;      // [M][K / 2]
-  const uint8_t* x_scales;     // [M][4 * planes(K)]
   uint8_t* h_codes;            // [R][I / 2]
-  uint8_t* h_scales;           // [R][4 * planes(I)]
+  uint8_t* h_scales;           // [R][stages(I)][kScaleRec]
   float* part;                 // per CTA: [2][16][128] of h, [2][M][128] of out
   int32_t* counters;           // [R][I / 64] runs of h blocks, [R] blocks of h, [K / 128] runs of out blocks
   __half* out;
   int32_t* status;
 };
 
+// Gathers of rows: codes, 128 bytes of a row, and scales, the stage's record.
+struct FewMaps {
+  CUtensorMap x_codes, x_scales, h_codes, h_scales;
+};
+
 struct Tables {
-  int list[kMxFewRoutes];      // routes by expert
+  int list[kMxFewRoutes];      // routes by expert,
+  int token[kMxFewRoutes];     // and their tokens
   int tile_e[kMxFewRoutes];    // expert tiles: expert,
   int tile_row[kMxFewRoutes];  // first row (of list) | rows << 16
   float prob[kMxFewRoutes];
@@ -97,16 +105,26 @@ struct Product {
   __device__ __forceinline__ int block_of(int64_t at) const { return (int)(at / per()); }
 };
 
-// The segments of a CTA, in order.
+// The segments of a CTA, in order: its run, or for the down product the part behind the last
+// block boundary in it and then the part before.
 template <bool DOWN>
 struct Walk {
   const Product<DOWN>& p;
-  int64_t at, end;
+  int64_t at, end, begin, mid;
   __device__ __forceinline__ Walk(const Product<DOWN>& p_) : p(p_) {
-    at = p.begin_of(blockIdx.x);
-    end = p.begin_of(blockIdx.x + 1);
+    begin = p.begin_of(blockIdx.x);
+    mid = end = p.begin_of(blockIdx.x + 1);
+    at = begin;
+    if (DOWN && end > begin) {
+      const int64_t edge = (end - 1) / p.per() * p.per();
+      if (edge > begin) at = mid = edge;
+    }
   }
   __device__ __forceinline__ bool next(Seg& s) {
+    if (DOWN && at == end && mid < end) {
+      at = begin;
+      end = mid;
+    }
     if (at >= end) return false;
     const int64_t unit = at / p.KB;
     s.kb0 = (int)(at - unit * p.KB);
@@ -165,7 +183,10 @@ __device__ __forceinline__ void make_tables(const FewArgs& a, Tables& t, int* co
   }
   if (e0 < a.E && e1 == a.E) t.tiles = run >> 16;
   __syncthreads();
-  if (e >= 0) t.list[count[e] + pos] = tid;
+  if (e >= 0) {
+    t.list[count[e] + pos] = tid;
+    t.token[count[e] + pos] = tid / a.topK;
+  }
   __syncthreads();
 }
 
@@ -196,13 +217,13 @@ struct Pipe {
 
 template <bool DOWN>
 __device__ __forceinline__ bool load_weights(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<DOWN>& p,
-                                             uint32_t elected, RingPos& at, int& n) {
+                                             uint32_t elected, RingPos& at) {
   Walk<DOWN> walk(p);
   Seg s;
   while (walk.next(s)) {
     const uint8_t* wb =
         (DOWN ? a.w2 : a.w1) + ((size_t)t.tile_e[s.tile] * p.NB + s.nb) * (size_t)p.KB * kMxBlockBytes;
-    for (int kb = s.kb0; kb < s.kb1; ++kb, ++n, at.next(kStages)) {
+    for (int kb = s.kb0; kb < s.kb1; ++kb, at.next(kStages)) {
       if (!warp_wait(&pp.empty[at.slot], at.phase ^ 1u, pp.abort_flag, pp.status)) return false;
       const uint32_t bar = smem_u32(&pp.full[at.slot]);
       expect_tx_elect(elected, bar, kMxBlockBytes);
@@ -244,84 +265,88 @@ __device__ __forceinline__ bool issue_mmas(const FewArgs& a, const Pipe& pp, con
   return true;
 }
 
-// A stage's token rows and scales: rows of x by token, or of h by route, 16 of 128 bytes and a
-// scale word for each half of the stage.
+// A stage's token rows: of x by token, or of h by route once all blocks of the tile's h are there.
 template <bool DOWN>
-__device__ __forceinline__ bool prepare_stages(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<DOWN>& p,
-                                               int who, int lane, RingPos& at, RingPos& old, int& n) {
-  const int depth = DOWN ? a.I : a.K, planes = (depth + 127) / 128;
-  const uint8_t* codes = DOWN ? a.h_codes : a.x_codes;
-  const uint32_t* scales = reinterpret_cast<const uint32_t*>(DOWN ? a.h_scales : a.x_scales);
+__device__ __forceinline__ bool load_tokens(const FewArgs& a, const FewMaps& maps, const Tables& t, const Pipe& pp,
+                                            const Product<DOWN>& p, uint32_t elected, int lane, RingPos& at) {
   const int32_t* ready = a.counters + (size_t)a.R * (a.I / 64);
+  const int* list = DOWN ? t.list : t.token;
+  int seen = -1;  // the last tile whose h was waited for
   Walk<DOWN> walk(p);
   Seg s;
   while (walk.next(s)) {
-    const int row0 = t.tile_row[s.tile] & 0xffff, rows = t.tile_row[s.tile] >> 16;
-    bool waited = !DOWN;
-    for (int kb = s.kb0; kb < s.kb1; ++kb, ++n, at.next(kStages)) {
-      if (n > kSfStages) old.next(kStages);
-      if (n % kPrepWarps != who) continue;
-      if (!waited) {  // all blocks of the tile's h
-        const bool ok = *pp.abort_flag == 0 && (lane != 0 || count_wait_bounded(ready + s.tile, a.I / 64));
-        if (!__all_sync(0xffffffffu, ok)) {
-          if (*pp.abort_flag == 0 && lane == 0) record_status(pp.status, MOE_ERR_TIMEOUT);
-          *pp.abort_flag = 1;
-          return false;
-        }
-        waited = true;
+    if (DOWN && s.tile != seen) {
+      const bool ok = *pp.abort_flag == 0 && (lane != 0 || count_wait_bounded(ready + s.tile, a.I / 64));
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (*pp.abort_flag == 0 && lane == 0) record_status(pp.status, MOE_ERR_TIMEOUT);
+        *pp.abort_flag = 1;
+        return false;
       }
-      // lane: rows lane / 8 + 4 i, 16-byte chunk lane % 8
-      uint4 row[4];
-      const int chunk = kb * 8 + (lane & 7);
+      fence_proxy_async_global();
+      seen = s.tile;
+    }
+    const int row0 = t.tile_row[s.tile] & 0xffff, last = (t.tile_row[s.tile] >> 16) - 1, groups = (last + 4) >> 2;
+    int4 y[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int c = (lane >> 3) + 4 * i;
-        row[i] = make_uint4(0, 0, 0, 0);
-        if (c < rows && chunk * 32 < depth) {
-          const int r = t.list[row0 + c];
-          row[i] = __ldcg(reinterpret_cast<const uint4*>(codes + (size_t)(DOWN ? r : r / a.topK) * (depth / 2) + chunk * 16));
-        }
-      }
-      uint32_t word = 0;
-      const int c = lane & 15, plane = 2 * kb + (lane >> 4);
-      if (c < rows && plane < planes) {
-        const int r = t.list[row0 + c];
-        word = __ldcg(scales + (size_t)(DOWN ? r : r / a.topK) * planes + plane);
-      }
-      // The stage that used the scale columns is done, and with it the slot's previous use: only
-      // then is `full` known to be in this use's phase (copies complete in any order).
-      if (n >= kSfStages && !warp_wait(&pp.empty[old.slot], old.phase, pp.abort_flag, pp.status)) return false;
-      uint8_t* st = pp.ring_g + at.slot * kStageBytes;
+    for (int g = 0; g < 4; ++g)
+      y[g] = make_int4(list[row0 + min(4 * g, last)], list[row0 + min(4 * g + 1, last)],
+                       list[row0 + min(4 * g + 2, last)], list[row0 + min(4 * g + 3, last)]);
+    for (int kb = s.kb0; kb < s.kb1; ++kb, at.next(kStages)) {
+      if (!warp_wait(&pp.empty[at.slot], at.phase ^ 1u, pp.abort_flag, pp.status)) return false;
+      const uint32_t bar = smem_u32(&pp.full[at.slot]), st = pp.ring + at.slot * kStageBytes;
+      expect_tx_elect(elected, bar, groups * 4 * (128 + kScaleRec));
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        *reinterpret_cast<uint4*>(st + kTokens + mx_chunk_at((lane >> 3) + 4 * i, lane & 7)) = row[i];
-      *reinterpret_cast<uint32_t*>(st + kTokenScales + (lane >> 4) * 512 + (lane & 15) * 16) = word;
-      if (!warp_wait(&pp.full[at.slot], at.phase, pp.abort_flag, pp.status)) return false;
-      const uint4 w0 = mx_scale_words(st + kMxCodeBytes, lane), w1 = mx_scale_words(st + kMxCodeBytes + 512, lane);
-      __syncwarp();
-      mx_put_scale_words(st + kMxCodeBytes, w0, lane);
-      mx_put_scale_words(st + kMxCodeBytes + 512, w1, lane);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&pp.sf[at.slot]);
+      for (int g = 0; g < 4; ++g)
+        if (g < groups) {
+          tma_gather4_elect(elected, st + kTokens + g * 512, DOWN ? &maps.h_codes : &maps.x_codes, kb * 128, y[g], bar);
+          tma_gather4_elect(elected, st + kTokenScales + g * 128, DOWN ? &maps.h_scales : &maps.x_scales,
+                            kb * kScaleRec, y[g], bar);
+        }
     }
   }
   return true;
 }
 
+// Puts the scales of this warp's stages, every kScaleWarps-th of the CTA's, in order.
+__device__ __forceinline__ void arrange_scales(const Pipe& pp, int who, int lane, int stages) {
+  for (int n = who; n < stages; n += kScaleWarps) {
+    // The stage that used the scale columns is done, and with it the slot's previous use: only
+    // then is `full` known to be in this use's phase (copies complete in any order).
+    const int old = n - kSfStages, slot = n % kStages;
+    if (old >= 0 && !warp_wait(&pp.empty[old % kStages], (old / kStages) & 1, pp.abort_flag, pp.status)) return;
+    if (!warp_wait(&pp.full[slot], (n / kStages) & 1, pp.abort_flag, pp.status)) return;
+    uint8_t* st = pp.ring_g + slot * kStageBytes;
+    const uint4 w0 = mx_scale_words(st + kMxCodeBytes, lane), w1 = mx_scale_words(st + kMxCodeBytes + 512, lane);
+    uint2 x = make_uint2(0, 0);
+    if (lane < kRows) x = *reinterpret_cast<const uint2*>(st + kTokenScales + (lane >> 2) * 128 + (lane & 3) * kScaleRec);
+    __syncwarp();
+    mx_put_scale_words(st + kMxCodeBytes, w0, lane);
+    mx_put_scale_words(st + kMxCodeBytes + 512, w1, lane);
+    if (lane < kRows) {
+      *reinterpret_cast<uint32_t*>(st + kTokenScales + lane * 16) = x.x;
+      *reinterpret_cast<uint32_t*>(st + kTokenScales + 512 + lane * 16) = x.y;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&pp.sf[slot]);
+  }
+}
+
 // The epilogue warps' barrier.
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// A run's sums of a block are in `mine` (global, visible to this thread's CTA only so far):
-// counts it, and returns whether all `runs` of the block's are there.
+// The CTA's sums of a block are in global memory: counts its run, and returns whether all `runs`
+// of the block's are there.  The barriers carry the other threads' writes and reads with the
+// first thread's fences.
 __device__ __forceinline__ bool last_run(int32_t* counter, int runs, bool first_thread, int* s_last) {
-  __threadfence();
   epi_sync();
-  if (first_thread) *s_last = atomicAdd(counter, 1) == runs - 1;
+  if (first_thread) {
+    __threadfence();
+    *s_last = atomicAdd(counter, 1) == runs - 1;
+    __threadfence();
+  }
   epi_sync();
-  const bool last = *s_last != 0;
-  if (last) __threadfence();
-  return last;
+  return *s_last != 0;
 }
 
 // The sums of segment u: 16 columns of this lane's channel.
@@ -340,36 +365,55 @@ __device__ __forceinline__ bool take_sums(const Pipe& pp, int u, int quarter, in
 
 __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<false>& p,
                                          float* xchg, int quarter, int lane, int& u, int* s_last) {
-  const int pair = quarter >> 1, odd = quarter & 1, ch = quarter * 32 + lane, planes = (a.I + 127) / 128;
+  const int pair = quarter >> 1, odd = quarter & 1, ch = quarter * 32 + lane;
+  const size_t rec_pitch = (size_t)((a.I + 255) / 256) * kScaleRec;
   float* give = xchg + pair * 512 + odd * 256 + lane;
   const float* take = xchg + pair * 512 + (odd ^ 1) * 256 + lane;
   int32_t* ready = a.counters + (size_t)a.R * (a.I / 64);
   const size_t cta_part = (size_t)2 * (16 + a.M) * 128;
   Walk<false> walk(p);
-  const int64_t begin = walk.at;
   Seg s;
   while (walk.next(s)) {
+    const int row0 = t.tile_row[s.tile] & 0xffff, rows = t.tile_row[s.tile] >> 16;
+    const int block = s.tile * p.NB + s.nb;
+    int c0 = blockIdx.x, c1 = c0;
+    if (s.kb1 - s.kb0 < p.KB) {
+      c0 = p.run_of((int64_t)block * p.KB);
+      c1 = p.run_of((int64_t)block * p.KB + p.KB - 1);
+    }
+    auto part_of = [&](int c) { return a.part + c * cta_part + (block != p.block_of(p.begin_of(c))) * 16 * 128 + ch; };
+    // Of two runs, the one that has the block's second half began with it long ago: its sums are
+    // read while this run's last MMAs are under way, and nothing need be written.  (Two sums add
+    // to the same bits in either order.)
+    float other[16];
+    bool there = false;
+    if (c1 - c0 == 1) {
+      there = epi_all(ld_acquire(a.counters + block) == 1);
+      if (there) {
+        const float* q = part_of(c0 == (int)blockIdx.x ? c1 : c0);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) other[i] = i < rows ? __ldcg(q + i * 128) : 0.0f;
+      }
+    }
     uint32_t v[16];
     if (!take_sums(pp, u, quarter, lane, v)) return false;
     ++u;
-    const int row0 = t.tile_row[s.tile] & 0xffff, rows = t.tile_row[s.tile] >> 16;
-    if (s.kb1 - s.kb0 < p.KB) {
-      const int block = s.tile * p.NB + s.nb;
-      const int64_t b0 = (int64_t)block * p.KB;
-      float* part = a.part + blockIdx.x * cta_part + (block != p.block_of(begin)) * 16 * 128;
+    if (there) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + other[i]);
+    } else if (c1 > c0) {
+      float* mine = part_of(blockIdx.x);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
-        if (i < rows) __stcg(part + i * 128 + ch, __uint_as_float(v[i]));
-      const int c0 = p.run_of(b0), c1 = p.run_of(b0 + p.KB - 1);
+        if (i < rows) __stcg(mine + i * 128, __uint_as_float(v[i]));
       if (!last_run(a.counters + block, c1 - c0 + 1, quarter == 0 && lane == 0, s_last)) continue;
       float acc[16] = {};
       for (int c = c0; c <= c1; ++c) {
-        const float* q = a.part + c * cta_part + (block != p.block_of(p.begin_of(c))) * 16 * 128 + ch;
-        float o[16];
+        const float* q = part_of(c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) o[i] = i < rows ? __ldcg(q + i * 128) : 0.0f;
+        for (int i = 0; i < 16; ++i) other[i] = i < rows ? __ldcg(q + i * 128) : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] += o[i];
+        for (int i = 0; i < 16; ++i) acc[i] += other[i];
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(acc[i]);
@@ -392,15 +436,18 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
       const int r = t.list[row0 + c], k = s.nb * 2 + pair;
       *reinterpret_cast<uint32_t*>(a.h_codes + (size_t)r * (a.I / 2) + k * 16 + (lane >> 3) * 4) = w;
       if (lane < 8) {
-        uint8_t* sc = a.h_scales + (size_t)r * planes * 4 + k;
+        uint8_t* sc = a.h_scales + r * rec_pitch + (k >> 3) * kScaleRec + (k & 7);
         *sc = (uint8_t)byte;
         if (k == a.I / 32 - 1)  // bytes of the word past the last block
           for (int z = 1; (k + z) & 3; ++z) sc[z] = 0;
       }
     }
-    __threadfence();
+    fence_proxy_async_global();
     epi_sync();  // h is written, and the exchange free
-    if (quarter == 0 && lane == 0) atomicAdd(ready + s.tile, 1);
+    if (quarter == 0 && lane == 0) {
+      __threadfence();
+      atomicAdd(ready + s.tile, 1);
+    }
   }
   return true;
 }
@@ -411,7 +458,6 @@ __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, co
   const size_t cta_part = (size_t)2 * (16 + a.M) * 128;
   int32_t* counters = a.counters + (size_t)a.R * (a.I / 64) + a.R;
   Walk<true> walk(p);
-  const int64_t begin = walk.at;
   Seg s;
   for (int i = 0; i < a.M; ++i) sums[i * 128 + ch] = 0.0f;
   if (p.tiles == 0)  // no route at all
@@ -426,26 +472,26 @@ __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, co
     for (int i = 0; i < 16; ++i)
       if (i < rows) {
         const int r = t.list[row0 + i];
-        float* o = sums + (r / a.topK) * 128 + ch;
+        float* o = sums + t.token[row0 + i] * 128 + ch;
         *o = fmaf(t.prob[r], __uint_as_float(v[i]), *o);
       }
     if (walk.at < walk.end && (s.tile < p.tiles - 1 || s.kb1 < p.KB)) continue;
     // the run's share of this output block is complete
     const int64_t b0 = (int64_t)s.nb * p.per(), b1 = b0 + p.per();
     __half* out = a.out + s.nb * 128;
-    if (begin <= b0 && walk.end >= b1) {
+    const int c0 = p.run_of(b0), c1 = p.run_of(b1 - 1);
+    if (c0 == c1) {
       for (int i = 0; i < a.M; ++i) {
         out[(size_t)i * a.K + ch] = from_f32<__half>(sums[i * 128 + ch]);
         sums[i * 128 + ch] = 0.0f;
       }
       continue;
     }
-    float* part = a.part + blockIdx.x * cta_part + 2 * 16 * 128 + (s.nb != p.block_of(begin)) * a.M * 128;
+    float* part = a.part + blockIdx.x * cta_part + 2 * 16 * 128 + (s.nb != p.block_of(walk.begin)) * a.M * 128;
     for (int i = 0; i < a.M; ++i) {
       __stcg(part + i * 128 + ch, sums[i * 128 + ch]);
       sums[i * 128 + ch] = 0.0f;
     }
-    const int c0 = p.run_of(b0), c1 = p.run_of(b1 - 1);
     if (!last_run(counters + s.nb, c1 - c0 + 1, quarter == 0 && lane == 0, s_last)) continue;
     // a token to a warp, four channels to a lane, the runs' sums four at a time
     for (int i = quarter; i < a.M; i += 4) {
@@ -476,14 +522,14 @@ __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, co
   return true;
 }
 
-__global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], sf_bar[kStages], accfull_bar[2],
       accempty_bar[2], final_bar;
   __shared__ Tables s_t;
   __shared__ int s_wsum[kThreads / 32];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_issued, s_last;
+  __shared__ int s_abort, s_last;
   const int warp = warp_index(), lane = threadIdx.x & 31;
   Pipe pp;
   pp.full = full_bar;
@@ -499,13 +545,12 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const FewArgs a) {
 
   if (threadIdx.x == 0) {
     s_abort = 0;
-    s_issued = 0;
   }
   if (warp == kMmaWarp) {
     tmem_alloc<false, kTmemCols>(&s_tmem);
     if (lane == 0) {
       for (int s = 0; s < kStages; ++s) {
-        mbar_init(&full_bar[s], 1);
+        mbar_init(&full_bar[s], 2);
         mbar_init(&empty_bar[s], 1);
         mbar_init(&sf_bar[s], 1);
       }
@@ -528,9 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const FewArgs a) {
   if (warp == kWeightWarp) {
     const uint32_t elected = elect_one();
     RingPos at;
-    int n = 0;
-    if (load_weights<false>(a, s_t, pp, up, elected, at, n)) load_weights<true>(a, s_t, pp, down, elected, at, n);
-    if (lane == 0) s_issued = n;
+    if (load_weights<false>(a, s_t, pp, up, elected, at)) load_weights<true>(a, s_t, pp, down, elected, at);
   } else if (warp == kMmaWarp) {
     const uint32_t elected = elect_one();
     RingPos at, sf;
@@ -539,12 +582,17 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const FewArgs a) {
     __syncwarp();
     mx_commit<false>(elected, smem_u32(&final_bar));  // every MMA done before tensor memory is freed
     mbar_wait_sleep_bounded(&final_bar, 0);
-  } else if (warp >= kPrepWarp0 && warp < kPrepWarp0 + kPrepWarps) {
+  } else if (warp == kTokenWarp) {
     asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's x and counters
-    RingPos at, old;  // old: the stage kSfStages before
-    int n = 0;
-    if (prepare_stages<false>(a, s_t, pp, up, warp - kPrepWarp0, lane, at, old, n))
-      prepare_stages<true>(a, s_t, pp, down, warp - kPrepWarp0, lane, at, old, n);
+    fence_proxy_async_global();
+    const uint32_t elected = elect_one();
+    RingPos at;
+    if (load_tokens<false>(a, maps, s_t, pp, up, elected, lane, at))
+      load_tokens<true>(a, maps, s_t, pp, down, elected, lane, at);
+  } else if (warp >= kScaleWarp0 && warp < kScaleWarp0 + kScaleWarps) {
+    const int b = blockIdx.x;
+    arrange_scales(pp, warp - kScaleWarp0, lane,
+                   (int)(up.begin_of(b + 1) - up.begin_of(b) + down.begin_of(b + 1) - down.begin_of(b)));
   } else if (warp >= kEpiWarp0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int u = 0;
@@ -555,11 +603,11 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const FewArgs a) {
     }
   }
 
+  // Every copy has been waited for, unless the CTA gave up: then those still under way get the
+  // time that they could take before shared memory is released.
   __syncthreads();
-  if (threadIdx.x == 0) {  // copies still in flight (only after an abort) land before shared memory is released
-    const int n1 = s_issued;
-    for (int n = max(0, n1 - kStages); n < n1; ++n) mbar_wait_bounded(&full_bar[n % kStages], (n / kStages) & 1);
-  }
+  if (s_abort && threadIdx.x == 0)
+    for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < kWaitLimitNs / 100;) __nanosleep(1000);
   tc_fence_before();
   __syncthreads();
   __syncwarp();
@@ -599,7 +647,10 @@ __global__ void __launch_bounds__(kXThreads) mx_few_x_kernel(const __half* x, in
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = mx_scaled(v[j], mult, b);
   *reinterpret_cast<uint32_t*>(codes + (size_t)t * (K / 2) + k / 2) = mx_codes8(v);
-  if ((threadIdx.x & 3) == 0) scales[(size_t)t * (K / 32) + k / 32] = (uint8_t)b;
+  if ((threadIdx.x & 3) == 0) {
+    const int c = k / 32;  // scaled block of the row
+    scales[((size_t)t * ((K + 255) / 256) + (c >> 3)) * kScaleRec + (c & 7)] = (uint8_t)b;
+  }
 }
 
 int counters_of(int M, int K, int I, int topK) { return M * topK * (I / 64 + 1) + K / 128; }
@@ -607,6 +658,8 @@ int counters_of(int M, int K, int I, int topK) { return M * topK * (I / 64 + 1) 
 }  // namespace
 
 size_t mx_few_part_bytes(int M) { return (size_t)sm_count() * 2 * (16 + M) * 128 * 4; }
+// Bytes of the scales of `rows` rows of depth D in the records of kernel 2.
+size_t mx_few_scale_bytes(int rows, int D) { return (size_t)rows * mx_depth_blocks(D) * kScaleRec; }
 size_t mx_few_counter_bytes(int M, int K, int I, int topK) { return (size_t)counters_of(M, K, I, topK) * 4; }
 
 // Whether every CTA of kernel 2 can be resident at once: one per SM.
@@ -631,25 +684,31 @@ cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
   const int n_counters = counters_of(p.M, p.K, p.I, p.topK);
   const int x_blocks = (int)(((size_t)p.M * p.K / 8 + kXThreads - 1) / kXThreads);
   mx_few_x_kernel<<<x_blocks, kXThreads, 0, stream>>>(reinterpret_cast<const __half*>(p.x), p.M, p.K, p.x_codes,
-                                                      reinterpret_cast<uint8_t*>(p.x_scales), p.counters, n_counters,
+                                                      p.x_scales, p.counters, n_counters,
                                                       p.status);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  const int R = p.M * p.topK;
+  const uint64_t xs = (uint64_t)mx_depth_blocks(p.K) * kScaleRec, hs = (uint64_t)mx_depth_blocks(p.I) * kScaleRec;
+  FewMaps maps;
+  if (!encode_tensor_map_rows(&maps.x_codes, p.x_codes, p.K / 2, p.K / 2, p.M, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tensor_map_rows(&maps.h_codes, p.h_codes, p.I / 2, p.I / 2, R, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !encode_tensor_map_rows(&maps.x_scales, p.x_scales, xs, xs, p.M, kScaleRec, CU_TENSOR_MAP_SWIZZLE_NONE) ||
+      !encode_tensor_map_rows(&maps.h_scales, p.h_scales, hs, hs, R, kScaleRec, CU_TENSOR_MAP_SWIZZLE_NONE))
+    return cudaErrorInvalidValue;
   FewArgs a;
   a.M = p.M;
   a.K = p.K;
   a.I = p.I;
   a.E = p.E;
   a.topK = p.topK;
-  a.R = p.M * p.topK;
+  a.R = R;
   a.expert_idx = p.expert_idx;
   a.probs = p.probs;
   a.w1 = p.w1;
   a.w2 = p.w2;
-  a.x_codes = p.x_codes;
-  a.x_scales = reinterpret_cast<const uint8_t*>(p.x_scales);
   a.h_codes = p.h_codes;
-  a.h_scales = reinterpret_cast<uint8_t*>(p.h_scales);
+  a.h_scales = p.h_scales;
   a.part = p.part;
   a.counters = p.counters;
   a.out = reinterpret_cast<__half*>(p.out);
@@ -664,7 +723,7 @@ cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
   after.val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = &after;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mx_few_kernel, a);
+  return cudaLaunchKernelEx(&cfg, mx_few_kernel, maps, a);
 }
 
 }  // namespace moe

@@ -53,6 +53,20 @@ inline bool encode_tensor_map_words(CUtensorMap* m, const void* base, uint64_t i
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of bytes of any pitch that is a multiple of 16, box_inner x 1, for gathers of rows.
+inline bool encode_tensor_map_rows(CUtensorMap* m, const void* base, uint64_t inner, uint64_t pitch, uint64_t rows,
+                                   uint32_t box_inner, CUtensorMapSwizzle swizzle) {
+  PFN_encodeTiled fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[2] = {inner, rows};
+  cuuint64_t strides[1] = {pitch};
+  cuuint32_t box[2] = {box_inner, 1};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Per-device, once-only host state (kernel attributes, SM counts): devices 0..63.
 constexpr int kMaxDevices = 64;
 inline int current_device() {
