@@ -68,7 +68,7 @@ struct MxFewProblem {
   uint16_t* out;
   int32_t* status;
 };
-size_t mx_few_part_bytes(int M);
+size_t mx_few_part_bytes(int M, int topK);
 size_t mx_few_scale_bytes(int rows, int D);
 size_t mx_few_counter_bytes(int M, int K, int I, int topK);
 cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream);

@@ -49,7 +49,7 @@ Layout layout_of(const moe_dims_t* d) {
   L.status = take(gmm_workspace_bytes());
   const bool few = moe::mx_few(d->M, d->topK);
   if (few) {
-    L.part = take(moe::mx_few_part_bytes((int)M));
+    L.part = take(moe::mx_few_part_bytes((int)M, d->topK));
     L.counters = take(moe::mx_few_counter_bytes((int)M, (int)K, (int)I, d->topK));
     L.x_rec = take(moe::mx_few_scale_bytes((int)M, (int)K));
     L.h_rec = take(moe::mx_few_scale_bytes((int)R, (int)I));

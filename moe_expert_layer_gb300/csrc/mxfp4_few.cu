@@ -8,18 +8,21 @@
 // dispatched or permuted in memory.
 //
 // Kernel 2 is persistent, one CTA per SM, with one pipeline for both products, so that the
-// down projection's weights are on their way while the last of h is made: warp 0 copies
-// weight blocks; warps 4-11 in turn gather a stage's token rows into the MMA's operand, read a
-// turn ahead, and put its weight scales in order; warp 1 copies the scales to tensor memory and issues the MMAs,
-// weight channels as rows, up to 16 routes of one expert as columns; warps 8-11 take the
-// sums.  The stages of each product are cut into equal runs, one per CTA:
-//   - of (expert tile, 128-channel block, stage): where runs meet in a block each leaves its
-//     sums in the workspace, and the CTA that finishes last adds them in order of the runs,
-//     does the SwiGLU and counts the block on its tile;
-//   - of (output block, expert tile, stage), a tile's stages after all its blocks of h: a run's
-//     sums add up in shared memory over experts and stages alike, and meet the same way.  A
-//     run that goes over the end of a block takes the block it ends in first: the tiles whose
-//     h was made last come last.
+// down projection's weights are on their way while the last of h is made: warp 0 copies weight
+// blocks; warp 2 gathers the token rows and their scales, by tensor copies too (plain loads wait
+// behind the ~170 KB of copies that an SM has under way); warps 4-7 in turn put a stage's scales
+// in tensor-memory order; warp 1 copies those on and issues the MMAs, weight channels as rows, up
+// to 16 routes of one expert as columns; warps 8-11 take the sums.
+//   - Of the gate and up product's (expert tile, 128-channel block) units, in this order, the
+//     first, as many as do not fill a whole round of the CTAs, are cut into one run of stages per
+//     CTA: where runs meet in a unit each leaves its sums in the workspace, and the CTA that
+//     finishes last adds them in order.  The others are dealt out whole, in turn, so that the
+//     tiles' h come one after the other and the last of them without a meeting.  The CTA that has
+//     a unit's sums does the SwiGLU and counts the unit on its tile.
+//   - The down product's stages, in order of (output block, expert tile, stage), are cut into one
+//     run per CTA, whose sums add up in shared memory over experts and stages alike and meet the
+//     same way.  A run that goes over the end of a block takes the block it ends in first: the
+//     tiles whose h is made last come last, and nothing waits for most of h.
 // It is launched as a programmatic dependent of kernel 1: tables and first weights come while
 // that still runs.  A CTA waits for others' h, so all of them have to be resident: one per SM,
 // which the host checks fit.  Every wait is bounded, as in the grouped product.
@@ -37,7 +40,7 @@ constexpr int kTokenScales = kTokens + kRows * 128;        // and their scales: 
                                                            // to 128, as copied; then arranged
 constexpr int kScaleRec = 16;                              // a row's scales of a stage: 8 bytes, padded
 constexpr int kStageBytes = kTokenScales + 2 * 512;
-constexpr int kStages = 10, kSfStages = 8;
+constexpr int kStages = 6, kSfStages = 5;
 constexpr int kSfCols = 16, kSf0 = 2 * kRows, kTmemCols = 256;
 static_assert(kStageBytes % 1024 == 0 && kTokens % 1024 == 0, "swizzled rows");
 static_assert(kSf0 + kSfStages * kSfCols <= kTmemCols && kSfStages < kStages, "tensor memory");
@@ -55,7 +58,7 @@ struct FewArgs {
   const uint8_t *w1, *w2;
   uint8_t* h_codes;            // [R][I / 2]
   uint8_t* h_scales;           // [R][stages(I)][kScaleRec]
-  float* part;                 // per CTA: [2][16][128] of h, [2][M][128] of out
+  float* part;                 // [runs][2][rows][128] of h, [runs][2][M][128] of out
   int32_t* counters;           // [R][I / 64] runs of h blocks, [R] blocks of h, [K / 128] runs of out blocks
   __half* out;
   int32_t* status;
@@ -80,22 +83,27 @@ struct Seg {
   int nb, tile, kb0, kb1;
 };
 
-// One of the two products: its blocks of 128 channels, 256-deep stages, and runs.
+// One of the two products: its blocks of 128 channels, 256-deep stages, and the stages that are
+// cut into one run per CTA: all of the down product's, those of the first `head` units of the
+// gate and up product.
 template <bool DOWN>
 struct Product {
-  int NB, KB, tiles, runs;
-  int64_t total;
+  int NB, KB, tiles, units, head, runs;
+  int64_t cut;  // stages in runs
   __device__ __forceinline__ Product(const FewArgs& a, int tiles_) {
+    const int G = gridDim.x;
     tiles = tiles_;
     NB = DOWN ? a.K / 128 : a.I / 64;
     KB = ((DOWN ? a.I : a.K) + 255) / 256;
-    total = (int64_t)NB * tiles * KB;
-    runs = (int)min((int64_t)gridDim.x, total);  // none empty
+    units = NB * tiles;
+    head = DOWN ? units : units % G;
+    cut = (int64_t)head * KB;
+    runs = (int)min((int64_t)G, cut);  // none empty
   }
-  __device__ __forceinline__ int64_t begin_of(int run) const { return runs ? total * min(run, runs) / runs : 0; }
+  __device__ __forceinline__ int64_t begin_of(int run) const { return runs ? cut * min(run, runs) / runs : 0; }
   // The run that holds stage `at`.
   __device__ __forceinline__ int run_of(int64_t at) const {
-    int c = (int)(at * runs / total);
+    int c = (int)(at * runs / cut);
     while (begin_of(c + 1) <= at) ++c;
     while (begin_of(c) > at) --c;
     return c;
@@ -103,33 +111,46 @@ struct Product {
   // Stages of a block whose sums belong together, and the block that holds stage `at`.
   __device__ __forceinline__ int per() const { return DOWN ? tiles * KB : KB; }
   __device__ __forceinline__ int block_of(int64_t at) const { return (int)(at / per()); }
+  // Stages of this CTA.
+  __device__ __forceinline__ int stages() const {
+    const int b = blockIdx.x, G = gridDim.x;
+    return (int)(begin_of(b + 1) - begin_of(b)) + (units - head > b ? (units - head - b + G - 1) / G * KB : 0);
+  }
 };
 
-// The segments of a CTA, in order: its run, or for the down product the part behind the last
-// block boundary in it and then the part before.
+// The segments of a CTA, in order: those of its run, then its whole units; or those of its run
+// behind the last block boundary in it, then those before.
 template <bool DOWN>
 struct Walk {
   const Product<DOWN>& p;
   int64_t at, end, begin, mid;
+  int unit;  // the next whole one
   __device__ __forceinline__ Walk(const Product<DOWN>& p_) : p(p_) {
-    begin = p.begin_of(blockIdx.x);
+    begin = at = p.begin_of(blockIdx.x);
     mid = end = p.begin_of(blockIdx.x + 1);
-    at = begin;
+    unit = p.head + blockIdx.x;
     if (DOWN && end > begin) {
       const int64_t edge = (end - 1) / p.per() * p.per();
       if (edge > begin) at = mid = edge;
     }
   }
   __device__ __forceinline__ bool next(Seg& s) {
-    if (DOWN && at == end && mid < end) {
-      at = begin;
-      end = mid;
+    if (at == end) {
+      if (DOWN) {
+        if (mid == end) return false;
+        at = begin;
+        end = mid;
+      } else {
+        if (unit >= p.units) return false;
+        at = (int64_t)unit * p.KB;
+        end = at + p.KB;
+        unit += gridDim.x;
+      }
     }
-    if (at >= end) return false;
-    const int64_t unit = at / p.KB;
-    s.kb0 = (int)(at - unit * p.KB);
-    s.tile = (int)(DOWN ? unit % p.tiles : unit / p.NB);
-    s.nb = (int)(DOWN ? unit / p.tiles : unit % p.NB);
+    const int64_t u = at / p.KB;
+    s.kb0 = (int)(at - u * p.KB);
+    s.tile = (int)(DOWN ? u % p.tiles : u / p.NB);
+    s.nb = (int)(DOWN ? u / p.tiles : u % p.NB);
     s.kb1 = (int)min((int64_t)p.KB, s.kb0 + (end - at));
     at += s.kb1 - s.kb0;
     return true;
@@ -332,6 +353,9 @@ __device__ __forceinline__ void arrange_scales(const Pipe& pp, int who, int lane
   }
 }
 
+// Words of the workspace that hold sums of h, two units to a run, before those of out.
+__host__ __device__ inline size_t part_words_of_h(int G, int R) { return (size_t)G * 2 * (R < kRows ? R : kRows) * 128; }
+
 // The epilogue warps' barrier.
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -370,53 +394,52 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
   float* give = xchg + pair * 512 + odd * 256 + lane;
   const float* take = xchg + pair * 512 + (odd ^ 1) * 256 + lane;
   int32_t* ready = a.counters + (size_t)a.R * (a.I / 64);
-  const size_t cta_part = (size_t)2 * (16 + a.M) * 128;
+  const size_t part_rows = min(kRows, a.R);
   Walk<false> walk(p);
   Seg s;
   while (walk.next(s)) {
     const int row0 = t.tile_row[s.tile] & 0xffff, rows = t.tile_row[s.tile] >> 16;
-    const int block = s.tile * p.NB + s.nb;
-    int c0 = blockIdx.x, c1 = c0;
+    const int block = s.tile * p.NB + s.nb, run = blockIdx.x;
+    int c0 = run, c1 = run;
     if (s.kb1 - s.kb0 < p.KB) {
       c0 = p.run_of((int64_t)block * p.KB);
       c1 = p.run_of((int64_t)block * p.KB + p.KB - 1);
     }
-    auto part_of = [&](int c) { return a.part + c * cta_part + (block != p.block_of(p.begin_of(c))) * 16 * 128 + ch; };
-    // Of two runs, the one that has the block's second half began with it long ago: its sums are
-    // read while this run's last MMAs are under way, and nothing need be written.  (Two sums add
-    // to the same bits in either order.)
-    float other[16];
-    bool there = false;
-    if (c1 - c0 == 1) {
-      there = epi_all(ld_acquire(a.counters + block) == 1);
-      if (there) {
-        const float* q = part_of(c0 == (int)blockIdx.x ? c1 : c0);
+    auto part_of = [&](int c) {
+      return a.part + ((size_t)c * 2 + (block != p.block_of(p.begin_of(c)))) * part_rows * 128 + ch;
+    };
+    // The unit's last run, if the others have been counted already, reads their sums while its
+    // own MMAs are under way and writes nothing.
+    float sum[16] = {};
+    auto add = [&](int c) {
+      float o[16];
+      const float* q = part_of(c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) other[i] = i < rows ? __ldcg(q + i * 128) : 0.0f;
-      }
+      for (int i = 0; i < 16; ++i) o[i] = i < rows ? __ldcg(q + i * 128) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sum[i] += o[i];
+    };
+    bool there = false;
+    if (c1 > c0 && run == c1) {
+      there = epi_all(ld_acquire(a.counters + block) == c1 - c0);
+      if (there)
+        for (int c = c0; c < c1; ++c) add(c);
     }
     uint32_t v[16];
     if (!take_sums(pp, u, quarter, lane, v)) return false;
     ++u;
     if (there) {
 #pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + other[i]);
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[i] + __uint_as_float(v[i]));
     } else if (c1 > c0) {
-      float* mine = part_of(blockIdx.x);
+      float* mine = part_of(run);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (i < rows) __stcg(mine + i * 128, __uint_as_float(v[i]));
       if (!last_run(a.counters + block, c1 - c0 + 1, quarter == 0 && lane == 0, s_last)) continue;
-      float acc[16] = {};
-      for (int c = c0; c <= c1; ++c) {
-        const float* q = part_of(c);
+      for (int c = c0; c <= c1; ++c) add(c);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) other[i] = i < rows ? __ldcg(q + i * 128) : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) acc[i] += other[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(acc[i]);
+      for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[i]);
     }
     // warps in pairs, 32 gate channels and the 32 up channels that multiply them: of 16 rows
     // each warp finishes 8, with the other's half through shared memory
@@ -455,7 +478,7 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
 __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<true>& p,
                                            float* sums, int quarter, int lane, int& u, int* s_last) {
   const int ch = quarter * 32 + lane;
-  const size_t cta_part = (size_t)2 * (16 + a.M) * 128;
+  float* parts = a.part + part_words_of_h(gridDim.x, a.R);
   int32_t* counters = a.counters + (size_t)a.R * (a.I / 64) + a.R;
   Walk<true> walk(p);
   Seg s;
@@ -487,7 +510,7 @@ __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, co
       }
       continue;
     }
-    float* part = a.part + blockIdx.x * cta_part + 2 * 16 * 128 + (s.nb != p.block_of(walk.begin)) * a.M * 128;
+    float* part = parts + ((size_t)blockIdx.x * 2 + (s.nb != p.block_of(walk.begin))) * a.M * 128;
     for (int i = 0; i < a.M; ++i) {
       __stcg(part + i * 128 + ch, sums[i * 128 + ch]);
       sums[i * 128 + ch] = 0.0f;
@@ -501,8 +524,8 @@ __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, co
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           o[k] = c + k <= c1 ? __ldcg(reinterpret_cast<const float4*>(
-                                   a.part + (c + k) * cta_part + 2 * 16 * 128 +
-                                   (s.nb != p.block_of(p.begin_of(c + k))) * a.M * 128 + i * 128) + lane)
+                                   parts + ((size_t)(c + k) * 2 + (s.nb != p.block_of(p.begin_of(c + k)))) * a.M * 128 +
+                                   i * 128) + lane)
                              : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -590,9 +613,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_consta
     if (load_tokens<false>(a, maps, s_t, pp, up, elected, lane, at))
       load_tokens<true>(a, maps, s_t, pp, down, elected, lane, at);
   } else if (warp >= kScaleWarp0 && warp < kScaleWarp0 + kScaleWarps) {
-    const int b = blockIdx.x;
-    arrange_scales(pp, warp - kScaleWarp0, lane,
-                   (int)(up.begin_of(b + 1) - up.begin_of(b) + down.begin_of(b + 1) - down.begin_of(b)));
+    arrange_scales(pp, warp - kScaleWarp0, lane, up.stages() + down.stages());
   } else if (warp >= kEpiWarp0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int u = 0;
@@ -657,7 +678,9 @@ int counters_of(int M, int K, int I, int topK) { return M * topK * (I / 64 + 1) 
 
 }  // namespace
 
-size_t mx_few_part_bytes(int M) { return (size_t)sm_count() * 2 * (16 + M) * 128 * 4; }
+size_t mx_few_part_bytes(int M, int topK) {
+  return (part_words_of_h(sm_count(), M * topK) + (size_t)sm_count() * 2 * M * 128) * 4;
+}
 // Bytes of the scales of `rows` rows of depth D in the records of kernel 2.
 size_t mx_few_scale_bytes(int rows, int D) { return (size_t)rows * mx_depth_blocks(D) * kScaleRec; }
 size_t mx_few_counter_bytes(int M, int K, int I, int topK) { return (size_t)counters_of(M, K, I, topK) * 4; }
