@@ -139,10 +139,26 @@ def _p(t):
     return t.data_ptr()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """A function that gives torch's current stream as a raw handle: straight from torch's core where
+    it has it (the public call builds a Stream object each time, microseconds of a short call)."""
+    import torch
+    core = torch._C
+    if hasattr(core, "_cuda_getCurrentRawStream") and hasattr(core, "_cuda_getDevice"):
+        torch.cuda.current_stream()  # initialises CUDA
+        return lambda: core._cuda_getCurrentRawStream(core._cuda_getDevice())
+    return lambda: torch.cuda.current_stream().cuda_stream
+
+
 def _stream(stream):
+    global _current_stream
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -357,21 +373,25 @@ def moe_route_sort_noalloc(d, expert_idx, sorted_src_route, expanded_row_idx, to
 TYPE_F32, TYPE_F16, TYPE_BF16 = 0, 1, 2
 SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
 _TYPES = {"torch.float32": TYPE_F32, "torch.float16": TYPE_F16, "torch.bfloat16": TYPE_BF16}
+_types = {}  # the same by torch.dtype, filled as they come (a lookup by name takes a microsecond)
 
 
 def _type(t):
-    try:
-        return _TYPES[str(t.dtype)]
-    except KeyError:
-        raise ValueError("float32, float16 or bfloat16 wanted; got %s" % t.dtype) from None
+    k = _types.get(t.dtype)
+    if k is None:
+        if str(t.dtype) not in _TYPES:
+            raise ValueError("float32, float16 or bfloat16 wanted; got %s" % t.dtype)
+        k = _types[t.dtype] = _TYPES[str(t.dtype)]
+    return k
 
 
 def _rows(t):
     """Pointer and row stride (elements) of a 2-D tensor whose rows are dense."""
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or (strides[1] != 1 and shape[1] > 1):
         raise ValueError("a 2-D tensor with dense rows wanted; got shape %s, strides %s"
-                         % (tuple(t.shape), tuple(t.stride())))
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+                         % (tuple(shape), tuple(strides)))
+    return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1]
 
 
 def _sized(t, n, size, what):

@@ -1,77 +1,112 @@
 // MXFP4 quantisation of rows and weights, its inverse, and the packing of MXFP4 weights
-// into blocks (include/moe_mxfp4.h).  One thread per scaled block of 32 elements.
+// into blocks (include/moe_mxfp4.h).
+//
+// Bound by bytes: eight elements to a lane, so that a warp reads 512 bytes (16-bit types) and
+// writes 128 bytes of codes of one row at a time, and a scaled block of 32 is four neighbouring
+// lanes, whose maximum is two shuffles.  The four scale bytes of 128 elements are put together
+// by shuffles too and written as one word.
 #include "mxfp4.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
 
+// Blocks for `items` threads' worth of work, at most a few for each the device can hold: the
+// kernels go on in strides.
 inline int grid_of(size_t items) {
-  const size_t b = (items + kThreads - 1) / kThreads;
-  return (int)(b < ((size_t)1 << 30) ? b : ((size_t)1 << 30));
+  const size_t b = (items + kThreads - 1) / kThreads, most = (size_t)sm_count() * 32;
+  return (int)(b < most ? b : most);
 }
 
-// The block of 32 at p: its code chunk and scale byte.
-template <typename T>
-__device__ __forceinline__ uint4 quant_block(const T* p, uint32_t& b) {
-  float v[32];
+// Eight elements at p (VEC: p aligned to 16 bytes) as fp32.
+template <typename T, bool VEC>
+__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+  if (VEC) {
+    union {
+      T t[8];
+      uint4 u[sizeof(T) / 2];
+    } r;
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(r.t[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(p[i]);
+  }
+}
+
+// The codes of this lane's eight elements and the scale byte of the block of its four lanes
+// (an aligned group of four lanes enters together).
+__device__ __forceinline__ uint32_t quant8(float (&v)[8], uint32_t& b) {
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    v[i] = to_f32<T>(p[i]);
-    a = max(a, abs_bits(v[i]));
-  }
+  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[i]));
+  const uint32_t group = 0xfu << (threadIdx.x & 28u);
+  a = max(a, __shfl_xor_sync(group, a, 1));
+  a = max(a, __shfl_xor_sync(group, a, 2));
   b = mx_scale_byte(a);
   const float mult = mx_multiplier(b);
-  uint32_t w[4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    float s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) s[i] = mx_scaled(v[8 * k + i], mult, b);
-    w[k] = mx_codes8(s);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+  for (int i = 0; i < 8; ++i) v[i] = mx_scaled(v[i], mult, b);
+  return mx_codes8(v);
 }
 
-template <typename T>
-__global__ void quant_rows_kernel(int M, int D, const T* x, int64_t stride, const int32_t* row_map, int copies, int rows,
-                                  uint8_t* codes, uint8_t* scales, int pitch) {
-  const int nblk = (D + 127) / 128 * 4;  // blocks of a row, those past D included (scale 0)
-  const size_t n = (size_t)M * nblk;
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kThreads) {
-    const int t = (int)(i / nblk), k = (int)(i % nblk);
-    uint32_t b = 0;
-    uint4 c = make_uint4(0, 0, 0, 0);
-    if (k * 32 < D) c = quant_block<T>(x + (int64_t)t * stride + k * 32, b);
+// One thread per eight elements of a row of x, the row rounded up to 128 elements (16 lanes, so
+// that a word of four scale bytes is made by lanes of one warp; zero bytes past D).
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(kThreads) quant_rows_kernel(int M, int D, const T* x, int64_t stride,
+                                                              const int32_t* row_map, int copies, int rows,
+                                                              uint8_t* codes, uint32_t* scales, int pitch) {
+  const int per = (D + 127) / 128 * 16;
+  const int64_t n = (int64_t)M * per, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+    const int t = (int)(i / per), c = (int)(i - (int64_t)t * per);  // chunk of eight
+    uint32_t b = 0, w = 0;
+    if (c * 8 < D) {  // D is a multiple of 32: a group of four lanes has the same answer
+      float v[8];
+      load8<T, VEC>(x + (int64_t)t * stride + c * 8, v);
+      w = quant8(v, b);
+    }
+    // bytes of lanes 0, 4, 8, 12 of the 16
+    const uint32_t half = 0xffffu << (threadIdx.x & 16u);
+    uint32_t word = b << (8 * ((c >> 2) & 3));
+    word |= __shfl_xor_sync(half, word, 4);
+    word |= __shfl_xor_sync(half, word, 8);
     for (int j = 0; j < copies; ++j) {
-      const int d = row_map ? row_map[(size_t)t * copies + j] : t;
+      const int d = row_map ? __ldg(row_map + (int64_t)t * copies + j) : t;
       if (d < 0 || d >= rows) continue;
-      if (k * 32 < D) *reinterpret_cast<uint4*>(codes + (size_t)d * (D / 2) + k * 16) = c;
-      scales[((size_t)(k >> 2) * pitch + d) * 4 + (k & 3)] = (uint8_t)b;
+      if (c * 8 < D) *reinterpret_cast<uint32_t*>(codes + (size_t)d * (D / 2) + c * 4) = w;
+      if ((c & 15) == 0) scales[(size_t)(c >> 4) * pitch + d] = word;
     }
   }
 }
 
+// One thread per eight elements.
 template <typename T>
-__global__ void dequant_rows_kernel(int rows, int D, const uint8_t* codes, const uint8_t* scales, int pitch, T* out) {
-  const int nblk = D / 32;
-  const size_t n = (size_t)rows * nblk;
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += (size_t)gridDim.x * kThreads) {
-    const size_t r = i / nblk;
-    const int k = (int)(i % nblk);
-    const float s = mx_scale_value(scales[((size_t)(k >> 2) * pitch + r) * 4 + (k & 3)]);
-    const uint8_t* c = codes + r * (D / 2) + k * 16;
-    T* o = out + r * D + k * 32;
-    for (int j = 0; j < 16; ++j) {
-      o[2 * j] = from_f32<T>(mx_value(c[j] & 15u) * s);
-      o[2 * j + 1] = from_f32<T>(mx_value(c[j] >> 4) * s);
-    }
+__global__ void __launch_bounds__(kThreads) dequant_rows_kernel(int rows, int D, const uint8_t* codes,
+                                                                const uint32_t* scales, int pitch, T* out) {
+  const int per = D / 8;
+  const int64_t n = (int64_t)rows * per, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+    const int r = (int)(i / per), c = (int)(i - (int64_t)r * per);
+    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
+    const uint32_t b = (__ldg(scales + (size_t)(c >> 4) * pitch + r) >> (8 * ((c >> 2) & 3))) & 255u;
+    const float s = mx_scale_value(b);
+    union {
+      T t[8];
+      uint4 u[sizeof(T) / 2];
+    } o;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) o.t[k] = from_f32<T>(mx_value((w >> (4 * k)) & 15u) * s);
+#pragma unroll
+    for (int k = 0; k < (int)sizeof(T) / 2; ++k) reinterpret_cast<uint4*>(out)[i * (sizeof(T) / 2) + k] = o.u[k];
   }
 }
 
-// Item i -> chunk c of row r of block `blk` (nb, kb of expert e), and its source row.
+// Chunk c (32 elements) of row r of weight block `blk`, and its source row.
 struct BlockItem {
   size_t blk, row;
   int r, c, k;  // k: scaled block along D
@@ -90,27 +125,36 @@ __device__ __forceinline__ BlockItem block_item(size_t i, int N, int KB, bool ga
   return it;
 }
 
+// Four threads to a chunk.
 template <typename T>
-__global__ void quant_weights_kernel(int N, int D, int KB, bool gate_up, size_t items, const T* w, uint8_t* blocks) {
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < items; i += (size_t)gridDim.x * kThreads) {
-    const BlockItem it = block_item(i, N, KB, gate_up);
-    uint32_t b = 0;
-    uint4 c = make_uint4(0, 0, 0, 0);
-    if (it.k * 32 < D) c = quant_block<T>(w + it.row * D + it.k * 32, b);
+__global__ void __launch_bounds__(kThreads) quant_weights_kernel(int N, int D, int KB, bool gate_up, size_t items,
+                                                                 const T* w, uint8_t* blocks) {
+  const size_t n = items * 4, step = (size_t)gridDim.x * kThreads;
+  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+    const BlockItem it = block_item(i >> 2, N, KB, gate_up);
+    const int part = (int)i & 3;
+    uint32_t b = 0, c = 0;
+    if (it.k * 32 < D) {
+      float v[8];
+      load8<T, true>(w + it.row * D + it.k * 32 + part * 8, v);
+      c = quant8(v, b);
+    }
     uint8_t* blk = blocks + it.blk * kMxBlockBytes;
-    *reinterpret_cast<uint4*>(blk + mx_chunk_at(it.r, it.c)) = c;
-    blk[mx_scale_at(it.r, it.c)] = (uint8_t)b;
+    *reinterpret_cast<uint32_t*>(blk + mx_chunk_at(it.r, it.c) + part * 4) = c;
+    if (part == 0) blk[mx_scale_at(it.r, it.c)] = (uint8_t)b;
   }
 }
 
-__global__ void pack_weights_kernel(int N, int D, int KB, bool gate_up, size_t items, const uint8_t* codes,
-                                    const uint8_t* scales, uint8_t* blocks) {
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < items; i += (size_t)gridDim.x * kThreads) {
+__global__ void __launch_bounds__(kThreads) pack_weights_kernel(int N, int D, int KB, bool gate_up, size_t items,
+                                                                const uint8_t* codes, const uint8_t* scales,
+                                                                uint8_t* blocks) {
+  const size_t step = (size_t)gridDim.x * kThreads;
+  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < items; i += step) {
     const BlockItem it = block_item(i, N, KB, gate_up);
     uint8_t b = 0;
     uint4 c = make_uint4(0, 0, 0, 0);
     if (it.k * 32 < D) {
-      c = *reinterpret_cast<const uint4*>(codes + it.row * (D / 2) + it.k * 16);
+      c = __ldg(reinterpret_cast<const uint4*>(codes + it.row * (D / 2) + it.k * 16));
       b = scales[it.row * (D / 32) + it.k];
     }
     uint8_t* blk = blocks + it.blk * kMxBlockBytes;
@@ -119,53 +163,63 @@ __global__ void pack_weights_kernel(int N, int D, int KB, bool gate_up, size_t i
   }
 }
 
+template <typename T>
+cudaError_t quant_rows(int M, int D, const void* x, int64_t stride, const int32_t* row_map, int copies, int rows,
+                       uint8_t* codes, uint32_t* scales, cudaStream_t stream) {
+  const int grid = grid_of((size_t)M * mx_scale_planes(D) * 16), pitch = mx_scale_pitch(rows);
+  const T* p = static_cast<const T*>(x);
+  if (stride * sizeof(T) % 16 == 0)
+    quant_rows_kernel<T, true><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, scales,
+                                                              pitch);
+  else  // rows that do not start on 16 bytes
+    quant_rows_kernel<T, false><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, scales,
+                                                               pitch);
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t dequant_rows(int rows, int D, const uint8_t* codes, const uint32_t* scales, void* out,
+                         cudaStream_t stream) {
+  dequant_rows_kernel<T><<<grid_of((size_t)rows * (D / 8)), kThreads, 0, stream>>>(
+      rows, D, codes, scales, mx_scale_pitch(rows), static_cast<T*>(out));
+  return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t quant_weights(int E, int N, int D, bool gate_up, const void* w, uint8_t* blocks, cudaStream_t stream) {
+  const size_t items = mx_weights_bytes(E, N, D) / kMxBlockBytes * 1024;
+  quant_weights_kernel<T><<<grid_of(items * 4), kThreads, 0, stream>>>(N, D, mx_depth_blocks(D), gate_up, items,
+                                                                       static_cast<const T*>(w), blocks);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_mx_quant(int M, int D, const void* x, int type, int64_t stride, const int32_t* row_map, int copies,
                             int rows, uint8_t* codes, uint32_t* scales, cudaStream_t stream) {
-  const int grid = grid_of((size_t)M * mx_scale_planes(D) * 4), pitch = mx_scale_pitch(rows);
-  uint8_t* sc = reinterpret_cast<uint8_t*>(scales);
-  if (type == MOE_TYPE_F32)
-    quant_rows_kernel<float><<<grid, kThreads, 0, stream>>>(M, D, static_cast<const float*>(x), stride, row_map, copies,
-                                                            rows, codes, sc, pitch);
-  else if (type == MOE_TYPE_F16)
-    quant_rows_kernel<__half><<<grid, kThreads, 0, stream>>>(M, D, static_cast<const __half*>(x), stride, row_map,
-                                                             copies, rows, codes, sc, pitch);
-  else
-    quant_rows_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(M, D, static_cast<const __nv_bfloat16*>(x), stride,
-                                                                    row_map, copies, rows, codes, sc, pitch);
-  return cudaGetLastError();
+  switch (type) {
+    case MOE_TYPE_F32: return quant_rows<float>(M, D, x, stride, row_map, copies, rows, codes, scales, stream);
+    case MOE_TYPE_F16: return quant_rows<__half>(M, D, x, stride, row_map, copies, rows, codes, scales, stream);
+    default: return quant_rows<__nv_bfloat16>(M, D, x, stride, row_map, copies, rows, codes, scales, stream);
+  }
 }
 
 cudaError_t launch_mx_dequant(int rows, int D, const uint8_t* codes, const uint32_t* scales, void* out, int type,
                               cudaStream_t stream) {
-  const int grid = grid_of((size_t)rows * (D / 32)), pitch = mx_scale_pitch(rows);
-  const uint8_t* sc = reinterpret_cast<const uint8_t*>(scales);
-  if (type == MOE_TYPE_F32)
-    dequant_rows_kernel<float><<<grid, kThreads, 0, stream>>>(rows, D, codes, sc, pitch, static_cast<float*>(out));
-  else if (type == MOE_TYPE_F16)
-    dequant_rows_kernel<__half><<<grid, kThreads, 0, stream>>>(rows, D, codes, sc, pitch, static_cast<__half*>(out));
-  else
-    dequant_rows_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(rows, D, codes, sc, pitch,
-                                                                      static_cast<__nv_bfloat16*>(out));
-  return cudaGetLastError();
+  switch (type) {
+    case MOE_TYPE_F32: return dequant_rows<float>(rows, D, codes, scales, out, stream);
+    case MOE_TYPE_F16: return dequant_rows<__half>(rows, D, codes, scales, out, stream);
+    default: return dequant_rows<__nv_bfloat16>(rows, D, codes, scales, out, stream);
+  }
 }
 
 cudaError_t launch_mx_quant_weights(int E, int N, int D, bool gate_up, const void* w, int type, uint8_t* blocks,
                                     cudaStream_t stream) {
-  const int KB = mx_depth_blocks(D);
-  const size_t items = mx_weights_bytes(E, N, D) / kMxBlockBytes * 1024;
-  const int grid = grid_of(items);
-  if (type == MOE_TYPE_F32)
-    quant_weights_kernel<float><<<grid, kThreads, 0, stream>>>(N, D, KB, gate_up, items, static_cast<const float*>(w),
-                                                               blocks);
-  else if (type == MOE_TYPE_F16)
-    quant_weights_kernel<__half><<<grid, kThreads, 0, stream>>>(N, D, KB, gate_up, items,
-                                                                static_cast<const __half*>(w), blocks);
-  else
-    quant_weights_kernel<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(N, D, KB, gate_up, items,
-                                                                       static_cast<const __nv_bfloat16*>(w), blocks);
-  return cudaGetLastError();
+  switch (type) {
+    case MOE_TYPE_F32: return quant_weights<float>(E, N, D, gate_up, w, blocks, stream);
+    case MOE_TYPE_F16: return quant_weights<__half>(E, N, D, gate_up, w, blocks, stream);
+    default: return quant_weights<__nv_bfloat16>(E, N, D, gate_up, w, blocks, stream);
+  }
 }
 
 cudaError_t launch_mx_pack_weights(int E, int N, int D, bool gate_up, const uint8_t* codes, const uint8_t* scales,

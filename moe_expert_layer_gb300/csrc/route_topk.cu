@@ -1,29 +1,26 @@
-// Top-k router (moe_route_topk in include/moe_mxfp4.h): one warp per token.
+// Top-k router (moe_route_topk in include/moe_mxfp4.h): one warp per token, reading its logits
+// once.
 //
-// The row's logits stay in the lanes' registers (element e in lane e % 32), so the row is
-// read once.  The softmax needs the row maximum and the sum of exponentials, two warp
-// reductions; a selection is one warp maximum of (key, lowest expert), packed in 64 bits
-// so that a single integer comparison orders both.
+// Lane l holds the V consecutive experts l * V .. + V - 1 and the largest key among those not
+// yet chosen.  A selection is one warp maximum of the lanes' keys, mapped to unsigned integers
+// in the floats' order (redux.sync), and the lowest lane that has it: equal keys go to the lower
+// expert because lanes and registers are in the experts' order.  Only that lane then looks for
+// its next key.  Where the weights need no sum over the row (sigmoid, or softmax made to sum to
+// one over the chosen, which cancels it) only the chosen logits go through exp, one to a lane.
+// Bound by instructions, ~300 a row: 65521 x 256 fp32 logits, 8 chosen, XXX us (with 64-bit keys
+// through shuffles and every logit's exp 140 us; reading them takes 10).
 #include "mxfp4.cuh"
 
 namespace moe {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr float kLargest = 3.402823466e38f;
 
-// Order-preserving map of a float (no NaN) to unsigned.
+// Order-preserving map of a float (no NaN) to unsigned, above 0 for all but -infinity; -0 as +0.
 __device__ __forceinline__ uint32_t order_bits(float v) {
-  const uint32_t u = __float_as_uint(v + 0.0f);  // -0 -> +0: equal keys tie
-  return (u & 0x80000000u) ? ~u : u | 0x80000000u;
-}
-
-__device__ __forceinline__ uint64_t warp_max_u64(uint64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const uint64_t w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = w > v ? w : v;
-  }
-  return v;
+  const uint32_t u = __float_as_uint(v + 0.0f);
+  return v == -INFINITY ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -31,86 +28,173 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 
-template <typename T, int V>
-__global__ void route_topk_kernel(int M, int E, int topK, const T* logits, int64_t stride, const float* bias, int score,
-                                  bool renormalise, float scale, int32_t* expert_idx, float* probs) {
+struct RouteArgs {
+  int M, E, topK, score;
+  int64_t stride;
+  const float* bias;
+  bool renormalise;
+  float scale;
+  int32_t* expert_idx;
+  float* probs;
+};
+
+// Lane's V logits, masked ones (NaN too) -infinity, +infinity the largest finite value.
+template <typename T, int V, bool VEC>
+__device__ __forceinline__ void load_logits(const T* row, int E, int lane, float (&l)[V]) {
+  if (VEC) {
+    constexpr int kBytes = V * sizeof(T);  // 4, 8 or a multiple of 16 per lane
+    union {
+      T t[V];
+      uint32_t u1;
+      uint2 u2;
+      uint4 u4[kBytes >= 16 ? kBytes / 16 : 1];
+    } r;
+    const bool in = lane * V < E;  // E is a multiple of V
+    if (in) {
+      const T* p = row + lane * V;
+      if (kBytes == 4) {
+        r.u1 = __ldg(reinterpret_cast<const uint32_t*>(p));
+      } else if (kBytes == 8) {
+        r.u2 = __ldg(reinterpret_cast<const uint2*>(p));
+      } else {
+#pragma unroll
+        for (int i = 0; i < kBytes / 16; ++i) r.u4[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = in ? to_f32<T>(r.t[i]) : -INFINITY;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = lane * V + i < E ? to_f32<T>(row[lane * V + i]) : -INFINITY;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) l[i] = l[i] != l[i] ? -INFINITY : fminf(l[i], kLargest);
+}
+
+__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+
+// ALL: every expert's p is needed (a bias on the keys, or softmax weights as they are).
+template <typename T, int V, bool VEC, bool ALL>
+__global__ void __launch_bounds__(32 * kWarps) route_topk_kernel(const T* logits, const RouteArgs a) {
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (t >= M) return;
-  const T* row = logits + (int64_t)t * stride;
-  constexpr float kMax = 3.402823466e38f;
-  float l[V];
-  float top = -INFINITY;
+  if (t >= a.M) return;
+  float l[V];  // logits, or with ALL the p
+  load_logits<T, V, VEC>(logits + (int64_t)t * a.stride, a.E, lane, l);
+  uint32_t key[V];
+  if (ALL) {
+    float top = -INFINITY, sum = 0.0f;
+    if (a.score == MOE_SCORE_SOFTMAX) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    const float v = e < E ? to_f32<T>(row[e]) : -INFINITY;
-    l[i] = v != v ? -INFINITY : fminf(v, kMax);
-    top = fmaxf(top, l[i]);
-  }
-  top = warp_max(top);
-  float p[V];
-  float sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    if (score == MOE_SCORE_SOFTMAX) {
-      p[i] = l[i] == -INFINITY ? 0.0f : expf(l[i] - top);
-      sum += p[i];
-    } else {
-      p[i] = l[i] == -INFINITY ? 0.0f : 1.0f / (1.0f + expf(-l[i]));
+      for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+      top = warp_max(top);
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const bool masked = l[i] == -INFINITY;
+      const float p = masked ? 0.0f : a.score == MOE_SCORE_SOFTMAX ? expf(l[i] - top) : sigmoid(l[i]);
+      sum += p;
+      key[i] = masked ? 0u : order_bits(l[i]);
+      l[i] = p;
+    }
+    if (a.score == MOE_SCORE_SOFTMAX) {
+      sum = warp_sum(sum);
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = sum > 0.0f ? l[i] / sum : 0.0f;
+    }
+    if (a.bias) {
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (key[i]) key[i] = order_bits(l[i] + __ldg(a.bias + lane * V + i));
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = order_bits(l[i]);
   }
-  const float total = score == MOE_SCORE_SOFTMAX ? warp_sum(sum) : 1.0f;
-  uint64_t key[V];  // 0: not to be chosen
+  uint32_t best = 0;
+  int at = 0;
+  auto rescan = [&]() {  // the lane's largest key, the first of equals
+    best = key[0];
+    at = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    if (total > 0.0f) p[i] = p[i] / total;
-    const float k = bias && e < E ? p[i] + bias[e] : l[i];
-    key[i] = l[i] == -INFINITY ? 0ull : ((uint64_t)order_bits(k) << 32) | (uint32_t)(1024 - e);
-  }
-  float chosen = 0.0f;
-  for (int j = 0; j < topK; ++j) {
-    uint64_t best = 0;
-#pragma unroll
-    for (int i = 0; i < V; ++i) best = key[i] > best ? key[i] : best;
-    best = warp_max_u64(best);
-    const int e = best ? 1024 - (int)(uint32_t)best : -1;
-    float pe = 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (best && key[i] == best) {
-        pe = p[i];
-        key[i] = 0;
+    for (int i = 1; i < V; ++i)
+      if (key[i] > best) {
+        best = key[i];
+        at = i;
       }
-    pe = warp_sum(pe);  // one lane has it
-    chosen += pe;
-    if (lane == 0) {
-      expert_idx[(int64_t)t * topK + j] = e;
-      probs[(int64_t)t * topK + j] = pe * scale;
+  };
+  rescan();
+  int64_t out = (int64_t)t * a.topK;
+  float total = 0.0f, top = 0.0f;  // sum of the chosen p; the largest chosen logit
+  // 32 slots at a time: lane s keeps slot s
+  for (int j0 = 0; j0 < a.topK; j0 += 32) {
+    int mine = -1;
+    float val = 0.0f;  // its logit, or p
+    const int n = min(32, a.topK - j0);
+    for (int s = 0; s < n; ++s) {
+      const uint32_t win = __reduce_max_sync(0xffffffffu, best);
+      if (win == 0) break;  // nothing is left
+      const int who = __ffs(__ballot_sync(0xffffffffu, best == win)) - 1;
+      float v = l[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i)
+        if (at == i) v = l[i];
+      const int e = __shfl_sync(0xffffffffu, lane * V + at, who);
+      v = __shfl_sync(0xffffffffu, v, who);
+      if (lane == s) {
+        mine = e;
+        val = v;
+      }
+      if (lane == who) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (at == i) key[i] = 0;
+        rescan();
+      }
+    }
+    float p = val;
+    if (!ALL) {
+      if (j0 == 0) top = __shfl_sync(0xffffffffu, val, 0);
+      p = mine < 0 ? 0.0f : a.score == MOE_SCORE_SOFTMAX ? expf(val - top) : sigmoid(val);
+    }
+    if (a.renormalise) total += warp_sum(p);
+    if (lane < n) {
+      a.expert_idx[out + j0 + lane] = mine;
+      // final unless the sum has more slots to come
+      a.probs[out + j0 + lane] =
+          !a.renormalise || a.topK > 32 ? p * a.scale : total > 0.0f ? p / total * a.scale : 0.0f;
     }
   }
-  if (renormalise) {
+  if (a.renormalise && a.topK > 32) {
     __syncwarp();
-    for (int j = lane; j < topK; j += 32) {
-      float* q = probs + (int64_t)t * topK + j;
-      *q = chosen > 0.0f ? *q / chosen : 0.0f;
+    for (int j = lane; j < a.topK; j += 32) {
+      float* q = a.probs + out + j;
+      *q = total > 0.0f ? *q / total : 0.0f;
     }
   }
 }
 
-template <typename T>
-cudaError_t launch(int M, int E, int topK, const void* logits, int64_t stride, const float* bias, int score,
-                   bool renormalise, float scale, int32_t* expert_idx, float* probs, cudaStream_t stream) {
-  const int blocks = (M + kWarps - 1) / kWarps;
+template <typename T, int V>
+cudaError_t launch(const void* logits, const RouteArgs& a, cudaStream_t stream) {
+  const int blocks = (a.M + kWarps - 1) / kWarps;
   const T* x = static_cast<const T*>(logits);
-  if (E <= 256)
-    route_topk_kernel<T, 8><<<blocks, 32 * kWarps, 0, stream>>>(M, E, topK, x, stride, bias, score, renormalise, scale,
-                                                                expert_idx, probs);
-  else
-    route_topk_kernel<T, 32><<<blocks, 32 * kWarps, 0, stream>>>(M, E, topK, x, stride, bias, score, renormalise, scale,
-                                                                 expert_idx, probs);
+  // a lane's logits as whole vectors: every row aligned to them, and none across the row's end
+  constexpr int kAlign = V * sizeof(T) < 16 ? V * sizeof(T) : 16;
+  const bool vec = kAlign >= 4 && a.stride * sizeof(T) % kAlign == 0 && a.E % V == 0;
+  const bool all = a.bias || (a.score == MOE_SCORE_SOFTMAX && !a.renormalise);
+  if (vec && all) route_topk_kernel<T, V, (kAlign >= 4), true><<<blocks, 32 * kWarps, 0, stream>>>(x, a);
+  else if (vec) route_topk_kernel<T, V, (kAlign >= 4), false><<<blocks, 32 * kWarps, 0, stream>>>(x, a);
+  else if (all) route_topk_kernel<T, V, false, true><<<blocks, 32 * kWarps, 0, stream>>>(x, a);
+  else route_topk_kernel<T, V, false, false><<<blocks, 32 * kWarps, 0, stream>>>(x, a);
   return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_type(const void* logits, const RouteArgs& a, cudaStream_t stream) {
+  if (a.E <= 64) return launch<T, 2>(logits, a, stream);
+  if (a.E <= 128) return launch<T, 4>(logits, a, stream);
+  if (a.E <= 256) return launch<T, 8>(logits, a, stream);
+  return launch<T, 32>(logits, a, stream);
 }
 
 }  // namespace
@@ -118,14 +202,21 @@ cudaError_t launch(int M, int E, int topK, const void* logits, int64_t stride, c
 cudaError_t launch_route_topk(int M, int E, int topK, const void* logits, int type, int64_t stride, const float* bias,
                               int score, bool renormalise, float scale, int32_t* expert_idx, float* probs,
                               cudaStream_t stream) {
+  RouteArgs a;
+  a.M = M;
+  a.E = E;
+  a.topK = topK;
+  a.score = score;
+  a.stride = stride;
+  a.bias = bias;
+  a.renormalise = renormalise;
+  a.scale = scale;
+  a.expert_idx = expert_idx;
+  a.probs = probs;
   switch (type) {
-    case MOE_TYPE_F32:
-      return launch<float>(M, E, topK, logits, stride, bias, score, renormalise, scale, expert_idx, probs, stream);
-    case MOE_TYPE_F16:
-      return launch<__half>(M, E, topK, logits, stride, bias, score, renormalise, scale, expert_idx, probs, stream);
-    default:
-      return launch<__nv_bfloat16>(M, E, topK, logits, stride, bias, score, renormalise, scale, expert_idx, probs,
-                                   stream);
+    case MOE_TYPE_F32: return launch_type<float>(logits, a, stream);
+    case MOE_TYPE_F16: return launch_type<__half>(logits, a, stream);
+    default: return launch_type<__nv_bfloat16>(logits, a, stream);
   }
 }
 
