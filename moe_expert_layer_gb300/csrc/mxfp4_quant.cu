@@ -4,43 +4,68 @@
 // Bound by bytes: eight elements to a lane, so that a warp reads 512 bytes (16-bit types) and
 // writes 128 bytes of codes of one row at a time, and a scaled block of 32 is four neighbouring
 // lanes, whose maximum is two shuffles.  The four scale bytes of 128 elements are put together
-// by shuffles too and written as one word.
+// by shuffles too and written as one word.  A thread takes kItems such pieces at a time, a grid
+// apart, and reads them all first: one read of 16 bytes to a thread keeps too few under way.
 #include "mxfp4.cuh"
 #include "tensor_map.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kItems = 4;
 
 // Blocks for `items` threads' worth of work, at most a few for each the device can hold: the
 // kernels go on in strides.
 inline int grid_of(size_t items) {
-  const size_t b = (items + kThreads - 1) / kThreads, most = (size_t)sm_count() * 32;
+  const size_t b = (items + kThreads - 1) / kThreads, most = (size_t)sm_count() * 8;
   return (int)(b < most ? b : most);
 }
 
-// Eight elements at p (VEC: p aligned to 16 bytes) as fp32.
+// The pieces of a thread: piece `c` of row `t`, `per` to a row, a grid apart, without a division
+// after the first.
+struct Pieces {
+  int t, c, per, dt, dc;
+  __device__ __forceinline__ Pieces(int per_) : per(per_) {
+    const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x, step = (int64_t)gridDim.x * kThreads;
+    t = (int)(first / per);
+    c = (int)(first - (int64_t)t * per);
+    dt = (int)(step / per);
+    dc = (int)(step - (int64_t)dt * per);
+  }
+  __device__ __forceinline__ void next() {
+    t += dt;
+    c += dc;
+    if (c >= per) {
+      c -= per;
+      ++t;
+    }
+  }
+};
+
+// Eight elements at p (VEC: p aligned to 16 bytes).
+template <typename T>
+union Eight {
+  T t[8];
+  uint4 u[sizeof(T) / 2];
+};
 template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, float (&v)[8]) {
+__device__ __forceinline__ void load8(const T* p, Eight<T>& r) {
   if (VEC) {
-    union {
-      T t[8];
-      uint4 u[sizeof(T) / 2];
-    } r;
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(r.t[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(p[i]);
+    for (int i = 0; i < 8; ++i) r.t[i] = p[i];
   }
 }
 
 // The codes of this lane's eight elements and the scale byte of the block of its four lanes
 // (an aligned group of four lanes enters together).
-__device__ __forceinline__ uint32_t quant8(float (&v)[8], uint32_t& b) {
+template <typename T>
+__device__ __forceinline__ uint32_t quant8(const Eight<T>& r, uint32_t& b) {
+  float v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(r.t[i]);
   uint32_t a = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[i]));
@@ -60,26 +85,32 @@ template <typename T, bool VEC>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(int M, int D, const T* x, int64_t stride,
                                                               const int32_t* row_map, int copies, int rows,
                                                               uint8_t* codes, uint32_t* scales, int pitch) {
-  const int per = (D + 127) / 128 * 16;
-  const int64_t n = (int64_t)M * per, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-    const int t = (int)(i / per), c = (int)(i - (int64_t)t * per);  // chunk of eight
-    uint32_t b = 0, w = 0;
-    if (c * 8 < D) {  // D is a multiple of 32: a group of four lanes has the same answer
-      float v[8];
-      load8<T, VEC>(x + (int64_t)t * stride + c * 8, v);
-      w = quant8(v, b);
+  Pieces at((D + 127) / 128 * 16);
+  while (at.t < M) {
+    Eight<T> r[kItems];
+    int t[kItems], c[kItems];  // t: M or more past the end; D is a multiple of 32: groups of four agree
+#pragma unroll
+    for (int k = 0; k < kItems; ++k, at.next()) {
+      t[k] = at.t;
+      c[k] = at.c;
+      if (t[k] < M && c[k] * 8 < D) load8<T, VEC>(x + (int64_t)t[k] * stride + c[k] * 8, r[k]);
     }
-    // bytes of lanes 0, 4, 8, 12 of the 16
-    const uint32_t half = 0xffffu << (threadIdx.x & 16u);
-    uint32_t word = b << (8 * ((c >> 2) & 3));
-    word |= __shfl_xor_sync(half, word, 4);
-    word |= __shfl_xor_sync(half, word, 8);
-    for (int j = 0; j < copies; ++j) {
-      const int d = row_map ? __ldg(row_map + (int64_t)t * copies + j) : t;
-      if (d < 0 || d >= rows) continue;
-      if (c * 8 < D) *reinterpret_cast<uint32_t*>(codes + (size_t)d * (D / 2) + c * 4) = w;
-      if ((c & 15) == 0) scales[(size_t)(c >> 4) * pitch + d] = word;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      if (t[k] >= M) break;  // the pieces after it too; 16 lanes agree
+      uint32_t b = 0, w = 0;
+      if (c[k] * 8 < D) w = quant8<T>(r[k], b);
+      // bytes of lanes 0, 4, 8, 12 of the 16
+      const uint32_t half = 0xffffu << (threadIdx.x & 16u);
+      uint32_t word = b << (8 * ((c[k] >> 2) & 3));
+      word |= __shfl_xor_sync(half, word, 4);
+      word |= __shfl_xor_sync(half, word, 8);
+      for (int j = 0; j < copies; ++j) {
+        const int d = row_map ? __ldg(row_map + (int64_t)t[k] * copies + j) : t[k];
+        if (d < 0 || d >= rows) continue;
+        if (c[k] * 8 < D) *reinterpret_cast<uint32_t*>(codes + (size_t)d * (D / 2) + c[k] * 4) = w;
+        if ((c[k] & 15) == 0) scales[(size_t)(c[k] >> 4) * pitch + d] = word;
+      }
     }
   }
 }
@@ -88,21 +119,31 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(int M, int D, cons
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dequant_rows_kernel(int rows, int D, const uint8_t* codes,
                                                                 const uint32_t* scales, int pitch, T* out) {
-  const int per = D / 8;
-  const int64_t n = (int64_t)rows * per, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-    const int r = (int)(i / per), c = (int)(i - (int64_t)r * per);
-    const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(codes) + i);
-    const uint32_t b = (__ldg(scales + (size_t)(c >> 4) * pitch + r) >> (8 * ((c >> 2) & 3))) & 255u;
-    const float s = mx_scale_value(b);
-    union {
-      T t[8];
-      uint4 u[sizeof(T) / 2];
-    } o;
+  Pieces at(D / 8);
+  while (at.t < rows) {
+    uint32_t w[kItems], sw[kItems];
+    size_t i[kItems];
+    int t[kItems], c[kItems];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) o.t[k] = from_f32<T>(mx_value((w >> (4 * k)) & 15u) * s);
+    for (int k = 0; k < kItems; ++k, at.next()) {
+      t[k] = at.t;
+      c[k] = at.c;
+      i[k] = (size_t)t[k] * (D / 8) + c[k];
+      if (t[k] < rows) {
+        w[k] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i[k]);
+        sw[k] = __ldg(scales + (size_t)(c[k] >> 4) * pitch + t[k]);
+      }
+    }
 #pragma unroll
-    for (int k = 0; k < (int)sizeof(T) / 2; ++k) reinterpret_cast<uint4*>(out)[i * (sizeof(T) / 2) + k] = o.u[k];
+    for (int k = 0; k < kItems; ++k) {
+      if (t[k] >= rows) break;
+      const float s = mx_scale_value((sw[k] >> (8 * ((c[k] >> 2) & 3))) & 255u);
+      Eight<T> o;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) o.t[q] = from_f32<T>(mx_value((w[k] >> (4 * q)) & 15u) * s);
+#pragma unroll
+      for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<uint4*>(out)[i[k] * (sizeof(T) / 2) + q] = o.u[q];
+    }
   }
 }
 
@@ -135,9 +176,9 @@ __global__ void __launch_bounds__(kThreads) quant_weights_kernel(int N, int D, i
     const int part = (int)i & 3;
     uint32_t b = 0, c = 0;
     if (it.k * 32 < D) {
-      float v[8];
-      load8<T, true>(w + it.row * D + it.k * 32 + part * 8, v);
-      c = quant8(v, b);
+      Eight<T> r;
+      load8<T, true>(w + it.row * D + it.k * 32 + part * 8, r);
+      c = quant8<T>(r, b);
     }
     uint8_t* blk = blocks + it.blk * kMxBlockBytes;
     *reinterpret_cast<uint32_t*>(blk + mx_chunk_at(it.r, it.c) + part * 4) = c;

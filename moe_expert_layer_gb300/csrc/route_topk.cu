@@ -1,14 +1,17 @@
 // Top-k router (moe_route_topk in include/moe_mxfp4.h): one warp per token, reading its logits
 // once.
 //
-// Lane l holds the V consecutive experts l * V .. + V - 1 and the largest key among those not
-// yet chosen.  A selection is one warp maximum of the lanes' keys, mapped to unsigned integers
-// in the floats' order (redux.sync), and the lowest lane that has it: equal keys go to the lower
-// expert because lanes and registers are in the experts' order.  Only that lane then looks for
-// its next key.  Where the weights need no sum over the row (sigmoid, or softmax made to sum to
-// one over the chosen, which cancels it) only the chosen logits go through exp, one to a lane.
-// Bound by instructions, ~300 a row: 65521 x 256 fp32 logits, 8 chosen, XXX us (with 64-bit keys
-// through shuffles and every logit's exp 140 us; reading them takes 10).
+// Lane l holds the keys of the V consecutive experts l * V .. + V - 1, mapped to unsigned
+// integers in the floats' order, and the two largest of those not yet chosen.  A selection is
+// one warp maximum (redux.sync) of the lanes' largest and the lowest lane that has it: equal
+// keys go to the lower expert because lanes and registers are in the experts' order.  Only that
+// lane goes on to its second largest, and looks through its keys again when both are spent.
+// Each slot's logit is read back from its key.  Where the weights need no sum over the row
+// (sigmoid, or softmax made to sum to one over the chosen, which cancels it) only the chosen
+// logits go through exp, one to a lane.
+// Bound by instructions: 65521 x 256 fp32 logits, 8 chosen, XXX us, of which reading them would
+// take 10 (with a search through a lane's keys after each of its selections 58 us; with 64-bit
+// keys through shuffles and every logit's exp 140 us).
 #include "mxfp4.cuh"
 
 namespace moe {
@@ -21,6 +24,9 @@ constexpr float kLargest = 3.402823466e38f;
 __device__ __forceinline__ uint32_t order_bits(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
   return v == -INFINITY ? 0u : (u & 0x80000000u) ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float of_order_bits(uint32_t k) {
+  return __uint_as_float((k & 0x80000000u) ? k ^ 0x80000000u : ~k);
 }
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
@@ -79,84 +85,84 @@ __global__ void __launch_bounds__(32 * kWarps) route_topk_kernel(const T* logits
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kWarps + (threadIdx.x >> 5);
   if (t >= a.M) return;
-  float l[V];  // logits, or with ALL the p
-  load_logits<T, V, VEC>(logits + (int64_t)t * a.stride, a.E, lane, l);
+  const T* row = logits + (int64_t)t * a.stride;
+  float l[V];
+  load_logits<T, V, VEC>(row, a.E, lane, l);
   uint32_t key[V];
-  if (ALL) {
-    float top = -INFINITY, sum = 0.0f;
-    if (a.score == MOE_SCORE_SOFTMAX) {
+  float row_top = 0.0f, row_sum = 1.0f;  // of the row's softmax, where it is needed
+  if (ALL && a.score == MOE_SCORE_SOFTMAX) {
+    row_top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
-      top = warp_max(top);
-    }
+    for (int i = 0; i < V; ++i) row_top = fmaxf(row_top, l[i]);
+    row_top = warp_max(row_top);
+    row_sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) row_sum += l[i] == -INFINITY ? 0.0f : expf(l[i] - row_top);
+    row_sum = warp_sum(row_sum);
+  }
+  // a chosen or keyed expert's p, where ALL
+  auto score = [&](float v) { return a.score == MOE_SCORE_SOFTMAX ? expf(v - row_top) / row_sum : sigmoid(v); };
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] = order_bits(l[i]);
+    if (ALL && a.bias && key[i]) key[i] = order_bits(score(l[i]) + __ldg(a.bias + lane * V + i));
+  }
+  // the lane's two largest keys, the first of equals first; 0: none
+  uint32_t best, second, gone = 0;
+  int at, at2;
+  bool two;
+  auto scan = [&]() {
+    best = second = 0;
+    at = at2 = 0;
+    two = true;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const bool masked = l[i] == -INFINITY;
-      const float p = masked ? 0.0f : a.score == MOE_SCORE_SOFTMAX ? expf(l[i] - top) : sigmoid(l[i]);
-      sum += p;
-      key[i] = masked ? 0u : order_bits(l[i]);
-      l[i] = p;
-    }
-    if (a.score == MOE_SCORE_SOFTMAX) {
-      sum = warp_sum(sum);
-#pragma unroll
-      for (int i = 0; i < V; ++i) l[i] = sum > 0.0f ? l[i] / sum : 0.0f;
-    }
-    if (a.bias) {
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (key[i]) key[i] = order_bits(l[i] + __ldg(a.bias + lane * V + i));
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = order_bits(l[i]);
-  }
-  uint32_t best = 0;
-  int at = 0;
-  auto rescan = [&]() {  // the lane's largest key, the first of equals
-    best = key[0];
-    at = 0;
-#pragma unroll
-    for (int i = 1; i < V; ++i)
-      if (key[i] > best) {
-        best = key[i];
+      const uint32_t k = (gone >> i) & 1u ? 0u : key[i];
+      if (k > best) {
+        second = best;
+        at2 = at;
+        best = k;
         at = i;
+      } else if (k > second) {
+        second = k;
+        at2 = i;
       }
+    }
   };
-  rescan();
-  int64_t out = (int64_t)t * a.topK;
+  scan();
+  const int64_t out = (int64_t)t * a.topK;
   float total = 0.0f, top = 0.0f;  // sum of the chosen p; the largest chosen logit
   // 32 slots at a time: lane s keeps slot s
   for (int j0 = 0; j0 < a.topK; j0 += 32) {
     int mine = -1;
-    float val = 0.0f;  // its logit, or p
+    uint32_t mine_key = 0;
     const int n = min(32, a.topK - j0);
     for (int s = 0; s < n; ++s) {
       const uint32_t win = __reduce_max_sync(0xffffffffu, best);
       if (win == 0) break;  // nothing is left
       const int who = __ffs(__ballot_sync(0xffffffffu, best == win)) - 1;
-      float v = l[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i)
-        if (at == i) v = l[i];
       const int e = __shfl_sync(0xffffffffu, lane * V + at, who);
-      v = __shfl_sync(0xffffffffu, v, who);
       if (lane == s) {
         mine = e;
-        val = v;
+        mine_key = win;
       }
+      bool spent = false;
       if (lane == who) {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-          if (at == i) key[i] = 0;
-        rescan();
+        gone |= 1u << at;
+        best = second;
+        at = at2;
+        spent = !two;
+        two = false;
+      }
+      if (__any_sync(0xffffffffu, spent)) {
+        if (spent) scan();
+        __syncwarp();
       }
     }
-    float p = val;
-    if (!ALL) {
-      if (j0 == 0) top = __shfl_sync(0xffffffffu, val, 0);
-      p = mine < 0 ? 0.0f : a.score == MOE_SCORE_SOFTMAX ? expf(val - top) : sigmoid(val);
-    }
+    float val = mine < 0 ? 0.0f : of_order_bits(mine_key), p = 0.0f;
+    if (ALL && a.bias && mine >= 0) val = fminf(to_f32<T>(row[mine]), kLargest);  // the key was not the logit
+    if (!ALL && j0 == 0) top = __shfl_sync(0xffffffffu, val, 0);
+    if (mine >= 0) p = ALL ? score(val) : a.score == MOE_SCORE_SOFTMAX ? expf(val - top) : sigmoid(val);
     if (a.renormalise) total += warp_sum(p);
     if (lane < n) {
       a.expert_idx[out + j0 + lane] = mine;
