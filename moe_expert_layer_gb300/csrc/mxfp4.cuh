@@ -47,12 +47,23 @@ __device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8]) {
   return r;
 }
 
-// One e2m1 code -> fp32.  The magnitude bits (two of exponent, one of mantissa) placed in a
-// binary16's low exponent and top mantissa bits are the value times 2^-14, subnormals
-// included.
-__device__ __forceinline__ float mx_value(uint32_t code) {
-  const float m = __half2float(__ushort_as_half((unsigned short)((code & 7u) << 9))) * 16384.0f;
-  return (code & 8u) ? -m : m;
+// Eight e2m1 codes -> fp32, by the conversion instruction to binary16 (exact).
+__device__ __forceinline__ void mx_values8(uint32_t w, float (&v)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+      "mov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
 }
 
 // x * 2^(127 - b) for a block that may hold non-finite values (b = 255 -> 0).
@@ -71,6 +82,18 @@ template <typename T> __device__ __forceinline__ float to_f32(T v);
 template <> __device__ __forceinline__ float to_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ float to_f32<__half>(__half v) { return __half2float(v); }
 template <> __device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+// Two values, the first in the low half where a type has 16 bits.
+template <typename T> __device__ __forceinline__ void from_f32x2(float a, float b, T* o);
+template <> __device__ __forceinline__ void from_f32x2<float>(float a, float b, float* o) {
+  o[0] = a;
+  o[1] = b;
+}
+template <> __device__ __forceinline__ void from_f32x2<__half>(float a, float b, __half* o) {
+  *reinterpret_cast<__half2*>(o) = f2h2_sat(a, b);
+}
+template <> __device__ __forceinline__ void from_f32x2<__nv_bfloat16>(float a, float b, __nv_bfloat16* o) {
+  *reinterpret_cast<__nv_bfloat162*>(o) = __floats2bfloat162_rn(a, b);
+}
 template <typename T> __device__ __forceinline__ T from_f32(float v);
 template <> __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <> __device__ __forceinline__ __half from_f32<__half>(float v) { return __low2half(f2h2_sat(v, v)); }

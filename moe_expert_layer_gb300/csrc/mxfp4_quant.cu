@@ -3,9 +3,10 @@
 //
 // Bound by bytes: eight elements to a lane, so that a warp reads 512 bytes (16-bit types) and
 // writes 128 bytes of codes of one row at a time, and a scaled block of 32 is four neighbouring
-// lanes, whose maximum is two shuffles.  The four scale bytes of 128 elements are put together
-// by shuffles too and written as one word.  A thread takes kItems such pieces at a time, a grid
+// lanes, whose maximum is two shuffles.  A thread takes kItems such pieces at a time, a grid
 // apart, and reads them all first: one read of 16 bytes to a thread keeps too few under way.
+// Instructions are not far behind: magnitudes of 16-bit types are compared two to an
+// instruction, on their bits.
 #include "mxfp4.cuh"
 #include "tensor_map.h"
 
@@ -59,57 +60,84 @@ __device__ __forceinline__ void load8(const T* p, Eight<T>& r) {
   }
 }
 
-// The codes of this lane's eight elements and the scale byte of the block of its four lanes
-// (an aligned group of four lanes enters together).
-template <typename T>
-__device__ __forceinline__ uint32_t quant8(const Eight<T>& r, uint32_t& b) {
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(r.t[i]);
+// abs_bits of the largest magnitude of eight elements and of the other three lanes' of an
+// aligned group of four.  16-bit types order by their magnitude bits as fp32 does, infinities
+// above finite values and NaN above infinities.
+__device__ __forceinline__ uint32_t group_max(const Eight<float>& r) {
   uint32_t a = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(v[i]));
-  const uint32_t group = 0xfu << (threadIdx.x & 28u);
-  a = max(a, __shfl_xor_sync(group, a, 1));
-  a = max(a, __shfl_xor_sync(group, a, 2));
-  b = mx_scale_byte(a);
+  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(r.t[i]));
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  return max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+}
+__device__ __forceinline__ uint32_t group_max16(const uint4& u) {
+  uint32_t a = __vmaxu2(__vmaxu2(u.x & 0x7fff7fffu, u.y & 0x7fff7fffu), __vmaxu2(u.z & 0x7fff7fffu, u.w & 0x7fff7fffu));
+  a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = __vmaxu2(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  return max(a >> 16, a & 0xffffu);
+}
+__device__ __forceinline__ uint32_t group_max(const Eight<__half>& r) {
+  return abs_bits(__half2float(__ushort_as_half((unsigned short)group_max16(r.u[0]))));
+}
+__device__ __forceinline__ uint32_t group_max(const Eight<__nv_bfloat16>& r) { return group_max16(r.u[0]) << 16; }
+
+// The codes of this lane's eight elements and the scale byte of the block of its four lanes; a
+// whole warp enters.
+template <typename T>
+__device__ __forceinline__ uint32_t quant8(const Eight<T>& r, uint32_t& b) {
+  b = mx_scale_byte(group_max(r));
   const float mult = mx_multiplier(b);
+  float v[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = mx_scaled(v[i], mult, b);
-  return mx_codes8(v);
+  for (int i = 0; i < 8; ++i) v[i] = to_f32<T>(r.t[i]) * mult;
+  const uint32_t w = mx_codes8(v);
+  return b == 255u ? 0u : w;
 }
 
-// One thread per eight elements of a row of x, the row rounded up to 128 elements (16 lanes, so
-// that a word of four scale bytes is made by lanes of one warp; zero bytes past D).
-template <typename T, bool VEC>
+// One thread per eight elements of a row of x, the row rounded up to 128 elements, whose last
+// word of scale bytes is written whole (0 past D).  MAP: rows go where row_map says.
+template <typename T, bool VEC, bool MAP>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(int M, int D, const T* x, int64_t stride,
                                                               const int32_t* row_map, int copies, int rows,
-                                                              uint8_t* codes, uint32_t* scales, int pitch) {
+                                                              uint8_t* codes, uint8_t* scales, int pitch) {
   Pieces at((D + 127) / 128 * 16);
-  while (at.t < M) {
+  while (__any_sync(0xffffffffu, at.t < M)) {
     Eight<T> r[kItems];
-    int t[kItems], c[kItems];  // t: M or more past the end; D is a multiple of 32: groups of four agree
+    int t[kItems], c[kItems];
 #pragma unroll
     for (int k = 0; k < kItems; ++k, at.next()) {
       t[k] = at.t;
       c[k] = at.c;
-      if (t[k] < M && c[k] * 8 < D) load8<T, VEC>(x + (int64_t)t[k] * stride + c[k] * 8, r[k]);
+      if (t[k] < M && c[k] * 8 < D) {
+        load8<T, VEC>(x + (int64_t)t[k] * stride + c[k] * 8, r[k]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) r[k].u[i] = make_uint4(0, 0, 0, 0);
+      }
     }
 #pragma unroll
     for (int k = 0; k < kItems; ++k) {
-      if (t[k] >= M) break;  // the pieces after it too; 16 lanes agree
-      uint32_t b = 0, w = 0;
-      if (c[k] * 8 < D) w = quant8<T>(r[k], b);
-      // bytes of lanes 0, 4, 8, 12 of the 16
-      const uint32_t half = 0xffffu << (threadIdx.x & 16u);
-      uint32_t word = b << (8 * ((c[k] >> 2) & 3));
-      word |= __shfl_xor_sync(half, word, 4);
-      word |= __shfl_xor_sync(half, word, 8);
-      for (int j = 0; j < copies; ++j) {
-        const int d = row_map ? __ldg(row_map + (int64_t)t[k] * copies + j) : t[k];
-        if (d < 0 || d >= rows) continue;
-        if (c[k] * 8 < D) *reinterpret_cast<uint32_t*>(codes + (size_t)d * (D / 2) + c[k] * 4) = w;
-        if ((c[k] & 15) == 0) scales[(size_t)(c[k] >> 4) * pitch + d] = word;
+      uint32_t b;
+      const uint32_t w = quant8<T>(r[k], b);
+      const bool in = c[k] * 8 < D;
+      auto put = [&](int d) {
+        if (in) *reinterpret_cast<uint32_t*>(codes + (size_t)d * (D / 2) + c[k] * 4) = w;
+        if ((c[k] & 3) == 0) scales[((size_t)(c[k] >> 4) * pitch + d) * 4 + ((c[k] >> 2) & 3)] = (uint8_t)b;
+      };
+      if (t[k] < M) {
+        if (MAP) {
+          const int32_t* to = row_map + (int64_t)t[k] * copies;
+          for (int j = 0; j < copies; j += 4) {
+            int d[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) d[q] = j + q < copies ? __ldg(to + j + q) : -1;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              if (d[q] >= 0 && d[q] < rows) put(d[q]);
+          }
+        } else {
+          put(t[k]);
+        }
       }
     }
   }
@@ -138,9 +166,11 @@ __global__ void __launch_bounds__(kThreads) dequant_rows_kernel(int rows, int D,
     for (int k = 0; k < kItems; ++k) {
       if (t[k] >= rows) break;
       const float s = mx_scale_value((sw[k] >> (8 * ((c[k] >> 2) & 3))) & 255u);
+      float v[8];
+      mx_values8(w[k], v);
       Eight<T> o;
 #pragma unroll
-      for (int q = 0; q < 8; ++q) o.t[q] = from_f32<T>(mx_value((w[k] >> (4 * q)) & 15u) * s);
+      for (int q = 0; q < 8; q += 2) from_f32x2<T>(v[q] * s, v[q + 1] * s, o.t + q);
 #pragma unroll
       for (int q = 0; q < (int)sizeof(T) / 2; ++q) reinterpret_cast<uint4*>(out)[i[k] * (sizeof(T) / 2) + q] = o.u[q];
     }
@@ -170,19 +200,32 @@ __device__ __forceinline__ BlockItem block_item(size_t i, int N, int KB, bool ga
 template <typename T>
 __global__ void __launch_bounds__(kThreads) quant_weights_kernel(int N, int D, int KB, bool gate_up, size_t items,
                                                                  const T* w, uint8_t* blocks) {
-  const size_t n = items * 4, step = (size_t)gridDim.x * kThreads;
-  for (size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-    const BlockItem it = block_item(i >> 2, N, KB, gate_up);
-    const int part = (int)i & 3;
-    uint32_t b = 0, c = 0;
-    if (it.k * 32 < D) {
-      Eight<T> r;
-      load8<T, true>(w + it.row * D + it.k * 32 + part * 8, r);
-      c = quant8<T>(r, b);
+  const size_t n = items * 4, step = (size_t)gridDim.x * kThreads;  // n: a multiple of 4096
+  for (size_t i0 = (size_t)blockIdx.x * kThreads + threadIdx.x; i0 < n; i0 += kItems * step) {
+    Eight<T> r[kItems];
+    BlockItem it[kItems];
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const size_t i = i0 + k * step;
+      if (i >= n) break;
+      it[k] = block_item(i >> 2, N, KB, gate_up);
+      if (it[k].k * 32 < D) {
+        load8<T, true>(w + it[k].row * D + it[k].k * 32 + (i & 3) * 8, r[k]);
+      } else {
+#pragma unroll
+        for (int q = 0; q < (int)sizeof(T) / 2; ++q) r[k].u[q] = make_uint4(0, 0, 0, 0);
+      }
     }
-    uint8_t* blk = blocks + it.blk * kMxBlockBytes;
-    *reinterpret_cast<uint32_t*>(blk + mx_chunk_at(it.r, it.c) + part * 4) = c;
-    if (part == 0) blk[mx_scale_at(it.r, it.c)] = (uint8_t)b;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      const size_t i = i0 + k * step;
+      if (i >= n) break;
+      uint32_t b;
+      const uint32_t c = quant8<T>(r[k], b);
+      uint8_t* blk = blocks + it[k].blk * kMxBlockBytes;
+      *reinterpret_cast<uint32_t*>(blk + mx_chunk_at(it[k].r, it[k].c) + (i & 3) * 4) = c;
+      if ((i & 3) == 0) blk[mx_scale_at(it[k].r, it[k].c)] = (uint8_t)b;
+    }
   }
 }
 
@@ -209,12 +252,16 @@ cudaError_t quant_rows(int M, int D, const void* x, int64_t stride, const int32_
                        uint8_t* codes, uint32_t* scales, cudaStream_t stream) {
   const int grid = grid_of((size_t)M * mx_scale_planes(D) * 16), pitch = mx_scale_pitch(rows);
   const T* p = static_cast<const T*>(x);
-  if (stride * sizeof(T) % 16 == 0)
-    quant_rows_kernel<T, true><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, scales,
-                                                              pitch);
-  else  // rows that do not start on 16 bytes
-    quant_rows_kernel<T, false><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, scales,
-                                                               pitch);
+  uint8_t* sc = reinterpret_cast<uint8_t*>(scales);
+  const bool vec = stride * sizeof(T) % 16 == 0;  // else rows that do not start on 16 bytes
+  if (vec && row_map)
+    quant_rows_kernel<T, true, true><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
+  else if (vec)
+    quant_rows_kernel<T, true, false><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
+  else if (row_map)
+    quant_rows_kernel<T, false, true><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
+  else
+    quant_rows_kernel<T, false, false><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
   return cudaGetLastError();
 }
 
