@@ -143,6 +143,66 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(int M, int D, cons
   }
 }
 
+// The dispatch of many rows to several places each: one warp per row, which makes the row's codes
+// and scale words in shared memory and sends them off whole, the codes by one bulk copy per
+// place (from lane j to place j), the words a plane to a lane.  The kernel above computes every
+// address and stores every word once per place: 8192 x 4096 binary16 rows to 6 places each 58 us,
+// here 36 us; but a warp per row takes longer to get through a few long rows (one row of 7168,
+// eight places: 9 us against 5).
+constexpr int kRowWarps = 4;
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(32 * kRowWarps) quant_dispatch_kernel(int M, int D, const T* x, int64_t stride,
+                                                                        const int32_t* row_map, int copies, int rows,
+                                                                        uint8_t* codes, uint32_t* scales, int pitch) {
+  extern __shared__ __align__(128) uint8_t s_rows[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int planes = (D + 127) / 128, row_bytes = D / 2;  // a multiple of 16
+  uint8_t* s_codes = s_rows + (size_t)warp * (row_bytes + planes * 4 + 15 & ~15);
+  uint8_t* s_scales = s_codes + row_bytes;
+  for (int t = blockIdx.x * kRowWarps + warp; t < M; t += gridDim.x * kRowWarps) {
+    const T* row = x + (int64_t)t * stride;
+    bulk_wait_read_all();  // the row before has left
+    __syncwarp();
+    for (int e0 = 0; e0 < planes * 128; e0 += 256 * kItems) {
+      Eight<T> r[kItems];
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int e = e0 + 256 * k + lane * 8;
+        if (e < D) {
+          load8<T, VEC>(row + e, r[k]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < (int)sizeof(T) / 2; ++i) r[k].u[i] = make_uint4(0, 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int e = e0 + 256 * k + lane * 8;
+        uint32_t b;
+        const uint32_t w = quant8<T>(r[k], b);
+        if (e < D) *reinterpret_cast<uint32_t*>(s_codes + e / 2) = w;
+        if ((lane & 3) == 0 && e < planes * 128) s_scales[e / 32] = (uint8_t)b;
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    const int32_t* to = row_map + (int64_t)t * copies;
+    for (int j0 = 0; j0 < copies; j0 += 32) {
+      int d = j0 + lane < copies ? __ldg(to + j0 + lane) : -1;
+      if (d >= rows) d = -1;
+      if (d >= 0) bulk_store(codes + (size_t)d * row_bytes, s_codes, (uint32_t)row_bytes);
+      for (int j = 0; j < min(32, copies - j0); ++j) {
+        const int dj = __shfl_sync(0xffffffffu, d, j);
+        if (dj < 0) continue;
+        for (int q = lane; q < planes; q += 32)
+          scales[(size_t)q * pitch + dj] = reinterpret_cast<const uint32_t*>(s_scales)[q];
+      }
+    }
+    bulk_commit_group();
+  }
+  bulk_wait_all();
+}
+
 // One thread per eight elements.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dequant_rows_kernel(int rows, int D, const uint8_t* codes,
@@ -254,6 +314,16 @@ cudaError_t quant_rows(int M, int D, const void* x, int64_t stride, const int32_
   const T* p = static_cast<const T*>(x);
   uint8_t* sc = reinterpret_cast<uint8_t*>(scales);
   const bool vec = stride * sizeof(T) % 16 == 0;  // else rows that do not start on 16 bytes
+  // a warp per row from about as many rows on as it takes to gain (1024 rows of 7168 to 8 places: 15 us, above 17; 64: 11 and 7)
+  if (row_map && M >= sm_count() * 8) {
+    const size_t smem = (size_t)kRowWarps * ((D / 2 + mx_scale_planes(D) * 4 + 15) & ~15);  // at most 34 KB
+    const int blocks = (M + kRowWarps - 1) / kRowWarps;
+    if (vec)
+      quant_dispatch_kernel<T, true><<<blocks, 32 * kRowWarps, smem, stream>>>(M, D, p, stride, row_map, copies, rows, codes, scales, pitch);
+    else
+      quant_dispatch_kernel<T, false><<<blocks, 32 * kRowWarps, smem, stream>>>(M, D, p, stride, row_map, copies, rows, codes, scales, pitch);
+    return cudaGetLastError();
+  }
   if (vec && row_map)
     quant_rows_kernel<T, true, true><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
   else if (vec)

@@ -170,6 +170,27 @@ def test_quant_dispatches_rows_and_strides():
     assert np.array_equal(host(scales).view(np.uint32), planes)
 
 
+@pytest.mark.parametrize("M,D,copies,kind", [(2500, 96, 2, "f16"), (3000, 1056, 3, "f32"), (2433, 288, 33, "bf16")])
+def test_quant_dispatches_many_rows(M, D, copies, kind):
+    """The warp-per-row form: every copy of a row equals the row quantised by itself, nothing else is written."""
+    rng = np.random.default_rng(M)
+    for extra in (0, 3):  # rows on 16-byte boundaries, and not
+        wide, _ = typed(rng.standard_normal((M, D + extra)), kind)
+        x = wide[:, :D]
+        codes, scales = quant_device(x.contiguous())
+        rows = M * copies + 7
+        place = rng.permutation(rows)[:M * copies].astype(np.int32)
+        place[rng.random(M * copies) < 0.1] = -1
+        place[17] = rows
+        got_c, got_s = quant_device(x, rows, dev(place), copies)
+        want_c = np.full((rows, D // 2), 0x5A, np.uint8)
+        want_s = np.full(tuple(got_s.shape), 0x5A5A5A5A, np.int32)
+        at = np.nonzero((place >= 0) & (place < rows))[0]
+        want_c[place[at]] = host(codes)[at // copies]
+        want_s[:, place[at]] = host(scales)[:, at // copies]
+        assert np.array_equal(host(got_c), want_c) and np.array_equal(host(got_s), want_s)
+
+
 @pytest.mark.parametrize("E,N,D", [(1, 128, 32), (2, 256, 288), (3, 384, 1408), (1, 128, 256)])
 @pytest.mark.parametrize("gate_up", [False, True])
 def test_weight_blocks(E, N, D, gate_up):
