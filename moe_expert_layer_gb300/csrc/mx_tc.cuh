@@ -234,6 +234,22 @@ __device__ __forceinline__ float mx_swiglu(float g, float u) {
   return __fdividef(g, 1.0f + __expf(-g)) * u;
 }
 
+// Eight values of a scaled block that four neighbouring lanes hold -> their code word and the
+// block's scale byte.  A whole warp enters.
+__device__ __forceinline__ uint32_t mx_quant_group8(float (&h)[8], uint32_t& byte) {
+  uint32_t a = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max(a, abs_bits(h[i]));
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 1));
+  a = max(a, __shfl_xor_sync(0xffffffffu, a, 2));
+  byte = mx_scale_byte(a);
+  const float mult = mx_multiplier(byte);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) h[i] *= mult;
+  const uint32_t w = mx_codes8(h);
+  return byte == 255u ? 0u : w;
+}
+
 // Eight values of one channel (lane) and eight rows (index) -> the MXFP4 block of 32
 // channels of each row.  On return lane l holds row l % 8's code word of channels
 // 8 (l / 8) .. + 7, and that row's scale byte.  The block maximum is a warp maximum of the

@@ -20,7 +20,7 @@
 // scales and the rows' words of the two scale planes; warp 2 loads the rows' codes, in tensor
 // copies of 64, 32 and 16 rows; warps 4-7 in turn put a stage's scale words in tensor-memory order;
 // warp 1 issues the copies of the scales and the MMAs; warps 8-23 are four epilogue groups, two
-// for each of the two accumulators, taking its columns in turn, 16 at a time.  Every wait is bounded: one that gives up records
+// for each of the two accumulators, taking its columns in turn.  Every wait is bounded: one that gives up records
 // MOE_ERR_TIMEOUT and the CTA winds down.
 #include "mx_tc.cuh"
 #include "tensor_map.h"
@@ -31,7 +31,7 @@ namespace {
 constexpr int kThreads = 768;
 constexpr int kWeightWarp = 0, kMmaWarp = 1, kTokenWarp = 2, kScaleWarp0 = 4, kEpiWarp0 = 8;
 constexpr int kMaxExperts = 1024;
-constexpr int kEpiGroups = 4, kEpiBytes = 4096;  // an epilogue group's shared memory
+constexpr int kEpiGroups = 4, kEpiBytes = 8192;  // an epilogue group's shared memory
 
 template <int NT, bool PAIR>
 struct Cfg {
@@ -50,11 +50,11 @@ struct Cfg {
   static constexpr int kSfStages = 5;
   static constexpr int kSf0 = 2 * NT;                    // accumulators in columns [0, 2 NT)
   static constexpr int kTmemCols = (kSf0 + kSfStages * kSfCols) <= 128 ? 128 : (kSf0 + kSfStages * kSfCols) <= 256 ? 256 : 512;
-  static constexpr int kSmem = kStages * kStageBytes + kEpiGroups * kEpiBytes + 1024;
+  static constexpr int kSmem = kStages * kStageBytes + kEpiGroups * kEpiBytes;
   static_assert(kSfStages < kStages, "a stage's scale columns are waited for after its slot's last use");
   static_assert(NT % kStep == 0 && kSf0 + kSfStages * kSfCols <= 512, "tensor memory");
   static_assert(kMxBlockBytes % 1024 == 0 && kScales % 128 == 0 && kStageBytes % 1024 == 0, "swizzled rows");
-  static_assert(kSmem + 8704 <= 227 * 1024, "shared memory, with ~8.5 KB static");
+  static_assert(kSmem + 9 * 1024 <= 227 * 1024, "shared memory, with ~8.4 KB static");
 };
 
 struct GmmArgs {
@@ -72,8 +72,9 @@ struct GmmArgs {
 // multiple of 16, are copied as a sum of them), of the scale words, 2 planes x kPlaneWords rows,
 // and of the output.
 constexpr int kBoxes = 3, kBoxRows = 64;
+constexpr int kOutRows = 32;
 struct Maps {
-  CUtensorMap box[kBoxes], scales, c;  // c: the output, 128 channels x 16 rows
+  CUtensorMap box[kBoxes], scales, c;  // c: the output, 128 channels x kOutRows rows
 };
 
 struct Item {
@@ -134,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mx_gmm_kernel(const __grid_constant__ Maps maps, const GmmArgs a) {
   using C = Cfg<NT, PAIR>;
   constexpr int S = C::kStages;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // swizzled rows: 1024-byte groups
   __shared__ __align__(8) uint64_t full_bar[S], empty_bar[S], sf_bar[S], accfull_bar[2], accempty_bar[2], final_bar;
   __shared__ int s_pref[kMaxExperts + 1], s_end[kMaxExperts], s_wsum[kThreads / 32];
   __shared__ uint32_t s_tmem;
@@ -207,8 +208,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   wl.E = E;
   const int total = s_pref[E];
   const uint32_t tmem = s_tmem;
-  const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* ring_g = smem_raw + (ring - smem_u32(smem_raw));
+  const uint32_t ring = smem_u32(smem_raw);
+  uint8_t* ring_g = smem_raw;
   // a stage: weight codes at 0, their scales at 16384, token codes at 17408, their scales behind them
   const int planes = (a.D + 127) / 128;
 
@@ -339,69 +340,76 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int rows = nb < NB ? it.rows : 0;  // a pair's block past the last channel stores nothing
       const int skip = it.skip;
       if (!SWIGLU) {
-        // 16 rows x 128 channels of binary16 gathered in shared memory and stored from there by one
+        // 32 rows x 128 channels of binary16 gathered in shared memory and stored from there by one
         // tensor copy, or, where the tile's first or last rows are not its own, row by row
-        for (int c0 = 16 * (group >> 1); c0 < it.n; c0 += 32) {
-          uint32_t v[16];
+        for (int c0 = kOutRows * (group >> 1); c0 < it.n; c0 += 2 * kOutRows) {
+          uint32_t v[2][16];
           __syncwarp();
-          tmem_ld16(t + c0, v);
+          tmem_ld16(t + c0, v[0]);
+          if (!PAIR && c0 + 16 >= it.n) {  // a single CTA's tile may end after 16 columns
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[1][i] = 0;
+          } else {
+            tmem_ld16(t + c0 + 16, v[1]);
+          }
           if (quarter == 0) bulk_wait_read_all();
           tmem_wait_ld();
           asm volatile("bar.sync %0, 128;" ::"r"(9 + group) : "memory");
           __half* o = reinterpret_cast<__half*>(own) + quarter * 32 + lane;
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const __half2 h = f2h2_sat(__uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+          for (int i = 0; i < 32; i += 2) {
+            const __half2 h = f2h2_sat(__uint_as_float(v[i >> 4][i & 15]), __uint_as_float(v[i >> 4][(i & 15) + 1]));
             o[i * 128] = __low2half(h);
             o[i * 128 + 128] = __high2half(h);
           }
           fence_proxy_async_smem();
           asm volatile("bar.sync %0, 128;" ::"r"(9 + group) : "memory");
           if (quarter == 0) {
-            if (c0 >= skip && c0 + 16 <= rows) {
+            if (c0 >= skip && c0 + kOutRows <= rows) {
               if (lane == 0) tma_store_2d(&maps.c, nb * 128, it.row0 + c0, own);
-            } else if (lane < 16 && c0 + lane >= skip && c0 + lane < rows) {
+            } else if (c0 + lane >= skip && c0 + lane < rows) {
               bulk_store(a.c + (size_t)(it.row0 + c0 + lane) * a.N + nb * 128, own + lane * 256, 256);
             }
             bulk_commit_group();
           }
         }
       } else {
-        // warps in pairs: the even one holds 32 gate channels, the odd one the up channels
-        // that multiply them.  Of 16 rows each finishes 8, with the other's half through
-        // shared memory.
-        const int pair = (warp - kEpiWarp0) >> 1, odd = warp & 1;
-        float* x = reinterpret_cast<float*>(own) + (pair & 1) * 512;
-        float* give = x + odd * 256 + lane;
-        const float* take = x + (odd ^ 1) * 256 + lane;
-        const int k = nb * 2 + (quarter >> 1), I = a.N / 2;  // scaled block of h
-        uint8_t* sc = a.h_scales + ((size_t)(k >> 2) * a.pitch + it.row0) * 4;
-        uint8_t* co = a.h_codes + (size_t)it.row0 * (I / 2) + k * 16 + (lane >> 3) * 4;
+        // Warps in pairs: the even one holds 32 gate channels, the odd one the up channels that
+        // multiply them.  16 rows of both go through shared memory to threads that each take
+        // eight channels of a row: the scaled block's maximum is then two shuffles, and its
+        // scale is found once for eight values (a row at a time across the lanes instead took
+        // twice the instructions, and the epilogue longer than the MMAs).  Odd rows have their
+        // 16-byte pieces swapped in pairs, which keeps reads off each other's banks.
+        const int pair = (warp - kEpiWarp0) >> 1, odd = warp & 1, th = odd * 32 + lane;
+        float* x = reinterpret_cast<float*>(own) + (pair & 1) * 1024;  // [16][64]
+        const int k = nb * 2 + (quarter >> 1), I = a.N / 2;            // scaled block of h
+        const int row = th >> 2, seg = th & 3;
+        const float4* gate = reinterpret_cast<const float4*>(x + row * 64 + ((seg * 8) ^ ((row & 1) << 2)));
+        const float4* gate2 = reinterpret_cast<const float4*>(x + row * 64 + ((seg * 8 + 4) ^ ((row & 1) << 2)));
+        uint8_t* sc = a.h_scales + ((size_t)(k >> 2) * a.pitch + it.row0 + row) * 4;
+        uint8_t* co = a.h_codes + (size_t)(it.row0 + row) * (I / 2) + k * 16 + seg * 4;
         const bool tail = k == I / 32 - 1 && (k & 3) != 3;  // bytes of the word past the last block: 0
         for (int c0 = 16 * (group >> 1); c0 < it.n; c0 += 32) {
           uint32_t v[16];
           __syncwarp();
           tmem_ld16(t + c0, v);
           tmem_wait_ld();
+          asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");  // both have read the rows before
 #pragma unroll
-          for (int i = 0; i < 8; ++i) give[i * 32] = __uint_as_float(odd ? v[i] : v[8 + i]);
+          for (int i = 0; i < 16; ++i) x[i * 64 + (th ^ ((i & 1) << 2))] = __uint_as_float(v[i]);
           asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
-          float h[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float o = take[i * 32];
-            h[i] = odd ? mx_swiglu(o, __uint_as_float(v[8 + i])) : mx_swiglu(__uint_as_float(v[i]), o);
-          }
-          asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");  // both have taken
+          const float4 g0 = gate[0], g1 = gate2[0], u0 = gate[8], u1 = gate2[8];  // up: 32 floats on
+          float h[8] = {mx_swiglu(g0.x, u0.x), mx_swiglu(g0.y, u0.y), mx_swiglu(g0.z, u0.z), mx_swiglu(g0.w, u0.w),
+                        mx_swiglu(g1.x, u1.x), mx_swiglu(g1.y, u1.y), mx_swiglu(g1.z, u1.z), mx_swiglu(g1.w, u1.w)};
           uint32_t byte;
-          const uint32_t w = mx_quant_rows8(h, lane, byte);
-          const int r = c0 + odd * 8 + (lane & 7);
+          const uint32_t w = mx_quant_group8(h, byte);
+          const int r = c0 + row;
           if (r >= skip && r < rows) {
-            *reinterpret_cast<uint32_t*>(co + (size_t)r * (I / 2)) = w;
-            if (lane < 8) {
+            *reinterpret_cast<uint32_t*>(co + (size_t)c0 * (I / 2)) = w;
+            if (seg == 0) {
               if (tail)
-                for (int z = (k & 3) + 1; z < 4; ++z) sc[r * 4 + z] = 0;
-              sc[r * 4 + (k & 3)] = (uint8_t)byte;
+                for (int z = (k & 3) + 1; z < 4; ++z) sc[c0 * 4 + z] = 0;
+              sc[c0 * 4 + (k & 3)] = (uint8_t)byte;
             }
           }
         }
@@ -442,7 +450,7 @@ cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   if (!encode_tensor_map_words(&maps.scales, p.scales, (uint64_t)mx_scale_pitch(p.R), (uint64_t)mx_scale_planes(p.D),
                                C::kPlaneWords, 2))
     return cudaErrorInvalidValue;
-  if (!SWIGLU && !encode_tensor_map_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p.c, (uint64_t)p.N, rows, 128, 16,
+  if (!SWIGLU && !encode_tensor_map_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p.c, (uint64_t)p.N, rows, 128, kOutRows,
                                        CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   static PerContextOnce set;
