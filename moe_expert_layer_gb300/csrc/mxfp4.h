@@ -51,7 +51,12 @@ cudaError_t launch_mx_gmm(const MxGemmProblem& p, cudaStream_t stream);
 
 // The layer for a few tokens in two kernels (mxfp4_few.cu).
 constexpr int kMxFewTokens = 32, kMxFewRoutes = 256;
-inline bool mx_few(int M, int topK) { return M <= kMxFewTokens && M * topK <= kMxFewRoutes; }
+constexpr int kMxFewStages = 1 << 24;  // 256-deep stages of a product: times the SMs, its kernel's 32 bits hold them
+inline bool mx_few(int M, int K, int I, int topK) {
+  return M <= kMxFewTokens && M * topK <= kMxFewRoutes &&
+         (int64_t)M * topK * (I / 64) * ((K + 255) / 256) <= kMxFewStages &&
+         (int64_t)M * topK * (K / 128) * ((I + 255) / 256) <= kMxFewStages;
+}
 bool mx_few_resident();  // whether its second kernel's CTAs, which wait for one another, fit the device at once
 struct MxFewProblem {
   int M, K, I, E, topK;

@@ -47,7 +47,7 @@ Layout layout_of(const moe_dims_t* d) {
     return at;
   };
   L.status = take(gmm_workspace_bytes());
-  const bool few = moe::mx_few(d->M, d->topK);
+  const bool few = moe::mx_few(d->M, d->K, d->I, d->topK);
   if (few) {
     L.part = take(moe::mx_few_part_bytes((int)M, d->topK));
     L.counters = take(moe::mx_few_counter_bytes((int)M, (int)K, (int)I, d->topK));
@@ -77,7 +77,7 @@ int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_
                   const uint8_t* w1, const uint8_t* w2, uint16_t* out, void* ws, const Layout& L, cudaStream_t st) {
   const int M = d->M, K = d->K, I = d->I, E = d->E, topK = d->topK, R = M * topK;
   cudaError_t e;
-  if (moe::mx_few(M, topK) && moe::mx_few_resident()) {
+  if (moe::mx_few(M, K, I, topK) && moe::mx_few_resident()) {
     moe::MxFewProblem p;
     p.M = M;
     p.K = K;

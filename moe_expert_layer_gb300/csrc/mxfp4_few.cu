@@ -18,7 +18,11 @@
 //     CTA: where runs meet in a unit each leaves its sums in the workspace, and the CTA that
 //     finishes last adds them in order.  The others are dealt out whole, in turn, so that the
 //     tiles' h come one after the other and the last of them without a meeting.  The CTA that has
-//     a unit's sums does the SwiGLU and counts the unit on its tile.
+//     a unit's sums does the SwiGLU and counts the unit on its tile.  Between one and two rounds
+//     of units none is cut: each CTA gets one and takes its next by ticket, when it is ready to
+//     load it, because the SMs do not get equal shares of the memory's rate.  (One token, 256
+//     units: 45 us cut, 41.4 by tickets; 8 tokens, 512 units: 66 and 72, the last whole units
+//     standing alone.)
 //   - The down product's stages, in order of (output block, expert tile, stage), are cut into one
 //     run per CTA, whose sums add up in shared memory over experts and stages alike and meet the
 //     same way.  A run that goes over the end of a block takes the block it ends in first: the
@@ -46,8 +50,8 @@ static_assert(kStageBytes % 1024 == 0 && kTokens % 1024 == 0, "swizzled rows");
 static_assert(kSf0 + kSfStages * kSfCols <= kTmemCols && kSfStages < kStages, "tensor memory");
 static_assert(kMxFewRoutes <= 256 && kMxFewRoutes <= kThreads, "a route per thread");
 
-// Shared memory behind the ring: the experts' counts while the tables are made, then the gate
-// and up exchange, then the output sums.
+// Shared memory behind the ring: what the tables are made with, then the gate and up exchange,
+// then the output sums.
 inline int scratch_bytes(int M) { return M * 512 > 4096 ? M * 512 : 4096; }
 inline int smem_bytes(int M) { return kStages * kStageBytes + scratch_bytes(M) + 1024; }
 
@@ -59,7 +63,7 @@ struct FewArgs {
   uint8_t* h_codes;            // [R][I / 2]
   uint8_t* h_scales;           // [R][stages(I)][kScaleRec]
   float* part;                 // [runs][2][rows][128] of h, [runs][2][M][128] of out
-  int32_t* counters;           // [R][I / 64] runs of h blocks, [R] blocks of h, [K / 128] runs of out blocks
+  int32_t* counters;           // [R][I / 64] runs of h blocks, [R] blocks of h, [K / 128] runs of out blocks, tickets
   __half* out;
   int32_t* status;
 };
@@ -68,6 +72,12 @@ struct FewArgs {
 struct FewMaps {
   CUtensorMap x_codes, x_scales, h_codes, h_scales;
 };
+
+// Where in the counters the tickets are given out: behind the others.
+__host__ __device__ inline int counters_of(int M, int K, int I, int topK) {
+  return M * topK * (I / 64 + 1) + K / 128 + 1;
+}
+__device__ __forceinline__ int ticket_at(const FewArgs& a) { return counters_of(a.M, a.K, a.I, a.topK) - 1; }
 
 struct Tables {
   int list[kMxFewRoutes];      // routes by expert,
@@ -89,125 +99,140 @@ struct Seg {
 template <bool DOWN>
 struct Product {
   int NB, KB, tiles, units, head, runs;
-  int64_t cut;  // stages in runs
+  bool tickets;
+  int cut;  // stages in runs; times the runs below 2^32 (kMxFewStages, and 256 SMs at most)
   __device__ __forceinline__ Product(const FewArgs& a, int tiles_) {
     const int G = gridDim.x;
     tiles = tiles_;
     NB = DOWN ? a.K / 128 : a.I / 64;
     KB = ((DOWN ? a.I : a.K) + 255) / 256;
     units = NB * tiles;
-    head = DOWN ? units : units % G;
-    cut = (int64_t)head * KB;
-    runs = (int)min((int64_t)G, cut);  // none empty
+    tickets = !DOWN && units >= G && units < 2 * G;
+    head = DOWN ? units : tickets ? 0 : units % G;
+    cut = head * KB;
+    runs = min(G, cut);  // none empty
   }
-  __device__ __forceinline__ int64_t begin_of(int run) const { return runs ? cut * min(run, runs) / runs : 0; }
+  __device__ __forceinline__ int begin_of(int run) const {
+    return runs ? (int)((unsigned)cut * (unsigned)min(run, runs) / (unsigned)runs) : 0;
+  }
   // The run that holds stage `at`.
-  __device__ __forceinline__ int run_of(int64_t at) const {
-    int c = (int)(at * runs / cut);
+  __device__ __forceinline__ int run_of(int at) const {
+    int c = (int)((unsigned)at * (unsigned)runs / (unsigned)cut);
     while (begin_of(c + 1) <= at) ++c;
     while (begin_of(c) > at) --c;
     return c;
   }
   // Stages of a block whose sums belong together, and the block that holds stage `at`.
   __device__ __forceinline__ int per() const { return DOWN ? tiles * KB : KB; }
-  __device__ __forceinline__ int block_of(int64_t at) const { return (int)(at / per()); }
-  // Stages of this CTA.
-  __device__ __forceinline__ int stages() const {
-    const int b = blockIdx.x, G = gridDim.x;
-    return (int)(begin_of(b + 1) - begin_of(b)) + (units - head > b ? (units - head - b + G - 1) / G * KB : 0);
-  }
+  __device__ __forceinline__ int block_of(int at) const { return at / per(); }
 };
 
-// The segments of a CTA, in order: those of its run, then its whole units; or those of its run
-// behind the last block boundary in it, then those before.
+// The units that a CTA has got by tickets, for its roles: its i-th (i >= 1) stands in
+// unit[(i - 1) % kUnits] once phase (i - 1) / kUnits of its barrier is complete; -1 ends them.  The
+// weight warp publishes them and runs a ring of stages ahead of the others at most.
+constexpr int kUnits = 32;
+static_assert(kUnits > kStages + 4, "no role is that many units behind another");
+struct Pipe;
+__device__ __forceinline__ bool wait_unit(const Pipe& pp, int i, int& unit);
+
+// The segments of a CTA, in order: those of its run, then its whole units, the i-th by turn or by
+// ticket; or for the down product those of its run behind the last block boundary in it, then
+// those before.
 template <bool DOWN>
 struct Walk {
   const Product<DOWN>& p;
-  int64_t at, end, begin, mid;
-  int unit;  // the next whole one
-  __device__ __forceinline__ Walk(const Product<DOWN>& p_) : p(p_) {
+  int at, end, begin, mid, i;
+  __device__ __forceinline__ Walk(const Product<DOWN>& p_) : p(p_), i(0) {
     begin = at = p.begin_of(blockIdx.x);
     mid = end = p.begin_of(blockIdx.x + 1);
-    unit = p.head + blockIdx.x;
     if (DOWN && end > begin) {
-      const int64_t edge = (end - 1) / p.per() * p.per();
+      const int edge = (end - 1) / p.per() * p.per();
       if (edge > begin) at = mid = edge;
     }
   }
-  __device__ __forceinline__ bool next(Seg& s) {
+  // unit_of(i, unit): the i-th unit's ticket; false if the CTA gives up
+  template <typename F>
+  __device__ __forceinline__ bool next(Seg& s, F unit_of) {
     if (at == end) {
       if (DOWN) {
         if (mid == end) return false;
         at = begin;
         end = mid;
       } else {
-        if (unit >= p.units) return false;
-        at = (int64_t)unit * p.KB;
+        int unit = p.head + blockIdx.x + i * gridDim.x;
+        if (p.tickets && i && !unit_of(i, unit)) return false;
+        ++i;
+        if (unit < 0 || unit >= p.units) return false;
+        at = unit * p.KB;
         end = at + p.KB;
-        unit += gridDim.x;
       }
     }
-    const int64_t u = at / p.KB;
-    s.kb0 = (int)(at - u * p.KB);
-    s.tile = (int)(DOWN ? u % p.tiles : u / p.NB);
-    s.nb = (int)(DOWN ? u / p.tiles : u % p.NB);
-    s.kb1 = (int)min((int64_t)p.KB, s.kb0 + (end - at));
+    const int u = at / p.KB;
+    s.kb0 = at - u * p.KB;
+    s.tile = DOWN ? u % p.tiles : u / p.NB;
+    s.nb = DOWN ? u / p.tiles : u % p.NB;
+    s.kb1 = min(p.KB, s.kb0 + (end - at));
     at += s.kb1 - s.kb0;
     return true;
   }
+  __device__ __forceinline__ bool next(Seg& s, const Pipe& pp) {
+    return next(s, [&](int i, int& unit) { return wait_unit(pp, i, unit); });
+  }
 };
 
-// The routes by expert, in order of the routes, and the tiles of up to 16 of them.
-__device__ __forceinline__ void make_tables(const FewArgs& a, Tables& t, int* count, int* wsum) {
+// The routes by expert, in order of the routes, and the tiles of up to 16 of them.  A thread per
+// route finds its place by comparing with all the others; the routes that begin a tile are then
+// numbered in the order of the places, by ballots.  `tmp`: 2 * kMxFewRoutes words.
+__device__ __forceinline__ void make_tables(const FewArgs& a, Tables& t, int* tmp, int* wsum) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  for (int e = tid; e < a.E; e += kThreads) count[e] = 0;
-  __syncthreads();
-  int e = -1, pos = 0;
+  int e = -1;
   if (tid < a.R) {
     e = __ldg(a.expert_idx + tid);
     if (e < 0 || e >= a.E) e = -1;
     t.prob[tid] = __ldg(a.probs + tid);
   }
-  // a warp at a time, so that an expert's routes keep their order
-  for (int w = 0; w * 32 < a.R; ++w) {
-    if (warp == w) {
-      const uint32_t same = __match_any_sync(0xffffffffu, e);
-      if (e >= 0) pos = count[e] + __popc(same & ((1u << lane) - 1u));
-      __syncwarp();
-      if (e >= 0 && (same >> lane) == 1u) count[e] += __popc(same);
-    }
-    __syncthreads();
-  }
-  // first row and first tile of each expert: a scan of rows | tiles << 16
-  const int per = (a.E + kThreads - 1) / kThreads;
-  const int e0 = min(a.E, tid * per), e1 = min(a.E, e0 + per);
-  int sum = 0;
-  for (int i = e0; i < e1; ++i) sum += count[i] | ((count[i] + kRows - 1) / kRows) << 16;
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += n;
-  }
-  if (lane == 31) wsum[warp] = incl;
+  if (tid < kMxFewRoutes) tmp[tid] = e;
   __syncthreads();
-  int run = incl - sum;
-  for (int w = 0; w < warp; ++w) run += wsum[w];
-  for (int i = e0; i < e1; ++i) {
-    const int c = count[i], n = (c + kRows - 1) / kRows, row = run & 0xffff, tile = run >> 16;
-    for (int k = 0; k < n; ++k) {
-      t.tile_e[tile + k] = i;
-      t.tile_row[tile + k] = (row + k * kRows) | min(kRows, c - k * kRows) << 16;
+  int less = 0, before = 0, same = 0;  // routes of lower experts; of this one, before this route, and in all
+  if (e >= 0) {
+    for (int r = 0; r < a.R; r += 4) {
+      const int4 o = reinterpret_cast<const int4*>(tmp)[r >> 2];
+      const int v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        less += v[k] >= 0 && v[k] < e;
+        same += v[k] == e;
+        before += v[k] == e && r + k < tid;
+      }
     }
-    count[i] = row;
-    run += c | n << 16;
   }
-  if (e0 < a.E && e1 == a.E) t.tiles = run >> 16;
+  __syncthreads();
+  const int place = less + before;
+  if (tid < kMxFewRoutes) tmp[kMxFewRoutes + tid] = -1;
   __syncthreads();
   if (e >= 0) {
-    t.list[count[e] + pos] = tid;
-    t.token[count[e] + pos] = tid / a.topK;
+    t.list[place] = tid;
+    t.token[place] = tid / a.topK;
+    if (before % kRows == 0) {  // begins a tile
+      tmp[place] = place | min(kRows, same - before) << 16;
+      tmp[kMxFewRoutes + place] = e;
+    }
   }
+  __syncthreads();
+  const int first = tid < kMxFewRoutes ? tmp[kMxFewRoutes + tid] : -1;
+  const uint32_t begins = __ballot_sync(0xffffffffu, first >= 0);
+  if (lane == 0) wsum[warp] = __popc(begins);
+  __syncthreads();
+  int tile = __popc(begins & ((1u << lane) - 1u)), tiles = 0;
+  for (int w = 0; w < kMxFewRoutes / 32; ++w) {
+    if (w < warp) tile += wsum[w];
+    tiles += wsum[w];
+  }
+  if (first >= 0) {
+    t.tile_e[tile] = first;
+    t.tile_row[tile] = tmp[tid];
+  }
+  if (tid == 0) t.tiles = tiles;
   __syncthreads();
 }
 
@@ -228,7 +253,8 @@ __device__ __forceinline__ bool epi_all(bool ok) {
 // Barriers and shared memory of kernel 2's pipeline, and what its roles keep from product to
 // product.
 struct Pipe {
-  uint64_t *full, *empty, *sf, *accfull, *accempty;
+  uint64_t *full, *empty, *sf, *accfull, *accempty, *unit_bar;
+  int* unit;
   uint32_t ring;
   uint8_t* ring_g;
   uint32_t tmem;
@@ -236,12 +262,29 @@ struct Pipe {
   int32_t* status;
 };
 
+__device__ __forceinline__ bool wait_unit(const Pipe& pp, int i, int& unit) {
+  --i;
+  if (!warp_wait(&pp.unit_bar[i % kUnits], (i / kUnits) & 1, pp.abort_flag, pp.status)) return false;
+  unit = *reinterpret_cast<volatile int*>(pp.unit + i % kUnits);
+  return true;
+}
+
 template <bool DOWN>
 __device__ __forceinline__ bool load_weights(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<DOWN>& p,
-                                             uint32_t elected, RingPos& at) {
+                                             uint32_t elected, int lane, RingPos& at) {
   Walk<DOWN> walk(p);
   Seg s;
-  while (walk.next(s)) {
+  int ticket = 0;  // of the next unit: asked for when a unit is begun, needed when it ends
+  auto publish = [&](int i, int& unit) {
+    unit = gridDim.x + __shfl_sync(0xffffffffu, ticket, 0);
+    if (unit >= p.units) unit = -1;
+    if (lane == 0) {
+      *reinterpret_cast<volatile int*>(pp.unit + (i - 1) % kUnits) = unit;
+      mbar_arrive(&pp.unit_bar[(i - 1) % kUnits]);
+    }
+    return true;
+  };
+  while (walk.next(s, publish)) {
     const uint8_t* wb =
         (DOWN ? a.w2 : a.w1) + ((size_t)t.tile_e[s.tile] * p.NB + s.nb) * (size_t)p.KB * kMxBlockBytes;
     for (int kb = s.kb0; kb < s.kb1; ++kb, at.next(kStages)) {
@@ -249,6 +292,10 @@ __device__ __forceinline__ bool load_weights(const FewArgs& a, const Tables& t, 
       const uint32_t bar = smem_u32(&pp.full[at.slot]);
       expect_tx_elect(elected, bar, kMxBlockBytes);
       bulk_load_elect(elected, pp.ring + at.slot * kStageBytes, wb + (size_t)kb * kMxBlockBytes, kMxBlockBytes, bar);
+      if (p.tickets && kb == s.kb0) {
+        if (walk.i == 1) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1 clears the tickets
+        if (lane == 0) ticket = atomicAdd(a.counters + ticket_at(a), 1);
+      }
     }
   }
   return true;
@@ -261,7 +308,7 @@ __device__ __forceinline__ bool issue_mmas(const FewArgs& a, const Pipe& pp, con
   const int last = ((DOWN ? a.I : a.K) - (p.KB - 1) * 256 + 127) >> 7;  // 128-deep halves of the last stage
   Walk<DOWN> walk(p);
   Seg s;
-  while (walk.next(s)) {
+  while (walk.next(s, pp)) {
     const int buf = u & 1;
     if (!warp_wait(&pp.accempty[buf], ((u >> 1) & 1) ^ 1, pp.abort_flag, pp.status)) return false;
     tc_fence_after();
@@ -286,6 +333,13 @@ __device__ __forceinline__ bool issue_mmas(const FewArgs& a, const Pipe& pp, con
   return true;
 }
 
+// Bounded wait until *count >= target, polled closely: a CTA has nothing else to do.
+__device__ __forceinline__ bool ready_wait(const int32_t* count, int target) {
+  for (int i = 0; i < 4096; ++i)
+    if (ld_acquire(count) >= target) return true;
+  return count_wait_bounded(count, target);
+}
+
 // A stage's token rows: of x by token, or of h by route once all blocks of the tile's h are there.
 template <bool DOWN>
 __device__ __forceinline__ bool load_tokens(const FewArgs& a, const FewMaps& maps, const Tables& t, const Pipe& pp,
@@ -295,9 +349,9 @@ __device__ __forceinline__ bool load_tokens(const FewArgs& a, const FewMaps& map
   int seen = -1;  // the last tile whose h was waited for
   Walk<DOWN> walk(p);
   Seg s;
-  while (walk.next(s)) {
+  while (walk.next(s, pp)) {
     if (DOWN && s.tile != seen) {
-      const bool ok = *pp.abort_flag == 0 && (lane != 0 || count_wait_bounded(ready + s.tile, a.I / 64));
+      const bool ok = *pp.abort_flag == 0 && (lane != 0 || ready_wait(ready + s.tile, a.I / 64));
       if (!__all_sync(0xffffffffu, ok)) {
         if (*pp.abort_flag == 0 && lane == 0) record_status(pp.status, MOE_ERR_TIMEOUT);
         *pp.abort_flag = 1;
@@ -328,47 +382,62 @@ __device__ __forceinline__ bool load_tokens(const FewArgs& a, const FewMaps& map
   return true;
 }
 
-// Puts the scales of this warp's stages, every kScaleWarps-th of the CTA's, in order.
-__device__ __forceinline__ void arrange_scales(const Pipe& pp, int who, int lane, int stages) {
-  for (int n = who; n < stages; n += kScaleWarps) {
-    // The stage that used the scale columns is done, and with it the slot's previous use: only
-    // then is `full` known to be in this use's phase (copies complete in any order).
-    const int old = n - kSfStages, slot = n % kStages;
-    if (old >= 0 && !warp_wait(&pp.empty[old % kStages], (old / kStages) & 1, pp.abort_flag, pp.status)) return;
-    if (!warp_wait(&pp.full[slot], (n / kStages) & 1, pp.abort_flag, pp.status)) return;
-    uint8_t* st = pp.ring_g + slot * kStageBytes;
-    const uint4 w0 = mx_scale_words(st + kMxCodeBytes, lane), w1 = mx_scale_words(st + kMxCodeBytes + 512, lane);
-    uint2 x = make_uint2(0, 0);
-    if (lane < kRows) x = *reinterpret_cast<const uint2*>(st + kTokenScales + (lane >> 2) * 128 + (lane & 3) * kScaleRec);
-    __syncwarp();
-    mx_put_scale_words(st + kMxCodeBytes, w0, lane);
-    mx_put_scale_words(st + kMxCodeBytes + 512, w1, lane);
-    if (lane < kRows) {
-      *reinterpret_cast<uint32_t*>(st + kTokenScales + lane * 16) = x.x;
-      *reinterpret_cast<uint32_t*>(st + kTokenScales + 512 + lane * 16) = x.y;
+// Puts the scales of this warp's stages, every kScaleWarps-th of the CTA's, in order.  n: the
+// CTA's stages before this product's, and then with them.
+template <bool DOWN>
+__device__ __forceinline__ bool arrange_scales(const Pipe& pp, const Product<DOWN>& p, int who, int lane, int& n) {
+  Walk<DOWN> walk(p);
+  Seg s;
+  while (walk.next(s, pp)) {
+    for (int kb = s.kb0; kb < s.kb1; ++kb, ++n) {
+      if (n % kScaleWarps != who) continue;
+      // The stage that used the scale columns is done, and with it the slot's previous use: only
+      // then is `full` known to be in this use's phase (copies complete in any order).
+      const int old = n - kSfStages, slot = n % kStages;
+      if (old >= 0 && !warp_wait(&pp.empty[old % kStages], (old / kStages) & 1, pp.abort_flag, pp.status)) return false;
+      if (!warp_wait(&pp.full[slot], (n / kStages) & 1, pp.abort_flag, pp.status)) return false;
+      uint8_t* st = pp.ring_g + slot * kStageBytes;
+      const uint4 w0 = mx_scale_words(st + kMxCodeBytes, lane), w1 = mx_scale_words(st + kMxCodeBytes + 512, lane);
+      uint2 x = make_uint2(0, 0);
+      if (lane < kRows)
+        x = *reinterpret_cast<const uint2*>(st + kTokenScales + (lane >> 2) * 128 + (lane & 3) * kScaleRec);
+      __syncwarp();
+      mx_put_scale_words(st + kMxCodeBytes, w0, lane);
+      mx_put_scale_words(st + kMxCodeBytes + 512, w1, lane);
+      if (lane < kRows) {
+        *reinterpret_cast<uint32_t*>(st + kTokenScales + lane * 16) = x.x;
+        *reinterpret_cast<uint32_t*>(st + kTokenScales + 512 + lane * 16) = x.y;
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&pp.sf[slot]);
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&pp.sf[slot]);
   }
+  return true;
 }
 
 // Words of the workspace that hold sums of h, two units to a run, before those of out.
 __host__ __device__ inline size_t part_words_of_h(int G, int R) { return (size_t)G * 2 * (R < kRows ? R : kRows) * 128; }
 
+// Adds one to a count of the device.
+__device__ __forceinline__ int add_acq_rel(int32_t* count) {
+  int before;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(count) : "memory");
+  return before;
+}
+__device__ __forceinline__ void add_release(int32_t* count) {
+  asm volatile("red.add.release.gpu.global.s32 [%0], 1;" ::"l"(count) : "memory");
+}
+
 // The epilogue warps' barrier.
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
 // The CTA's sums of a block are in global memory: counts its run, and returns whether all `runs`
-// of the block's are there.  The barriers carry the other threads' writes and reads with the
-// first thread's fences.
+// of the block's are there.  The first thread's addition releases and acquires; the barriers carry
+// the other threads' writes and reads with it.
 __device__ __forceinline__ bool last_run(int32_t* counter, int runs, bool first_thread, int* s_last) {
   epi_sync();
-  if (first_thread) {
-    __threadfence();
-    *s_last = atomicAdd(counter, 1) == runs - 1;
-    __threadfence();
-  }
+  if (first_thread) *s_last = add_acq_rel(counter) == runs - 1;
   epi_sync();
   return *s_last != 0;
 }
@@ -397,13 +466,13 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
   const size_t part_rows = min(kRows, a.R);
   Walk<false> walk(p);
   Seg s;
-  while (walk.next(s)) {
+  while (walk.next(s, pp)) {
     const int row0 = t.tile_row[s.tile] & 0xffff, rows = t.tile_row[s.tile] >> 16;
     const int block = s.tile * p.NB + s.nb, run = blockIdx.x;
     int c0 = run, c1 = run;
     if (s.kb1 - s.kb0 < p.KB) {
-      c0 = p.run_of((int64_t)block * p.KB);
-      c1 = p.run_of((int64_t)block * p.KB + p.KB - 1);
+      c0 = p.run_of(block * p.KB);
+      c1 = p.run_of(block * p.KB + p.KB - 1);
     }
     auto part_of = [&](int c) {
       return a.part + ((size_t)c * 2 + (block != p.block_of(p.begin_of(c)))) * part_rows * 128 + ch;
@@ -411,19 +480,26 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
     // The unit's last run, if the others have been counted already, reads their sums while its
     // own MMAs are under way and writes nothing.
     float sum[16] = {};
-    auto add = [&](int c) {
-      float o[16];
-      const float* q = part_of(c);
+    auto add = [&](int from, int to) {  // in order; two runs' read at a time
+      for (int c = from; c <= to; c += 2) {
+        float o[2][16];
 #pragma unroll
-      for (int i = 0; i < 16; ++i) o[i] = i < rows ? __ldcg(q + i * 128) : 0.0f;
+        for (int k = 0; k < 2; ++k) {
+          const float* q = part_of(min(c + k, to));
 #pragma unroll
-      for (int i = 0; i < 16; ++i) sum[i] += o[i];
+          for (int i = 0; i < 16; ++i) o[k][i] = i < rows ? __ldcg(q + i * 128) : 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          sum[i] += o[0][i];
+          if (c < to) sum[i] += o[1][i];
+        }
+      }
     };
     bool there = false;
     if (c1 > c0 && run == c1) {
       there = epi_all(ld_acquire(a.counters + block) == c1 - c0);
-      if (there)
-        for (int c = c0; c < c1; ++c) add(c);
+      if (there) add(c0, c1 - 1);
     }
     uint32_t v[16];
     if (!take_sums(pp, u, quarter, lane, v)) return false;
@@ -437,7 +513,7 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
       for (int i = 0; i < 16; ++i)
         if (i < rows) __stcg(mine + i * 128, __uint_as_float(v[i]));
       if (!last_run(a.counters + block, c1 - c0 + 1, quarter == 0 && lane == 0, s_last)) continue;
-      for (int c = c0; c <= c1; ++c) add(c);
+      add(c0, c1);
 #pragma unroll
       for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(sum[i]);
     }
@@ -467,10 +543,7 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
     }
     fence_proxy_async_global();
     epi_sync();  // h is written, and the exchange free
-    if (quarter == 0 && lane == 0) {
-      __threadfence();
-      atomicAdd(ready + s.tile, 1);
-    }
+    if (quarter == 0 && lane == 0) add_release(ready + s.tile);
   }
   return true;
 }
@@ -486,7 +559,7 @@ __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, co
   if (p.tiles == 0)  // no route at all
     for (int nb = blockIdx.x; nb < p.NB; nb += gridDim.x)
       for (int i = 0; i < a.M; ++i) a.out[(size_t)i * a.K + nb * 128 + ch] = __float2half(0.0f);
-  while (walk.next(s)) {
+  while (walk.next(s, pp)) {
     uint32_t v[16];
     if (!take_sums(pp, u, quarter, lane, v)) return false;
     ++u;
@@ -500,7 +573,7 @@ __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, co
       }
     if (walk.at < walk.end && (s.tile < p.tiles - 1 || s.kb1 < p.KB)) continue;
     // the run's share of this output block is complete
-    const int64_t b0 = (int64_t)s.nb * p.per(), b1 = b0 + p.per();
+    const int b0 = s.nb * p.per(), b1 = b0 + p.per();
     __half* out = a.out + s.nb * 128;
     const int c0 = p.run_of(b0), c1 = p.run_of(b1 - 1);
     if (c0 == c1) {
@@ -548,7 +621,8 @@ __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, co
 __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_constant__ FewMaps maps, const FewArgs a) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full_bar[kStages], empty_bar[kStages], sf_bar[kStages], accfull_bar[2],
-      accempty_bar[2], final_bar;
+      accempty_bar[2], unit_bar[kUnits], final_bar;
+  __shared__ int s_unit[kUnits];
   __shared__ Tables s_t;
   __shared__ int s_wsum[kThreads / 32];
   __shared__ uint32_t s_tmem;
@@ -560,6 +634,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_consta
   pp.sf = sf_bar;
   pp.accfull = accfull_bar;
   pp.accempty = accempty_bar;
+  pp.unit_bar = unit_bar;
+  pp.unit = s_unit;
   pp.ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
   pp.ring_g = smem_raw + (pp.ring - smem_u32(smem_raw));
   pp.abort_flag = &s_abort;
@@ -581,6 +657,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_consta
         mbar_init(&accfull_bar[s], 1);
         mbar_init(&accempty_bar[s], 4);
       }
+      for (int s = 0; s < kUnits; ++s) mbar_init(&unit_bar[s], 1);
       mbar_init(&final_bar, 1);
       fence_barrier_init();
     }
@@ -596,7 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_consta
   if (warp == kWeightWarp) {
     const uint32_t elected = elect_one();
     RingPos at;
-    if (load_weights<false>(a, s_t, pp, up, elected, at)) load_weights<true>(a, s_t, pp, down, elected, at);
+    if (load_weights<false>(a, s_t, pp, up, elected, lane, at)) load_weights<true>(a, s_t, pp, down, elected, lane, at);
   } else if (warp == kMmaWarp) {
     const uint32_t elected = elect_one();
     RingPos at, sf;
@@ -613,7 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_consta
     if (load_tokens<false>(a, maps, s_t, pp, up, elected, lane, at))
       load_tokens<true>(a, maps, s_t, pp, down, elected, lane, at);
   } else if (warp >= kScaleWarp0 && warp < kScaleWarp0 + kScaleWarps) {
-    arrange_scales(pp, warp - kScaleWarp0, lane, up.stages() + down.stages());
+    int n = 0;
+    if (arrange_scales<false>(pp, up, warp - kScaleWarp0, lane, n)) arrange_scales<true>(pp, down, warp - kScaleWarp0, lane, n);
   } else if (warp >= kEpiWarp0) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     int u = 0;
@@ -674,8 +752,6 @@ __global__ void __launch_bounds__(kXThreads) mx_few_x_kernel(const __half* x, in
   }
 }
 
-int counters_of(int M, int K, int I, int topK) { return M * topK * (I / 64 + 1) + K / 128; }
-
 }  // namespace
 
 size_t mx_few_part_bytes(int M, int topK) {
@@ -692,11 +768,16 @@ bool mx_few_resident() {
   const int dev = current_device();
   if (queried.needed(dev)) {
     int n = 0;
+    // kernel 1 with the same division of L1 as kernel 2, which can then begin beside it
     ok[dev] = cudaFuncSetAttribute(mx_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    smem_bytes(kMxFewTokens)) == cudaSuccess &&
+              cudaFuncSetAttribute(mx_few_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                   cudaSharedmemCarveoutMaxShared) == cudaSuccess &&
+              cudaFuncSetAttribute(mx_few_x_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                   cudaSharedmemCarveoutMaxShared) == cudaSuccess &&
               cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, mx_few_kernel, kThreads, smem_bytes(kMxFewTokens)) ==
                   cudaSuccess &&
-              n >= 1;
+              n >= 1 && sm_count() <= 256;
     if (!ok[dev]) cudaGetLastError();
     queried.done(dev);
   }
@@ -704,13 +785,6 @@ bool mx_few_resident() {
 }
 
 cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
-  const int n_counters = counters_of(p.M, p.K, p.I, p.topK);
-  const int x_blocks = (int)(((size_t)p.M * p.K / 8 + kXThreads - 1) / kXThreads);
-  mx_few_x_kernel<<<x_blocks, kXThreads, 0, stream>>>(reinterpret_cast<const __half*>(p.x), p.M, p.K, p.x_codes,
-                                                      p.x_scales, p.counters, n_counters,
-                                                      p.status);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
   const int R = p.M * p.topK;
   const uint64_t xs = (uint64_t)mx_depth_blocks(p.K) * kScaleRec, hs = (uint64_t)mx_depth_blocks(p.I) * kScaleRec;
   FewMaps maps;
@@ -719,6 +793,12 @@ cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
       !encode_tensor_map_rows(&maps.x_scales, p.x_scales, xs, xs, p.M, kScaleRec, CU_TENSOR_MAP_SWIZZLE_NONE) ||
       !encode_tensor_map_rows(&maps.h_scales, p.h_scales, hs, hs, R, kScaleRec, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
+  const int n_counters = counters_of(p.M, p.K, p.I, p.topK);
+  const int x_blocks = (int)(((size_t)p.M * p.K / 8 + kXThreads - 1) / kXThreads);
+  mx_few_x_kernel<<<x_blocks, kXThreads, 0, stream>>>(reinterpret_cast<const __half*>(p.x), p.M, p.K, p.x_codes,
+                                                      p.x_scales, p.counters, n_counters, p.status);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   FewArgs a;
   a.M = p.M;
   a.K = p.K;
