@@ -177,18 +177,15 @@ __device__ __forceinline__ void tmem_dealloc(uint32_t tmem) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kCols) : "memory");
 }
 
-// The words of 128 rows at `tile`, read by all lanes (rows 4 l .. 4 l + 3 to lane l), and
-// written back as row r's word at byte (r % 32) * 16 + (r / 32) * 4.  Between the two the
-// warp synchronises.
+// The words of 128 rows at `tile`, read by all lanes (rows l, l + 32, l + 64, l + 96 to lane l),
+// and written back as row r's word at byte (r % 32) * 16 + (r / 32) * 4: no bank conflicts either
+// way.  Between the two the warp synchronises.
 __device__ __forceinline__ uint4 mx_scale_words(const uint8_t* tile, int lane) {
-  return reinterpret_cast<const uint4*>(tile)[lane];
+  const uint32_t* p = reinterpret_cast<const uint32_t*>(tile) + lane;
+  return make_uint4(p[0], p[32], p[64], p[96]);
 }
 __device__ __forceinline__ void mx_put_scale_words(uint8_t* tile, uint4 w, int lane) {
-  uint32_t* p = reinterpret_cast<uint32_t*>(tile) + (lane & 7) * 16 + (lane >> 3);
-  p[0] = w.x;
-  p[4] = w.y;
-  p[8] = w.z;
-  p[12] = w.w;
+  reinterpret_cast<uint4*>(tile)[lane] = w;
 }
 
 // 512 bytes of arranged scale words -> four tensor-memory columns, in each of the four lane
