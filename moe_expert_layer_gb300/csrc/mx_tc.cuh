@@ -225,6 +225,19 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, volati
   return __all_sync(0xffffffffu, wait_or_abort(bar, parity, abort_flag, status));
 }
 
+// Whether a barrier's phase is complete, without waiting.
+__device__ __forceinline__ uint32_t mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok;
+}
+
 // silu(g) * u in fp32; the fast exponential and division are a few units off in the last
 // place, far inside the 4-bit rounding that follows.
 __device__ __forceinline__ float mx_swiglu(float g, float u) {

@@ -97,7 +97,13 @@ __device__ __forceinline__ int tiles_of(int start, int end) {
 
 template <int NT, int STEP>
 __device__ __forceinline__ Item decode_item(int j, const WorkList& wl, int& e_hint) {
-  int lo = e_hint, hi = wl.E;  // pref[lo] <= j < pref[hi]
+  // pref[lo] <= j < pref[hi]: mostly the same expert as the item before, or one of the next
+  int lo = e_hint, hi = lo + 1, step = 1;
+  while (hi < wl.E && wl.pref[hi] <= j) {
+    lo = hi;
+    hi = min(hi + step, wl.E);
+    step *= 2;
+  }
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
     if (wl.pref[mid] <= j) lo = mid; else hi = mid;
@@ -253,6 +259,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       RingPos at, sf;
       int e_hint = 0, u = 0;
       bool ok = true;
+      // a barrier's answer takes as long as issuing several MMAs: the next stage's is asked for
+      // before this one's are issued
+      uint32_t there = mbar_test(&sf_bar[0], 0);
       for (int j = first; ok && j < total; j += stride, ++u) {
         const Item it = decode_item<NT, C::kStep>(j, wl, e_hint);
         const int buf = u & 1;
@@ -260,12 +269,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t idesc = mx_idesc(PAIR ? 256 : 128, it.n), d = t0 + buf * NT;
         const int last = (a.D - (KB - 1) * 256 + 127) >> 7;  // 128-deep halves of the last stage
-        for (int kb = 0; kb < KB; ++kb, at.next(S), sf.next(C::kSfStages)) {
+        for (int kb = 0; kb < KB; ++kb, sf.next(C::kSfStages)) {
           // the scale warps arrive after they have seen the stage's copies complete
-          if (!(ok = warp_wait(&sf_bar[at.slot], at.phase, abort_flag, a.status))) break;
+          if (!__all_sync(0xffffffffu, there) &&
+              !(ok = warp_wait(&sf_bar[at.slot], at.phase, abort_flag, a.status)))
+            break;
           tc_fence_after();
           const uint32_t st = ring + at.slot * C::kStageBytes, t_sf = t0 + C::kSf0 + sf.slot * C::kSfCols;
           const uint64_t da = sw128_desc(st), db = sw128_desc(st + kMxBlockBytes);
+          const uint32_t done = smem_u32(&empty_bar[at.slot]);
+          at.next(S);
+          there = mbar_test(&sf_bar[at.slot], at.phase);
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             mx_copy_scales<PAIR>(elected, t_sf + 4 * q, st + kMxCodeBytes + 512 * q);
@@ -277,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mx_mma2<PAIR>(elected, d, da, db, 0, idesc, t_sf, t_sf + 8, kb ? 1u : 0u);
           if (kb < KB - 1 || last == 2)
             mx_mma2<PAIR>(elected, d, da, db, 1, idesc, t_sf + 4, t_sf + 8 + C::kSfbPlane, 1u);
-          mx_commit<PAIR>(elected, smem_u32(&empty_bar[at.slot]));
+          mx_commit<PAIR>(elected, done);
         }
         if (ok) mx_commit<PAIR>(elected, smem_u32(&accfull_bar[buf]));
       }
