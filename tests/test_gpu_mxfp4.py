@@ -410,3 +410,47 @@ def test_route_then_layer():
     ref, err = mx.layer(mx.values(*mx.quantise(x.astype(np.float64))), host(ei), host(pr), v1, v2)
     got = host(out).astype(np.float64)
     assert (np.abs(got - ref) <= err).all() and (got[4] == 0).all()
+
+
+@pytest.mark.parametrize("tiles,I", [(5, 1024), (19, 512), (12, 1024), (19, 1024), (24, 1024), (17, 1216)])
+def test_few_tokens_share_of_the_device(tiles, I):
+    """A few tokens' gate and up product in fewer units (64 channels of h x experts) than SMs, as many,
+    between one and two of them each, twice as many, more: every way the kernel deals them out."""
+    K, topK = 256, 1
+    x, _, probs, w1, v1, w2, v2 = layer_case(tiles, K, I, tiles, topK, tiles + I)
+    x = (x * np.float16(2.0 ** -6)).astype(np.float16)
+    ei = np.random.default_rng(tiles).permutation(tiles).astype(np.int32)[:, None]
+    args = (dev(x), dev(ei), dev(probs), w1, w2, I, tiles)
+    out, ws = run_layer(*args)
+    assert moe.moe_workspace_status(ws) == 0
+    ref, err = mx.layer(mx.values(*mx.quantise(x.astype(np.float64))), ei, probs, v1, v2)
+    over = np.abs(ref) + err > 65504
+    assert (np.abs(host(out).astype(np.float64) - ref) <= err)[~over].all()
+
+
+@pytest.mark.parametrize("M,K,I,E,topK", [(1, 2048, 1408, 16, 8), (9, 512, 1024, 16, 2), (30, 1024, 256, 4, 4),
+                                          (200, 1024, 512, 2, 2)])
+def test_layer_repeats_bit_for_bit(M, K, I, E, topK):
+    """Whichever CTA finishes first, sums that meet are added in the same order."""
+    x, ei, probs, w1, _, w2, _ = layer_case(M, K, I, E, topK, M + I)
+    args = (dev(x), dev(ei), dev(probs), w1, w2, I, E)
+    out, ws = run_layer(*args)
+    differ = torch.zeros((), dtype=torch.int64, device="cuda")
+    for _ in range(300):
+        again, _ = run_layer(*args, ws=ws)
+        differ += (again.view(torch.int16) != out.view(torch.int16)).sum()
+    assert differ.item() == 0 and moe.moe_workspace_status(ws) == 0
+
+
+def test_example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "mxfp4_experts.py")
+    spec = importlib.util.spec_from_file_location("mxfp4_experts", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    # Each of the three products' factors is off by four bits' 2^-2 / sqrt(3) of its size at most, a
+    # uniform error of half a step: x, W1, h, W2 independent, sqrt(4) * 0.145, and more through SwiGLU.
+    for tokens in (1, 40):
+        _, distance = example.run(tokens=tokens, hidden=512, intermediate=256, experts=8, topk=2, steps=2)
+        assert 0.01 < distance < 0.5
