@@ -152,28 +152,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
   volatile int* abort_flag = &s_abort;
 
-  // ---- work list, barriers, tensor memory
+  // ---- work list, barriers, tensor memory.  Launched as a programmatic dependent, which hides the
+  // setup (a layer of 128 tokens x 4096, 1408 channels, 64 experts, 6 each: 127 us without, 119
+  // with): what the kernels before this one wrote is read behind the wait only.
   {
-    const int per = (E + kThreads - 1) / kThreads;
-    const int e0 = min(E, (int)threadIdx.x * per), e1 = min(E, e0 + per);
-    int local = 0;
-    for (int e = e0; e < e1; ++e) {
-      const int hi = min(max(__ldg(a.cumsum + e), 0), a.R);
-      const int lo = e ? min(max(__ldg(a.cumsum + e - 1), 0), a.R) : 0;
-      s_end[e] = hi;
-      local += tiles_of<NT>(lo, hi) * CB;
-    }
-    int incl = local;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int n = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += n;
-    }
-    if (lane == 31) s_wsum[warp] = incl;
-    if (threadIdx.x == 0) {
-      s_abort = 0;
-      s_issued[0] = s_issued[1] = 0;
-    }
     if (warp == kMmaWarp) {
       tmem_alloc<PAIR, C::kTmemCols>(&s_tmem);
       if (lane == 0) {
@@ -193,6 +175,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_barrier_init();
       }
       tc_fence_before();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int per = (E + kThreads - 1) / kThreads;
+    const int e0 = min(E, (int)threadIdx.x * per), e1 = min(E, e0 + per);
+    int local = 0;
+    for (int e = e0; e < e1; ++e) {
+      const int hi = min(max(__ldg(a.cumsum + e), 0), a.R);
+      const int lo = e ? min(max(__ldg(a.cumsum + e - 1), 0), a.R) : 0;
+      s_end[e] = hi;
+      local += tiles_of<NT>(lo, hi) * CB;
+    }
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) s_wsum[warp] = incl;
+    if (threadIdx.x == 0) {
+      s_abort = 0;
+      s_issued[0] = s_issued[1] = 0;
     }
     __syncthreads();
     int run = incl - local;
@@ -249,6 +252,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+    // the next kernel's setup beside the last items
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     // the last stages' releases: commits arrive in both CTAs of a pair, and neither may leave
     // before an arrival that is still on its way to it
     for (int s = 0; ok && s < S; ++s, at.next(S)) ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status);
@@ -494,12 +499,14 @@ cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
-  cudaLaunchAttribute cluster;
-  cluster.id = cudaLaunchAttributeClusterDimension;
-  cluster.val.clusterDim.x = PAIR ? 2 : 1;
-  cluster.val.clusterDim.y = cluster.val.clusterDim.z = 1;
-  cfg.attrs = &cluster;
-  cfg.numAttrs = 1;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = PAIR ? 2 : 1;
+  attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, mx_gmm_kernel<NT, SWIGLU, PAIR>, maps, a);
 }
 
@@ -509,6 +516,7 @@ constexpr int kCombineThreads = 256;
 __global__ void __launch_bounds__(kCombineThreads) mx_combine_kernel(const __half* c2, const int32_t* expanded,
                                                                      const float* probs, int M, int K, int topK,
                                                                      __half* out) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // a programmatic dependent of the product
   const int per = K / 8;
   const int64_t i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x;
   const int t = (int)(i / per), k = (int)(i - (int64_t)t * per);
@@ -558,9 +566,19 @@ cudaError_t launch_mx_gmm(const MxGemmProblem& p, cudaStream_t stream) {
 cudaError_t launch_mx_combine(const uint16_t* c2, const int32_t* expanded, const float* probs, int M, int K, int topK,
                               uint16_t* out, cudaStream_t stream) {
   const int64_t n = (int64_t)M * (K / 8);
-  mx_combine_kernel<<<(unsigned)((n + kCombineThreads - 1) / kCombineThreads), kCombineThreads, 0, stream>>>(
-      reinterpret_cast<const __half*>(c2), expanded, probs, M, K, topK, reinterpret_cast<__half*>(out));
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((n + kCombineThreads - 1) / kCombineThreads));
+  cfg.blockDim = dim3(kCombineThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute after;
+  after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  after.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &after;
+  // early where all blocks fit beside each other: at 128 tokens x 4096 119 us a layer for 121; 8192
+  // tokens' 16384 blocks took 489 us a layer launched early, 480 in order
+  cfg.numAttrs = cfg.gridDim.x <= 8u * (unsigned)sm_count() ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, mx_combine_kernel, reinterpret_cast<const __half*>(c2), expanded, probs, M, K, topK,
+                            reinterpret_cast<__half*>(out));
 }
 
 }  // namespace moe

@@ -100,6 +100,7 @@ template <typename T, bool VEC, bool MAP>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(int M, int D, const T* x, int64_t stride,
                                                               const int32_t* row_map, int copies, int rows,
                                                               uint8_t* codes, uint8_t* scales, int pitch) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product's setup beside the last rows
   Pieces at((D + 127) / 128 * 16);
   while (__any_sync(0xffffffffu, at.t < M)) {
     Eight<T> r[kItems];
