@@ -511,9 +511,12 @@ cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
 }
 
 // One thread per eight channels of a token: each row's 16 bytes, four rows read at a time, then
-// the sums in order of the routes.  Bound by reading c2.
+// the sums in order of the routes.  Bound by reading c2: 8192 tokens x 4096, six rows each, 78 us
+// for 470 MB.  c2 is binary16, as the product's users get it, and rounded once: over the output's
+// own rounding (2.1e-4 of its norm) that makes 3.0e-4; in 32 bits the product would write and this
+// kernel read 800 MB more, some 120 us of the layer's 485.
 constexpr int kCombineThreads = 256;
-__global__ void __launch_bounds__(kCombineThreads) mx_combine_kernel(const __half* c2, const int32_t* expanded,
+__global__ void __launch_bounds__(kCombineThreads, 6) mx_combine_kernel(const __half* c2, const int32_t* expanded,
                                                                      const float* probs, int M, int K, int topK,
                                                                      __half* out) {
   asm volatile("griddepcontrol.wait;" ::: "memory");  // a programmatic dependent of the product
