@@ -7,7 +7,7 @@ MXFP4 blocks, and runs a batch of tokens through the router and the expert layer
 
 It prints the weights' sizes, the time of a router and layer call, and how far the output is from
 the same layer with the weights and activations in 32 bits (what four bits cost).  With random
-weights and activations that is about 0.2 of the output's norm.
+weights and activations that is about 0.3 of the output's norm.
 """
 import argparse
 import os

@@ -9,18 +9,25 @@
 // channel blocks innermost, so that CTAs working at the same time share an expert's rows and
 // its weights through L2.  Persistent CTAs, one per SM, in two forms:
 //   - few rows per expert: single CTAs, 128 channels, tiles of up to 32 rows: the weights
-//     stream past;
+//     stream past (128 tokens x 7168, N = 4096, 256 experts, 8 each: 555 us with the rows'
+//     quantisation, the weights at 1.04 of the measured copy rate);
 //   - more: CTA pairs (cta_group::2), 256 channels, tiles of up to 192 rows.  Each CTA loads
 //     half of the rows: the copies through shared memory, which bound a single CTA's 128 x 208
-//     (325 us at 49152 rows, N = 2816, D = 4096, 64 experts), are fewer for each MMA.
+//     (325 us at 49152 rows, N = 2816, D = 4096, 64 experts, where the pairs take 221), are fewer
+//     for each MMA.  The tensor pipe is then 61% busy.  Nothing else is full: what sets the pace is
+//     the turn of the ring, a copy's latency, the scale words' way to tensor memory, the MMAs and
+//     their commit, over the six stages that fit (five: 17 us more; tiles of 224 rows and five
+//     stages: 17 more; 128 rows and seven: 28 more).
 // A tile starts on a multiple of four rows (a 16-byte boundary of the scale words), so an
 // expert's first one may begin with up to three rows of the expert before, not stored.
 //
 // Roles: warp 0 loads, per 256-deep stage, one 17408-byte copy of a weight block with its
 // scales and the rows' words of the two scale planes; warp 2 loads the rows' codes, in tensor
-// copies of 64, 32 and 16 rows; warps 4-7 in turn put a stage's scale words in tensor-memory order;
-// warp 1 issues the copies of the scales and the MMAs; warps 8-23 are four epilogue groups, two
-// for each of the two accumulators, taking its columns in turn.  Every wait is bounded: one that gives up records
+// copies of 64, 32 and 16 rows; warps 4-7 in turn put a stage's scale words in tensor-memory
+// order (sharing each stage instead: 296 us for 264; through registers to tensor memory by two
+// warpgroups, or ahead of the codes in a ring of their own: no faster); warp 1 issues the copies
+// of the scales and the MMAs; warps 8-23 are four epilogue groups, two for each of the two
+// accumulators, taking its columns in turn.  Every wait is bounded: one that gives up records
 // MOE_ERR_TIMEOUT and the CTA winds down.
 #include "mx_tc.cuh"
 #include "tensor_map.h"

@@ -7,6 +7,8 @@
 // apart, and reads them all first: one read of 16 bytes to a thread keeps too few under way.
 // Instructions are not far behind: magnitudes of 16-bit types are compared two to an
 // instruction, on their bits.
+// 90112 x 4096 bfloat16: 168 us and, back, 155, for 934 MB each (0.82 and 0.89 of the measured
+// copy rate); the integer pipe is 69% busy in the first.
 #include "mxfp4.cuh"
 #include "tensor_map.h"
 
