@@ -46,6 +46,7 @@ struct MxGemmProblem {
   uint8_t* h_codes;        // [R][N / 4] or null
   uint32_t* h_scales;      // [planes(N / 2)][pitch(R)]
   int32_t* status;
+  bool clear_status;       // the call's first product
 };
 cudaError_t launch_mx_gmm(const MxGemmProblem& p, cudaStream_t stream);
 

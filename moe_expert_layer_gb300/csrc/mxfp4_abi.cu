@@ -101,7 +101,6 @@ int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_
   }
   int32_t* expanded = at<int32_t>(ws, L.expanded);
   int32_t* cumsum = at<int32_t>(ws, L.cumsum);
-  if ((e = cudaMemsetAsync(ws, 0, 16, st)) != cudaSuccess) return launch_status(e);
   if ((e = moe::launch_route_sort(expert_idx, R, E, at<int32_t>(ws, L.sorted), expanded, at<int32_t>(ws, L.tpe), cumsum,
                                   at<void>(ws, L.sort_ws), st)) != cudaSuccess)
     return launch_status(e);
@@ -120,6 +119,7 @@ int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_
   g.h_codes = at<uint8_t>(ws, L.h_codes);
   g.h_scales = at<uint32_t>(ws, L.h_scales);
   g.status = at<int32_t>(ws, L.status);
+  g.clear_status = true;
   if ((e = moe::launch_mx_gmm(g, st)) != cudaSuccess) return launch_status(e);
   g.codes = g.h_codes;
   g.scales = g.h_scales;
@@ -129,6 +129,7 @@ int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_
   g.c = at<uint16_t>(ws, L.c2);
   g.h_codes = nullptr;
   g.h_scales = nullptr;
+  g.clear_status = false;
   if ((e = moe::launch_mx_gmm(g, st)) != cudaSuccess) return launch_status(e);
   return launch_status(moe::launch_mx_combine(g.c, expanded, probs, M, K, topK, out, st));
 }
@@ -219,9 +220,6 @@ int32_t moe_mxfp4_gmm(int32_t R, int32_t E, int32_t N, int32_t D, const uint8_t*
   if (workspace_bytes < gmm_workspace_bytes()) return MOE_ERR_WORKSPACE;
   int32_t rc;
   if ((rc = check_device()) != MOE_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if ((e = cudaMemsetAsync(workspace, 0, 16, st)) != cudaSuccess) return launch_status(e);
   moe::MxGemmProblem p{};
   p.R = R;
   p.E = E;
@@ -233,7 +231,8 @@ int32_t moe_mxfp4_gmm(int32_t R, int32_t E, int32_t N, int32_t D, const uint8_t*
   p.w = w;
   p.c = c;
   p.status = static_cast<int32_t*>(workspace);
-  return launch_status(moe::launch_mx_gmm(p, st));
+  p.clear_status = true;
+  return launch_status(moe::launch_mx_gmm(p, static_cast<cudaStream_t>(stream)));
 }
 
 int32_t moe_mxfp4_gmm_swiglu(int32_t R, int32_t E, int32_t I, int32_t D, const uint8_t* codes, const uint32_t* scales,
@@ -245,9 +244,6 @@ int32_t moe_mxfp4_gmm_swiglu(int32_t R, int32_t E, int32_t I, int32_t D, const u
   if (workspace_bytes < gmm_workspace_bytes()) return MOE_ERR_WORKSPACE;
   int32_t rc;
   if ((rc = check_device()) != MOE_OK) return rc;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e;
-  if ((e = cudaMemsetAsync(workspace, 0, 16, st)) != cudaSuccess) return launch_status(e);
   moe::MxGemmProblem p{};
   p.R = R;
   p.E = E;
@@ -260,7 +256,8 @@ int32_t moe_mxfp4_gmm_swiglu(int32_t R, int32_t E, int32_t I, int32_t D, const u
   p.h_codes = h_codes;
   p.h_scales = h_scales;
   p.status = static_cast<int32_t*>(workspace);
-  return launch_status(moe::launch_mx_gmm(p, st));
+  p.clear_status = true;
+  return launch_status(moe::launch_mx_gmm(p, static_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_mxfp4_layer_workspace_size(const moe_dims_t* d) {

@@ -73,6 +73,7 @@ struct GmmArgs {
   uint8_t* h_codes;
   uint8_t* h_scales;
   int32_t* status;
+  bool clear;
 };
 
 // Tensor maps of the codes, 256 elements x 64, 32 and 16 rows (a CTA's rows of a tile, a
@@ -184,6 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // long before any wait can run out; a memory set of its own took 2 us
+    if (a.clear && blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;
     const int per = (E + kThreads - 1) / kThreads;
     const int e0 = min(E, (int)threadIdx.x * per), e1 = min(E, e0 + per);
     int local = 0;
@@ -501,6 +504,7 @@ cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   a.h_codes = p.h_codes;
   a.h_scales = reinterpret_cast<uint8_t*>(p.h_scales);
   a.status = p.status;
+  a.clear = p.clear_status;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(PAIR ? sm_count() & ~1 : sm_count()));
   cfg.blockDim = dim3(kThreads);
