@@ -454,3 +454,60 @@ def test_example():
     for tokens in (1, 40):
         _, distance = example.run(tokens=tokens, hidden=512, intermediate=256, experts=8, topk=2, steps=2)
         assert 0.01 < distance < 0.5
+
+
+def test_many_tokens_on_another_stream_and_in_a_graph():
+    """The path of many tokens, whose launches overlap: the same bits on a second stream behind work of its
+    own, from a CUDA graph, and with calls on two workspaces in flight at once."""
+    M, K, I, E, topK = 150, 512, 128, 4, 2
+    x, ei, probs, w1, _, w2, _ = layer_case(M, K, I, E, topK, 17)
+    dx, de, dp = dev(x), dev(ei), dev(probs)
+    want, ws = run_layer(dx, de, dp, w1, w2, I, E)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    late = torch.zeros_like(dx)
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(1000000)
+        late.copy_(dx)
+        there, ws2 = run_layer(late, de, dp, w1, w2, I, E)
+    here, _ = run_layer(dx, de, dp, w1, w2, I, E, ws=ws)
+    s.synchronize()
+    assert torch.equal(there, want) and torch.equal(here, want)
+    d = moe.dims(M, K, I, E, topK)
+    out = torch.empty_like(want)
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        moe.moe_mxfp4_layer_fwd(d, dx, de, dp, w1, w2, out, ws)
+        moe.moe_mxfp4_layer_fwd(d, dx, de, dp, w1, w2, out, ws2)
+    for _ in range(5):
+        out.fill_(0)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+    assert moe.moe_workspace_status(ws) == 0 and moe.moe_workspace_status(ws2) == 0
+
+
+def test_product_behind_the_quantisation_that_feeds_it():
+    """Rows quantised and multiplied back to back with new rows each time: a product that began before
+    its operands were written would use the call's before."""
+    rng = np.random.default_rng(5)
+    E, N, D, per = 3, 256, 1056, 40
+    R = E * per
+    cum = dev(np.arange(1, E + 1, dtype=np.int32) * per)
+    w, _ = make_weights(rng, E, N, D, False)
+    ws = empty(moe.moe_mxfp4_gmm_workspace_size(R, E, N, D), torch.uint8)
+    codes, scales = empty((R, D // 2), torch.uint8), empty((moe.moe_mxfp4_scale_words(R, D),), torch.int32)
+    xs = [torch.randn(R, D, device="cuda", dtype=torch.float16) for _ in range(8)]
+
+    def product(x):
+        c = empty((R, N), torch.float16)
+        moe.moe_mxfp4_quant(x, codes, scales)
+        moe.moe_mxfp4_gmm(codes, scales, cum, w, c, ws)
+        return c
+
+    alone = []
+    for x in xs:
+        alone.append(product(x))
+        torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(alone, [product(x) for x in xs]))
