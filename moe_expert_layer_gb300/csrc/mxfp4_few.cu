@@ -8,7 +8,7 @@
 // dispatched or permuted in memory.
 // Measured, depth 7168, 2048 channels: one token, 8 of 256 experts, 41 us, where its 187 MB take
 // 28 at the measured copy rate; 8 tokens on 16 experts 66 us (55); depth 4096, 1408 channels: 29
-// tokens on 64 experts 101 us (82).  The rest is the start, the wait between the two products
+// tokens on 64 experts 94 us (82).  The rest is the start, the wait between the two products
 // for the last sums of h (its 6 stages in flight cover half of it) and the meeting at the end.
 //
 // Kernel 2 is persistent, one CTA per SM, with one pipeline for both products, so that the
@@ -184,9 +184,11 @@ struct Walk {
   }
 };
 
-// The routes by expert, in order of the routes, and the tiles of up to 16 of them.  A thread per
-// route finds its place by comparing with all the others; the routes that begin a tile are then
-// numbered in the order of the places, by ballots.  `tmp`: 2 * kMxFewRoutes words.
+// The routes by expert, in order of the routes, and the tiles of up to 16 of them.  A route's
+// place comes from comparing it with all the others, which as many threads share as there are for
+// each route (174 routes: 3.5 us by a thread alone, which the first weights wait for); the routes
+// that begin a tile are then numbered in the order of the places, by ballots.  `tmp`: 2 *
+// kMxFewRoutes words.
 __device__ __forceinline__ void make_tables(const FewArgs& a, Tables& t, int* tmp, int* wsum) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int e = -1;
@@ -195,23 +197,30 @@ __device__ __forceinline__ void make_tables(const FewArgs& a, Tables& t, int* tm
     if (e < 0 || e >= a.E) e = -1;
     t.prob[tid] = __ldg(a.probs + tid);
   }
-  if (tid < kMxFewRoutes) tmp[tid] = e;
-  __syncthreads();
-  int less = 0, before = 0, same = 0;  // routes of lower experts; of this one, before this route, and in all
-  if (e >= 0) {
-    for (int r = 0; r < a.R; r += 4) {
-      const int4 o = reinterpret_cast<const int4*>(tmp)[r >> 2];
-      const int v[4] = {o.x, o.y, o.z, o.w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        less += v[k] >= 0 && v[k] < e;
-        same += v[k] == e;
-        before += v[k] == e && r + k < tid;
-      }
-    }
+  if (tid < kMxFewRoutes) {
+    tmp[tid] = e;
+    tmp[kMxFewRoutes + tid] = 0;
   }
   __syncthreads();
-  const int place = less + before;
+  // counted for a route, in 10 bits each: routes of lower experts; of its own, before it; in all
+  const int R32 = (a.R + 31) & ~31, share = kThreads / R32, who = tid / R32, mine = tid - who * R32;
+  const int words = (a.R + 3) >> 2, per = (words + share - 1) / share;
+  const int e_mine = who < share ? tmp[mine] : -1;
+  if (e_mine >= 0) {
+    int count = 0;
+    for (int w = who * per; w < min(words, (who + 1) * per); ++w) {
+      const int4 o = reinterpret_cast<const int4*>(tmp)[w];
+      const int v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        count += v[k] < 0 ? 0 : v[k] < e_mine ? 1 : v[k] > e_mine ? 0 : 4 * w + k < mine ? (1 << 20) + (1 << 10) : 1 << 20;
+    }
+    if (count) atomicAdd(tmp + kMxFewRoutes + mine, count);
+  }
+  __syncthreads();
+  const int count = tid < kMxFewRoutes ? tmp[kMxFewRoutes + tid] : 0;
+  const int before = count >> 10 & 1023, same = count >> 20, place = (count & 1023) + before;
+  __syncthreads();
   if (tid < kMxFewRoutes) tmp[kMxFewRoutes + tid] = -1;
   __syncthreads();
   if (e >= 0) {
@@ -552,6 +561,47 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
   return true;
 }
 
+// out of block nb from the sums of runs c0 .. c1, added in this order: every fourth token to a warp,
+// four channels to a lane, and two runs' sums of all its tokens read at a time (29 tokens read one
+// after the other took 12 us; four runs of two tokens, for up to 8, no less than this).
+__device__ __forceinline__ void add_parts(const FewArgs& a, const Product<true>& p, const float* parts, int nb, int c0, int c1,
+                                          __half* out, int quarter, int lane) {
+  constexpr int kMine = kMxFewTokens / 4, kRuns = 2;
+  float4 acc[kMine];
+#pragma unroll
+  for (int k = 0; k < kMine; ++k) acc[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  for (int c = c0; c <= c1; c += kRuns) {
+    float4 o[kRuns][kMine];
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j) {
+      const int run = min(c + j, c1);
+      const float* q = parts + ((size_t)run * 2 + (nb != p.block_of(p.begin_of(run)))) * a.M * 128 + lane * 4;
+#pragma unroll
+      for (int k = 0; k < kMine; ++k)
+        if (quarter + 4 * k < a.M) o[j][k] = __ldcg(reinterpret_cast<const float4*>(q + (quarter + 4 * k) * 128));
+    }
+#pragma unroll
+    for (int j = 0; j < kRuns; ++j)
+#pragma unroll
+      for (int k = 0; k < kMine; ++k)
+        if (c + j <= c1 && quarter + 4 * k < a.M) {
+          acc[k].x += o[j][k].x;
+          acc[k].y += o[j][k].y;
+          acc[k].z += o[j][k].z;
+          acc[k].w += o[j][k].w;
+        }
+  }
+#pragma unroll
+  for (int k = 0; k < kMine; ++k)
+    if (quarter + 4 * k < a.M) {
+      uint2 h;
+      const __half2 lo = f2h2_sat(acc[k].x, acc[k].y), hi = f2h2_sat(acc[k].z, acc[k].w);
+      h.x = *reinterpret_cast<const uint32_t*>(&lo);
+      h.y = *reinterpret_cast<const uint32_t*>(&hi);
+      *reinterpret_cast<uint2*>(out + (size_t)(quarter + 4 * k) * a.K + lane * 4) = h;
+    }
+}
+
 __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<true>& p,
                                            float* sums, int quarter, int lane, int& u, int* s_last) {
   const int ch = quarter * 32 + lane;
@@ -593,31 +643,7 @@ __device__ __forceinline__ bool finish_out(const FewArgs& a, const Tables& t, co
       sums[i * 128 + ch] = 0.0f;
     }
     if (!last_run(counters + s.nb, c1 - c0 + 1, quarter == 0 && lane == 0, s_last)) continue;
-    // a token to a warp, four channels to a lane, the runs' sums four at a time
-    for (int i = quarter; i < a.M; i += 4) {
-      float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      for (int c = c0; c <= c1; c += 4) {
-        float4 o[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          o[k] = c + k <= c1 ? __ldcg(reinterpret_cast<const float4*>(
-                                   parts + ((size_t)(c + k) * 2 + (s.nb != p.block_of(p.begin_of(c + k)))) * a.M * 128 +
-                                   i * 128) + lane)
-                             : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          acc.x += o[k].x;
-          acc.y += o[k].y;
-          acc.z += o[k].z;
-          acc.w += o[k].w;
-        }
-      }
-      uint2 h;
-      const __half2 lo = f2h2_sat(acc.x, acc.y), hi = f2h2_sat(acc.z, acc.w);
-      h.x = *reinterpret_cast<const uint32_t*>(&lo);
-      h.y = *reinterpret_cast<const uint32_t*>(&hi);
-      *reinterpret_cast<uint2*>(out + (size_t)i * a.K + lane * 4) = h;
-    }
+    add_parts(a, p, parts, s.nb, c0, c1, out, quarter, lane);
   }
   return true;
 }
