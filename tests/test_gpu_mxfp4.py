@@ -511,3 +511,34 @@ def test_product_behind_the_quantisation_that_feeds_it():
         alone.append(product(x))
         torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(alone, [product(x) for x in xs]))
+
+
+def test_offsets_past_32_bits():
+    """Elements and bytes past 2^32: the last rows of large arrays are those of a call on them alone."""
+    rows, D, last = 270000, 16384, 37  # 2^32 elements are 262144 rows
+    x = torch.zeros(rows, D, dtype=torch.float16, device="cuda")
+    x[-last:] = torch.randn(last, D, device="cuda", dtype=torch.float16)
+    codes, scales = quant_device(x)
+    want_codes, want_scales = quant_device(x[-last:].contiguous())
+    planes = scales.view(D // 128, -1)[:, rows - last:rows]
+    assert torch.equal(codes[-last:], want_codes)
+    assert torch.equal(planes, want_scales.view(D // 128, -1)[:, :last])
+    assert not codes[:-last].any() and not scales.view(D // 128, -1)[:, :rows - last].any()
+    back = x.fill_(1.0)
+    moe.moe_mxfp4_dequant(codes, scales, back)
+    small = empty((last, D), torch.float16)
+    moe.moe_mxfp4_dequant(want_codes, want_scales, small)
+    assert torch.equal(back[-last:], small) and not back[:-last].any()
+    del x, back, codes, scales
+
+    R, N, D = 70004, 65536, 64  # 2^32 outputs are 65536 rows
+    rng = np.random.default_rng(8)
+    w, _ = make_weights(rng, 1, N, D, False)
+    a = torch.randn(R, D, device="cuda", dtype=torch.float16)
+    codes, scales = quant_device(a)
+    few_codes, few_scales = quant_device(a[-last:].contiguous())
+    ws = empty(moe.moe_mxfp4_gmm_workspace_size(R, 1, N, D), torch.uint8)
+    c, want = empty((R, N), torch.float16), empty((last, N), torch.float16)
+    moe.moe_mxfp4_gmm(codes, scales, dev(np.array([R], np.int32)), w, c, ws)
+    moe.moe_mxfp4_gmm(few_codes, few_scales, dev(np.array([last], np.int32)), w, want, ws)
+    assert torch.equal(c[-last:], want)
