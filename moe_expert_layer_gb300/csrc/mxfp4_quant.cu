@@ -103,7 +103,9 @@ template <typename T, bool VEC, bool MAP>
 __global__ void __launch_bounds__(kThreads) quant_rows_kernel(int M, int D, const T* x, int64_t stride,
                                                               const int32_t* row_map, int copies, int rows,
                                                               uint8_t* codes, uint8_t* scales, int pitch) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the product's setup beside the last rows
+  // a programmatic dependent of the kernel before, and the product's setup beside the last rows
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   Pieces at((D + 127) / 128 * 16);
   while (__any_sync(0xffffffffu, at.t < M)) {
     Eight<T> r[kItems];
@@ -329,15 +331,18 @@ cudaError_t quant_rows(int M, int D, const void* x, int64_t stride, const int32_
       quant_dispatch_kernel<T, false><<<blocks, 32 * kRowWarps, smem, stream>>>(M, D, p, stride, row_map, copies, rows, codes, scales, pitch);
     return cudaGetLastError();
   }
-  if (vec && row_map)
-    quant_rows_kernel<T, true, true><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
-  else if (vec)
-    quant_rows_kernel<T, true, false><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
-  else if (row_map)
-    quant_rows_kernel<T, false, true><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
-  else
-    quant_rows_kernel<T, false, false><<<grid, kThreads, 0, stream>>>(M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
-  return cudaGetLastError();
+  auto* kernel = vec ? (row_map ? quant_rows_kernel<T, true, true> : quant_rows_kernel<T, true, false>)
+                     : (row_map ? quant_rows_kernel<T, false, true> : quant_rows_kernel<T, false, false>);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute after;
+  after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  after.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &after;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
 }
 
 template <typename T>
