@@ -171,6 +171,10 @@ size_t moe_mxfp4_layer_workspace_size(const moe_dims_t* d);
  *   w1  blocks of [E][2I][K] in gate_up order;  w2  blocks of [E][K][I], plain order
  *   workspace >= moe_mxfp4_layer_workspace_size(d) bytes; its first word is the status word
  *              that moe_workspace_status reads.  Its contents on entry do not matter.
+ * Up to 32 tokens and 256 routes (at sizes that fit the device) one kernel does most of
+ * it, whose blocks wait for one another: calls in flight on streams of different
+ * priorities can keep each other's blocks off the device until the wait's limit, about
+ * two seconds, and then report MOE_ERR_TIMEOUT in the status word.
  */
 int32_t moe_mxfp4_layer_fwd(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_idx, const float* probs,
                             const uint8_t* w1, const uint8_t* w2, uint16_t* out, void* workspace,

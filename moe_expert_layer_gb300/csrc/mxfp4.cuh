@@ -69,6 +69,24 @@ __device__ __forceinline__ void mx_values8(uint32_t w, float (&v)[8]) {
 // x * 2^(127 - b) for a block that may hold non-finite values (b = 255 -> 0).
 __device__ __forceinline__ float mx_scaled(float x, float mult, uint32_t b) { return b == 255u ? 0.0f : x * mult; }
 
+// Launches a kernel as a programmatic dependent of the one before it in the stream: it may start
+// when that one's blocks have all asked for dependents or ended, and has to wait
+// (griddepcontrol.wait) before it touches anything that earlier work writes or reads.
+template <typename... P, typename... A>
+cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute after;
+  after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  after.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &after;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
+}
+
 // Byte offset, in its weight block, of 16-byte chunk c of channel row r, and of its scale.
 __device__ __forceinline__ int mx_chunk_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
 __device__ __forceinline__ int mx_scale_at(int r, int c) { return kMxCodeBytes + (c >> 2) * 512 + r * 4 + (c & 3); }

@@ -6,9 +6,9 @@
 // streaming past (17408 bytes per 128 channels x 256 reduction steps), so everything else is
 // done beside that stream: each CTA makes the routes' tables itself, and no row is
 // dispatched or permuted in memory.
-// Measured, depth 7168, 2048 channels: one token, 8 of 256 experts, 41 us, where its 187 MB take
-// 28 at the measured copy rate; 8 tokens on 16 experts 66 us (55); depth 4096, 1408 channels: 29
-// tokens on 64 experts 94 us (82).  The rest is the start, the wait between the two products
+// Measured, depth 7168, 2048 channels: one token, 8 of 256 experts, 40 us, where its 187 MB take
+// 28 at the measured copy rate; 8 tokens on 16 experts 63 us (55); depth 4096, 1408 channels: 29
+// tokens on 64 experts 92 us (82).  The rest is the start, the wait between the two products
 // for the last sums of h (its 6 stages in flight cover half of it) and the meeting at the end.
 //
 // Kernel 2 is persistent, one CTA per SM, with one pipeline for both products, so that the
@@ -31,8 +31,8 @@
 //     run per CTA, whose sums add up in shared memory over experts and stages alike and meet the
 //     same way.  A run that goes over the end of a block takes the block it ends in first: the
 //     tiles whose h is made last come last, and nothing waits for most of h.
-// It is launched as a programmatic dependent of kernel 1: tables and first weights come while
-// that still runs.  A CTA waits for others' h, so all of them have to be resident: one per SM,
+// Each kernel is launched as a programmatic dependent of the one before: tables and first weights
+// come while kernel 1 still runs.  A CTA waits for others' h, so all of them have to be resident: one per SM,
 // which the host checks fit.  Every wait is bounded, as in the grouped product.
 #include "mx_tc.cuh"
 #include "tensor_map.h"
@@ -750,6 +750,8 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_consta
 constexpr int kXThreads = 256;
 __global__ void __launch_bounds__(kXThreads) mx_few_x_kernel(const __half* x, int M, int K, uint8_t* codes, uint8_t* scales,
                                                              int32_t* counters, int n_counters, int32_t* status) {
+  // Only behind the wait may kernel 2 start: it reads routes and weights before it waits itself.
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int i = blockIdx.x * kXThreads + threadIdx.x;
   for (int c = i; c < n_counters; c += gridDim.x * kXThreads) counters[c] = 0;
@@ -824,10 +826,9 @@ cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
       !encode_tensor_map_rows(&maps.h_scales, p.h_scales, hs, hs, R, kScaleRec, CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   const int n_counters = counters_of(p.M, p.K, p.I, p.topK);
-  const int x_blocks = (int)(((size_t)p.M * p.K / 8 + kXThreads - 1) / kXThreads);
-  mx_few_x_kernel<<<x_blocks, kXThreads, 0, stream>>>(reinterpret_cast<const __half*>(p.x), p.M, p.K, p.x_codes,
-                                                      p.x_scales, p.counters, n_counters, p.status);
-  cudaError_t e = cudaGetLastError();
+  const unsigned x_blocks = (unsigned)(((size_t)p.M * p.K / 8 + kXThreads - 1) / kXThreads);
+  cudaError_t e = launch_dependent(mx_few_x_kernel, x_blocks, kXThreads, 0, stream, reinterpret_cast<const __half*>(p.x), p.M, p.K,
+                                   p.x_codes, p.x_scales, p.counters, n_counters, p.status);
   if (e != cudaSuccess) return e;
   FewArgs a;
   a.M = p.M;
@@ -846,17 +847,7 @@ cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
   a.counters = p.counters;
   a.out = reinterpret_cast<__half*>(p.out);
   a.status = p.status;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)sm_count());
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem_bytes(p.M);
-  cfg.stream = stream;
-  cudaLaunchAttribute after;
-  after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  after.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &after;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, mx_few_kernel, maps, a);
+  return launch_dependent(mx_few_kernel, (unsigned)sm_count(), kThreads, smem_bytes(p.M), stream, maps, a);
 }
 
 }  // namespace moe

@@ -580,19 +580,15 @@ cudaError_t launch_mx_gmm(const MxGemmProblem& p, cudaStream_t stream) {
 cudaError_t launch_mx_combine(const uint16_t* c2, const int32_t* expanded, const float* probs, int M, int K, int topK,
                               uint16_t* out, cudaStream_t stream) {
   const int64_t n = (int64_t)M * (K / 8);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((n + kCombineThreads - 1) / kCombineThreads));
-  cfg.blockDim = dim3(kCombineThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute after;
-  after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  after.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &after;
+  const unsigned blocks = (unsigned)((n + kCombineThreads - 1) / kCombineThreads);
+  const __half* rows = reinterpret_cast<const __half*>(c2);
+  __half* o = reinterpret_cast<__half*>(out);
   // early where all blocks fit beside each other: at 128 tokens x 4096 119 us a layer for 121; 8192
   // tokens' 16384 blocks took 489 us a layer launched early, 480 in order
-  cfg.numAttrs = cfg.gridDim.x <= 8u * (unsigned)sm_count() ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, mx_combine_kernel, reinterpret_cast<const __half*>(c2), expanded, probs, M, K, topK,
-                            reinterpret_cast<__half*>(out));
+  if (blocks <= 8u * (unsigned)sm_count())
+    return launch_dependent(mx_combine_kernel, blocks, kCombineThreads, 0, stream, rows, expanded, probs, M, K, topK, o);
+  mx_combine_kernel<<<blocks, kCombineThreads, 0, stream>>>(rows, expanded, probs, M, K, topK, o);
+  return cudaGetLastError();
 }
 
 }  // namespace moe

@@ -214,6 +214,8 @@ constexpr int kDequantBlocks = 4;  // to an SM
 template <typename T>
 __global__ void __launch_bounds__(kThreads) dequant_rows_kernel(int rows, int D, const uint8_t* codes,
                                                                 const uint32_t* scales, int pitch, T* out) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   Pieces at(D / 8);
   while (at.t < rows) {
     uint32_t w[kItems], sw[kItems];
@@ -333,24 +335,14 @@ cudaError_t quant_rows(int M, int D, const void* x, int64_t stride, const int32_
   }
   auto* kernel = vec ? (row_map ? quant_rows_kernel<T, true, true> : quant_rows_kernel<T, true, false>)
                      : (row_map ? quant_rows_kernel<T, false, true> : quant_rows_kernel<T, false, false>);
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)grid);
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute after;
-  after.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  after.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &after;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
+  return launch_dependent(kernel, (unsigned)grid, kThreads, 0, stream, M, D, p, stride, row_map, copies, rows, codes, sc, pitch);
 }
 
 template <typename T>
 cudaError_t dequant_rows(int rows, int D, const uint8_t* codes, const uint32_t* scales, void* out,
                          cudaStream_t stream) {
-  dequant_rows_kernel<T><<<grid_of((size_t)rows * (D / 8), kDequantBlocks), kThreads, 0, stream>>>(
-      rows, D, codes, scales, mx_scale_pitch(rows), static_cast<T*>(out));
-  return cudaGetLastError();
+  return launch_dependent(dequant_rows_kernel<T>, (unsigned)grid_of((size_t)rows * (D / 8), kDequantBlocks), kThreads, 0, stream,
+                          rows, D, codes, scales, mx_scale_pitch(rows), static_cast<T*>(out));
 }
 
 template <typename T>

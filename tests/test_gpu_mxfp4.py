@@ -542,3 +542,33 @@ def test_offsets_past_32_bits():
     moe.moe_mxfp4_gmm(codes, scales, dev(np.array([R], np.int32)), w, c, ws)
     moe.moe_mxfp4_gmm(few_codes, few_scales, dev(np.array([last], np.int32)), w, want, ws)
     assert torch.equal(c[-last:], want)
+
+
+def test_router_and_layer_behind_the_work_that_feeds_them():
+    """Logits and tokens written, routed and put through the layer without a pause, with new ones each
+    time: a kernel that read before the one in front of it had written would use the call's before."""
+    K, I, E, topK = 512, 128, 8, 2
+    rng = np.random.default_rng(33)
+    w1, _ = make_weights(rng, E, 2 * I, K, True)
+    w2, _ = make_weights(rng, E, K, I, False)
+    for M in (1, 6, 100):  # a few tokens, and many
+        d = moe.dims(M, K, I, E, topK)
+        ws = empty(moe.moe_mxfp4_layer_workspace_size(d), torch.uint8)
+        logits, x = empty((M, E), torch.float32), empty((M, K), torch.float16)
+        idx, probs = empty((M, topK), torch.int32), empty((M, topK), torch.float32)
+        sets = [(torch.randn(M, E, device="cuda"), torch.randn(M, K, device="cuda").half() / 64) for _ in range(10)]
+
+        def layer(s):
+            out = empty((M, K), torch.float16)
+            logits.copy_(s[0])
+            x.copy_(s[1])
+            moe.moe_route_topk(logits, idx, probs)
+            moe.moe_mxfp4_layer_fwd(d, x, idx, probs, w1, w2, out, ws)
+            return out
+
+        alone = []
+        for s in sets:
+            alone.append(layer(s))
+            torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(alone * 3, [layer(s) for s in sets * 3]))
+        assert moe.moe_workspace_status(ws) == 0
