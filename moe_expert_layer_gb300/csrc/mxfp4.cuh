@@ -71,7 +71,9 @@ __device__ __forceinline__ float mx_scaled(float x, float mult, uint32_t b) { re
 
 // Launches a kernel as a programmatic dependent of the one before it in the stream: it may start
 // when that one's blocks have all asked for dependents or ended, and has to wait
-// (griddepcontrol.wait) before it touches anything that earlier work writes or reads.
+// (griddepcontrol.wait) before it touches anything that earlier work writes or reads.  What earlier
+// kernels may still be writing at its launch it reads past the read-only path, which promises
+// nothing for data that changes in a kernel's lifetime.
 template <typename... P, typename... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg = {};

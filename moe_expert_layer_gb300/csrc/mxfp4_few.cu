@@ -193,9 +193,9 @@ __device__ __forceinline__ void make_tables(const FewArgs& a, Tables& t, int* tm
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int e = -1;
   if (tid < a.R) {
-    e = __ldg(a.expert_idx + tid);
+    e = __ldcg(a.expert_idx + tid);
     if (e < 0 || e >= a.E) e = -1;
-    t.prob[tid] = __ldg(a.probs + tid);
+    t.prob[tid] = __ldcg(a.probs + tid);
   }
   if (tid < kMxFewRoutes) {
     tmp[tid] = e;
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kXThreads) mx_few_x_kernel(const __half* x, in
   const int per = K / 8;  // lanes of a row; K is a multiple of 128, so four lanes stay together
   const int t = i / per, k = (i - t * per) * 8;
   if (t >= M) return;
-  const uint4 raw = __ldg(reinterpret_cast<const uint4*>(x + (size_t)t * K + k));
+  const uint4 raw = __ldcg(reinterpret_cast<const uint4*>(x + (size_t)t * K + k));
   const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
   float v[8];
   uint32_t amax = 0;

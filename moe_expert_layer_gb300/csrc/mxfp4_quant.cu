@@ -55,7 +55,7 @@ template <typename T, bool VEC>
 __device__ __forceinline__ void load8(const T* p, Eight<T>& r) {
   if (VEC) {
 #pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = __ldcg(reinterpret_cast<const uint4*>(p) + i);
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) r.t[i] = p[i];
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads) quant_rows_kernel(int M, int D, cons
           for (int j = 0; j < copies; j += 4) {
             int d[4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) d[q] = j + q < copies ? __ldg(to + j + q) : -1;
+            for (int q = 0; q < 4; ++q) d[q] = j + q < copies ? to[j + q] : -1;
 #pragma unroll
             for (int q = 0; q < 4; ++q)
               if (d[q] >= 0 && d[q] < rows) put(d[q]);
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(32 * kRowWarps) quant_dispatch_kernel(int M, i
     __syncwarp();
     const int32_t* to = row_map + (int64_t)t * copies;
     for (int j0 = 0; j0 < copies; j0 += 32) {
-      int d = j0 + lane < copies ? __ldg(to + j0 + lane) : -1;
+      int d = j0 + lane < copies ? to[j0 + lane] : -1;
       if (d >= rows) d = -1;
       if (d >= 0) bulk_store(codes + (size_t)d * row_bytes, s_codes, (uint32_t)row_bytes);
       for (int j = 0; j < min(32, copies - j0); ++j) {
@@ -227,8 +227,8 @@ __global__ void __launch_bounds__(kThreads) dequant_rows_kernel(int rows, int D,
       c[k] = at.c;
       i[k] = (size_t)t[k] * (D / 8) + c[k];
       if (t[k] < rows) {
-        w[k] = __ldg(reinterpret_cast<const uint32_t*>(codes) + i[k]);
-        sw[k] = __ldg(scales + (size_t)(c[k] >> 4) * pitch + t[k]);
+        w[k] = __ldcg(reinterpret_cast<const uint32_t*>(codes) + i[k]);
+        sw[k] = __ldcg(scales + (size_t)(c[k] >> 4) * pitch + t[k]);
       }
     }
 #pragma unroll
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kThreads) pack_weights_kernel(int N, int D, in
     uint8_t b = 0;
     uint4 c = make_uint4(0, 0, 0, 0);
     if (it.k * 32 < D) {
-      c = __ldg(reinterpret_cast<const uint4*>(codes + it.row * (D / 2) + it.k * 16));
+      c = __ldcg(reinterpret_cast<const uint4*>(codes + it.row * (D / 2) + it.k * 16));
       b = scales[it.row * (D / 32) + it.k];
     }
     uint8_t* blk = blocks + it.blk * kMxBlockBytes;

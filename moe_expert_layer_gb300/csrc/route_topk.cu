@@ -62,12 +62,12 @@ __device__ __forceinline__ void load_logits(const T* row, int E, int lane, float
     if (in) {
       const T* p = row + lane * V;
       if (kBytes == 4) {
-        r.u1 = __ldg(reinterpret_cast<const uint32_t*>(p));
+        r.u1 = __ldcg(reinterpret_cast<const uint32_t*>(p));
       } else if (kBytes == 8) {
-        r.u2 = __ldg(reinterpret_cast<const uint2*>(p));
+        r.u2 = __ldcg(reinterpret_cast<const uint2*>(p));
       } else {
 #pragma unroll
-        for (int i = 0; i < kBytes / 16; ++i) r.u4[i] = __ldg(reinterpret_cast<const uint4*>(p) + i);
+        for (int i = 0; i < kBytes / 16; ++i) r.u4[i] = __ldcg(reinterpret_cast<const uint4*>(p) + i);
       }
     }
 #pragma unroll
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(32 * kWarps) route_topk_kernel(const T* logits
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     key[i] = order_bits(l[i]);
-    if (ALL && a.bias && key[i] != kNone) key[i] = order_bits(score(l[i]) + __ldg(a.bias + lane * V + i));
+    if (ALL && a.bias && key[i] != kNone) key[i] = order_bits(score(l[i]) + __ldcg(a.bias + lane * V + i));
   }
   // the lane's two largest keys, the first of equals first
   uint32_t best, second;
