@@ -166,7 +166,8 @@ size_t moe_mxfp4_layer_workspace_size(const moe_dims_t* d);
 /*
  * out[t, :] = sum over the token's valid routes of probs[t, j] * FFN_e(x[t, :]): the
  * expert layer of moe_layer_fwd on MXFP4 weights and activations.  x is quantised to
- * MXFP4, h = SwiGLU(GMM1) again, both products accumulate in fp32.
+ * MXFP4, h = SwiGLU(GMM1) again, both products accumulate in fp32; the routes' rows are
+ * weighted and added in fp32 too, and out is rounded to binary16 once.
  *   x, expert_idx, probs, out: as moe_layer_fwd (d->weight_layout is not read)
  *   w1  blocks of [E][2I][K] in gate_up order;  w2  blocks of [E][K][I], plain order
  *   workspace >= moe_mxfp4_layer_workspace_size(d) bytes; its first word is the status word

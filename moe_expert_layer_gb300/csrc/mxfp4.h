@@ -33,9 +33,9 @@ cudaError_t launch_mx_quant_weights(int E, int N, int D, bool gate_up, const voi
 cudaError_t launch_mx_pack_weights(int E, int N, int D, bool gate_up, const uint8_t* codes, const uint8_t* scales,
                                    uint8_t* blocks, cudaStream_t stream);
 
-// Grouped product over expert-major MXFP4 rows (mxfp4_gmm.cu).  h_codes null: c gets the
-// binary16 sums; else N = 2 I channels in gate_up order, and the SwiGLU of the sums is
-// written as MXFP4 rows of depth N / 2.
+// Grouped product over expert-major MXFP4 rows (mxfp4_gmm.cu).  h_codes null: c gets the sums
+// rounded to binary16, or c32 the sums themselves; else N = 2 I channels in gate_up order, and
+// the SwiGLU of the sums is written as MXFP4 rows of depth N / 2.
 struct MxGemmProblem {
   int R, E, N, D;
   const uint8_t* codes;    // [R][D / 2]
@@ -43,6 +43,7 @@ struct MxGemmProblem {
   const int32_t* cumsum;   // [E]
   const uint8_t* w;        // blocks
   uint16_t* c;             // [R][N] or null
+  float* c32;              // [R][N] or null
   uint8_t* h_codes;        // [R][N / 4] or null
   uint32_t* h_scales;      // [planes(N / 2)][pitch(R)]
   int32_t* status;
@@ -80,7 +81,7 @@ size_t mx_few_counter_bytes(int M, int K, int I, int topK);
 cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream);
 
 // out[t] = sum over j of probs[t][j] * c2[expanded[t * topK + j]] (entries < 0 skipped)
-cudaError_t launch_mx_combine(const uint16_t* c2, const int32_t* expanded, const float* probs, int M, int K, int topK,
+cudaError_t launch_mx_combine(const float* c2, const int32_t* expanded, const float* probs, int M, int K, int topK,
                               uint16_t* out, cudaStream_t stream);
 
 }  // namespace moe

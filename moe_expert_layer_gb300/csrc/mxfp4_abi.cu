@@ -63,7 +63,7 @@ Layout layout_of(const moe_dims_t* d) {
   L.a_scales = take(moe_mxfp4_scale_words((int64_t)R, (int32_t)K) * 4);
   L.h_codes = take(R * (I / 2));
   L.h_scales = take(moe_mxfp4_scale_words((int64_t)R, (int32_t)I) * 4);
-  L.c2 = take(R * K * 2);
+  L.c2 = take(R * K * 4);
   L.total = off;
   return L;
 }
@@ -126,12 +126,12 @@ int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_
   g.N = K;
   g.D = I;
   g.w = w2;
-  g.c = at<uint16_t>(ws, L.c2);
+  g.c32 = at<float>(ws, L.c2);
   g.h_codes = nullptr;
   g.h_scales = nullptr;
   g.clear_status = false;
   if ((e = moe::launch_mx_gmm(g, st)) != cudaSuccess) return launch_status(e);
-  return launch_status(moe::launch_mx_combine(g.c, expanded, probs, M, K, topK, out, st));
+  return launch_status(moe::launch_mx_combine(g.c32, expanded, probs, M, K, topK, out, st));
 }
 
 }  // namespace

@@ -64,12 +64,16 @@ struct Cfg {
   static_assert(kSmem + 9 * 1024 <= 227 * 1024, "shared memory, with ~8.4 KB static");
 };
 
+// What becomes of the sums: binary16 rows, fp32 rows, or their SwiGLU as MXFP4 rows.
+enum class Out { kHalf, kFloat, kSwiglu };
+
 struct GmmArgs {
   int R, E, N, D, KB, pitch;
   const uint32_t* scales;
   const int32_t* cumsum;
   const uint8_t* w;
   __half* c;
+  float* c32;
   uint8_t* h_codes;
   uint8_t* h_scales;
   int32_t* status;
@@ -144,7 +148,7 @@ __device__ __forceinline__ bool group_all(int id, bool ok) {
   return r != 0;
 }
 
-template <int NT, bool SWIGLU, bool PAIR>
+template <int NT, Out OUT, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     mx_gmm_kernel(const __grid_constant__ Maps maps, const GmmArgs a) {
   using C = Cfg<NT, PAIR>;
@@ -169,7 +173,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         for (int b = 0; b < kBoxes; ++b) prefetch_tmap(&maps.box[b]);
         prefetch_tmap(&maps.scales);
-        if (!SWIGLU) prefetch_tmap(&maps.c);
+        if (OUT == Out::kHalf) prefetch_tmap(&maps.c);
         for (int s = 0; s < S; ++s) {
           mbar_init(&full_bar[s], 2);
           mbar_init(&empty_bar[s], 1);
@@ -368,7 +372,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int nb = PAIR ? 2 * it.cb + (int)rank : it.cb;
       const int rows = nb < NB ? it.rows : 0;  // a pair's block past the last channel stores nothing
       const int skip = it.skip;
-      if (!SWIGLU) {
+      if (OUT == Out::kHalf) {
         // 32 rows x 128 channels of binary16 gathered in shared memory and stored from there by one
         // tensor copy, or, where the tile's first or last rows are not its own, row by row
         for (int c0 = kOutRows * (group >> 1); c0 < it.n; c0 += 2 * kOutRows) {
@@ -401,6 +405,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             bulk_commit_group();
           }
+        }
+      } else if (OUT == Out::kFloat) {
+        // a warp's 32 channels of a row are whole 128-byte lines
+        for (int c0 = 16 * (group >> 1); c0 < it.n; c0 += 32) {
+          uint32_t v[16];
+          __syncwarp();
+          tmem_ld16(t + c0, v);
+          tmem_wait_ld();
+          float* o = a.c32 + (size_t)(it.row0 + c0) * a.N + nb * 128 + quarter * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (c0 + i >= skip && c0 + i < rows) o[i * a.N] = __uint_as_float(v[i]);
         }
       } else {
         // Warps in pairs: the even one holds 32 gate channels, the odd one the up channels that
@@ -449,7 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (PAIR) mbar_arrive_remote(cluster_addr(&accempty_bar[buf], 0)); else mbar_arrive(&accempty_bar[buf]);
       }
     }
-    if (!SWIGLU && quarter == 0) bulk_wait_all();  // stores done before shared memory is released
+    if (OUT == Out::kHalf && quarter == 0) bulk_wait_all();  // stores done before shared memory is released
   }
 
   __syncthreads();
@@ -468,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int NT, bool SWIGLU, bool PAIR>
+template <int NT, Out OUT, bool PAIR>
 cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   using C = Cfg<NT, PAIR>;
   Maps maps;
@@ -479,14 +495,14 @@ cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   if (!encode_tensor_map_words(&maps.scales, p.scales, (uint64_t)mx_scale_pitch(p.R), (uint64_t)mx_scale_planes(p.D),
                                C::kPlaneWords, 2))
     return cudaErrorInvalidValue;
-  if (!SWIGLU && !encode_tensor_map_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p.c, (uint64_t)p.N, rows, 128, kOutRows,
+  if (OUT == Out::kHalf && !encode_tensor_map_2d(&maps.c, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, p.c, (uint64_t)p.N, rows, 128, kOutRows,
                                        CU_TENSOR_MAP_SWIZZLE_NONE))
     return cudaErrorInvalidValue;
   static PerContextOnce set;
   const int dev = current_device();
   if (set.needed(dev)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(mx_gmm_kernel<NT, SWIGLU, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        cudaFuncSetAttribute(mx_gmm_kernel<NT, OUT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     set.done(dev);
   }
@@ -501,6 +517,7 @@ cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   a.cumsum = p.cumsum;
   a.w = p.w;
   a.c = reinterpret_cast<__half*>(p.c);
+  a.c32 = p.c32;
   a.h_codes = p.h_codes;
   a.h_scales = reinterpret_cast<uint8_t*>(p.h_scales);
   a.status = p.status;
@@ -518,31 +535,29 @@ cudaError_t launch_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   attrs[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, mx_gmm_kernel<NT, SWIGLU, PAIR>, maps, a);
+  return cudaLaunchKernelEx(&cfg, mx_gmm_kernel<NT, OUT, PAIR>, maps, a);
 }
 
-// One thread per eight channels of a token: each row's 16 bytes, four rows read at a time, then
-// the sums in order of the routes.  Bound by reading c2: 8192 tokens x 4096, six rows each, 78 us
-// for 470 MB.  c2 is binary16, as the product's users get it, and rounded once: over the output's
-// own rounding (2.1e-4 of its norm) that makes 3.0e-4; in 32 bits the product would write and this
-// kernel read 800 MB more, some 120 us of the layer's 485.
+// One thread per four channels of a token: each row's 16 bytes, four rows read at a time, then
+// the sums in order of the routes, rounded once.  c2 is fp32: a route's row may lie far outside
+// binary16 where its weight brings it back, or another route's row cancels it.
 constexpr int kCombineThreads = 256;
-__global__ void __launch_bounds__(kCombineThreads, 6) mx_combine_kernel(const __half* c2, const int32_t* expanded,
+__global__ void __launch_bounds__(kCombineThreads, 6) mx_combine_kernel(const float* c2, const int32_t* expanded,
                                                                      const float* probs, int M, int K, int topK,
                                                                      __half* out) {
   // A programmatic dependent of the product, launched once that one is past its own wait: of what is
   // read here only c2 is written after this kernel's launch, and nothing reads c2 before the wait,
   // so the read-only path holds no older lines of it (plain reads: 6 us longer at prefill).
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int per = K / 8;
+  const int per = K / 4;
   const int64_t i = (int64_t)blockIdx.x * kCombineThreads + threadIdx.x;
   const int t = (int)(i / per), k = (int)(i - (int64_t)t * per);
   if (t >= M) return;
-  float acc[8] = {};
+  float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   const int32_t* rows = expanded + (int64_t)t * topK;
   const float* p = probs + (int64_t)t * topK;
   for (int j = 0; j < topK; j += 4) {
-    uint4 v[4];
+    float4 v[4];
     float w[4];
     bool in[4];
 #pragma unroll
@@ -550,47 +565,45 @@ __global__ void __launch_bounds__(kCombineThreads, 6) mx_combine_kernel(const __
       const int d = j + q < topK ? __ldg(rows + j + q) : -1;
       in[q] = d >= 0;
       if (in[q]) {
-        v[q] = __ldg(reinterpret_cast<const uint4*>(c2 + (size_t)d * K) + k);
+        v[q] = __ldg(reinterpret_cast<const float4*>(c2 + (size_t)d * K) + k);
         w[q] = __ldg(p + j + q);
       }
     }
 #pragma unroll
     for (int q = 0; q < 4; ++q)
       if (in[q]) {
-        const uint32_t u[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[z]));
-          acc[2 * z] = fmaf(w[q], f.x, acc[2 * z]);
-          acc[2 * z + 1] = fmaf(w[q], f.y, acc[2 * z + 1]);
-        }
+        acc.x = fmaf(w[q], v[q].x, acc.x);
+        acc.y = fmaf(w[q], v[q].y, acc.y);
+        acc.z = fmaf(w[q], v[q].z, acc.z);
+        acc.w = fmaf(w[q], v[q].w, acc.w);
       }
   }
-  alignas(16) __half2 h[4];
-#pragma unroll
-  for (int z = 0; z < 4; ++z) h[z] = f2h2_sat(acc[2 * z], acc[2 * z + 1]);
-  reinterpret_cast<uint4*>(out)[i] = *reinterpret_cast<const uint4*>(h);
+  const __half2 lo = f2h2_sat(acc.x, acc.y), hi = f2h2_sat(acc.z, acc.w);
+  reinterpret_cast<uint2*>(out)[i] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
 }
 
 }  // namespace
 
 cudaError_t launch_mx_gmm(const MxGemmProblem& p, cudaStream_t stream) {
   if ((double)p.R / p.E <= 32.0)
-    return p.h_codes ? launch_gmm<32, true, false>(p, stream) : launch_gmm<32, false, false>(p, stream);
-  return p.h_codes ? launch_gmm<192, true, true>(p, stream) : launch_gmm<192, false, true>(p, stream);
+    return p.h_codes ? launch_gmm<32, Out::kSwiglu, false>(p, stream)
+           : p.c32   ? launch_gmm<32, Out::kFloat, false>(p, stream)
+                     : launch_gmm<32, Out::kHalf, false>(p, stream);
+  return p.h_codes ? launch_gmm<192, Out::kSwiglu, true>(p, stream)
+         : p.c32   ? launch_gmm<192, Out::kFloat, true>(p, stream)
+                   : launch_gmm<192, Out::kHalf, true>(p, stream);
 }
 
-cudaError_t launch_mx_combine(const uint16_t* c2, const int32_t* expanded, const float* probs, int M, int K, int topK,
+cudaError_t launch_mx_combine(const float* c2, const int32_t* expanded, const float* probs, int M, int K, int topK,
                               uint16_t* out, cudaStream_t stream) {
-  const int64_t n = (int64_t)M * (K / 8);
+  const int64_t n = (int64_t)M * (K / 4);
   const unsigned blocks = (unsigned)((n + kCombineThreads - 1) / kCombineThreads);
-  const __half* rows = reinterpret_cast<const __half*>(c2);
   __half* o = reinterpret_cast<__half*>(out);
   // early where all blocks fit beside each other: at 128 tokens x 4096 119 us a layer for 121; 8192
   // tokens' 16384 blocks took 489 us a layer launched early, 480 in order
   if (blocks <= 8u * (unsigned)sm_count())
-    return launch_dependent(mx_combine_kernel, blocks, kCombineThreads, 0, stream, rows, expanded, probs, M, K, topK, o);
-  mx_combine_kernel<<<blocks, kCombineThreads, 0, stream>>>(rows, expanded, probs, M, K, topK, o);
+    return launch_dependent(mx_combine_kernel, blocks, kCombineThreads, 0, stream, c2, expanded, probs, M, K, topK, o);
+  mx_combine_kernel<<<blocks, kCombineThreads, 0, stream>>>(c2, expanded, probs, M, K, topK, o);
   return cudaGetLastError();
 }
 
