@@ -8,8 +8,9 @@
 // memory: for 128 elements of depth, the four scale bytes of row r as one 32-bit word in
 // lane r % 32, column r / 32, the same in all four 32-lane groups; an MMA uses the low or
 // the high half of the words, which its instruction descriptor selects.  In global memory
-// and as copied the words stand one row after the other; a warp puts the 512 bytes of 128
-// rows into the order of the lanes in place (mx_arrange_scales), and tcgen05.cp, issued
+// and as copied the words stand one row after the other.  The grouped product's warps load them
+// from shared memory and store them to tensor memory, each to its 32 lanes; the few-token layer's
+// put the 512 bytes of 128 rows into the order of the lanes in place, and tcgen05.cp, issued
 // before the MMAs that use them by the same thread, copies them on.
 #pragma once
 #include "mxfp4.cuh"
@@ -188,26 +189,24 @@ __device__ __forceinline__ void mx_put_scale_words(uint8_t* tile, uint4 w, int l
   reinterpret_cast<uint4*>(tile)[lane] = w;
 }
 
+// Eight tensor-memory columns of this warp's 32 lanes.
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, uint4 a, uint4 b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr), "r"(a.x), "r"(a.y),
+               "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
 // 512 bytes of arranged scale words -> four tensor-memory columns, in each of the four lane
-// groups (and, PAIR, in both CTAs from their own shared memory).
-template <bool PAIR>
+// groups.
 __device__ __forceinline__ void mx_copy_scales(uint32_t elected, uint32_t taddr, uint32_t saddr) {
   // unswizzled: groups of 8 rows of 16 bytes, 128 bytes apart
   const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-  if (PAIR)
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "setp.ne.u32 e, %2, 0;\n\t"
-        "@e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-        "l"(desc), "r"(elected)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred e;\n\t"
-        "setp.ne.u32 e, %2, 0;\n\t"
-        "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
-        "l"(desc), "r"(elected)
-        : "memory");
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.u32 e, %2, 0;\n\t"
+      "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+      "l"(desc), "r"(elected)
+      : "memory");
 }
 
 // Two MMAs: 128 elements of depth, `half` (0, 1) of a 256-deep stage.

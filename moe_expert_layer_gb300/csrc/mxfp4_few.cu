@@ -333,8 +333,8 @@ __device__ __forceinline__ bool issue_mmas(const FewArgs& a, const Pipe& pp, con
       const uint64_t da = sw128_desc(st), db = sw128_desc(st + kTokens);
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        mx_copy_scales<false>(elected, t_sf + 4 * q, st + kMxCodeBytes + 512 * q);
-        mx_copy_scales<false>(elected, t_sf + 8 + 4 * q, st + kTokenScales + 512 * q);
+        mx_copy_scales(elected, t_sf + 4 * q, st + kMxCodeBytes + 512 * q);
+        mx_copy_scales(elected, t_sf + 8 + 4 * q, st + kTokenScales + 512 * q);
       }
       mx_mma2<false>(elected, d, da, db, 0, idesc, t_sf, t_sf + 8, kb > s.kb0 ? 1u : 0u);
       if (kb < p.KB - 1 || last == 2) mx_mma2<false>(elected, d, da, db, 1, idesc, t_sf + 4, t_sf + 12, 1u);

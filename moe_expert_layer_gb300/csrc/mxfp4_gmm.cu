@@ -23,20 +23,22 @@
 //
 // Roles: warp 0 loads, per 256-deep stage, one 17408-byte copy of a weight block with its
 // scales and the rows' words of the two scale planes; warp 2 loads the rows' codes, in tensor
-// copies of 64, 32 and 16 rows; warps 4-7 in turn put a stage's scale words in tensor-memory
-// order (sharing each stage instead: 296 us for 264; through registers to tensor memory by two
-// warpgroups, or ahead of the codes in a ring of their own: no faster); warp 1 issues the copies
-// of the scales and the MMAs; warps 8-23 are four epilogue groups, two for each of the two
-// accumulators, taking its columns in turn.  Every wait is bounded: one that gives up records
-// MOE_ERR_TIMEOUT and the CTA winds down.
+// copies of 64, 32 and 16 rows; warps 4-11, two groups in turn, read a stage's scale words and store
+// them to tensor memory, each warp to its 32 lanes (one group: 328 us for 265); warp 1 issues the
+// MMAs; warps 12-27 are four epilogue groups, two for each of the two accumulators, taking its
+// columns in turn.  In a pair the first CTA's MMAs use what the second CTA's scale warps have
+// stored: tensor memory, which the tcgen05 fences order across the pair around the barrier.  (Put
+// in order in shared memory for tcgen05.cp to copy, the words would need release and acquire at
+// cluster scope: 337 us for 255 at 8192 tokens x 4096, N = 2816, 64 experts, six each.)  Every wait
+// is bounded: one that gives up records MOE_ERR_TIMEOUT and the CTA winds down.
 #include "mx_tc.cuh"
 #include "tensor_map.h"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 768;
-constexpr int kWeightWarp = 0, kMmaWarp = 1, kTokenWarp = 2, kScaleWarp0 = 4, kEpiWarp0 = 8;
+constexpr int kThreads = 896;
+constexpr int kWeightWarp = 0, kMmaWarp = 1, kTokenWarp = 2, kScaleWarp0 = 4, kScaleGroups = 2, kEpiWarp0 = 12;
 constexpr int kMaxExperts = 1024;
 constexpr int kEpiGroups = 4, kEpiBytes = 8192;  // an epilogue group's shared memory
 
@@ -51,9 +53,8 @@ struct Cfg {
   static constexpr int kStages = PAIR ? 6 : 8;
   static constexpr int kSfbPlane = 4 * kRowTiles;        // tensor-memory columns per 128 elements of depth
   static constexpr int kSfCols = 8 + 2 * kSfbPlane;      // and of a stage's scales
-  // Stages whose scales are in tensor memory.  Copies are executed before the MMAs that
-  // follow them, but not after the MMAs that precede them: a slot is written again only when
-  // the MMAs of the stage that used it have completed.
+  // Stages whose scales are in tensor memory.  A slot is written again only when the MMAs of the
+  // stage that used it have completed.
   static constexpr int kSfStages = 5;
   static constexpr int kSf0 = 2 * NT;                    // accumulators in columns [0, 2 NT)
   static constexpr int kTmemCols = (kSf0 + kSfStages * kSfCols) <= 128 ? 128 : (kSf0 + kSfStages * kSfCols) <= 256 ? 256 : 512;
@@ -178,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_init(&full_bar[s], 2);
           mbar_init(&empty_bar[s], 1);
         }
-        for (int s = 0; s < S; ++s) mbar_init(&sf_bar[s], PAIR ? 2 : 1);
+        for (int s = 0; s < S; ++s) mbar_init(&sf_bar[s], PAIR ? 8 : 4);
         for (int s = 0; s < 2; ++s) {
           mbar_init(&accfull_bar[s], 1);
           mbar_init(&accempty_bar[s], PAIR ? 16 : 8);
@@ -299,14 +300,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint32_t done = smem_u32(&empty_bar[at.slot]);
           at.next(S);
           there = mbar_test(&sf_bar[at.slot], at.phase);
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            mx_copy_scales<PAIR>(elected, t_sf + 4 * q, st + kMxCodeBytes + 512 * q);
-#pragma unroll
-            for (int h = 0; h < C::kRowTiles; ++h)
-              mx_copy_scales<PAIR>(elected, t_sf + 8 + C::kSfbPlane * q + 4 * h,
-                                   st + C::kScales + (C::kRowTiles * q + h) * 512);
-          }
           mx_mma2<PAIR>(elected, d, da, db, 0, idesc, t_sf, t_sf + 8, kb ? 1u : 0u);
           if (kb < KB - 1 || last == 2)
             mx_mma2<PAIR>(elected, d, da, db, 1, idesc, t_sf + 4, t_sf + 8 + C::kSfbPlane, 1u);
@@ -320,20 +313,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kScaleWarp0 && warp < kEpiWarp0) {
     // bytes of the last plane past D are no scales
     const uint32_t last_mask = a.D % 128 ? (1u << (a.D % 128 / 4)) - 1u : 0xffffffffu;
-    RingPos at, old;  // old: the stage kSfStages before
+    const int group = (warp - kScaleWarp0) >> 2;
+    const uint32_t t_sf = tmem + ((uint32_t)(warp & 3) << 21) + C::kSf0;
+    RingPos at, old, sf;  // old: the stage kSfStages before
     int n = 0;
     bool ok = true;
     for (int j = first; ok && j < total; j += stride) {
-      for (int kb = 0; kb < KB; ++kb, ++n, at.next(S)) {
+      for (int kb = 0; kb < KB; ++kb, ++n, at.next(S), sf.next(C::kSfStages)) {
         if (n > C::kSfStages) old.next(S);
-        if ((n & 3) != warp - kScaleWarp0) continue;
+        if (n % kScaleGroups != group) continue;
         // The scale columns are free once the MMAs of the stage that used them are done.  This wait
-        // comes first for another reason too: a warp that takes every fourth stage has not itself
+        // comes first for another reason too: a warp that takes every second stage has not itself
         // seen the slot's previous copies complete, and copies complete in any order; only after
         // that stage's MMAs is the barrier known to be in this use's phase.
         if (n >= C::kSfStages && !(ok = warp_wait(&empty_bar[old.slot], old.phase, abort_flag, a.status))) break;
         if (!(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status))) break;
-        uint8_t* st = ring_g + at.slot * C::kStageBytes;
+        tc_fence_after();
+        const uint8_t* st = ring_g + at.slot * C::kStageBytes;
         uint4 w[2 + 2 * C::kRowTiles];
 #pragma unroll
         for (int i = 0; i < 2 + 2 * C::kRowTiles; ++i) {
@@ -348,9 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 2 + 2 * C::kRowTiles; ++i)
-          mx_put_scale_words(i < 2 ? st + kMxCodeBytes + 512 * i : st + C::kScales + 512 * (i - 2), w[i], lane);
-        fence_proxy_async_smem();
+        for (int i = 0; i < 2 + 2 * C::kRowTiles; i += 2) tmem_st8(t_sf + sf.slot * C::kSfCols + 4 * i, w[i], w[i + 1]);
+        tmem_wait_st();
+        tc_fence_before();
         __syncwarp();
         if (lane == 0) {
           if (PAIR) mbar_arrive_remote(cluster_addr(&sf_bar[at.slot], 0)); else mbar_arrive(&sf_bar[at.slot]);

@@ -24,7 +24,8 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
 // Default semantics: an arrive with cluster-scope release costs ~320 cycles on
 // GB300, this one ~6; the data it publishes is tensor memory (ordered by
 // tcgen05.wait + tcgen05.fence) or TMA-written shared memory whose barrier the
-// signalling thread has already seen complete.
+// signalling thread has already seen complete.  What threads have stored themselves it does
+// not publish to the other CTA.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t caddr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
