@@ -181,6 +181,18 @@ int32_t moe_mxfp4_layer_fwd(const moe_dims_t* d, const uint16_t* x, const int32_
                             const uint8_t* w1, const uint8_t* w2, uint16_t* out, void* workspace,
                             size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------ */
+/* Diagnostics                                                               */
+/* ------------------------------------------------------------------------ */
+
+/*
+ * Exercises the wait of the few-token kernel's epilogue warps for their next unit of work, in a
+ * block that has given up: one warp looks before the unit is there, three after.  They have to
+ * answer alike, since they wait for one another afterwards: *answers (device int32 [4]) gets four
+ * times 0 (given up).  Asynchronous on `stream`.
+ */
+int32_t moe_selftest_mxfp4_tickets(int32_t* answers, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -34,7 +34,7 @@ EXPORTS = [
     "moe_weight_tiles_bytes", "moe_pack_weight_tiles",
     "moe_route_topk", "moe_mxfp4_scale_words", "moe_mxfp4_quant", "moe_mxfp4_dequant", "moe_mxfp4_weights_bytes",
     "moe_mxfp4_quant_weights", "moe_mxfp4_pack_weights", "moe_mxfp4_gmm_workspace_size", "moe_mxfp4_gmm",
-    "moe_mxfp4_gmm_swiglu", "moe_mxfp4_layer_workspace_size", "moe_mxfp4_layer_fwd",
+    "moe_mxfp4_gmm_swiglu", "moe_mxfp4_layer_workspace_size", "moe_mxfp4_layer_fwd", "moe_selftest_mxfp4_tickets",
 ]
 
 # weight layouts (moe_dims_t.weight_layout)
@@ -116,6 +116,7 @@ def load_library(path=None):
         "moe_mxfp4_gmm_swiglu": ([i32] * 4 + [vp] * 7 + [sz, vp], i32),
         "moe_mxfp4_layer_workspace_size": ([D], sz),
         "moe_mxfp4_layer_fwd": ([D] + [vp] * 7 + [sz, vp], i32),
+        "moe_selftest_mxfp4_tickets": ([vp, vp], i32),
     }
     for name, (args, res) in sigs.items():
         f = getattr(lib, name)
@@ -497,3 +498,8 @@ def moe_mxfp4_layer_fwd(d, x, expert_idx, probs, w1, w2, out, workspace, stream=
     _check("moe_mxfp4_layer_fwd", load_library().moe_mxfp4_layer_fwd(
         ctypes.byref(d), _p(x), _p(expert_idx), _p(probs), _p(w1), _p(w2), _p(out), _p(workspace),
         _nbytes(workspace), _stream(stream)))
+
+
+def moe_selftest_mxfp4_tickets(answers, stream=None):
+    """Runs the self-test of the few-token kernel's joint wait; answers: int32 device tensor [4]."""
+    _check("moe_selftest_mxfp4_tickets", load_library().moe_selftest_mxfp4_tickets(_sized(answers, 4, 4, "answers"), _stream(stream)))

@@ -79,6 +79,7 @@ size_t mx_few_part_bytes(int M, int topK);
 size_t mx_few_scale_bytes(int rows, int D);
 size_t mx_few_counter_bytes(int M, int K, int I, int topK);
 cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream);
+cudaError_t launch_mx_ticket_probe(int32_t* answers, cudaStream_t stream);
 
 // out[t] = sum over j of probs[t][j] * c2[expanded[t * topK + j]] (entries < 0 skipped)
 cudaError_t launch_mx_combine(const float* c2, const int32_t* expanded, const float* probs, int M, int K, int topK,

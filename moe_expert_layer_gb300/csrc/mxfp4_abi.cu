@@ -277,4 +277,12 @@ int32_t moe_mxfp4_layer_fwd(const moe_dims_t* d, const uint16_t* x, const int32_
   return run_layer(d, x, expert_idx, probs, w1, w2, out, workspace, L, static_cast<cudaStream_t>(stream));
 }
 
+int32_t moe_selftest_mxfp4_tickets(int32_t* answers, void* stream) {
+  if (!answers) return MOE_ERR_NULL;
+  if (!aligned16(answers)) return MOE_ERR_ALIGN;
+  int32_t rc;
+  if ((rc = check_device()) != MOE_OK) return rc;
+  return launch_status(moe::launch_mx_ticket_probe(answers, static_cast<cudaStream_t>(stream)));
+}
+
 }  // extern "C"

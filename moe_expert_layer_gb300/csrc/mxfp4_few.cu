@@ -282,6 +282,13 @@ __device__ __forceinline__ bool wait_unit(const Pipe& pp, int i, int& unit) {
   return true;
 }
 
+// The same by the four epilogue warps, who wait for one another below: none goes on, and none
+// gives up, alone (one that saw the CTA give up where the others still saw the unit would leave
+// them at their next barrier).
+__device__ __forceinline__ bool wait_unit_together(const Pipe& pp, int i, int& unit) {
+  return epi_all(wait_unit(pp, i, unit));
+}
+
 template <bool DOWN>
 __device__ __forceinline__ bool load_weights(const FewArgs& a, const Tables& t, const Pipe& pp, const Product<DOWN>& p,
                                              uint32_t elected, int lane, RingPos& at) {
@@ -479,7 +486,8 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
   const size_t part_rows = min(kRows, a.R);
   Walk<false> walk(p);
   Seg s;
-  while (walk.next(s, pp)) {
+  auto unit_of = [&](int i, int& unit) { return wait_unit_together(pp, i, unit); };
+  while (walk.next(s, unit_of)) {
     const int row0 = t.tile_row[s.tile] & 0xffff, rows = t.tile_row[s.tile] >> 16;
     const int block = s.tile * p.NB + s.nb, run = blockIdx.x;
     int c0 = run, c1 = run;
@@ -784,7 +792,44 @@ __global__ void __launch_bounds__(kXThreads) mx_few_x_kernel(const __half* x, in
   }
 }
 
+// Four epilogue warps of a CTA that has given up ask for a ticket that arrives between the first
+// warp's look at it and the others'.
+__global__ void ticket_probe_kernel(int32_t* answers) {
+  __shared__ __align__(8) uint64_t unit_bar[kUnits], asked;
+  __shared__ int s_unit[kUnits], s_abort;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    mbar_init(unit_bar, 1);
+    mbar_init(&asked, 1);
+    fence_barrier_init();
+    s_abort = 1;
+  }
+  __syncthreads();
+  if (warp == 4) {
+    if (lane == 0) {
+      for (const uint64_t t0 = globaltimer_ns(); globaltimer_ns() - t0 < 1000000;) __nanosleep(1000);
+      s_unit[0] = 0;
+      mbar_arrive(unit_bar);
+      mbar_arrive(&asked);
+    }
+    return;
+  }
+  Pipe pp = {};
+  pp.unit_bar = unit_bar;
+  pp.unit = s_unit;
+  pp.abort_flag = &s_abort;
+  if (warp) mbar_wait_bounded(&asked, 0);
+  int unit = -1;
+  const bool ok = wait_unit_together(pp, 1, unit);
+  if (lane == 0) answers[warp] = ok;
+}
+
 }  // namespace
+
+cudaError_t launch_mx_ticket_probe(int32_t* answers, cudaStream_t stream) {
+  ticket_probe_kernel<<<1, 160, 0, stream>>>(answers);
+  return cudaGetLastError();
+}
 
 size_t mx_few_part_bytes(int M, int topK) {
   return (part_words_of_h(sm_count(), M * topK) + (size_t)sm_count() * 2 * M * 128) * 4;
