@@ -173,9 +173,9 @@ size_t moe_mxfp4_layer_workspace_size(const moe_dims_t* d);
  *   workspace >= moe_mxfp4_layer_workspace_size(d) bytes; its first word is the status word
  *              that moe_workspace_status reads.  Its contents on entry do not matter.
  * Up to 32 tokens and 256 routes (at sizes that fit the device) one kernel does most of
- * it, whose blocks wait for one another: calls in flight on streams of different
- * priorities can keep each other's blocks off the device until the wait's limit, about
- * two seconds, and then report MOE_ERR_TIMEOUT in the status word.
+ * it, whose blocks wait for one another.  It is launched cooperatively, so it starts when
+ * all of its blocks, one on every SM, can run beside what else is on the device.  On a stream
+ * that may use fewer SMs than the device has, these calls take the path of the larger ones.
  */
 int32_t moe_mxfp4_layer_fwd(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_idx, const float* probs,
                             const uint8_t* w1, const uint8_t* w2, uint16_t* out, void* workspace,

@@ -78,6 +78,7 @@ struct MxFewProblem {
 size_t mx_few_part_bytes(int M, int topK);
 size_t mx_few_scale_bytes(int rows, int D);
 size_t mx_few_counter_bytes(int M, int K, int I, int topK);
+// cudaErrorCooperativeLaunchTooLarge where the stream may use fewer SMs than the device has.
 cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream);
 cudaError_t launch_mx_ticket_probe(int32_t* answers, cudaStream_t stream);
 

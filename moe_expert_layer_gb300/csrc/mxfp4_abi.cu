@@ -97,7 +97,9 @@ int32_t run_layer(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_
     p.counters = at<int32_t>(ws, L.counters);
     p.out = out;
     p.status = at<int32_t>(ws, L.status);
-    return launch_status(moe::launch_mx_few(p, st));
+    e = moe::launch_mx_few(p, st);
+    if (e != cudaErrorCooperativeLaunchTooLarge) return launch_status(e);
+    cudaGetLastError();  // not an error of this call, which goes on with the other path
   }
   int32_t* expanded = at<int32_t>(ws, L.expanded);
   int32_t* cumsum = at<int32_t>(ws, L.cumsum);

@@ -6,9 +6,9 @@
 // streaming past (17408 bytes per 128 channels x 256 reduction steps), so everything else is
 // done beside that stream: each CTA makes the routes' tables itself, and no row is
 // dispatched or permuted in memory.
-// Measured, depth 7168, 2048 channels: one token, 8 of 256 experts, 40 us, where its 187 MB take
-// 28 at the measured copy rate; 8 tokens on 16 experts 63 us (55); depth 4096, 1408 channels: 29
-// tokens on 64 experts 92 us (82).  The rest is the start, the wait between the two products
+// Measured, depth 7168, 2048 channels: one token, 8 of 256 experts, 43 us, where its 187 MB take
+// 28 at the measured copy rate; 8 tokens on 16 experts 67 us (55); depth 4096, 1408 channels: 29
+// tokens on 64 experts 95 us (82).  The rest is the start, the wait between the two products
 // for the last sums of h (its 6 stages in flight cover half of it) and the meeting at the end.
 //
 // Kernel 2 is persistent, one CTA per SM, with one pipeline for both products, so that the
@@ -31,9 +31,10 @@
 //     run per CTA, whose sums add up in shared memory over experts and stages alike and meet the
 //     same way.  A run that goes over the end of a block takes the block it ends in first: the
 //     tiles whose h is made last come last, and nothing waits for most of h.
-// Each kernel is launched as a programmatic dependent of the one before: tables and first weights
-// come while kernel 1 still runs.  A CTA waits for others' h, so all of them have to be resident: one per SM,
-// which the host checks fit.  Every wait is bounded, as in the grouped product.
+// A CTA of kernel 2 waits for others' h, so all of them have to be resident, one per SM: its launch
+// is cooperative, which sees to it whatever else runs, and is refused where the stream has fewer
+// SMs than the device.  It cannot be a programmatic dependent too (the attribute then changes
+// nothing), which costs 3.4 us a call.  Every wait is bounded, as in the grouped product.
 #include "mx_tc.cuh"
 #include "tensor_map.h"
 
@@ -313,7 +314,6 @@ __device__ __forceinline__ bool load_weights(const FewArgs& a, const Tables& t, 
       expect_tx_elect(elected, bar, kMxBlockBytes);
       bulk_load_elect(elected, pp.ring + at.slot * kStageBytes, wb + (size_t)kb * kMxBlockBytes, kMxBlockBytes, bar);
       if (p.tickets && kb == s.kb0) {
-        if (walk.i == 1) asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1 clears the tickets
         if (lane == 0) ticket = atomicAdd(a.counters + ticket_at(a), 1);
       }
     }
@@ -721,8 +721,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_consta
     mx_commit<false>(elected, smem_u32(&final_bar));  // every MMA done before tensor memory is freed
     mbar_wait_sleep_bounded(&final_bar, 0);
   } else if (warp == kTokenWarp) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // kernel 1's x and counters
-    fence_proxy_async_global();
     const uint32_t elected = elect_one();
     RingPos at;
     if (load_tokens<false>(a, maps, s_t, pp, up, elected, lane, at))
@@ -731,7 +729,6 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_consta
     int n = 0;
     if (arrange_scales<false>(pp, up, warp - kScaleWarp0, lane, n)) arrange_scales<true>(pp, down, warp - kScaleWarp0, lane, n);
   } else if (warp >= kEpiWarp0) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     int u = 0;
     float* shared = reinterpret_cast<float*>(scratch);
     if (finish_h(a, s_t, pp, up, shared, warp & 3, lane, u, &s_last)) {
@@ -758,9 +755,7 @@ __global__ void __launch_bounds__(kThreads, 1) mx_few_kernel(const __grid_consta
 constexpr int kXThreads = 256;
 __global__ void __launch_bounds__(kXThreads) mx_few_x_kernel(const __half* x, int M, int K, uint8_t* codes, uint8_t* scales,
                                                              int32_t* counters, int n_counters, int32_t* status) {
-  // Only behind the wait may kernel 2 start: it reads routes and weights before it waits itself.
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // a programmatic dependent of the kernel before
   const int i = blockIdx.x * kXThreads + threadIdx.x;
   for (int c = i; c < n_counters; c += gridDim.x * kXThreads) counters[c] = 0;
   if (i == 0) *status = 0;
@@ -845,7 +840,7 @@ bool mx_few_resident() {
   const int dev = current_device();
   if (queried.needed(dev)) {
     int n = 0;
-    // kernel 1 with the same division of L1 as kernel 2, which can then begin beside it
+    // kernel 1 with the same division of L1 as kernel 2, which then need not wait for a change
     ok[dev] = cudaFuncSetAttribute(mx_few_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                    smem_bytes(kMxFewTokens)) == cudaSuccess &&
               cudaFuncSetAttribute(mx_few_kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
@@ -892,7 +887,17 @@ cudaError_t launch_mx_few(const MxFewProblem& p, cudaStream_t stream) {
   a.counters = p.counters;
   a.out = reinterpret_cast<__half*>(p.out);
   a.status = p.status;
-  return launch_dependent(mx_few_kernel, (unsigned)sm_count(), kThreads, smem_bytes(p.M), stream, maps, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)sm_count());
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem_bytes(p.M);
+  cfg.stream = stream;
+  cudaLaunchAttribute together;
+  together.id = cudaLaunchAttributeCooperative;
+  together.val.cooperative = 1;
+  cfg.attrs = &together;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, mx_few_kernel, maps, a);
 }
 
 }  // namespace moe
