@@ -377,6 +377,8 @@ __device__ __forceinline__ bool load_tokens(const FewArgs& a, const FewMaps& map
         *pp.abort_flag = 1;
         return false;
       }
+      // what lane 0 has acquired, for the lane that issues the copies too: a vote orders no memory
+      __syncwarp();
       fence_proxy_async_global();
       seen = s.tile;
     }

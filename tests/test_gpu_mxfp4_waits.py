@@ -119,3 +119,29 @@ def test_few_token_layer_with_part_of_the_device(narrow_stream):
     over = np.abs(ref) + bound > 65504
     assert over.mean() < 0.5
     assert (np.abs(host(out).astype(np.float64) - ref) <= bound)[~over].all()
+
+
+@pytest.mark.parametrize("M,K,I,E,topK", [(1, 2048, 1024, 16, 8), (8, 1024, 1024, 16, 4), (32, 512, 704, 8, 4)])
+def test_h_is_that_of_the_call(M, K, I, E, topK):
+    """The down product's rows come from other blocks of the kernel, through the workspace: with other
+    tokens and routes in every call, a row read before its block had written it is that of a call before."""
+    rng = np.random.default_rng(M + I)
+    w1, _ = make_weights(rng, E, 2 * I, K, True)
+    w2, _ = make_weights(rng, E, K, I, False)
+    d = moe.dims(M, K, I, E, topK)
+    ws = empty(moe.moe_mxfp4_layer_workspace_size(d), torch.uint8)
+    sets = [layer_inputs(rng, M, K, E, topK) for _ in range(16)]
+
+    def layer(x, ei, probs, workspace):
+        out = empty((M, K), torch.float16)
+        moe.moe_mxfp4_layer_fwd(d, x, ei, probs, w1, w2, out, workspace)
+        return out
+
+    alone = []
+    for s in sets:
+        alone.append(layer(*s, torch.full_like(ws, 0xEE)))
+        torch.cuda.synchronize()
+    for _ in range(10):
+        outs = [layer(*s, ws) for s in sets]
+        assert all(torch.equal(a, b) for a, b in zip(alone, outs))
+    assert moe.moe_workspace_status(ws) == 0
