@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
     import moe_expert_layer_gb300 as moe
     from gpu_util import dev, host
-    from test_gpu_mxfp4 import layer_case, run_layer
+    from test_gpu_mxfp4 import layer_case, make_weights, run_layer
 
 
 def routes64(x, ei, w1, w2):
@@ -82,3 +82,33 @@ def test_output_is_rounded_once(M, K, I, E, topK):
     over = np.abs(ref) + bound > 65504
     assert over.mean() < 0.5 and moe.moe_workspace_status(ws) == 0
     assert (np.abs(host(out).astype(np.float64) - ref) <= bound)[~over].all()
+
+
+@pytest.mark.parametrize("M", [880, 960])
+def test_combine_reads_the_rows_of_its_call(M):
+    """On both sides of the batch up to which the weighted sum is launched beside the product whose rows
+    it reads (912 blocks on 152 SMs, one per token here): with other tokens and routes in every call,
+    a line read early is that of a call before."""
+    K, I, E, topK = 1024, 64, 8, 2
+    rng = np.random.default_rng(M)
+    w1, _ = make_weights(rng, E, 2 * I, K, True)
+    w2, _ = make_weights(rng, E, K, I, False)
+    d = moe.dims(M, K, I, E, topK)
+    ws = torch.full((moe.moe_mxfp4_layer_workspace_size(d),), 0xEE, dtype=torch.uint8, device="cuda")
+    sets = [(torch.randn(M, K, device="cuda").half() / 64,
+             torch.rand(M, E, device="cuda").topk(topK, 1).indices.int().contiguous(), torch.rand(M, topK, device="cuda"))
+            for _ in range(8)]
+
+    def layer(x, ei, probs):
+        out = torch.empty((M, K), dtype=torch.float16, device="cuda")
+        moe.moe_mxfp4_layer_fwd(d, x, ei, probs, w1, w2, out, ws)
+        return out
+
+    alone = []
+    for s in sets:
+        alone.append(layer(*s))
+        torch.cuda.synchronize()
+    for _ in range(10):
+        outs = [layer(*s) for s in sets]
+        assert all(torch.equal(a, b) for a, b in zip(alone, outs))
+    assert moe.moe_workspace_status(ws) == 0
