@@ -31,9 +31,8 @@ class Mxfp4Experts:
         self.w2 = torch.empty(moe.moe_mxfp4_weights_bytes(self.E, self.K, self.I), dtype=torch.uint8, device=dev)
         moe.moe_mxfp4_quant_weights(w1, self.w1, gate_up=True)
         moe.moe_mxfp4_quant_weights(w2, self.w2)
-        # a few tokens take another path, which can need more than some larger batches
-        sizes = [moe.moe_mxfp4_layer_workspace_size(self.dims(m)) for m in [*range(1, min(64, max_tokens)), max_tokens]]
-        self.workspace = torch.empty(max(sizes), dtype=torch.uint8, device=dev)
+        size = moe.moe_mxfp4_layer_workspace_size(self.dims(max_tokens))  # enough for fewer tokens too
+        self.workspace = torch.empty(size, dtype=torch.uint8, device=dev)
         self.expert_idx = torch.empty(max_tokens, topk, dtype=torch.int32, device=dev)
         self.probs = torch.empty(max_tokens, topk, dtype=torch.float32, device=dev)
 

@@ -160,7 +160,8 @@ int32_t moe_mxfp4_gmm_swiglu(int32_t R, int32_t E, int32_t I, int32_t D, const u
 /* Whole layer                                                               */
 /* ------------------------------------------------------------------------ */
 
-/* Bytes of workspace of moe_mxfp4_layer_fwd (0 if the dimensions are invalid). */
+/* Bytes of workspace of moe_mxfp4_layer_fwd with up to d->M tokens, the other dimensions as they
+ * are (0 if the dimensions are invalid). */
 size_t moe_mxfp4_layer_workspace_size(const moe_dims_t* d);
 
 /*
@@ -170,8 +171,9 @@ size_t moe_mxfp4_layer_workspace_size(const moe_dims_t* d);
  * weighted and added in fp32 too, and out is rounded to binary16 once.
  *   x, expert_idx, probs, out: as moe_layer_fwd (d->weight_layout is not read)
  *   w1  blocks of [E][2I][K] in gate_up order;  w2  blocks of [E][K][I], plain order
- *   workspace >= moe_mxfp4_layer_workspace_size(d) bytes; its first word is the status word
- *              that moe_workspace_status reads.  Its contents on entry do not matter.
+ *   workspace >= moe_mxfp4_layer_workspace_size of these dimensions, or of a larger M; its
+ *              first word is the status word that moe_workspace_status reads.  Its contents on
+ *              entry do not matter.
  * Up to 32 tokens and 256 routes (at sizes that fit the device) one kernel does most of
  * it, whose blocks wait for one another.  It is launched cooperatively, so it starts when
  * all of its blocks, one on every SM, can run beside what else is on the device.  On a stream

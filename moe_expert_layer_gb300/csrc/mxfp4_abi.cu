@@ -263,7 +263,13 @@ int32_t moe_mxfp4_gmm_swiglu(int32_t R, int32_t E, int32_t I, int32_t D, const u
 }
 
 size_t moe_mxfp4_layer_workspace_size(const moe_dims_t* d) {
-  return check_shape(d) == MOE_OK ? layout_of(d).total : 0;
+  if (check_shape(d) != MOE_OK) return 0;
+  // the few-token path asks for more than some larger batches do, and a workspace of d serves fewer tokens too
+  moe_dims_t few = *d;
+  if (few.M > moe::kMxFewTokens) few.M = moe::kMxFewTokens;
+  while (few.M > 1 && !moe::mx_few(few.M, few.K, few.I, few.topK)) --few.M;
+  const size_t own = layout_of(d).total, fewer = layout_of(&few).total;
+  return own > fewer ? own : fewer;
 }
 
 int32_t moe_mxfp4_layer_fwd(const moe_dims_t* d, const uint16_t* x, const int32_t* expert_idx, const float* probs,
