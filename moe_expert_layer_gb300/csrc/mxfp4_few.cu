@@ -545,12 +545,14 @@ __device__ __forceinline__ bool finish_h(const FewArgs& a, const Tables& t, cons
 #pragma unroll
     for (int i = 0; i < 8; ++i) give[i * 32] = __uint_as_float(odd ? v[i] : v[8 + i]);
     epi_sync();
-    float h[8];
+    float gate[8], up[8], h[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float o = take[i * 32];
-      h[i] = odd ? mx_swiglu(o, __uint_as_float(v[8 + i])) : mx_swiglu(__uint_as_float(v[i]), o);
+      gate[i] = odd ? o : __uint_as_float(v[i]);
+      up[i] = odd ? __uint_as_float(v[8 + i]) : o;
     }
+    mx_swiglu8(gate, up, h);
     uint32_t byte;
     const uint32_t w = mx_quant_rows8(h, lane, byte);
     const int c = odd * 8 + (lane & 7);

@@ -440,8 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 16; ++i) x[i * 64 + (th ^ ((i & 1) << 2))] = __uint_as_float(v[i]);
           asm volatile("bar.sync %0, 64;" ::"r"(1 + pair) : "memory");
           const float4 g0 = gate[0], g1 = gate2[0], u0 = gate[8], u1 = gate2[8];  // up: 32 floats on
-          float h[8] = {mx_swiglu(g0.x, u0.x), mx_swiglu(g0.y, u0.y), mx_swiglu(g0.z, u0.z), mx_swiglu(g0.w, u0.w),
-                        mx_swiglu(g1.x, u1.x), mx_swiglu(g1.y, u1.y), mx_swiglu(g1.z, u1.z), mx_swiglu(g1.w, u1.w)};
+          const float g[8] = {g0.x, g0.y, g0.z, g0.w, g1.x, g1.y, g1.z, g1.w};
+          const float u[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+          float h[8];
+          mx_swiglu8(g, u, h);
           uint32_t byte;
           const uint32_t w = mx_quant_group8(h, byte);
           const int r = c0 + row;

@@ -42,3 +42,41 @@ def test_pair_uses_both_halves_scale_words(counts, N, D):
         want = 32 * torch.bmm((1 << sa).double()[:, None], (1 << sw).double()[expert].transpose(1, 2))[:, 0]
         wrong += (c.double() != want).sum()
     assert wrong.item() == 0 and moe.moe_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("rows", [1, 9, 40])
+def test_swiglu_of_very_negative_gates(rows):
+    """h = g / (1 + exp(-g)) u where exp(-g) is near fp32's end and past it, but h, with u large, is far
+    from MXFP4's: gates from -70 to -165, one to a scaled block, whose sums are exact (whole numbers)."""
+    rng = np.random.default_rng(rows)
+    gates = np.array([-70, -79, -80, -81, -86, -87, -88, -89, -90, -95, -103, -104, -120, -140, -160, -165], np.float64)
+    I, D = 32 * len(gates), 32
+    code, scale = np.zeros((1, 2 * I, D), np.uint8), np.full((1, 2 * I, 1), 127, np.uint8)
+    for b, g in enumerate(gates):  # -6 as often as it fits, and the rest
+        sixes, rest = divmod(int(-g), 6)
+        code[0, 32 * b:32 * b + 32, :sixes] = 15
+        code[0, 32 * b:32 * b + 32, sixes] = 8 + [0, 2, 4, 5, 6, 7][rest] if rest < 5 else 14
+        if rest == 5:
+            code[0, 32 * b:32 * b + 32, sixes + 1] = 10
+    code[0, I:, 0] = rng.integers(1, 16, I)
+    code[0, I:, 0][code[0, I:, 0] == 8] = 3
+    scale[0, I:] = 127 + 110  # u: up to 6 2^110
+    wv = mx.values(code, scale)
+    g, u = wv[0, :I].sum(-1)[None].repeat(rows, 0), wv[0, I:].sum(-1)[None].repeat(rows, 0)
+    assert np.array_equal(g[0, ::32], gates)
+    w = empty((moe.moe_mxfp4_weights_bytes(1, 2 * I, D),), torch.uint8)
+    moe.moe_mxfp4_pack_weights(dev(mx.pack(code)), dev(scale), w, True)
+    a = np.full((rows, D), 2, np.uint8)  # ones
+    words = dev(mx.scale_planes(np.full((rows, 1), 127, np.uint8)).view(np.int32))
+    hc = empty((rows, I // 2), torch.uint8)
+    hs = empty((moe.moe_mxfp4_scale_words(rows, I),), torch.int32)
+    ws = empty(moe.moe_mxfp4_gmm_workspace_size(rows, 1, 2 * I, D), torch.uint8)
+    moe.moe_mxfp4_gmm_swiglu(dev(mx.pack(a)), words, dev(np.array([rows], np.int32)), w, hc, hs, ws)
+    h, eh = mx.silu_mul(g, u, np.zeros_like(g), np.zeros_like(u))
+    least, most, s0, s1 = mx.quantise_interval(h, eh)
+    assert s0.min() > 0
+    planes = host(hs).view(np.uint32).reshape((I + 127) // 128, -1)
+    s = np.ascontiguousarray(planes[:, :rows].T).view(np.uint8).reshape(rows, -1)[:, :I // 32]
+    v = np.abs(mx.values(np.stack([host(hc) & 15, host(hc) >> 4], -1).reshape(rows, I), s))
+    assert (s >= s0).all() and (s <= s1).all()
+    assert (v >= least).all() and (v <= most).all()
