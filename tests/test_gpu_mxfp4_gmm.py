@@ -10,6 +10,7 @@ pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     import moe_expert_layer_gb300 as moe
+    import test_gpu_mxfp4 as base
     from gpu_util import dev, empty, host
     from test_gpu_mxfp4 import make_rows, make_weights
 
@@ -80,3 +81,58 @@ def test_swiglu_of_very_negative_gates(rows):
     v = np.abs(mx.values(np.stack([host(hc) & 15, host(hc) >> 4], -1).reshape(rows, I), s))
     assert (s >= s0).all() and (s <= s1).all()
     assert (v >= least).all() and (v <= most).all()
+
+
+# experts of more than 32 rows where the average is less: single CTAs with several tiles for an expert,
+# of sizes around the tile's, behind experts that end on any row
+SKEWED = [([100, 0, 1, 3, 0, 0, 37, 5], 256, 288), ([100, 0, 1, 3, 0, 0, 37, 5], 384, 64), ([33, 0, 31], 128, 160),
+          ([1, 64, 0, 0, 0], 128, 512), ([2, 65, 3, 0, 0, 0], 640, 256), ([200] + [0] * 9 + [1], 256, 1408),
+          ([3, 97, 0, 0, 96, 5, 0, 34, 2, 0], 256, 224)]
+
+
+@pytest.mark.parametrize("counts,N,D", SKEWED)
+def test_gmm_of_skewed_experts(counts, N, D):
+    assert (sum(counts) + 5) / len(counts) <= 32 < max(counts)
+    base.test_gmm(counts, N, D)
+
+
+@pytest.mark.parametrize("counts,N,D", SKEWED)
+def test_gmm_swiglu_of_skewed_experts(counts, N, D):
+    assert (sum(counts) + 3) / len(counts) <= 32 < max(counts)
+    base.test_gmm_swiglu(counts, N // 2, D)
+
+
+@pytest.mark.parametrize("counts", [[64, 65, 66], [192, 1, 193, 383], [31, 193, 0, 0, 200], [385, 0, 7]])
+@pytest.mark.parametrize("N,D", [(128, 96), (384, 320)])
+def test_gmm_of_pairs_around_their_tiles(counts, N, D):
+    assert sum(counts) / len(counts) > 32
+    base.test_gmm(counts, N, D)
+    base.test_gmm_swiglu(counts, N // 2, D)
+
+
+@pytest.mark.parametrize("R,E", [(20, 2), (200, 2), (500, 3)])
+def test_nan_rows_and_channels_stay_alone(R, E):
+    """A NaN block of a row makes the row's sums NaN, one of a channel the channel's, on single CTAs and on
+    pairs; prefix entries outside 0 .. R are held there."""
+    rng = np.random.default_rng(R)
+    N, D = 256, 384
+    codes, scales, a = make_rows(rng, R, D)
+    bad_row = R - 9
+    planes = host(scales).copy()
+    planes.view(np.uint8).reshape(D // 128, -1, 4)[1, bad_row, 2] = 255
+    code = rng.integers(0, 16, (E, N, D), dtype=np.uint8)
+    scale = rng.integers(115, 128, (E, N, D // 32)).astype(np.uint8)
+    scale[E - 1, 77, 5] = 255
+    w = empty((moe.moe_mxfp4_weights_bytes(E, N, D),), torch.uint8)
+    moe.moe_mxfp4_pack_weights(dev(mx.pack(code)), dev(scale), w)
+    wv = mx.values(code, scale)[E - 1]
+    cum = np.array([-5, 1 << 30] if E == 2 else [-1, -7, 1 << 30], np.int32)
+    c = torch.full((R, N), 7.0, dtype=torch.float16, device="cuda")
+    ws = empty(moe.moe_mxfp4_gmm_workspace_size(R, E, N, D), torch.uint8)
+    moe.moe_mxfp4_gmm(codes, dev(planes), dev(cum), w, c, ws)
+    assert moe.moe_workspace_status(ws) == 0
+    got, n = host(c).astype(np.float64), np.arange(N) != 77
+    assert np.isnan(got[bad_row]).all() and np.isnan(got[:, 77]).all() and np.isnan(got).sum() == R + N - 1
+    keep = np.arange(R) != bad_row
+    ref, err = a[keep] @ wv[n].T, mx.sum_error(a[keep], wv[n])
+    assert (np.abs(got[keep][:, n] - ref.clip(-65504, 65504)) <= err + mx.f16_error(np.abs(ref) + err)).all()

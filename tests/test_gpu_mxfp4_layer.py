@@ -10,7 +10,8 @@ pytestmark = pytest.mark.gpu
 
 if torch.cuda.is_available():
     import moe_expert_layer_gb300 as moe
-    from gpu_util import dev, host
+    import test_gpu_mxfp4 as base
+    from gpu_util import dev, empty, host
     from test_gpu_mxfp4 import layer_case, make_weights, run_layer
 
 
@@ -112,3 +113,48 @@ def test_combine_reads_the_rows_of_its_call(M):
         outs = [layer(*s) for s in sets]
         assert all(torch.equal(a, b) for a, b in zip(alone, outs))
     assert moe.moe_workspace_status(ws) == 0
+
+
+@pytest.mark.parametrize("M,K,I,E,topK", [(128, 128, 64, 64, 6), (40, 256, 128, 16, 2), (200, 128, 192, 33, 3)])
+@pytest.mark.parametrize("skew", [False, True])
+def test_layer_of_many_tokens_on_many_experts(M, K, I, E, topK, skew):
+    """Past the few-token path with up to 32 rows per expert on average; skewed: half of the tokens on one
+    set of experts, which then have more."""
+    x, ei, probs, w1, v1, w2, v2 = layer_case(M, K, I, E, topK, M + E)
+    if skew:
+        ei[::2] = np.arange(topK)
+    x = (x * np.float16(2.0 ** -6)).astype(np.float16)
+    y, err = routes64(mx.values(*mx.quantise(x.astype(np.float64))), ei, v1, v2)
+    ref, bound = weighted(y, err, probs)
+    assert M * topK / E <= 32 and (not skew or np.bincount(ei[(ei >= 0) & (ei < E)]).max() >= M // 2)
+    out, ws = run_layer(dev(x), dev(ei), dev(probs), w1, w2, I, E)
+    over = np.abs(ref) + bound > 65504
+    assert over.mean() < 0.5 and moe.moe_workspace_status(ws) == 0
+    assert (np.abs(host(out).astype(np.float64) - ref) <= bound)[~over].all()
+
+
+def signed(codes, D):
+    """Values of packed codes [..][D / 2], their signs with them."""
+    c = host(codes)
+    return mx.E2M1[np.stack([c & 15, c >> 4], -1).reshape(c.shape[:-1] + (D,))]
+
+
+@pytest.mark.parametrize("kind", ["f32", "f16", "bf16"])
+def test_signs_of_dispatched_rows_and_weights(kind):
+    rng = np.random.default_rng(14)
+    M, D, copies = 53, 160, 2
+    x, v = base.typed(base.awkward(rng, M, D), kind)
+    place = rng.permutation(M * copies).astype(np.int32)
+    codes, _ = base.quant_device(x, M * copies, dev(place), copies)
+    want = mx.E2M1[mx.quantise(v)[0]]
+    assert np.array_equal(signed(codes, D)[place], want.repeat(copies, 0))
+    for gate_up in (False, True):
+        E, N, D = 2, 256, 288
+        w, v = base.typed(base.awkward(rng, E * N, D).reshape(E, N, D), kind)
+        c, s = mx.quantise(v)
+        out = empty((moe.moe_mxfp4_weights_bytes(E, N, D),), torch.uint8)
+        moe.moe_mxfp4_quant_weights(w, out, gate_up)
+        got, ref = host(out).reshape(-1, 17408), mx.blocks(c, s, gate_up).reshape(-1, 17408)
+        assert np.array_equal(got[:, 16384:], ref[:, 16384:])
+        assert np.array_equal(mx.E2M1[got[:, :16384] & 15], mx.E2M1[ref[:, :16384] & 15])
+        assert np.array_equal(mx.E2M1[got[:, :16384] >> 4], mx.E2M1[ref[:, :16384] >> 4])
