@@ -403,21 +403,31 @@ def _sized(t, n, size, what):
     return _p(t)
 
 
-# Element types that an array of a kind may have: binary16 also as its bits.
-_KINDS = {"binary16": ("torch.float16", "torch.int16", "torch.uint16"), "int32": ("torch.int32", "torch.uint32"),
-          "float32": ("torch.float32",)}
-_kinds = {}  # (torch.dtype, kind) -> whether it may
+class _Kind(set):
+    """Element types that an array of a kind may have: given by name, filled as they come (torch.dtype)."""
+
+    def __init__(self, name, *types):
+        super().__init__()
+        self.name, self.types = name, types
+
+    def takes(self, dtype):
+        if str(dtype) in self.types:
+            self.add(dtype)
+            return True
+        return False
+
+
+_BINARY16 = _Kind("binary16", "torch.float16", "torch.int16", "torch.uint16")  # also as its bits
+_INT32 = _Kind("int32", "torch.int32", "torch.uint32")
+_FLOAT32 = _Kind("float32", "torch.float32")
 
 
 def _typed(t, n, kind, what):
     """Pointer of a dense array that has to hold n elements of a kind; raw pointers and None go on as they are."""
     if t is None or isinstance(t, int):
         return t
-    ok = _kinds.get((t.dtype, kind))
-    if ok is None:
-        ok = _kinds[t.dtype, kind] = str(t.dtype) in _KINDS[kind]
-    if not ok or t.numel() < n:
-        raise ValueError("%s: %d elements of %s wanted; got %d of %s" % (what, n, kind, t.numel(), t.dtype))
+    if t.numel() < n or (t.dtype not in kind and not kind.takes(t.dtype)):
+        raise ValueError("%s: %d elements of %s wanted; got %d of %s" % (what, n, kind.name, t.numel(), t.dtype))
     return _p(t)
 
 
@@ -441,9 +451,9 @@ def moe_route_topk(logits, expert_idx, probs, bias=None, scoring=SCORE_SOFTMAX, 
     topK = expert_idx.shape[1]
     p, stride = _rows(logits)
     _check("moe_route_topk", load_library().moe_route_topk(
-        M, E, topK, p, _type(logits), stride, None if bias is None else _typed(bias, E, "float32", "bias"),
-        scoring, 1 if renormalise else 0, scale, _typed(expert_idx, M * topK, "int32", "expert_idx"),
-        _typed(probs, M * topK, "float32", "probs"), _stream(stream)))
+        M, E, topK, p, _type(logits), stride, None if bias is None else _typed(bias, E, _FLOAT32, "bias"),
+        scoring, 1 if renormalise else 0, scale, _typed(expert_idx, M * topK, _INT32, "expert_idx"),
+        _typed(probs, M * topK, _FLOAT32, "probs"), _stream(stream)))
 
 
 def moe_mxfp4_scale_words(rows, D):
@@ -460,7 +470,7 @@ def moe_mxfp4_quant(x, codes, scales, row_map=None, copies=1, stream=None):
     rows = codes.shape[0]
     p, stride = _rows(x)
     _check("moe_mxfp4_quant", load_library().moe_mxfp4_quant(
-        M, D, p, _type(x), stride, None if row_map is None else _typed(row_map, M * copies, "int32", "row_map"), copies,
+        M, D, p, _type(x), stride, None if row_map is None else _typed(row_map, M * copies, _INT32, "row_map"), copies,
         rows, _sized(codes, rows * D // 2, 1, "codes"), _scales(scales, rows, D), _stream(stream)))
 
 
@@ -503,8 +513,8 @@ def moe_mxfp4_gmm(codes, scales, cumsum, w, c, workspace, stream=None):
     R, N = c.shape
     E, D = cumsum.shape[0], 2 * codes.shape[1]
     _check("moe_mxfp4_gmm", load_library().moe_mxfp4_gmm(
-        R, E, N, D, _sized(codes, R * D // 2, 1, "codes"), _scales(scales, R, D), _typed(cumsum, E, "int32", "cumsum"),
-        _blocks(w, E, N, D), _typed(c, R * N, "binary16", "c"), _p(workspace), _nbytes(workspace), _stream(stream)))
+        R, E, N, D, _sized(codes, R * D // 2, 1, "codes"), _scales(scales, R, D), _typed(cumsum, E, _INT32, "cumsum"),
+        _blocks(w, E, N, D), _typed(c, R * N, _BINARY16, "c"), _p(workspace), _nbytes(workspace), _stream(stream)))
 
 
 def moe_mxfp4_gmm_swiglu(codes, scales, cumsum, w, h_codes, h_scales, workspace, stream=None):
@@ -512,7 +522,7 @@ def moe_mxfp4_gmm_swiglu(codes, scales, cumsum, w, h_codes, h_scales, workspace,
     R, I = h_codes.shape[0], 2 * h_codes.shape[1]
     E, D = cumsum.shape[0], 2 * codes.shape[1]
     _check("moe_mxfp4_gmm_swiglu", load_library().moe_mxfp4_gmm_swiglu(
-        R, E, I, D, _sized(codes, R * D // 2, 1, "codes"), _scales(scales, R, D), _typed(cumsum, E, "int32", "cumsum"),
+        R, E, I, D, _sized(codes, R * D // 2, 1, "codes"), _scales(scales, R, D), _typed(cumsum, E, _INT32, "cumsum"),
         _blocks(w, E, 2 * I, D), _sized(h_codes, R * I // 2, 1, "h_codes"), _scales(h_scales, R, I),
         _p(workspace), _nbytes(workspace), _stream(stream)))
 
@@ -525,9 +535,9 @@ def moe_mxfp4_layer_fwd(d, x, expert_idx, probs, w1, w2, out, workspace, stream=
     """The expert layer of x [M][K] (binary16) on MXFP4 blocks w1 (gate_up) and w2, into out [M][K] (binary16)."""
     lib, R = load_library(), d.M * d.topK
     _check("moe_mxfp4_layer_fwd", lib.moe_mxfp4_layer_fwd(
-        ctypes.byref(d), _typed(x, d.M * d.K, "binary16", "x"), _typed(expert_idx, R, "int32", "expert_idx"),
-        _typed(probs, R, "float32", "probs"), _holding(w1, lib.moe_mxfp4_weights_bytes(d.E, 2 * d.I, d.K), "w1"),
-        _holding(w2, lib.moe_mxfp4_weights_bytes(d.E, d.K, d.I), "w2"), _typed(out, d.M * d.K, "binary16", "out"),
+        ctypes.byref(d), _typed(x, d.M * d.K, _BINARY16, "x"), _typed(expert_idx, R, _INT32, "expert_idx"),
+        _typed(probs, R, _FLOAT32, "probs"), _holding(w1, lib.moe_mxfp4_weights_bytes(d.E, 2 * d.I, d.K), "w1"),
+        _holding(w2, lib.moe_mxfp4_weights_bytes(d.E, d.K, d.I), "w2"), _typed(out, d.M * d.K, _BINARY16, "out"),
         _p(workspace), _nbytes(workspace), _stream(stream)))
 
 
