@@ -6,9 +6,9 @@
 // streaming past (17408 bytes per 128 channels x 256 reduction steps), so everything else is
 // done beside that stream: each CTA makes the routes' tables itself, and no row is
 // dispatched or permuted in memory.
-// Measured, depth 7168, 2048 channels: one token, 8 of 256 experts, 43 us, where its 187 MB take
-// 28 at the measured copy rate; 8 tokens on 16 experts 67 us (55); depth 4096, 1408 channels: 29
-// tokens on 64 experts 95 us (82).  The rest is the start, the wait between the two products
+// Measured, depth 7168, 2048 channels: one token, 8 of 256 experts, 42 us, where its 187 MB take
+// 28 at the measured copy rate; 8 tokens on 16 experts 66 us (55); depth 4096, 1408 channels: 29
+// tokens on 64 experts 93 us (82).  The rest is the start, the wait between the two products
 // for the last sums of h (its 6 stages in flight cover half of it) and the meeting at the end.
 //
 // Kernel 2 is persistent, one CTA per SM, with one pipeline for both products, so that the

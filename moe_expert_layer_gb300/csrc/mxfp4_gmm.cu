@@ -9,12 +9,12 @@
 // channel blocks innermost, so that CTAs working at the same time share an expert's rows and
 // its weights through L2.  Persistent CTAs, one per SM, in two forms:
 //   - few rows per expert: single CTAs, 128 channels, tiles of up to 32 rows: the weights
-//     stream past (128 tokens x 7168, N = 4096, 256 experts, 8 each: 555 us with the rows'
+//     stream past (128 tokens x 7168, N = 4096, 256 experts, 8 each: 547 us with the rows'
 //     quantisation, the weights at 1.04 of the measured copy rate);
 //   - more: CTA pairs (cta_group::2), 256 channels, tiles of up to 192 rows.  Each CTA loads
 //     half of the rows: the copies through shared memory, which bound a single CTA's 128 x 208
-//     (325 us at 49152 rows, N = 2816, D = 4096, 64 experts, where the pairs take 221), are fewer
-//     for each MMA.  The tensor pipe is then 61% busy.  Nothing else is full: what sets the pace is
+//     (325 us at 49152 rows, N = 2816, D = 4096, 64 experts, where the pairs take 220), are fewer
+//     for each MMA.  The tensor pipe is then 58% busy, L2's path to the SMs 56%: what sets the pace is
 //     the turn of the ring, a copy's latency, the scale words' way to tensor memory, the MMAs and
 //     their commit, over the six stages that fit (five: 17 us more; tiles of 224 rows and five
 //     stages: 17 more; 128 rows and seven: 28 more).
