@@ -136,3 +136,9 @@ def test_nan_rows_and_channels_stay_alone(R, E):
     keep = np.arange(R) != bad_row
     ref, err = a[keep] @ wv[n].T, mx.sum_error(a[keep], wv[n])
     assert (np.abs(got[keep][:, n] - ref.clip(-65504, 65504)) <= err + mx.f16_error(np.abs(ref) + err)).all()
+
+
+@pytest.mark.parametrize("counts,N,D", [([3, 2], 128, 16384), ([50, 40], 128, 16384), ([1, 0, 1] * 341, 128, 64), ([2], 16384, 32)])
+def test_gmm_at_the_ends_of_its_ranges(counts, N, D):
+    base.test_gmm(counts, N, D)
+    base.test_gmm_swiglu(counts, N // 2, D)

@@ -158,3 +158,20 @@ def test_signs_of_dispatched_rows_and_weights(kind):
         assert np.array_equal(got[:, 16384:], ref[:, 16384:])
         assert np.array_equal(mx.E2M1[got[:, :16384] & 15], mx.E2M1[ref[:, :16384] & 15])
         assert np.array_equal(mx.E2M1[got[:, :16384] >> 4], mx.E2M1[ref[:, :16384] >> 4])
+
+
+@pytest.mark.parametrize("M,K,I,E,topK", [(4, 128, 64, 80, 64), (1, 256, 128, 256, 256), (32, 128, 64, 8, 8), (32, 128, 64, 9, 8),
+                                          (2, 128, 64, 1023, 100), (40, 128, 64, 1023, 3), (3, 16384, 64, 3, 2),
+                                          (2, 128, 8192, 3, 2), (50, 128, 8192, 2, 1)])
+def test_layer_at_the_ends_of_its_ranges(M, K, I, E, topK):
+    """As many routes and experts as there may be, the deepest products, and the few-token path's last sizes."""
+    x, ei, probs, w1, v1, w2, v2 = layer_case(M, K, I, E, topK, M + I)
+    x = (x * np.float16(2.0 ** -7)).astype(np.float16)
+    y, err = routes64(mx.values(*mx.quantise(x.astype(np.float64))), ei, v1, v2)
+    ref, bound = weighted(y, err, probs / 16)
+    # more than 15 routes: every addition may drop 2^-24 of the magnitudes
+    bound = bound + topK * 2.0 ** -24 * (np.abs(probs.astype(np.float64) / 16)[..., None] * np.abs(y)).sum(1)
+    out, ws = run_layer(dev(x), dev(ei), dev((probs / 16).astype(np.float32)), w1, w2, I, E)
+    over = np.abs(ref) + bound > 65504
+    assert over.mean() < 0.5 and moe.moe_workspace_status(ws) == 0
+    assert (np.abs(host(out).astype(np.float64) - ref) <= bound)[~over].all()

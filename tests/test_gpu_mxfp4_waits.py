@@ -76,6 +76,24 @@ def test_few_token_layers_on_several_streams(priorities):
         assert moe.moe_workspace_status(call(o[0])) == 0
 
 
+def test_few_token_layers_beside_large_ones():
+    """Few tokens on one stream, hundreds on two others, whose kernels hold every SM's shared memory and are
+    launched ahead of what they wait for."""
+    sizes = [2, 300, 25, 600]
+    calls, alone = layers(sizes, 1024, 512, 16, 4)
+    streams = [torch.cuda.Stream(priority=p) for p in (0, 0, -1, -1)]
+    outs = [[torch.zeros_like(a) for _ in range(30)] for a in alone]
+    torch.cuda.synchronize()
+    for i in range(30):
+        for s, call, o in zip(streams, calls, outs):
+            with torch.cuda.stream(s):
+                call(o[i])
+    torch.cuda.synchronize()
+    for call, o, want in zip(calls, outs, alone):
+        assert all(torch.equal(out, want) for out in o)
+        assert moe.moe_workspace_status(call(o[0])) == 0
+
+
 class DevResource(ctypes.Structure):
     """CUdevResource of the driver API; of its union only the number of SMs is read."""
     _fields_ = [("type", ctypes.c_int), ("padding", ctypes.c_ubyte * 92), ("sm_count", ctypes.c_uint),
