@@ -1,7 +1,8 @@
-"""GB300 (sm_103a) W8A8 mixture-of-experts expert layer, its router and its MXFP4 form.
+"""GB300 (sm_103a) W8A8 mixture-of-experts expert layer, its router, its MXFP4 form and the
+operators of 16-bit experts.
 
-Thin Python binding over the C ABI in ``include/moe_layer.h`` and
-``include/moe_mxfp4.h`` (library
+Thin Python binding over the C ABI in ``include/moe_layer.h``, ``include/moe_mxfp4.h`` and
+``include/moe_experts16.h`` (library
 ``_build/libmoe_layer.so``, built by ``moe_expert_layer_gb300.build``).  The
 functions below carry the ABI's names and only marshal arguments: torch
 tensors (device memory) become raw pointers, the stream defaults to torch's
@@ -20,7 +21,7 @@ STATUS = {0: "MOE_OK", -1: "MOE_ERR_NULL", -2: "MOE_ERR_SHAPE", -3: "MOE_ERR_ALI
           -4: "MOE_ERR_ARCH", -5: "MOE_ERR_WORKSPACE", -6: "MOE_ERR_LAUNCH",
           -8: "MOE_ERR_TIMEOUT"}
 
-# every entry point declared in include/moe_layer.h and include/moe_mxfp4.h
+# every entry point declared in include/*.h
 EXPORTS = [
     "moe_status_string", "moe_layer_workspace_size", "moe_layer_fwd",
     "moe_layer_host_workspace_size", "moe_layer_fwd_host", "moe_workspace_status",
@@ -35,6 +36,9 @@ EXPORTS = [
     "moe_route_topk", "moe_mxfp4_scale_words", "moe_mxfp4_quant", "moe_mxfp4_dequant", "moe_mxfp4_weights_bytes",
     "moe_mxfp4_quant_weights", "moe_mxfp4_pack_weights", "moe_mxfp4_gmm_workspace_size", "moe_mxfp4_gmm",
     "moe_mxfp4_gmm_swiglu", "moe_mxfp4_layer_workspace_size", "moe_mxfp4_layer_fwd", "moe_selftest_mxfp4_tickets",
+    "moe_gmm16_workspace_size", "moe_gmm16", "moe_gmm16_input_grad", "moe_gmm16_weight_grad", "moe_swiglu16",
+    "moe_swiglu16_grad", "moe_dispatch16", "moe_combine16", "moe_combine16_grad", "moe_lora16_workspace_size",
+    "moe_lora16",
 ]
 
 # weight layouts (moe_dims_t.weight_layout)
@@ -117,6 +121,17 @@ def load_library(path=None):
         "moe_mxfp4_layer_workspace_size": ([D], sz),
         "moe_mxfp4_layer_fwd": ([D] + [vp] * 7 + [sz, vp], i32),
         "moe_selftest_mxfp4_tickets": ([vp, vp], i32),
+        "moe_gmm16_workspace_size": ([i32] * 4, sz),
+        "moe_gmm16": ([i32] * 5 + [vp] * 5 + [sz, vp], i32),
+        "moe_gmm16_input_grad": ([i32] * 5 + [vp] * 5 + [sz, vp], i32),
+        "moe_gmm16_weight_grad": ([i32] * 5 + [vp] * 4 + [i32, i32, vp, sz, vp], i32),
+        "moe_swiglu16": ([i32] * 4 + [vp] * 4, i32),
+        "moe_swiglu16_grad": ([i32] * 4 + [vp] * 6, i32),
+        "moe_dispatch16": ([i32] * 5 + [vp] * 4, i32),
+        "moe_combine16": ([i32] * 5 + [vp] * 5, i32),
+        "moe_combine16_grad": ([i32] * 5 + [vp] * 7, i32),
+        "moe_lora16_workspace_size": ([i32] * 4, sz),
+        "moe_lora16": ([i32] * 6 + [vp] * 9 + [sz, vp], i32),
     }
     for name, (args, res) in sigs.items():
         f = getattr(lib, name)
@@ -544,3 +559,150 @@ def moe_mxfp4_layer_fwd(d, x, expert_idx, probs, w1, w2, out, workspace, stream=
 def moe_selftest_mxfp4_tickets(answers, stream=None):
     """Runs the self-test of the few-token kernel's joint wait; answers: int32 device tensor [4]."""
     _check("moe_selftest_mxfp4_tickets", load_library().moe_selftest_mxfp4_tickets(_sized(answers, 4, 4, "answers"), _stream(stream)))
+
+
+# --------------------------------------------------------------- include/moe_experts16.h
+_TYPES16 = {"torch.float16": TYPE_F16, "torch.bfloat16": TYPE_BF16}
+_types16 = {}
+_current_device = None
+
+
+def _type16(t, what):
+    k = _types16.get(t.dtype)
+    if k is None:
+        if str(t.dtype) not in _TYPES16:
+            raise ValueError("%s: float16 or bfloat16 wanted; got %s" % (what, t.dtype))
+        k = _types16[t.dtype] = _TYPES16[str(t.dtype)]
+    return k
+
+
+def _array(t, shape, dtype, what):
+    """Pointer of a dense array of exactly this shape and type."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError("%s: %s of %s wanted; got %s of %s" % (what, tuple(shape), dtype, tuple(t.shape), t.dtype))
+    return _p(t)
+
+
+def _int32s(t, n, what):
+    """Pointer of a dense array of n 32-bit integers, of any shape."""
+    if t.numel() != n or (t.dtype not in _INT32 and not _INT32.takes(t.dtype)):
+        raise ValueError("%s: %d elements of int32 wanted; got %d of %s" % (what, n, t.numel(), t.dtype))
+    return _p(t)
+
+
+def _here(*tensors):
+    """Every tensor in the memory of the current device: a call launches there, on its stream."""
+    global _current_device
+    if _current_device is None:
+        import torch
+        if not torch.cuda.is_available():
+            raise ValueError("arrays on the GPU wanted")
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    dev = _current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("arrays on the current device (%d) wanted; got one on %s" % (dev, t.device))
+
+
+def moe_gmm16_workspace_size(R, E, N, D):
+    return load_library().moe_gmm16_workspace_size(R, E, N, D)
+
+
+def moe_gmm16(a, cumsum, w, c, workspace, stream=None):
+    """c [R][N] = rows a [R][D] times their experts' w [E][N][D]^T, all of one 16-bit type."""
+    (R, D), (E, N, _), t = a.shape, w.shape, a.dtype
+    args = (R, E, N, D, _type16(a, "a"), _p(a), _int32s(cumsum, E, "cumsum"), _array(w, (E, N, D), t, "w"),
+            _array(c, (R, N), t, "c"), _p(workspace), _nbytes(workspace))
+    _here(a, cumsum, w, c, workspace)
+    _check("moe_gmm16", load_library().moe_gmm16(*args, _stream(stream)))
+
+
+def moe_gmm16_input_grad(dc, cumsum, w, da, workspace, stream=None):
+    """da [R][D] = rows dc [R][N] times their experts' w [E][N][D]."""
+    (R, N), (E, _, D), t = dc.shape, w.shape, dc.dtype
+    args = (R, E, N, D, _type16(dc, "dc"), _p(dc), _int32s(cumsum, E, "cumsum"), _array(w, (E, N, D), t, "w"),
+            _array(da, (R, D), t, "da"), _p(workspace), _nbytes(workspace))
+    _here(dc, cumsum, w, da, workspace)
+    _check("moe_gmm16_input_grad", load_library().moe_gmm16_input_grad(*args, _stream(stream)))
+
+
+def moe_gmm16_weight_grad(dc, a, cumsum, dw, workspace, accumulate=False, stream=None):
+    """dw [E][N][D] (the rows' type or float32) = sum over each expert's rows of dc [R][N]^T a [R][D]; accumulate
+    (float32) adds it to dw."""
+    (R, N), (E, _, D), t = dc.shape, dw.shape, dc.dtype
+    kind = _type16(dc, "dc")
+    out = kind if dw.dtype == t else _type(dw)
+    args = (R, E, N, D, kind, _p(dc), _array(a, (R, D), t, "a"), _int32s(cumsum, E, "cumsum"),
+            _array(dw, (E, N, D), dw.dtype, "dw"), out, 1 if accumulate else 0, _p(workspace), _nbytes(workspace))
+    _here(dc, a, cumsum, dw, workspace)
+    _check("moe_gmm16_weight_grad", load_library().moe_gmm16_weight_grad(*args, _stream(stream)))
+
+
+def moe_swiglu16(gu, cumsum, h, stream=None):
+    """h [R][I] = silu(g) u of the experts' rows gu [R][2 I] = (g, u)."""
+    (R, I), E = h.shape, cumsum.numel()
+    args = (R, E, I, _type16(gu, "gu"), _array(gu, (R, 2 * I), gu.dtype, "gu"), _int32s(cumsum, E, "cumsum"),
+            _array(h, (R, I), gu.dtype, "h"))
+    _here(gu, cumsum, h)
+    _check("moe_swiglu16", load_library().moe_swiglu16(*args, _stream(stream)))
+
+
+def moe_swiglu16_grad(dh, gu, cumsum, dgu, h=None, stream=None):
+    """dgu [R][2 I] (it may be gu) from dh [R][I] and gu; h [R][I], where given, gets moe_swiglu16's (it may be dh)."""
+    (R, I), E, t = dh.shape, cumsum.numel(), dh.dtype
+    args = (R, E, I, _type16(dh, "dh"), _p(dh), _array(gu, (R, 2 * I), t, "gu"), _int32s(cumsum, E, "cumsum"),
+            _array(dgu, (R, 2 * I), t, "dgu"), None if h is None else _array(h, (R, I), t, "h"))
+    _here(dh, gu, cumsum, dgu, h)
+    _check("moe_swiglu16_grad", load_library().moe_swiglu16_grad(*args, _stream(stream)))
+
+
+def moe_dispatch16(x, row_map, out, copies=1, stream=None):
+    """out [rows][D]: row row_map[t][j] = x[t], j < copies."""
+    (M, D), rows = x.shape, out.shape[0]
+    args = (M, D, copies, rows, _type16(x, "x"), _p(x), _int32s(row_map, M * copies, "row_map"),
+            _array(out, (rows, D), x.dtype, "out"))
+    _here(x, row_map, out)
+    _check("moe_dispatch16", load_library().moe_dispatch16(*args, _stream(stream)))
+
+
+def moe_combine16(y, row_map, probs, out, copies=1, stream=None):
+    """out [M][D] = sum over j < copies of probs[t][j] (None: 1) * y[row_map[t][j]]."""
+    (M, D), rows = out.shape, y.shape[0]
+    args = (M, D, copies, rows, _type16(y, "y"), _array(y, (rows, D), y.dtype, "y"),
+            _int32s(row_map, M * copies, "row_map"), None if probs is None else _floats(probs, M * copies, "probs"),
+            _array(out, (M, D), y.dtype, "out"))
+    _here(y, row_map, probs, out)
+    _check("moe_combine16", load_library().moe_combine16(*args, _stream(stream)))
+
+
+def moe_combine16_grad(dout, y, row_map, probs, dy, dprobs, copies=1, stream=None):
+    """dy [rows][D] (it may be y): row row_map[t][j] = probs[t][j] dout[t]; dprobs[t][j] = <dout[t], y[row_map[t][j]]>."""
+    (M, D), rows, t = dout.shape, y.shape[0], dout.dtype
+    args = (M, D, copies, rows, _type16(dout, "dout"), _p(dout), _array(y, (rows, D), t, "y"),
+            _int32s(row_map, M * copies, "row_map"), _floats(probs, M * copies, "probs"),
+            _array(dy, (rows, D), t, "dy"), _floats(dprobs, M * copies, "dprobs"))
+    _here(dout, y, row_map, probs, dy, dprobs)
+    _check("moe_combine16_grad", load_library().moe_combine16_grad(*args, _stream(stream)))
+
+
+def _floats(t, n, what):
+    """Pointer of a dense array of n fp32, of any shape."""
+    if t.numel() != n or (t.dtype not in _FLOAT32 and not _FLOAT32.takes(t.dtype)):
+        raise ValueError("%s: %d elements of float32 wanted; got %d of %s" % (what, n, t.numel(), t.dtype))
+    return _p(t)
+
+
+def moe_lora16_workspace_size(M, N, D, rank):
+    return load_library().moe_lora16_workspace_size(M, N, D, rank)
+
+
+def moe_lora16(x, route, cumsum, a, b, base, out, workspace, scales=None, stream=None):
+    """out [M][N] (it may be base) = base + scales[l] b[l] (a[l] x[t]), a [L][rank][D], b [L][N][rank], l the adapter of
+    token t; route [M], cumsum [L]: sorted_src_route and cumsum of moe_route_sort on the tokens' adapters."""
+    (M, D), (L, rank, _), N, t = x.shape, a.shape, b.shape[1], x.dtype
+    args = (M, N, D, rank, L, _type16(x, "x"), _p(x), _int32s(route, M, "route"), _int32s(cumsum, L, "cumsum"),
+            _array(a, (L, rank, D), t, "a"), _array(b, (L, N, rank), t, "b"),
+            None if scales is None else _floats(scales, L, "scales"), _array(base, (M, N), t, "base"),
+            _array(out, (M, N), t, "out"), _p(workspace), _nbytes(workspace))
+    _here(x, route, cumsum, a, b, scales, base, out, workspace)
+    _check("moe_lora16", load_library().moe_lora16(*args, _stream(stream)))

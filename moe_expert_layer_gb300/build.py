@@ -14,8 +14,9 @@ LIB_PATH = os.path.join(OUT_DIR, "libmoe_layer.so")
 SOURCES = ["route_sort.cu", "elementwise.cu", "gemm_hmma.cu", "gemm_tc.cu", "gemm_dispatch.cu", "moe_layer.cu",
            "route_sort_noalloc.cu", "selftest.cu", "weight_tiles.cu",
            "route_topk.cu", "mxfp4_quant.cu", "mxfp4_gmm.cu", "mxfp4_few.cu",
-           "mxfp4_abi.cu"]
-HEADERS = ["abi_checks.h", "common.cuh", "kernels.h", "mx_tc.cuh", "mxfp4.cuh", "mxfp4.h", "swiglu.cuh", "tc_common.cuh",
+           "mxfp4_abi.cu",
+           "rows16.cu", "gmm16.cu", "lora16.cu", "experts16_abi.cu"]
+HEADERS = ["abi_checks.h", "common.cuh", "experts16.h", "kernels.h", "mx_tc.cuh", "mxfp4.cuh", "mxfp4.h", "swiglu.cuh", "tc_common.cuh",
            "tensor_map.h"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc" if os.path.exists("/usr/local/cuda/bin/nvcc") else "nvcc")
 NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
@@ -25,7 +26,7 @@ NVCC_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", 
 def _inputs():
     root = os.path.dirname(HERE)
     return ([os.path.join(CSRC, s) for s in SOURCES + HEADERS]
-            + [os.path.join(root, "include", h) for h in ("moe_layer.h", "moe_mxfp4.h")] + [os.path.abspath(__file__)])
+            + [os.path.join(root, "include", h) for h in ("moe_layer.h", "moe_mxfp4.h", "moe_experts16.h")] + [os.path.abspath(__file__)])
 
 
 def up_to_date():

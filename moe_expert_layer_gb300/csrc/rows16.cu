@@ -1,0 +1,276 @@
+// Row operators of the 16-bit experts (include/moe_experts16.h): SwiGLU and its gradient, the
+// dispatch of tokens to expert-major rows, the weighted combine, and the combine's gradient.
+//
+// All are bound by bytes: eight elements (16 bytes) to a lane, arithmetic in fp32, one rounding at
+// the store.
+#include "mxfp4.cuh"
+#include "experts16.h"
+#include "tensor_map.h"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+// Eight 16-bit elements.
+template <typename T>
+union Eight {
+  T t[8];
+  uint4 u;
+};
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, Eight<T>& r) {
+  r.u = __ldcg(reinterpret_cast<const uint4*>(p));
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
+  Eight<T> r;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) from_f32x2<T>(v[i], v[i + 1], &r.t[i]);
+  *reinterpret_cast<uint4*>(p) = r.u;
+}
+
+// Rows that belong to an expert.
+__device__ __forceinline__ int valid_rows(const int32_t* cumsum, int E, int R) {
+  return min(max(__ldcg(cumsum + E - 1), 0), R);
+}
+
+// g s(g) with s(g) = 1 / (1 + exp(-g)), and s(g).  The exponential's relative error is about
+// 2^-22 |g|.  Below -80, where 1 is lost beside exp(-g) and before that leaves fp32, s is e^g taken
+// as a product of halves around the other factors (`half` = e^(g/2), 0 elsewhere).
+struct Gate {
+  float s, half;
+};
+__device__ __forceinline__ Gate gate_of(float g) {
+  Gate r;
+  r.s = __fdividef(1.0f, 1.0f + __expf(-g));
+  r.half = 0.0f;
+  if (g < -80.0f) r.half = __expf(0.5f * g);
+  return r;
+}
+__device__ __forceinline__ float swiglu(float g, float u, const Gate& k) {
+  return g < -80.0f ? (u * k.half) * (g * k.half) : g * k.s * u;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) swiglu16_kernel(int R, int E, int I, const T* gu, const int32_t* cumsum,
+                                                            T* h) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int per = I / 8;
+  const int64_t n = (int64_t)valid_rows(cumsum, E, R) * per, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+    const int64_t d = i / per;
+    const T* row = gu + d * 2 * I + (i - d * per) * 8;
+    Eight<T> g, u;
+    load8(row, g);
+    load8(row + I, u);
+    float o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float x = to_f32<T>(g.t[k]);
+      o[k] = swiglu(x, to_f32<T>(u.t[k]), gate_of(x));
+    }
+    store8(h + i * 8, o);
+  }
+}
+
+// dgu may be gu and h may be dh: a thread reads its elements before it writes them.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) swiglu16_grad_kernel(int R, int E, int I, const T* dh, const T* gu,
+                                                                 const int32_t* cumsum, T* dgu, T* h) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int per = I / 8;
+  const int64_t n = (int64_t)valid_rows(cumsum, E, R) * per, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+    const int64_t d = i / per, at = d * 2 * I + (i - d * per) * 8;
+    Eight<T> g8, u8, dh8;
+    load8(gu + at, g8);
+    load8(gu + at + I, u8);
+    load8(dh + i * 8, dh8);
+    float dg[8], du[8], o[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float g = to_f32<T>(g8.t[k]), u = to_f32<T>(u8.t[k]), y = to_f32<T>(dh8.t[k]);
+      const Gate s = gate_of(g);
+      o[k] = swiglu(g, u, s);
+      du[k] = swiglu(g, y, s);
+      const float slope = fmaf(g, 1.0f - s.s, 1.0f);
+      dg[k] = g < -80.0f ? (u * s.half * (1.0f + g)) * (y * s.half) : y * (s.s * slope) * u;
+    }
+    store8(dgu + at, dg);
+    store8(dgu + at + I, du);
+    if (h) store8(h + i * 8, o);
+  }
+}
+
+// One thread per eight channels of a token, to each of its rows.
+__global__ void __launch_bounds__(kThreads) dispatch16_kernel(int M, int D, int copies, int rows, const uint4* x,
+                                                              const int32_t* row_map, uint4* out) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int per = D / 8;
+  const int64_t n = (int64_t)M * per, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+    const int64_t t = i / per, c = i - t * per;
+    const uint4 v = __ldcg(x + i);
+    for (int j = 0; j < copies; ++j) {
+      const int d = __ldcg(row_map + t * copies + j);
+      if ((unsigned)d < (unsigned)rows) out[(int64_t)d * per + c] = v;
+    }
+  }
+}
+
+// One thread per eight channels of a token: four rows read at a time, then the sums in order.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) combine16_kernel(int M, int D, int copies, int rows, const T* y,
+                                                             const int32_t* row_map, const float* probs, T* out) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int per = D / 8;
+  const int64_t n = (int64_t)M * per, step = (int64_t)gridDim.x * kThreads;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+    const int64_t t = i / per, c = i - t * per;
+    float acc[8] = {};
+    for (int j = 0; j < copies; j += 4) {
+      Eight<T> v[4];
+      float w[4];
+      bool in[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int d = j + q < copies ? __ldcg(row_map + t * copies + j + q) : -1;
+        in[q] = (unsigned)d < (unsigned)rows;
+        if (in[q]) {
+          load8(y + (int64_t)d * D + c * 8, v[q]);
+          w[q] = probs ? __ldcg(probs + t * copies + j + q) : 1.0f;
+        }
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if (in[q]) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[q], to_f32<T>(v[q].t[k]), acc[k]);
+        }
+    }
+    store8(out + i * 8, acc);
+  }
+}
+
+// A block per token and group of G of its routes: dout is read once for the group, each y row once,
+// each dy row written, and the products with y summed over the block in a fixed order.
+template <typename T, int G>
+__global__ void __launch_bounds__(kThreads) combine16_grad_kernel(int M, int D, int copies, int rows, const T* dout,
+                                                                  const T* y, const int32_t* row_map,
+                                                                  const float* probs, T* dy, float* dprobs) {
+  __shared__ float part[G][kThreads / 32];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int groups = (copies + G - 1) / G, t = blockIdx.x / groups, j0 = (blockIdx.x - t * groups) * G;
+  const int per = D / 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int row[G];
+  float p[G], sum[G];
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+    const int64_t at = (int64_t)t * copies + j0 + q;
+    row[q] = j0 + q < copies ? __ldcg(row_map + at) : -1;
+    if ((unsigned)row[q] >= (unsigned)rows) row[q] = -1;
+    p[q] = row[q] >= 0 ? __ldcg(probs + at) : 0.0f;
+    sum[q] = 0.0f;
+  }
+  for (int c = threadIdx.x; c < per; c += kThreads) {
+    Eight<T> g, v[G];
+    load8(dout + (int64_t)t * D + c * 8, g);
+#pragma unroll
+    for (int q = 0; q < G; ++q)
+      if (row[q] >= 0) load8(y + (int64_t)row[q] * D + c * 8, v[q]);
+#pragma unroll
+    for (int q = 0; q < G; ++q)
+      if (row[q] >= 0) {
+        float o[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const float x = to_f32<T>(g.t[k]);
+          sum[q] = fmaf(x, to_f32<T>(v[q].t[k]), sum[q]);
+          o[k] = p[q] * x;
+        }
+        store8(dy + (int64_t)row[q] * D + c * 8, o);
+      }
+  }
+#pragma unroll
+  for (int q = 0; q < G; ++q) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], o);
+    if (lane == 0) part[q][warp] = sum[q];
+  }
+  __syncthreads();
+  if (threadIdx.x < G && j0 + (int)threadIdx.x < copies) {
+    float s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) s += part[threadIdx.x][w];
+    dprobs[(int64_t)t * copies + j0 + threadIdx.x] = s;
+  }
+}
+
+inline unsigned grid_of(int64_t items, int per_sm = 8) {
+  const int64_t b = (items + kThreads - 1) / kThreads, most = (int64_t)sm_count() * per_sm;
+  return (unsigned)(b < most ? b : most);
+}
+
+template <typename T>
+cudaError_t combine_grad(int M, int D, int copies, int rows, const void* dout, const void* y, const int32_t* row_map,
+                         const float* probs, void* dy, float* dprobs, cudaStream_t stream) {
+  const unsigned groups = (unsigned)(copies + 7) / 8;
+  return launch_dependent(combine16_grad_kernel<T, 8>, (unsigned)M * groups, kThreads, 0, stream, M, D, copies, rows,
+                          static_cast<const T*>(dout), static_cast<const T*>(y), row_map, probs, static_cast<T*>(dy),
+                          dprobs);
+}
+
+}  // namespace
+
+cudaError_t launch_swiglu16(int R, int E, int I, bool bf16, const void* gu, const int32_t* cumsum, void* h,
+                            cudaStream_t stream) {
+  const unsigned grid = grid_of((int64_t)R * (I / 8));
+  if (bf16)
+    return launch_dependent(swiglu16_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, R, E, I,
+                            static_cast<const __nv_bfloat16*>(gu), cumsum, static_cast<__nv_bfloat16*>(h));
+  return launch_dependent(swiglu16_kernel<__half>, grid, kThreads, 0, stream, R, E, I, static_cast<const __half*>(gu),
+                          cumsum, static_cast<__half*>(h));
+}
+
+cudaError_t launch_swiglu16_grad(int R, int E, int I, bool bf16, const void* dh, const void* gu, const int32_t* cumsum,
+                                 void* dgu, void* h, cudaStream_t stream) {
+  const unsigned grid = grid_of((int64_t)R * (I / 8));
+  if (bf16)
+    return launch_dependent(swiglu16_grad_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, R, E, I,
+                            static_cast<const __nv_bfloat16*>(dh), static_cast<const __nv_bfloat16*>(gu), cumsum,
+                            static_cast<__nv_bfloat16*>(dgu), static_cast<__nv_bfloat16*>(h));
+  return launch_dependent(swiglu16_grad_kernel<__half>, grid, kThreads, 0, stream, R, E, I,
+                          static_cast<const __half*>(dh), static_cast<const __half*>(gu), cumsum,
+                          static_cast<__half*>(dgu), static_cast<__half*>(h));
+}
+
+cudaError_t launch_dispatch16(int M, int D, int copies, int rows, const void* x, const int32_t* row_map, void* out,
+                              cudaStream_t stream) {
+  return launch_dependent(dispatch16_kernel, grid_of((int64_t)M * (D / 8)), kThreads, 0, stream, M, D, copies, rows,
+                          static_cast<const uint4*>(x), row_map, static_cast<uint4*>(out));
+}
+
+cudaError_t launch_combine16(int M, int D, int copies, int rows, bool bf16, const void* y, const int32_t* row_map,
+                             const float* probs, void* out, cudaStream_t stream) {
+  const unsigned grid = grid_of((int64_t)M * (D / 8));
+  if (bf16)
+    return launch_dependent(combine16_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, M, D, copies, rows,
+                            static_cast<const __nv_bfloat16*>(y), row_map, probs, static_cast<__nv_bfloat16*>(out));
+  return launch_dependent(combine16_kernel<__half>, grid, kThreads, 0, stream, M, D, copies, rows,
+                          static_cast<const __half*>(y), row_map, probs, static_cast<__half*>(out));
+}
+
+cudaError_t launch_combine16_grad(int M, int D, int copies, int rows, bool bf16, const void* dout, const void* y,
+                                  const int32_t* row_map, const float* probs, void* dy, float* dprobs,
+                                  cudaStream_t stream) {
+  return bf16 ? combine_grad<__nv_bfloat16>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
+              : combine_grad<__half>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
+}
+
+}  // namespace moe
