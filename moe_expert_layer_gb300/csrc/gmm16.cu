@@ -1,113 +1,625 @@
-// Products of 16-bit operands grouped by expert (include/moe_experts16.h): rows times their
-// expert's weights, and the two gradients.
+// Products of 16-bit operands grouped by expert (include/moe_experts16.h) on the tensor cores
+// (tcgen05.mma kind::f16, fp32 accumulators in tensor memory): rows times their expert's weights,
+// and the two gradients.
 //
-// A block computes 64 x 64 outputs from 16-deep slices of both operands in shared memory, in fp32.
-#include "mxfp4.cuh"
+//             MMA rows (operand A)             MMA columns (operand B)       reduction
+//   kForward  channels n of w[e]               rows of a                     k of D
+//   kInput    channels k of w[e] (MN-major)    rows of dc                    n of N
+//   kWeight   channels n of dc (MN-major)      channels k of a (MN-major)    rows of the expert
+//
+// An operand whose reduction index is not the contiguous one is "MN-major": a tensor copy brings
+// boxes of 64 channels x 64 steps of the reduction, and the MMA's descriptors name that order, so
+// nothing is transposed anywhere.
+//
+// kForward and kInput: the ragged side, an expert's rows, is the one whose size the instruction
+// takes in steps of 16 (32 for a pair): an expert of cnt rows is cut into ceil(cnt / NT) tiles of
+// equal size rounded up to that step.  Items (expert, row tile, channel block) are dealt out
+// expert-major, channel blocks innermost, so that CTAs working at the same time share an expert's
+// rows and its weights through L2.  kWeight: items are 256 x 256 blocks of dw[e]; the last stage of
+// an expert's rows also brings rows of the next expert, which are overwritten with zeros in shared
+// memory (up to the 16 rows that an MMA takes) before the MMAs see them.
+//
+// Persistent CTAs, one per SM, in two forms: single CTAs of 128 channels and tiles of up to 32 rows,
+// which stream the weights past few rows; and CTA pairs (cta_group::2) of 256 channels and tiles of
+// up to 256 rows, of which each CTA loads half.
+//
+// Roles: warp 0 loads operand A and warp 2 operand B, 64 steps of the reduction a stage, into a ring
+// in shared memory; warp 3 (pairs) tells the leading CTA that a stage has landed; warp 1 of the
+// leading CTA issues the MMAs; warps 4-11 are two groups, one for each of the two accumulators, that
+// round the sums and store them.  Every wait is bounded: one that gives up records MOE_ERR_TIMEOUT
+// and the CTA winds down.
 #include "experts16.h"
+#include "mx_tc.cuh"
+#include "tensor_map.h"
 
 namespace moe {
 namespace {
 
-constexpr int kTile = 64, kDeep = 16, kThreads = 256;
+constexpr int kThreads = 384;
+constexpr int kAWarp = 0, kMmaWarp = 1, kBWarp = 2, kRelayWarp = 3, kEpiWarp0 = 4;
+constexpr int kMaxExperts = 1024;
+constexpr int kABytes = 128 * 128;  // 128 channels x 64 steps
+constexpr int kOutRows = 32;        // of an epilogue group's store, x 128 channels
+constexpr int kBoxes = 3, kBoxRows = 64;
+
+template <Gmm16 KIND, int NT, bool PAIR>
+struct Cfg {
+  static constexpr bool kWeight = KIND == Gmm16::kWeight;
+  static constexpr int kStep = PAIR ? 32 : 16;
+  static constexpr int kCtaCols = PAIR ? NT / 2 : NT;
+  static constexpr int kStageBytes = kABytes + kCtaCols * 128;
+  static constexpr int kStages = PAIR ? 6 : 10;
+  // kWeight: 4 KB a warp (32 channels x 128 bytes); else 8 KB a group
+  static constexpr int kEpiBytes = kWeight ? 8 * 4096 : 2 * kOutRows * 256;
+  static constexpr int kTmemCols = 2 * NT <= 64 ? 64 : 512;
+  static constexpr int kSmem = kStages * kStageBytes + kEpiBytes;
+  static_assert(kStageBytes % 1024 == 0 && 2 * NT <= kTmemCols, "swizzled rows, tensor memory");
+  static_assert(kSmem + (kWeight ? 1024 : 9 * 1024) <= 227 * 1024, "shared memory");
+};
 
 struct Args {
   int R, E, N, D;
   const int32_t* cumsum;
-  const void *rows, *rows2, *w;
   void* out;
   int32_t* status;
-  bool accumulate;
+  bool bf16, out_f32, accumulate;
 };
+
+// a: operand A; b: operand B in boxes of 64, 32 and 16 rows (kWeight: b[0] alone); out.
+struct Maps {
+  CUtensorMap a, b[kBoxes], out;
+};
+
+// Instruction descriptor of kind::f16 with fp32 sums: operands both binary16 or both bfloat16, M =
+// 128 (a CTA) or 256 (a pair).
+__device__ __forceinline__ uint32_t f16_idesc(bool bf16, bool a_mn, bool b_mn, int m, int n) {
+  return (1u << 4) | ((uint32_t)bf16 << 7) | ((uint32_t)bf16 << 10) | ((uint32_t)a_mn << 15) | ((uint32_t)b_mn << 16) |
+         ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Descriptor of an MN-major operand in the 128-byte swizzle: boxes of 64 channels (128 bytes) x 64
+// steps of the reduction; 8 steps are 1024 bytes, the next 64 channels 8192 bytes on.
+__device__ __forceinline__ uint64_t sw128_mn_desc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(8192 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void f16_mma(uint32_t elected, uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "setp.ne.u32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "setp.ne.u32 e, %5, 0;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d_elect(uint32_t elected, uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                                  int32_t z, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred e;\n\t"
+      "setp.ne.u32 e, %6, 0;\n\t"
+      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(elected)
+      : "memory");
+}
+// Tiled store of a 3-D map's box, or its addition (fp32) to what is there.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t x, int32_t y, int32_t z, const void* src) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+__device__ __forceinline__ void tma_add_3d(const void* tmap, int32_t x, int32_t y, int32_t z, const void* src) {
+  asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(x), "r"(y), "r"(z), "r"(smem_u32(src))
+               : "memory");
+}
+
+// Two sums as a pair of the output's type (lo, hi): bits.
+__device__ __forceinline__ uint32_t pack16(bool bf16, uint32_t lo, uint32_t hi) {
+  const float a = __uint_as_float(lo), b = __uint_as_float(hi);
+  if (bf16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+  const __half2 h = f2h2_sat(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// An arrival on the leading CTA's barrier that publishes what this thread has stored itself, to the
+// whole cluster; and the wait for it.  Only stages with overwritten rows pay for these.
+__device__ __forceinline__ void mbar_arrive_remote_release(uint32_t caddr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
+}
+__device__ __forceinline__ void mbar_acquire_cluster(uint64_t* bar, uint32_t parity) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
+      "r"(parity)
+      : "memory");
+}
+
+struct Item {
+  int e, cb;          // expert, block of the MMA's rows (of a CTA or a pair)
+  int row0, rows, n;  // kForward, kInput: the tile's rows; MMA columns.  kWeight: the expert's rows
+  int col0;           // kWeight: first column
+};
+
+struct WorkList {
+  const int* pref;  // first item of each expert; pref[E] = their number
+  const int* end;   // last row of each expert + 1
+  int CB, E;
+};
+
+template <int NT>
+__device__ __forceinline__ int tiles_of(int start, int end) {
+  return end > start ? (end - start + NT - 1) / NT : 0;
+}
+
+// With t tiles of `size` rows (a multiple of the step, at most NT) none is empty: (t - 1) * size is
+// less than the rows, since size < rows / t + STEP and t > 1 only where rows > (t - 1) * NT.
+template <int NT, int STEP>
+__device__ __forceinline__ Item tile_item(int j, const WorkList& wl, int& e_hint) {
+  // pref[lo] <= j < pref[hi]: mostly the same expert as the item before, or one of the next
+  int lo = e_hint, hi = lo + 1, step = 1;
+  while (hi < wl.E && wl.pref[hi] <= j) {
+    lo = hi;
+    hi = min(hi + step, wl.E);
+    step *= 2;
+  }
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (wl.pref[mid] <= j) lo = mid; else hi = mid;
+  }
+  e_hint = lo;
+  const int start = lo ? wl.end[lo - 1] : 0, end = wl.end[lo];
+  const int t = tiles_of<NT>(start, end), size = ((end - start + t - 1) / t + STEP - 1) & -STEP;
+  const int local = j - wl.pref[lo], rt = local / wl.CB;
+  Item it;
+  it.e = lo;
+  it.cb = local - rt * wl.CB;
+  it.row0 = start + rt * size;
+  it.rows = min(size, end - it.row0);
+  it.n = (it.rows + STEP - 1) & -STEP;
+  it.col0 = 0;
+  return it;
+}
 
 __device__ __forceinline__ int end_of(const Args& a, int e) {
   return e < 0 ? 0 : min(max(__ldcg(a.cumsum + e), 0), a.R);
 }
 
-// out[m][n] = sum over k of A(m, k) B(k, n), m < rows, n < cols, k < depth.
-template <typename O, typename FA, typename FB>
-__device__ __forceinline__ void tile_product(int m0, int n0, int rows, int cols, int depth, FA A, FB B, O* out, int64_t ld,
-                                             bool accumulate) {
-  __shared__ float sa[kDeep][kTile + 1], sb[kDeep][kTile + 1];
-  float acc[4][4] = {};
-  const int tm = threadIdx.x / 16, tn = threadIdx.x % 16;
-  for (int k0 = 0; k0 < depth; k0 += kDeep) {
-    for (int i = threadIdx.x; i < kTile * kDeep; i += kThreads) {
-      const int k = i % kDeep, r = i / kDeep;
-      sa[k][r] = m0 + r < rows && k0 + k < depth ? A(m0 + r, k0 + k) : 0.0f;
-      sb[k][r] = n0 + r < cols && k0 + k < depth ? B(k0 + k, n0 + r) : 0.0f;
+// kWeight: blocks of 256 x 256, columns innermost.
+template <int NT, int STEP>
+__device__ __forceinline__ Item block_item(int j, int CB, const Args& a) {
+  const int cols = (a.D + NT - 1) / NT, per = CB * cols;
+  Item it;
+  it.e = j / per;
+  const int local = j - it.e * per;
+  it.cb = local / cols;
+  it.col0 = (local - it.cb * cols) * NT;
+  it.row0 = end_of(a, it.e - 1);
+  it.rows = max(end_of(a, it.e) - it.row0, 0);
+  it.n = (min(NT, a.D - it.col0) + STEP - 1) & -STEP;
+  return it;
+}
+
+// Whether `ok` holds in all four warps of a group (named barrier `id`).
+__device__ __forceinline__ bool group_all(int id, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+template <Gmm16 KIND, int NT, bool PAIR>
+__global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constant__ Maps maps, const Args a) {
+  using C = Cfg<KIND, NT, PAIR>;
+  constexpr int S = C::kStages;
+  constexpr bool W = C::kWeight, A_MN = KIND != Gmm16::kForward, RELAY = PAIR || W;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // swizzled rows: 1024-byte groups
+  __shared__ __align__(8) uint64_t full_bar[S], ready_bar[S], empty_bar[S], accfull_bar[2], accempty_bar[2], final_bar;
+  __shared__ int s_pref[W ? 1 : kMaxExperts + 1], s_end[W ? 1 : kMaxExperts], s_wsum[kThreads / 32];
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_issued[2];
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const int out_rows = KIND == Gmm16::kInput ? a.D : a.N;  // the MMA's rows in all
+  const int NB = (out_rows + 127) / 128, CB = PAIR ? (NB + 1) / 2 : NB;
+  const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
+  volatile int* abort_flag = &s_abort;
+
+  // ---- work list, barriers, tensor memory; what the kernels before this one wrote is read behind
+  // the wait only
+  if (warp == kMmaWarp) {
+    tmem_alloc<PAIR, C::kTmemCols>(&s_tmem);
+    if (lane == 0) {
+      prefetch_tmap(&maps.a);
+      for (int b = 0; b < (W ? 1 : kBoxes); ++b) prefetch_tmap(&maps.b[b]);
+      prefetch_tmap(&maps.out);
+      for (int s = 0; s < S; ++s) {
+        mbar_init(&full_bar[s], 2);
+        mbar_init(&ready_bar[s], PAIR ? 2 : 1);
+        mbar_init(&empty_bar[s], 1);
+      }
+      for (int s = 0; s < 2; ++s) {
+        mbar_init(&accfull_bar[s], 1);
+        mbar_init(&accempty_bar[s], PAIR ? 8 : 4);
+      }
+      mbar_init(&final_bar, 1);
+      fence_barrier_init();
     }
-    __syncthreads();
-#pragma unroll
-    for (int k = 0; k < kDeep; ++k)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[k][tm * 4 + i], sb[k][tn * 4 + j], acc[i][j]);
-    __syncthreads();
+    tc_fence_before();
   }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int m = m0 + tm * 4 + i, n = n0 + tn * 4 + j;
-      if (m < rows && n < cols) {
-        O* o = out + m * ld + n;
-        *o = from_f32<O>(accumulate ? to_f32<O>(*o) + acc[i][j] : acc[i][j]);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.status = 0;  // long before any wait can run out
+  if (threadIdx.x == 0) {
+    s_abort = 0;
+    s_issued[0] = s_issued[1] = 0;
+  }
+  int total;
+  if (W) {
+    total = a.E * CB * ((a.D + NT - 1) / NT);
+    __syncthreads();
+  } else {
+    const int E = a.E, per = (E + kThreads - 1) / kThreads;
+    const int e0 = min(E, (int)threadIdx.x * per), e1 = min(E, e0 + per);
+    int local = 0;
+    for (int e = e0; e < e1; ++e) {
+      s_end[e] = end_of(a, e);
+      local += tiles_of<NT>(end_of(a, e - 1), s_end[e]) * CB;
+    }
+    int incl = local;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int n = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += n;
+    }
+    if (lane == 31) s_wsum[warp] = incl;
+    __syncthreads();
+    int run = incl - local;
+    for (int w = 0; w < warp; ++w) run += s_wsum[w];
+    for (int e = e0; e < e1; ++e) {
+      s_pref[e] = run;
+      run += tiles_of<NT>(e ? s_end[e - 1] : 0, s_end[e]) * CB;
+    }
+    if (e0 < E && e1 == E) s_pref[E] = run;
+    __syncthreads();
+    total = s_pref[E];
+  }
+  __syncwarp();
+  if (PAIR) cluster_sync_all();  // the peer's barriers and tensor memory are ready
+  tc_fence_after();
+  const WorkList wl{s_pref, s_end, CB, a.E};
+  const uint32_t tmem = s_tmem;
+  const uint32_t ring = smem_u32(smem_raw);
+  // kForward, kInput: stages of every item
+  const int depth = KIND == Gmm16::kForward ? a.D : a.N;
+  auto item = [&](int j, int& e_hint) -> Item {
+    if constexpr (W) return block_item<NT, C::kStep>(j, CB, a);
+    else return tile_item<NT, C::kStep>(j, wl, e_hint);
+  };
+  auto steps = [&](const Item& it) { return W ? it.rows : depth; };  // of the reduction
+
+  if (warp == kAWarp || warp == kBWarp) {
+    const uint32_t elected = elect_one();
+    RingPos at;
+    int n = 0, e_hint = 0;
+    bool ok = true;
+    for (int j = first; ok && j < total; j += stride) {
+      const Item it = item(j, e_hint);
+      const int m0 = (PAIR ? 2 * it.cb + (int)rank : it.cb) * 128;  // past the last: the copies bring zeros
+      const int cta_cols = PAIR ? it.n / 2 : it.n, KB = (steps(it) + 63) / 64;
+      const int c0 = (W ? it.col0 : it.row0) + (int)rank * cta_cols;
+      for (int kb = 0; kb < KB; ++kb, ++n, at.next(S)) {
+        if (!(ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status))) break;
+        const uint32_t st = ring + at.slot * C::kStageBytes, bar = smem_u32(&full_bar[at.slot]);
+        if (warp == kAWarp) {
+          expect_tx_elect(elected, bar, kABytes);
+          if (KIND == Gmm16::kForward) {
+            tma_load_3d_elect(elected, st, &maps.a, kb * 64, m0, it.e, bar);
+          } else if (KIND == Gmm16::kInput) {
+            tma_load_3d_elect(elected, st, &maps.a, m0, kb * 64, it.e, bar);
+            tma_load_3d_elect(elected, st + 8192, &maps.a, m0 + 64, kb * 64, it.e, bar);
+          } else {
+            tma_load_2d_elect(elected, st, &maps.a, m0, it.row0 + kb * 64, bar);
+            tma_load_2d_elect(elected, st + 8192, &maps.a, m0 + 64, it.row0 + kb * 64, bar);
+          }
+        } else if (W) {
+          const int boxes = (cta_cols + 63) / 64;
+          expect_tx_elect(elected, bar, (uint32_t)boxes * 8192);
+          for (int b = 0; b < boxes; ++b)
+            tma_load_2d_elect(elected, st + kABytes + b * 8192, &maps.b[0], c0 + b * 64, it.row0 + kb * 64, bar);
+        } else {
+          expect_tx_elect(elected, bar, (uint32_t)cta_cols * 128);
+          int r = 0;
+#pragma unroll
+          for (int b = 0; b < kBoxes; ++b) {
+            const int rows = kBoxRows >> b;
+            for (; cta_cols - r >= rows; r += rows)
+              tma_load_2d_elect(elected, st + kABytes + r * 128, &maps.b[b], kb * 64, c0 + r, bar);
+          }
+        }
       }
     }
-}
-
-// blockIdx.x: 64-row tiles, an expert's rounded up (kWeight: channels); blockIdx.y: output columns;
-// blockIdx.z: experts (kWeight).
-template <typename T, typename O, Gmm16 KIND>
-__global__ void __launch_bounds__(kThreads) gmm16_kernel(const Args a) {
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.status = 0;
-  const T *rows = static_cast<const T*>(a.rows), *rows2 = static_cast<const T*>(a.rows2);
-  O* out = static_cast<O*>(a.out);
-  const int N = a.N, D = a.D, c0 = blockIdx.y * kTile;
-  if constexpr (KIND == Gmm16::kWeight) {
-    const int e = blockIdx.z, lo = end_of(a, e - 1), hi = end_of(a, e);
-    const T *x = rows + (int64_t)lo * N, *y = rows2 + (int64_t)lo * D;
-    tile_product(
-        blockIdx.x * kTile, c0, N, D, max(hi - lo, 0), [&](int m, int k) { return to_f32<T>(x[(int64_t)k * N + m]); },
-        [&](int k, int n) { return to_f32<T>(y[(int64_t)k * D + n]); }, out + (int64_t)e * N * D, (int64_t)D, a.accumulate);
-  } else {
-  for (int e = 0, tile = 0; e < a.E; ++e) {
-    const int lo = end_of(a, e - 1), hi = end_of(a, e), n = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
-    if ((int)blockIdx.x < tile + n) {
-      const int m0 = ((int)blockIdx.x - tile) * kTile;
-      const T* w = static_cast<const T*>(a.w) + (int64_t)e * N * D;
-      const int depth = KIND == Gmm16::kForward ? D : N, cols = KIND == Gmm16::kForward ? N : D;
-      const T* x = rows + (int64_t)lo * depth;
-      tile_product(
-          m0, c0, hi - lo, cols, depth, [&](int m, int k) { return to_f32<T>(x[(int64_t)m * depth + k]); },
-          [&](int k, int n) { return to_f32<T>(KIND == Gmm16::kForward ? w[(int64_t)n * D + k] : w[(int64_t)k * D + n]); },
-          out + (int64_t)lo * cols, (int64_t)cols, false);
-      return;
+    // the next kernel's setup beside the last items
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // the last stages' releases: commits arrive in both CTAs of a pair, and neither may leave
+    // before an arrival that is still on its way to it
+    for (int s = 0; ok && s < S; ++s, at.next(S)) ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status);
+    if (lane == 0) s_issued[warp == kBWarp] = n;
+  } else if (RELAY && warp == kRelayWarp) {
+    RingPos at;
+    int e_hint = 0;
+    bool ok = true;
+    for (int j = first; ok && j < total; j += stride) {
+      const Item it = item(j, e_hint);
+      const int n = steps(it), KB = (n + 63) / 64;
+      for (int kb = 0; kb < KB; ++kb, at.next(S)) {
+        if (!(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status))) break;
+        const uint32_t to = PAIR ? cluster_addr(&ready_bar[at.slot], 0) : smem_u32(&ready_bar[at.slot]);
+        const int left = n - kb * 64, upto = (left + 15) & ~15;
+        if (W && left < 64 && left < upto) {
+          // rows of the next expert, in the four boxes of both operands (a row is 128 bytes of each)
+          uint8_t* box = smem_raw + at.slot * C::kStageBytes + (lane >> 3) * 8192 + (lane & 7) * 16;
+          for (int r = left; r < upto; ++r) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote_release(to);
+        } else if (lane == 0) {
+          mbar_arrive_remote(to);
+        }
+      }
     }
-    tile += n;
+  } else if (warp == kMmaWarp) {
+    if (rank == 0) {
+      const uint32_t elected = elect_one(), t0 = __shfl_sync(0xffffffffu, tmem, 0);
+      uint64_t* there_bar = RELAY ? ready_bar : full_bar;
+      RingPos at;
+      int e_hint = 0, u = 0;
+      bool ok = true;
+      // a barrier's answer takes as long as issuing several MMAs: the next stage's is asked for
+      // before this one's are issued
+      uint32_t there = mbar_test(&there_bar[0], 0);
+      for (int j = first; ok && j < total; j += stride, ++u) {
+        const Item it = item(j, e_hint);
+        const int buf = u & 1, n = steps(it), KB = (n + 63) / 64;
+        if (!(ok = warp_wait(&accempty_bar[buf], ((u >> 1) & 1) ^ 1, abort_flag, a.status))) break;
+        tc_fence_after();
+        const uint32_t idesc = f16_idesc(a.bf16, A_MN, W, PAIR ? 256 : 128, it.n), d = t0 + buf * NT;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!__all_sync(0xffffffffu, there) &&
+              !(ok = warp_wait(&there_bar[at.slot], at.phase, abort_flag, a.status)))
+            break;
+          if (W && PAIR && kb == KB - 1) mbar_acquire_cluster(&there_bar[at.slot], at.phase);
+          tc_fence_after();
+          const uint32_t st = ring + at.slot * C::kStageBytes;
+          const uint64_t da = A_MN ? sw128_mn_desc(st) : sw128_desc(st);
+          const uint64_t db = W ? sw128_mn_desc(st + kABytes) : sw128_desc(st + kABytes);
+          const uint32_t done = smem_u32(&empty_bar[at.slot]);
+          at.next(S);
+          there = mbar_test(&there_bar[at.slot], at.phase);
+          const int last = kb < KB - 1 ? 4 : (n - kb * 64 + 15) >> 4;  // 16 steps an MMA
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (k < last)
+              f16_mma<PAIR>(elected, d, da + k * (A_MN ? 128 : 2), db + k * (W ? 128 : 2), idesc, kb || k ? 1u : 0u);
+          mx_commit<PAIR>(elected, done);
+        }
+        if (ok) mx_commit<PAIR>(elected, smem_u32(&accfull_bar[buf]));
+      }
+      mx_commit_local<PAIR>(elected, smem_u32(&final_bar));  // every MMA done before tensor memory is freed
+      mbar_wait_sleep_bounded(&final_bar, 0);
+    }
+  } else if (warp >= kEpiWarp0) {
+    const int group = (warp - kEpiWarp0) >> 2, quarter = warp & 3, buf = group;
+    const uint32_t lanes = (uint32_t)quarter << 21;  // 32 * quarter in the lane field
+    int e_hint = 0;
+    for (int u = buf, j = first + buf * stride; j < total; j += 2 * stride, u += 2) {
+      const Item it = item(j, e_hint);
+      bool ok = warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status);
+      ok = group_all(9 + group, ok);  // the group's warps wait for one another below
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t t = tmem + lanes + buf * NT;
+      const int m0 = (PAIR ? 2 * it.cb + (int)rank : it.cb) * 128;
+      if constexpr (W) {
+        // a warp's 32 channels, 128 bytes of columns at a time, in the 128-byte swizzle of the output's map
+        uint8_t* own = smem_raw + S * C::kStageBytes + (warp - kEpiWarp0) * 4096;
+        uint4* row = reinterpret_cast<uint4*>(own + lane * 128);
+        const int cols = a.out_f32 ? 32 : 64, n = min(NT, a.D - it.col0), y = m0 + quarter * 32;
+        if (y < a.N && !(it.rows == 0 && a.accumulate)) {
+          for (int c0 = 0; c0 < n; c0 += cols) {
+            uint32_t v[4][16];
+            __syncwarp();
+            if (it.rows) {
+              tmem_ld16(t + c0, v[0]);
+              if (c0 + 16 < it.n) tmem_ld16(t + c0 + 16, v[1]);
+              if (!a.out_f32) {
+                if (c0 + 32 < it.n) tmem_ld16(t + c0 + 32, v[2]);
+                if (c0 + 48 < it.n) tmem_ld16(t + c0 + 48, v[3]);
+              }
+              tmem_wait_ld();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 64; ++i) v[i >> 4][i & 15] = 0;
+            }
+            bulk_wait_read_all();
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              uint4 o;
+              if (a.out_f32) {
+                o = make_uint4(v[i >> 2][(i * 4) & 15], v[i >> 2][(i * 4 + 1) & 15], v[i >> 2][(i * 4 + 2) & 15],
+                               v[i >> 2][(i * 4 + 3) & 15]);
+              } else {
+                const uint32_t(&x)[16] = v[i >> 1];
+                const int k = (i & 1) * 8;
+                o = make_uint4(pack16(a.bf16, x[k], x[k + 1]), pack16(a.bf16, x[k + 2], x[k + 3]),
+                               pack16(a.bf16, x[k + 4], x[k + 5]), pack16(a.bf16, x[k + 6], x[k + 7]));
+              }
+              row[i ^ (lane & 7)] = o;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (a.accumulate) tma_add_3d(&maps.out, it.col0 + c0, y, it.e, own);
+              else tma_store_3d(&maps.out, it.col0 + c0, y, it.e, own);
+              bulk_commit_group();
+            }
+          }
+        }
+      } else {
+        // 32 rows x 128 channels gathered in shared memory and stored from there by one tensor copy,
+        // or, where the tile's last rows are not its own, row by row
+        uint8_t* own = smem_raw + S * C::kStageBytes + group * (kOutRows * 256);
+        const int width = min(128, out_rows - m0);  // channels; none of a pair's block past the last
+        const int rows = width > 0 ? it.rows : 0;
+        for (int c0 = 0; c0 < it.n; c0 += kOutRows) {
+          uint32_t v[2][16];
+          __syncwarp();
+          tmem_ld16(t + c0, v[0]);
+          if (!PAIR && c0 + 16 >= it.n) {  // a single CTA's tile may end after 16 columns
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[1][i] = 0;
+          } else {
+            tmem_ld16(t + c0 + 16, v[1]);
+          }
+          if (quarter == 0) bulk_wait_read_all();
+          tmem_wait_ld();
+          asm volatile("bar.sync %0, 128;" ::"r"(9 + group) : "memory");
+          uint16_t* o = reinterpret_cast<uint16_t*>(own) + quarter * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const uint32_t h = pack16(a.bf16, v[i >> 4][i & 15], v[i >> 4][(i & 15) + 1]);
+            o[i * 128] = (uint16_t)h;
+            o[i * 128 + 128] = (uint16_t)(h >> 16);
+          }
+          fence_proxy_async_smem();
+          asm volatile("bar.sync %0, 128;" ::"r"(9 + group) : "memory");
+          if (quarter == 0) {
+            if (c0 + kOutRows <= rows) {
+              if (lane == 0) tma_store_2d(&maps.out, m0, it.row0 + c0, own);
+            } else if (c0 + lane < rows) {
+              bulk_store(static_cast<uint16_t*>(a.out) + (size_t)(it.row0 + c0 + lane) * out_rows + m0, own + lane * 256,
+                         (uint32_t)width * 2);
+            }
+            bulk_commit_group();
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if (PAIR) mbar_arrive_remote(cluster_addr(&accempty_bar[buf], 0)); else mbar_arrive(&accempty_bar[buf]);
+      }
+    }
+    bulk_wait_all();  // stores done before shared memory is released
   }
+
+  __syncthreads();
+  if (threadIdx.x == 0) {  // copies still in flight (only after an abort) land before shared memory is released
+    const int n0 = min(s_issued[0], s_issued[1]), n1 = max(s_issued[0], s_issued[1]);
+    for (int n = n0; n < n1; ++n) mbar_arrive(&full_bar[n % S]);  // stages that one of the two loaders never began
+    for (int n = max(0, n1 - S); n < n1; ++n) mbar_wait_bounded(&full_bar[n % S], (n / S) & 1);
+  }
+  tc_fence_before();
+  __syncthreads();
+  __syncwarp();
+  if (PAIR) cluster_sync_all();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc<PAIR, C::kTmemCols>(tmem);
   }
 }
 
-template <typename T>
+// 3-D map [e][outer][inner] of `elem`-byte elements in the 128-byte swizzle.
+bool encode_tensor_map_3d(CUtensorMap* m, CUtensorMapDataType dt, size_t elem, const void* base, uint64_t inner,
+                          uint64_t outer, uint64_t e, uint32_t box_inner, uint32_t box_outer) {
+  PFN_encodeTiled fn = tensor_map_encoder();
+  if (!fn) return false;
+  cuuint64_t dims[3] = {inner, outer, e};
+  cuuint64_t strides[2] = {inner * elem, inner * outer * elem};
+  cuuint32_t box[3] = {box_inner, box_outer, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Gmm16 KIND, int NT, bool PAIR>
 cudaError_t launch(const Gmm16Problem& p, cudaStream_t stream) {
-  Args a{p.R, p.E, p.N, p.D, p.cumsum, p.rows, p.rows2, p.w, p.out, p.status, p.accumulate};
-  const unsigned tn = (unsigned)(p.N + kTile - 1) / kTile, td = (unsigned)(p.D + kTile - 1) / kTile;
-  const unsigned tiles = (unsigned)(p.R / kTile + (p.R < p.E ? p.R : p.E));  // an expert's last tile may be short
-  if (p.kind == Gmm16::kForward)
-    gmm16_kernel<T, T, Gmm16::kForward><<<dim3(tiles, tn), kThreads, 0, stream>>>(a);
-  else if (p.kind == Gmm16::kInput)
-    gmm16_kernel<T, T, Gmm16::kInput><<<dim3(tiles, td), kThreads, 0, stream>>>(a);
-  else if (p.out_f32)
-    gmm16_kernel<T, float, Gmm16::kWeight><<<dim3(tn, td, (unsigned)p.E), kThreads, 0, stream>>>(a);
-  else
-    gmm16_kernel<T, T, Gmm16::kWeight><<<dim3(tn, td, (unsigned)p.E), kThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  using C = Cfg<KIND, NT, PAIR>;
+  const CUtensorMapDataType t = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const uint64_t R = p.R, E = p.E, N = p.N, D = p.D;
+  Maps maps;
+  bool ok;
+  if (KIND == Gmm16::kWeight) {
+    ok = encode_tensor_map_2d(&maps.a, t, 2, p.rows, N, R, 64, 64) && encode_tensor_map_2d(&maps.b[0], t, 2, p.rows2, D, R, 64, 64) &&
+         (p.out_f32 ? encode_tensor_map_3d(&maps.out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.out, D, N, E, 32, 32)
+                    : encode_tensor_map_3d(&maps.out, t, 2, p.out, D, N, E, 64, 32));
+    maps.b[1] = maps.b[2] = maps.b[0];
+  } else {
+    const uint64_t depth = KIND == Gmm16::kForward ? D : N, outs = KIND == Gmm16::kForward ? N : D;
+    ok = encode_tensor_map_3d(&maps.a, t, 2, p.w, D, N, E, 64, KIND == Gmm16::kForward ? 128 : 64) &&
+         encode_tensor_map_2d(&maps.out, t, 2, p.out, outs, R, 128, kOutRows, CU_TENSOR_MAP_SWIZZLE_NONE);
+    for (int b = 0; ok && b < kBoxes; ++b)
+      ok = encode_tensor_map_2d(&maps.b[b], t, 2, p.rows, depth, R, 64, (uint32_t)kBoxRows >> b);
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  static PerContextOnce set;
+  const int dev = current_device();
+  if (set.needed(dev)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(gmm16_kernel<KIND, NT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    set.done(dev);
+  }
+  Args a{p.R, p.E, p.N, p.D, p.cumsum, p.out, p.status, p.bf16, p.out_f32, p.accumulate};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(PAIR ? sm_count() & ~1 : sm_count()));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = PAIR ? 2 : 1;
+  attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, gmm16_kernel<KIND, NT, PAIR>, maps, a);
 }
 
 }  // namespace
 
 cudaError_t launch_gmm16(const Gmm16Problem& p, cudaStream_t stream) {
-  return p.bf16 ? launch<__nv_bfloat16>(p, stream) : launch<__half>(p, stream);
+  if (p.kind == Gmm16::kWeight) return launch<Gmm16::kWeight, 256, true>(p, stream);
+  const bool few = (double)p.R / p.E <= 32.0;
+  if (p.kind == Gmm16::kForward)
+    return few ? launch<Gmm16::kForward, 32, false>(p, stream) : launch<Gmm16::kForward, 256, true>(p, stream);
+  return few ? launch<Gmm16::kInput, 32, false>(p, stream) : launch<Gmm16::kInput, 256, true>(p, stream);
 }
 
 }  // namespace moe
