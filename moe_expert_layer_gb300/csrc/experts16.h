@@ -51,7 +51,7 @@ struct Lora16Problem {
   void* out;
   float* v;  // workspace
 };
-size_t lora16_workspace_bytes(int M, int D, int rank);
+size_t lora16_workspace_bytes(int M, int rank);
 cudaError_t launch_lora16(const Lora16Problem& p, cudaStream_t stream);
 
 }  // namespace moe

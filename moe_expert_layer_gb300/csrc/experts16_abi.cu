@@ -160,7 +160,7 @@ int32_t moe_combine16_grad(int32_t M, int32_t D, int32_t copies, int32_t rows, i
 size_t moe_lora16_workspace_size(int32_t M, int32_t N, int32_t D, int32_t rank) {
   if (!rows_ok(M) || !size_ok(N, moe::kMax16Size) || !size_ok(D, moe::kMax16Size) || !size_ok(rank, moe::kMax16Rank))
     return 0;
-  return (moe::lora16_workspace_bytes(M, D, rank) + kAlign - 1) & ~(kAlign - 1);
+  return (moe::lora16_workspace_bytes(M, rank) + kAlign - 1) & ~(kAlign - 1);
 }
 
 int32_t moe_lora16(int32_t M, int32_t N, int32_t D, int32_t rank, int32_t L, int32_t type, const void* x,
