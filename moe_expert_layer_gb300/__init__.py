@@ -562,9 +562,23 @@ def moe_selftest_mxfp4_tickets(answers, stream=None):
 
 
 # --------------------------------------------------------------- include/moe_experts16.h
+# Arrays have exactly the shapes that a call names, and lie in the memory of the current device, where
+# the call is launched, on its current stream.  Short calls are bound by the host: one condition looks
+# at everything, and only a refusal finds out what was wrong.
 _TYPES16 = {"torch.float16": TYPE_F16, "torch.bfloat16": TYPE_BF16}
 _types16 = {}
-_current_device = None
+_device = None
+
+
+def _find_device():
+    """A function that gives the current device's index."""
+    global _device
+    import torch
+    if not torch.cuda.is_available():
+        return -2  # no tensor's
+    torch.cuda.current_stream()  # initialises CUDA
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _device()
 
 
 def _type16(t, what):
@@ -576,32 +590,33 @@ def _type16(t, what):
     return k
 
 
-def _array(t, shape, dtype, what):
-    """Pointer of a dense array of exactly this shape and type."""
-    if t.dtype != dtype or t.shape != shape:
-        raise ValueError("%s: %s of %s wanted; got %s of %s" % (what, tuple(shape), dtype, tuple(t.shape), t.dtype))
-    return _p(t)
+def _refuse(t, wanted, dev, what):
+    if t.get_device() != dev and t.is_contiguous():
+        raise ValueError("%s: %s on the current device wanted; got %s of %s on %s"
+                         % (what, wanted, tuple(t.shape), t.dtype, t.device))
+    raise ValueError("%s: %s, dense, wanted; got %s of %s with strides %s"
+                     % (what, wanted, tuple(t.shape), t.dtype, tuple(t.stride())))
 
 
-def _int32s(t, n, what):
-    """Pointer of a dense array of n 32-bit integers, of any shape."""
-    if t.numel() != n or (t.dtype not in _INT32 and not _INT32.takes(t.dtype)):
-        raise ValueError("%s: %d elements of int32 wanted; got %d of %s" % (what, n, t.numel(), t.dtype))
-    return _p(t)
+def _array(t, shape, dtype, dev, what):
+    """Pointer of a dense array of exactly this shape and type on the device."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, "%s of %s" % (tuple(shape), dtype), dev, what)
+    return t.data_ptr()
 
 
-def _here(*tensors):
-    """Every tensor in the memory of the current device: a call launches there, on its stream."""
-    global _current_device
-    if _current_device is None:
-        import torch
-        if not torch.cuda.is_available():
-            raise ValueError("arrays on the GPU wanted")
-        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-    dev = _current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("arrays on the current device (%d) wanted; got one on %s" % (dev, t.device))
+def _list(t, n, kind, dev, what):
+    """Pointer of a dense array of n elements of a kind, of any shape."""
+    if t.numel() != n or (t.dtype not in kind and not kind.takes(t.dtype)) or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, "%d elements of %s" % (n, kind.name), dev, what)
+    return t.data_ptr()
+
+
+def _space(t, dev):
+    """Pointer and bytes of a workspace."""
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, "an array", dev, "workspace")
+    return t.data_ptr(), t.numel() * t.element_size()
 
 
 def moe_gmm16_workspace_size(R, E, N, D):
@@ -611,85 +626,82 @@ def moe_gmm16_workspace_size(R, E, N, D):
 def moe_gmm16(a, cumsum, w, c, workspace, stream=None):
     """c [R][N] = rows a [R][D] times their experts' w [E][N][D]^T, all of one 16-bit type."""
     (R, D), (E, N, _), t = a.shape, w.shape, a.dtype
-    args = (R, E, N, D, _type16(a, "a"), _p(a), _int32s(cumsum, E, "cumsum"), _array(w, (E, N, D), t, "w"),
-            _array(c, (R, N), t, "c"), _p(workspace), _nbytes(workspace))
-    _here(a, cumsum, w, c, workspace)
-    _check("moe_gmm16", load_library().moe_gmm16(*args, _stream(stream)))
+    dev = _device() if _device else _find_device()
+    _check("moe_gmm16", load_library().moe_gmm16(
+        R, E, N, D, _type16(a, "a"), _array(a, (R, D), t, dev, "a"), _list(cumsum, E, _INT32, dev, "cumsum"),
+        _array(w, (E, N, D), t, dev, "w"), _array(c, (R, N), t, dev, "c"), *_space(workspace, dev), _stream(stream)))
 
 
 def moe_gmm16_input_grad(dc, cumsum, w, da, workspace, stream=None):
     """da [R][D] = rows dc [R][N] times their experts' w [E][N][D]."""
     (R, N), (E, _, D), t = dc.shape, w.shape, dc.dtype
-    args = (R, E, N, D, _type16(dc, "dc"), _p(dc), _int32s(cumsum, E, "cumsum"), _array(w, (E, N, D), t, "w"),
-            _array(da, (R, D), t, "da"), _p(workspace), _nbytes(workspace))
-    _here(dc, cumsum, w, da, workspace)
-    _check("moe_gmm16_input_grad", load_library().moe_gmm16_input_grad(*args, _stream(stream)))
+    dev = _device() if _device else _find_device()
+    _check("moe_gmm16_input_grad", load_library().moe_gmm16_input_grad(
+        R, E, N, D, _type16(dc, "dc"), _array(dc, (R, N), t, dev, "dc"), _list(cumsum, E, _INT32, dev, "cumsum"),
+        _array(w, (E, N, D), t, dev, "w"), _array(da, (R, D), t, dev, "da"), *_space(workspace, dev), _stream(stream)))
 
 
 def moe_gmm16_weight_grad(dc, a, cumsum, dw, workspace, accumulate=False, stream=None):
     """dw [E][N][D] (the rows' type or float32) = sum over each expert's rows of dc [R][N]^T a [R][D]; accumulate
     (float32) adds it to dw."""
     (R, N), (E, _, D), t = dc.shape, dw.shape, dc.dtype
-    kind = _type16(dc, "dc")
-    out = kind if dw.dtype == t else _type(dw)
-    args = (R, E, N, D, kind, _p(dc), _array(a, (R, D), t, "a"), _int32s(cumsum, E, "cumsum"),
-            _array(dw, (E, N, D), dw.dtype, "dw"), out, 1 if accumulate else 0, _p(workspace), _nbytes(workspace))
-    _here(dc, a, cumsum, dw, workspace)
-    _check("moe_gmm16_weight_grad", load_library().moe_gmm16_weight_grad(*args, _stream(stream)))
+    dev, kind = _device() if _device else _find_device(), _type16(dc, "dc")
+    out = kind if dw.dtype is t else _type(dw)
+    p, size = _space(workspace, dev)
+    _check("moe_gmm16_weight_grad", load_library().moe_gmm16_weight_grad(
+        R, E, N, D, kind, _array(dc, (R, N), t, dev, "dc"), _array(a, (R, D), t, dev, "a"),
+        _list(cumsum, E, _INT32, dev, "cumsum"), _array(dw, (E, N, D), dw.dtype, dev, "dw"), out,
+        1 if accumulate else 0, p, size, _stream(stream)))
 
 
 def moe_swiglu16(gu, cumsum, h, stream=None):
     """h [R][I] = silu(g) u of the experts' rows gu [R][2 I] = (g, u)."""
-    (R, I), E = h.shape, cumsum.numel()
-    args = (R, E, I, _type16(gu, "gu"), _array(gu, (R, 2 * I), gu.dtype, "gu"), _int32s(cumsum, E, "cumsum"),
-            _array(h, (R, I), gu.dtype, "h"))
-    _here(gu, cumsum, h)
-    _check("moe_swiglu16", load_library().moe_swiglu16(*args, _stream(stream)))
+    (R, I), E, t = h.shape, cumsum.numel(), gu.dtype
+    dev = _device() if _device else _find_device()
+    _check("moe_swiglu16", load_library().moe_swiglu16(
+        R, E, I, _type16(gu, "gu"), _array(gu, (R, 2 * I), t, dev, "gu"), _list(cumsum, E, _INT32, dev, "cumsum"),
+        _array(h, (R, I), t, dev, "h"), _stream(stream)))
 
 
 def moe_swiglu16_grad(dh, gu, cumsum, dgu, h=None, stream=None):
     """dgu [R][2 I] (it may be gu) from dh [R][I] and gu; h [R][I], where given, gets moe_swiglu16's (it may be dh)."""
     (R, I), E, t = dh.shape, cumsum.numel(), dh.dtype
-    args = (R, E, I, _type16(dh, "dh"), _p(dh), _array(gu, (R, 2 * I), t, "gu"), _int32s(cumsum, E, "cumsum"),
-            _array(dgu, (R, 2 * I), t, "dgu"), None if h is None else _array(h, (R, I), t, "h"))
-    _here(dh, gu, cumsum, dgu, h)
-    _check("moe_swiglu16_grad", load_library().moe_swiglu16_grad(*args, _stream(stream)))
+    dev = _device() if _device else _find_device()
+    _check("moe_swiglu16_grad", load_library().moe_swiglu16_grad(
+        R, E, I, _type16(dh, "dh"), _array(dh, (R, I), t, dev, "dh"), _array(gu, (R, 2 * I), t, dev, "gu"),
+        _list(cumsum, E, _INT32, dev, "cumsum"), _array(dgu, (R, 2 * I), t, dev, "dgu"),
+        None if h is None else _array(h, (R, I), t, dev, "h"), _stream(stream)))
 
 
 def moe_dispatch16(x, row_map, out, copies=1, stream=None):
     """out [rows][D]: row row_map[t][j] = x[t], j < copies."""
-    (M, D), rows = x.shape, out.shape[0]
-    args = (M, D, copies, rows, _type16(x, "x"), _p(x), _int32s(row_map, M * copies, "row_map"),
-            _array(out, (rows, D), x.dtype, "out"))
-    _here(x, row_map, out)
-    _check("moe_dispatch16", load_library().moe_dispatch16(*args, _stream(stream)))
+    (M, D), (rows, _), t = x.shape, out.shape, x.dtype
+    dev = _device() if _device else _find_device()
+    _check("moe_dispatch16", load_library().moe_dispatch16(
+        M, D, copies, rows, _type16(x, "x"), _array(x, (M, D), t, dev, "x"),
+        _list(row_map, M * copies, _INT32, dev, "row_map"), _array(out, (rows, D), t, dev, "out"), _stream(stream)))
 
 
 def moe_combine16(y, row_map, probs, out, copies=1, stream=None):
     """out [M][D] = sum over j < copies of probs[t][j] (None: 1) * y[row_map[t][j]]."""
-    (M, D), rows = out.shape, y.shape[0]
-    args = (M, D, copies, rows, _type16(y, "y"), _array(y, (rows, D), y.dtype, "y"),
-            _int32s(row_map, M * copies, "row_map"), None if probs is None else _floats(probs, M * copies, "probs"),
-            _array(out, (M, D), y.dtype, "out"))
-    _here(y, row_map, probs, out)
-    _check("moe_combine16", load_library().moe_combine16(*args, _stream(stream)))
+    (M, D), (rows, _), t = out.shape, y.shape, y.dtype
+    dev = _device() if _device else _find_device()
+    _check("moe_combine16", load_library().moe_combine16(
+        M, D, copies, rows, _type16(y, "y"), _array(y, (rows, D), t, dev, "y"),
+        _list(row_map, M * copies, _INT32, dev, "row_map"),
+        None if probs is None else _list(probs, M * copies, _FLOAT32, dev, "probs"), _array(out, (M, D), t, dev, "out"),
+        _stream(stream)))
 
 
 def moe_combine16_grad(dout, y, row_map, probs, dy, dprobs, copies=1, stream=None):
     """dy [rows][D] (it may be y): row row_map[t][j] = probs[t][j] dout[t]; dprobs[t][j] = <dout[t], y[row_map[t][j]]>."""
-    (M, D), rows, t = dout.shape, y.shape[0], dout.dtype
-    args = (M, D, copies, rows, _type16(dout, "dout"), _p(dout), _array(y, (rows, D), t, "y"),
-            _int32s(row_map, M * copies, "row_map"), _floats(probs, M * copies, "probs"),
-            _array(dy, (rows, D), t, "dy"), _floats(dprobs, M * copies, "dprobs"))
-    _here(dout, y, row_map, probs, dy, dprobs)
-    _check("moe_combine16_grad", load_library().moe_combine16_grad(*args, _stream(stream)))
-
-
-def _floats(t, n, what):
-    """Pointer of a dense array of n fp32, of any shape."""
-    if t.numel() != n or (t.dtype not in _FLOAT32 and not _FLOAT32.takes(t.dtype)):
-        raise ValueError("%s: %d elements of float32 wanted; got %d of %s" % (what, n, t.numel(), t.dtype))
-    return _p(t)
+    (M, D), (rows, _), t = dout.shape, y.shape, dout.dtype
+    dev = _device() if _device else _find_device()
+    _check("moe_combine16_grad", load_library().moe_combine16_grad(
+        M, D, copies, rows, _type16(dout, "dout"), _array(dout, (M, D), t, dev, "dout"),
+        _array(y, (rows, D), t, dev, "y"), _list(row_map, M * copies, _INT32, dev, "row_map"),
+        _list(probs, M * copies, _FLOAT32, dev, "probs"), _array(dy, (rows, D), t, dev, "dy"),
+        _list(dprobs, M * copies, _FLOAT32, dev, "dprobs"), _stream(stream)))
 
 
 def moe_lora16_workspace_size(M, N, D, rank):
@@ -700,9 +712,10 @@ def moe_lora16(x, route, cumsum, a, b, base, out, workspace, scales=None, stream
     """out [M][N] (it may be base) = base + scales[l] b[l] (a[l] x[t]), a [L][rank][D], b [L][N][rank], l the adapter of
     token t; route [M], cumsum [L]: sorted_src_route and cumsum of moe_route_sort on the tokens' adapters."""
     (M, D), (L, rank, _), N, t = x.shape, a.shape, b.shape[1], x.dtype
-    args = (M, N, D, rank, L, _type16(x, "x"), _p(x), _int32s(route, M, "route"), _int32s(cumsum, L, "cumsum"),
-            _array(a, (L, rank, D), t, "a"), _array(b, (L, N, rank), t, "b"),
-            None if scales is None else _floats(scales, L, "scales"), _array(base, (M, N), t, "base"),
-            _array(out, (M, N), t, "out"), _p(workspace), _nbytes(workspace))
-    _here(x, route, cumsum, a, b, scales, base, out, workspace)
-    _check("moe_lora16", load_library().moe_lora16(*args, _stream(stream)))
+    dev = _device() if _device else _find_device()
+    _check("moe_lora16", load_library().moe_lora16(
+        M, N, D, rank, L, _type16(x, "x"), _array(x, (M, D), t, dev, "x"), _list(route, M, _INT32, dev, "route"),
+        _list(cumsum, L, _INT32, dev, "cumsum"), _array(a, (L, rank, D), t, dev, "a"),
+        _array(b, (L, N, rank), t, dev, "b"), None if scales is None else _list(scales, L, _FLOAT32, dev, "scales"),
+        _array(base, (M, N), t, dev, "base"), _array(out, (M, N), t, dev, "out"), *_space(workspace, dev),
+        _stream(stream)))

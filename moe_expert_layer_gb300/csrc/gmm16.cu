@@ -25,8 +25,8 @@
 //
 // Roles: warp 0 loads operand A and warp 2 operand B, 64 steps of the reduction a stage, into a ring
 // in shared memory; warp 3 (pairs) tells the leading CTA that a stage has landed; warp 1 of the
-// leading CTA issues the MMAs; warps 4-11 are two groups, one for each of the two accumulators, that
-// round the sums and store them.  Every wait is bounded: one that gives up records MOE_ERR_TIMEOUT
+// leading CTA issues the MMAs; warps 4-11, two groups, round the sums of one accumulator and store them
+// while the MMAs fill the other.  Every wait is bounded: one that gives up records MOE_ERR_TIMEOUT
 // and the CTA winds down.
 #include "experts16.h"
 #include "mx_tc.cuh"
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(&accfull_bar[s], 1);
-        mbar_init(&accempty_bar[s], PAIR ? 8 : 4);
+        mbar_init(&accempty_bar[s], PAIR ? 16 : 8);
       }
       mbar_init(&final_bar, 1);
       fence_barrier_init();
@@ -432,11 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       mbar_wait_sleep_bounded(&final_bar, 0);
     }
   } else if (warp >= kEpiWarp0) {
-    const int group = (warp - kEpiWarp0) >> 2, quarter = warp & 3, buf = group;
+    // both groups take part in every item: while they drain one accumulator the MMAs fill the other
+    const int group = (warp - kEpiWarp0) >> 2, quarter = warp & 3;
     const uint32_t lanes = (uint32_t)quarter << 21;  // 32 * quarter in the lane field
     int e_hint = 0;
-    for (int u = buf, j = first + buf * stride; j < total; j += 2 * stride, u += 2) {
+    for (int u = 0, j = first; j < total; j += stride, ++u) {
       const Item it = item(j, e_hint);
+      const int buf = u & 1;
       bool ok = warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status);
       ok = group_all(9 + group, ok);  // the group's warps wait for one another below
       if (!ok) break;
@@ -449,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         uint4* row = reinterpret_cast<uint4*>(own + lane * 128);
         const int cols = a.out_f32 ? 32 : 64, n = min(NT, a.D - it.col0), y = m0 + quarter * 32;
         if (y < a.N && !(it.rows == 0 && a.accumulate)) {
-          for (int c0 = 0; c0 < n; c0 += cols) {
+          for (int c0 = group * cols; c0 < n; c0 += 2 * cols) {
             uint32_t v[4][16];
             __syncwarp();
             if (it.rows) {
@@ -495,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         uint8_t* own = smem_raw + S * C::kStageBytes + group * (kOutRows * 256);
         const int width = min(128, out_rows - m0);  // channels; none of a pair's block past the last
         const int rows = width > 0 ? it.rows : 0;
-        for (int c0 = 0; c0 < it.n; c0 += kOutRows) {
+        for (int c0 = group * kOutRows; c0 < it.n; c0 += 2 * kOutRows) {
           uint32_t v[2][16];
           __syncwarp();
           tmem_ld16(t + c0, v[0]);

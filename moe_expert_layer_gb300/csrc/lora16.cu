@@ -4,19 +4,25 @@
 // out once each, and the adapters' weights, which are all there is to read in a decode batch.
 //
 // Both products are warp-level MMAs (m16n8k16, fp32 sums): with ranks up to 128 they are far too thin
-// for tcgen05's 128 rows, and need no shared memory.  An MMA's order of the reduction index is free as
-// long as both operands have the same, so each lane takes its operands as 16 bytes straight from a
-// row: lane (g, t) holds elements 8 t .. 8 t + 7 of 32, the first four for one MMA and the others for
-// the next; a row's 64 bytes come with one load of four lanes.
+// for tcgen05's 128 rows.  An MMA's order of the reduction index is free as long as both operands have
+// the same, so a lane can take its operands as 16 bytes straight from a row: lane (g, t) holds elements
+// 8 t .. 8 t + 7 of 32, the first four for one MMA and the others for the next; a row's 64 bytes come
+// with one load of four lanes.
 //
-// Shrink: a block per tile and share of D; its warps take 32-deep slices in turn and add up over
-// shared memory.  The shares' sums are left in fp32 and added, in order, by the second kernel.
-// Expand: a block per tile and share of N.  v goes into the MMA as two 16-bit numbers, v 2^-e = hi +
-// lo with e the exponent of the token's largest: 16 significant bits or more, and no rank value
-// leaves binary16's range.  The columns of four MMAs are dealt out so that a lane gets eight
-// neighbouring channels of a token, 16 bytes of base and out.
+// Many tokens to an adapter, two kernels.  Shrink: a block per tile of 64 tokens and share of D; tokens and
+// ranks pass through a ring in shared memory, 64 deep a stage, and the warps divide the outputs.  The shares'
+// sums are left in fp32 and added, in order, by the second kernel.  Expand: a block per tile and share
+// of N.  It begins, as a programmatic dependent, once every block of the first kernel is past its own
+// wait: what that one does not write (tables, weights, base) is read ahead of this one's wait.
+// Few tokens: one kernel, a cluster per tile of 16.
+//
+// v goes into the second MMA as two 16-bit numbers, s v 2^-e = hi + lo with e the exponent of the token's
+// largest: 16 significant bits or more, and no rank value leaves binary16's range.  The columns of
+// four MMAs are dealt out so that a lane gets eight neighbouring channels of a token, 16 bytes of base
+// and out.
 #include "experts16.h"
 #include "mxfp4.cuh"
+#include "tc_common.cuh"
 #include "tensor_map.h"
 
 namespace moe {
@@ -28,14 +34,14 @@ template <typename T>
 __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1);
 template <>
 __device__ __forceinline__ void mma16<__half>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 template <>
 __device__ __forceinline__ void mma16<__nv_bfloat16>(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -53,107 +59,145 @@ __device__ __forceinline__ void mma32(float (&c)[4], const uint4& lo, const uint
 struct Tile {
   int l, start, rows;
 };
-// The whole block enters.  Thread i counts the tiles of adapters 4 i .. 4 i + 3 (L <= 1023).
-template <int TOKENS>
+// The whole block enters.  Thread i counts the tiles of the PER adapters from PER i (L <= 1023).
+template <int TOKENS, int THREADS>
 __device__ __forceinline__ Tile find_tile(int index, const int32_t* cumsum, int L, int M) {
-  __shared__ int s_warp[kWarps];
+  constexpr int PER = 1024 / THREADS, WARPS = THREADS / 32;
+  __shared__ int s_warp[WARPS];
   __shared__ Tile s_tile;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l0 = threadIdx.x * 4;
-  int end[5], count = 0;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l0 = threadIdx.x * PER;
+  int end[PER + 1], n[PER], count = 0;
 #pragma unroll
-  for (int i = 0; i < 5; ++i) end[i] = l0 + i - 1 < 0 ? 0 : l0 + i - 1 < L ? min(max(__ldcg(cumsum + l0 + i - 1), 0), M) : -1;
+  for (int i = 0; i <= PER; ++i) {
+    const int l = l0 + i - 1;
+    end[i] = l < 0 ? 0 : l < L ? min(max(__ldcg(cumsum + l), 0), M) : 0;
+  }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (end[i + 1] > end[i] && end[i] >= 0) count += (end[i + 1] - end[i] + TOKENS - 1) / TOKENS;
+  for (int i = 0; i < PER; ++i) {
+    n[i] = l0 + i < L && end[i + 1] > end[i] ? (end[i + 1] - end[i] + TOKENS - 1) / TOKENS : 0;
+    count += n[i];
+  }
   int incl = count;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int n = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += n;
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
   }
   if (lane == 31) s_warp[warp] = incl;
   if (threadIdx.x == 0) s_tile = Tile{-1, 0, 0};
   __syncthreads();
   int before = incl - count, all = 0;
-  for (int w = 0; w < kWarps; ++w) {
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += s_warp[w];
     all += s_warp[w];
   }
-  if (index >= before && index < before + count) {
-    int at = index - before;
-    for (int i = 0; i < 4; ++i) {
-      const int n = end[i + 1] > end[i] && end[i] >= 0 ? (end[i + 1] - end[i] + TOKENS - 1) / TOKENS : 0;
-      if (at < n) {
+  int at = index - before;
+  if (at >= 0 && at < count) {
+#pragma unroll
+    for (int i = 0; i < PER; ++i) {
+      if (at >= 0 && at < n[i])
         s_tile = Tile{l0 + i, end[i] + at * TOKENS, min(TOKENS, end[i + 1] - end[i] - at * TOKENS)};
-        break;
-      }
-      at -= n;
+      at -= n[i];
     }
   }
   if (threadIdx.x == 0 && index >= all) {
     const int start = min(max(__ldcg(cumsum + L - 1), 0), M) + (index - all) * TOKENS;
-    if (start < M && start >= 0) s_tile = Tile{-1, start, min(TOKENS, M - start)};
+    if (start < M) s_tile = Tile{-1, start, min(TOKENS, M - start)};
   }
   __syncthreads();
   return s_tile;
 }
 
-// MMA rows: ranks (MR x 16); columns: tokens (TN x 8).
-template <typename T, int MR, int TN>
-__global__ void __launch_bounds__(kThreads) lora16_shrink_kernel(const Lora16Problem p, int splits) {
-  extern __shared__ __align__(16) float s_part[];  // [kWarps][MR][TN][4][32]
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// Many tokens to an adapter.  MMA rows: tokens, 16 to each of four groups of two warps; columns:
+// ranks, MR x 8 to a warp.  A stage is 64 deep: rows of 128 bytes, their 16-byte pieces c at
+// c ^ (row % 8).
+constexpr int kManyTokens = 64, kStages = 4;
+template <typename T, int MR>
+__global__ void __launch_bounds__(kThreads) lora16_shrink_many_kernel(const Lora16Problem p, int splits) {
+  constexpr int kXBytes = kManyTokens * 128, kStage = kXBytes + MR * 16 * 128;
+  extern __shared__ __align__(128) uint8_t s_ring[];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int split = blockIdx.x % splits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const Tile tile = find_tile<TN * 8>(blockIdx.x / splits, p.cumsum, p.L, p.M);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int split = blockIdx.x % splits, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const Tile tile = find_tile<kManyTokens, kThreads>(blockIdx.x / splits, p.cumsum, p.L, p.M);
   if (tile.rows == 0 || tile.l < 0) return;
-  const int D = p.D, chunks = (D + 31) / 32, per = (chunks + splits - 1) / splits;
-  const int c1 = min(chunks, (split + 1) * per);
-  const T* a = static_cast<const T*>(p.a) + (int64_t)tile.l * p.rank * D;
-  const T* x[TN];
+  const int D = p.D, chunks = (D + 63) / 64, per = (chunks + splits - 1) / splits;
+  const int c0 = split * per, n = max(0, min(chunks - c0, per));
+  const int row = threadIdx.x >> 3, piece = threadIdx.x & 7;  // rows 32 apart
+  const T* x[2];
+  const T* any = static_cast<const T*>(p.x);
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int i = j * 8 + g, tok = i < tile.rows ? __ldcg(p.route + tile.start + i) : -1;
-    x[j] = (unsigned)tok < (unsigned)p.M ? static_cast<const T*>(p.x) + (int64_t)tok * D : nullptr;
+  for (int i = 0; i < 2; ++i) {
+    const int tok = row + 32 * i < tile.rows ? __ldcg(p.route + tile.start + row + 32 * i) : -1;
+    x[i] = (unsigned)tok < (unsigned)p.M ? any + (int64_t)tok * D : nullptr;
   }
-  float c[MR][TN][4] = {};
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-  for (int chunk = split * per + warp; chunk < c1; chunk += kWarps) {
-    const int k = chunk * 32 + t * 8;
-    const bool in = k < D;
-    uint4 b[TN], lo[MR], hi[MR];
+  const T* a = static_cast<const T*>(p.a) + (int64_t)tile.l * p.rank * D;
+  const uint32_t ring = smem_u32(s_ring), swizzled = (uint32_t)((piece ^ (row & 7)) << 4);
+  auto load = [&](int chunk, int stage) {
+    const int k = (c0 + chunk) * 64 + piece * 8;
+    const uint32_t st = ring + stage * kStage;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) b[j] = in && x[j] ? __ldcg(reinterpret_cast<const uint4*>(x[j] + k)) : zero;
-#pragma unroll
-    for (int m = 0; m < MR; ++m) {
-      const int r = m * 16 + g;
-      lo[m] = in && r < p.rank ? __ldcg(reinterpret_cast<const uint4*>(a + (int64_t)r * D + k)) : zero;
-      hi[m] = in && r + 8 < p.rank ? __ldcg(reinterpret_cast<const uint4*>(a + (int64_t)(r + 8) * D + k)) : zero;
+    for (int i = 0; i < 2; ++i) {
+      const bool in = x[i] && k < D;
+      copy16(st + (row + 32 * i) * 128 + swizzled, in ? x[i] + k : any, in);
     }
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-      if (TN <= 2 || j * 8 < tile.rows) {
+    for (int r0 = 0; r0 < MR * 16; r0 += 32) {
+      const int r = r0 + row;
+      const bool in = r < p.rank && k < D;
+      if (MR > 1 || r < 16) copy16(st + kXBytes + r * 128 + swizzled, in ? a + (int64_t)r * D + k : any, in);
+    }
+  };
 #pragma unroll
-        for (int m = 0; m < MR; ++m) mma32<T>(c[m][j], lo[m], hi[m], b[j]);
-      }
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (s < n) load(s, s);
+    asm volatile("cp.async.commit_group;" ::: "memory");
   }
+  const int tg = warp >> 1, half = warp & 1;  // tokens 16 tg .., ranks MR * 8 * half ..
+  const int arow = tg * 16 + (lane & 15), brow = half * MR * 8 + (lane & 7) + (MR > 1 ? (lane >> 4) * 8 : 0);
+  float c[MR][4] = {};
+  for (int i = 0; i < n; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncthreads();  // the stage has landed for all, and all are done with the one that is filled next
+    if (i + kStages - 1 < n) load(i + kStages - 1, (i + kStages - 1) % kStages);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint32_t st = ring + (i % kStages) * kStage;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint32_t f[4];
+      ldmatrix4(f, st + arow * 128 + (((2 * k + (lane >> 4)) ^ (arow & 7)) << 4));
+#pragma unroll
+      for (int m = 0; m < MR; m += 2) {
+        // two columns' tiles of eight ranks (with MR = 1 the second one is the first again)
+        uint32_t w[4];
+        const int r = brow + m * 8;
+        ldmatrix4(w, st + kXBytes + r * 128 + (((2 * k + ((lane >> 3) & 1)) ^ (r & 7)) << 4));
+        mma16<T>(c[m], f, w[0], w[1]);
+        if (m + 1 < MR) mma16<T>(c[m + 1], f, w[2], w[3]);
+      }
+    }
+  }
+  float* v = p.v + ((int64_t)split * p.M + tile.start) * p.rank;
 #pragma unroll
   for (int m = 0; m < MR; ++m)
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) s_part[((warp * MR + m) * TN + j) * 128 + q * 32 + lane] = c[m][j][q];
-  __syncthreads();
-  // element q of lane (g, t): rank 16 m + g + 8 (q / 2), token 8 j + 2 t + q % 2
-  float* v = p.v + ((int64_t)split * p.M + tile.start) * p.rank;
-  for (int i = threadIdx.x; i < MR * TN * 128; i += kThreads) {
-    float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += s_part[w * MR * TN * 128 + i];
-    const int l = i & 31, q = (i >> 5) & 3, j = (i >> 7) % TN, m = (i >> 7) / TN;
-    const int r = m * 16 + (l >> 2) + 8 * (q >> 1), tok = j * 8 + 2 * (l & 3) + (q & 1);
-    if (r < p.rank && tok < tile.rows) v[(int64_t)tok * p.rank + r] = s;
-  }
+    for (int h = 0; h < 2; ++h) {
+      const int tok = tg * 16 + (lane >> 2) + 8 * h, r = half * MR * 8 + m * 8 + (lane & 3) * 2;
+      if (tok < tile.rows && r < p.rank)
+        *reinterpret_cast<float2*>(v + (int64_t)tok * p.rank + r) = make_float2(c[m][2 * h], c[m][2 * h + 1]);
+    }
 }
 
 // 16-bit conversion that keeps infinities.
@@ -161,70 +205,179 @@ template <typename T> __device__ __forceinline__ T to16(float v);
 template <> __device__ __forceinline__ __half to16<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 to16<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// MMA rows: tokens (TM x 16); columns: channels, 32 in four MMAs; RC x 32 ranks.
-template <typename T, int RC, int TM>
-__global__ void __launch_bounds__(kThreads) lora16_expand_kernel(const Lora16Problem p, int splits, int shares) {
-  constexpr int kTokens = TM * 16, kPitch = RC * 32 + 8;  // elements: rows 16 bytes past a multiple of 64
-  __shared__ __align__(16) T s_hi[kTokens * kPitch], s_lo[kTokens * kPitch];
-  __shared__ float s_pow[kTokens];
-  __shared__ int s_tok[kTokens];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int share = blockIdx.x % shares, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const Tile tile = find_tile<kTokens>(blockIdx.x / shares, p.cumsum, p.L, p.M);
-  if (tile.rows == 0 || (tile.l < 0 && p.base == p.out)) return;
-  const int N = p.N, strips = (N + 31) / 32, per = (strips + shares - 1) / shares;
-  const int last = min(strips, (share + 1) * per);
+// s v of a token as 2^e (hi + lo), e the exponent of its largest finite value; a warp enters, lane r
+// with ranks q * 32 + r.  Returns 2^e.
+template <typename T, int RC>
+__device__ __forceinline__ float split_ranks(const float (&v)[RC], T* hi, T* lo, int lane) {
+  uint32_t most = 0;
+#pragma unroll
+  for (int q = 0; q < RC; ++q) {
+    const uint32_t f = (__float_as_uint(v[q]) >> 23) & 255u;
+    if (f != 255u) most = max(most, f);
+  }
+  most = max(__reduce_max_sync(0xffffffffu, most), 1u);  // 1 .. 254: 2^(most - 127)
+  const float down = most == 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - most) << 23);
+#pragma unroll
+  for (int q = 0; q < RC; ++q) {
+    const float x = v[q] * down;
+    const T h = to16<T>(x);
+    const float left = x - to_f32<T>(h);
+    hi[q * 32 + lane] = h;
+    lo[q * 32 + lane] = to16<T>(fabsf(x) < 4.0f ? left : 0.0f);  // infinities and NaN: hi alone
+  }
+  return __uint_as_float(most << 23);
+}
+
+// The sums of the shares of the rank values of tokens i, i + STRIDE, .. of a tile, times the adapter's
+// scale; four shares of all of them are read together.
+template <int RC, int TOKENS, int STRIDE>
+__device__ __forceinline__ void load_ranks(const Lora16Problem& p, int splits, const Tile& tile, int i, float scale,
+                                           int lane, float (&v)[TOKENS][RC]) {
+  const int64_t share = (int64_t)p.M * p.rank;
+#pragma unroll
+  for (int k = 0; k < TOKENS; ++k)
+#pragma unroll
+    for (int q = 0; q < RC; ++q) v[k][q] = 0.0f;
+  const float* part = p.v + (int64_t)(tile.start + i) * p.rank + lane;
+  for (int s = 0; s < splits; s += 4, part += 4 * share) {
+    float x[4][TOKENS][RC];
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int k = 0; k < TOKENS; ++k)
+#pragma unroll
+        for (int q = 0; q < RC; ++q)
+          x[d][k][q] = s + d < splits && i + k * STRIDE < tile.rows && q * 32 + lane < p.rank
+                           ? __ldcg(part + d * share + k * STRIDE * p.rank + q * 32)
+                           : 0.0f;
+#pragma unroll
+    for (int d = 0; d < 4; ++d)
+#pragma unroll
+      for (int k = 0; k < TOKENS; ++k)
+#pragma unroll
+        for (int q = 0; q < RC; ++q) v[k][q] += x[d][k][q];
+  }
+#pragma unroll
+  for (int k = 0; k < TOKENS; ++k)
+#pragma unroll
+    for (int q = 0; q < RC; ++q) v[k][q] *= scale;
+}
+
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Eight neighbouring channels of a token: base + 2^e sums, c[j][0], c[j][1] channels 2 j, 2 j + 1.
+template <typename T>
+__device__ __forceinline__ uint4 add_base(const uint4& y, const float (&c)[4][4], int h, float f) {
+  const T* yt = reinterpret_cast<const T*>(&y);
+  uint4 o;
+  T* ot = reinterpret_cast<T*>(&o);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    from_f32x2<T>(fmaf(c[j][2 * h], f, to_f32<T>(yt[2 * j])), fmaf(c[j][2 * h + 1], f, to_f32<T>(yt[2 * j + 1])), ot + 2 * j);
+  return o;
+}
+
+// Tokens without an adapter: the base itself, channels [n0, n1), eight pieces of a thread at a time.
+template <typename T, int THREADS>
+__device__ __forceinline__ void copy_base(const Lora16Problem& p, const int* tokens, int rows, int n0, int n1) {
+  constexpr int DEEP = 8;
   const T* base = static_cast<const T*>(p.base);
   T* out = static_cast<T*>(p.out);
-  if (threadIdx.x < kTokens) {
+  const int per = max(n1 - n0, 0) / 8, n = rows * per;
+  for (int i0 = threadIdx.x; i0 < n; i0 += THREADS * DEEP) {
+    uint4 v[DEEP];
+    int64_t at[DEEP];
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d) {
+      const int i = i0 + d * THREADS, tok = i < n ? tokens[i / per] : -1;
+      at[d] = tok >= 0 ? (int64_t)tok * p.N + n0 + i % per * 8 : -1;
+      if (at[d] >= 0) v[d] = __ldcg(reinterpret_cast<const uint4*>(base + at[d]));
+    }
+#pragma unroll
+    for (int d = 0; d < DEEP; ++d)
+      if (at[d] >= 0) *reinterpret_cast<uint4*>(out + at[d]) = v[d];
+  }
+}
+
+// Few tokens to an adapter: both products in one kernel, a cluster of CTAs per tile of 16 tokens.  Each CTA
+// takes a share of D: its warps take 32-deep slices straight from memory, DEEP of them under way, and
+// add up over its shared memory (MMA rows: ranks, MR x 16; columns: tokens).  Behind the cluster's barrier
+// every CTA adds the CTAs' sums, in order, and takes a share of N (MMA rows: tokens; columns: channels, 32 in
+// four MMAs); what its first strip needs is on the way meanwhile.
+constexpr int kFewTokens = 16;
+template <typename T, int MR, int DEEP>
+__global__ void __launch_bounds__(kThreads) lora16_few_kernel(const Lora16Problem p, int ctas) {
+  constexpr int TN = 2, RC = (MR + 1) / 2, kRanks = RC * 32, kPitch = kRanks + 8;  // elements
+  extern __shared__ __align__(16) float s_part[];  // [kWarps][MR][TN][4][32]
+  __shared__ float s_sum[kFewTokens][kRanks];
+  __shared__ __align__(16) T s_hi[kFewTokens * kPitch], s_lo[kFewTokens * kPitch];
+  __shared__ float s_pow[kFewTokens];
+  __shared__ int s_tok[kFewTokens];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int share = blockIdx.x % ctas, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const Tile tile = find_tile<kFewTokens, kThreads>(blockIdx.x / ctas, p.cumsum, p.L, p.M);  // the cluster's
+  if (tile.rows == 0) return;
+  const int D = p.D, N = p.N, strips = (N + 31) / 32, per_n = (strips + ctas - 1) / ctas;
+  const int last = min(strips, (share + 1) * per_n);
+  if (threadIdx.x < kFewTokens) {
     const int tok = (int)threadIdx.x < tile.rows ? __ldcg(p.route + tile.start + threadIdx.x) : -1;
     s_tok[threadIdx.x] = (unsigned)tok < (unsigned)p.M ? tok : -1;
   }
-  if (tile.l < 0) {  // no adapter: the base itself
-    __syncthreads();
-    const int n0 = share * per * 32, n1 = min(N, last * 32);
-    for (int i = warp; i < tile.rows; i += kWarps)
-      if (s_tok[i] >= 0)
-        for (int n = n0 + lane * 8; n < n1; n += 256)
-          *reinterpret_cast<uint4*>(out + (int64_t)s_tok[i] * N + n) =
-              __ldcg(reinterpret_cast<const uint4*>(base + (int64_t)s_tok[i] * N + n));
+  __syncthreads();
+  if (tile.l < 0) {
+    if (p.base != p.out) copy_base<T, kThreads>(p, s_tok, tile.rows, share * per_n * 32, min(N, last * 32));
     return;
   }
-  // a warp per token: its rank values, their largest finite exponent, the two 16-bit parts
-  for (int i = warp; i < kTokens; i += kWarps) {
-    float v[RC];
-    uint32_t most = 0;
-#pragma unroll
-    for (int q = 0; q < RC; ++q) {
-      const int r = q * 32 + lane;
-      v[q] = 0.0f;
-      if (i < tile.rows && r < p.rank)
-        for (int s = 0; s < splits; ++s) v[q] += __ldcg(p.v + ((int64_t)s * p.M + tile.start + i) * p.rank + r);
-      const uint32_t f = (__float_as_uint(v[q]) >> 23) & 255u;
-      if (f != 255u) most = max(most, f);
-    }
-    most = max(__reduce_max_sync(0xffffffffu, most), 1u);  // 1 .. 254: 2^(most - 127)
-    const float down = most == 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - most) << 23);
-#pragma unroll
-    for (int q = 0; q < RC; ++q) {
-      const float x = v[q] * down;
-      const T hi = to16<T>(x);
-      const float left = x - to_f32<T>(hi);
-      s_hi[i * kPitch + q * 32 + lane] = hi;
-      s_lo[i * kPitch + q * 32 + lane] = to16<T>(fabsf(x) < 4.0f ? left : 0.0f);  // infinities and NaN: hi alone
-    }
-    if (lane == 0) s_pow[i] = __uint_as_float(most << 23);
-  }
-  __syncthreads();
-  const float scale = p.scales ? __ldcg(p.scales + tile.l) : 1.0f;
-  const T* b = static_cast<const T*>(p.b) + (int64_t)tile.l * N * p.rank;
+  const int tok[2] = {s_tok[g], s_tok[g + 8]};
   const uint4 zero = make_uint4(0, 0, 0, 0);
-  const int tiles = (tile.rows + 15) / 16;
-  for (int strip = share * per + warp; strip < last; strip += kWarps) {
-    // column c of MMA j is channel 8 (c / 2) + 2 j + c % 2 of the strip: lane (g, t) then holds channels
-    // 8 t .. 8 t + 7 of tokens g and g + 8
-    uint4 w[4][RC];
+  {
+    const int chunks = (D + 31) / 32, per = (chunks + ctas - 1) / ctas, c1 = min(chunks, (share + 1) * per);
+    const T* a = static_cast<const T*>(p.a) + (int64_t)tile.l * p.rank * D;
+    const T* x[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) x[j] = tok[j] >= 0 ? static_cast<const T*>(p.x) + (int64_t)tok[j] * D : nullptr;
+    float c[MR][TN][4] = {};
+    for (int chunk = share * per + warp; chunk < c1; chunk += kWarps * DEEP) {
+      uint4 b[DEEP][TN], lo[DEEP][MR], hi[DEEP][MR];
+#pragma unroll
+      for (int d = 0; d < DEEP; ++d) {
+        const int k = (chunk + d * kWarps) * 32 + t * 8;
+        const bool in = k < D && chunk + d * kWarps < c1;
+#pragma unroll
+        for (int m = 0; m < MR; ++m) {
+          const int r = m * 16 + g;
+          lo[d][m] = in && r < p.rank ? __ldcg(reinterpret_cast<const uint4*>(a + (int64_t)r * D + k)) : zero;
+          hi[d][m] = in && r + 8 < p.rank ? __ldcg(reinterpret_cast<const uint4*>(a + (int64_t)(r + 8) * D + k)) : zero;
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j) b[d][j] = in && x[j] ? __ldcg(reinterpret_cast<const uint4*>(x[j] + k)) : zero;
+      }
+#pragma unroll
+      for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int m = 0; m < MR; ++m) mma32<T>(c[m][j], lo[d][m], hi[d][m], b[d][j]);
+    }
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) s_part[((warp * MR + m) * TN + j) * 128 + q * 32 + lane] = c[m][j][q];
+  }
+  // a strip of 32 channels: column c of MMA j is channel 8 (c / 2) + 2 j + c % 2, so that lane (g, t)
+  // holds channels 8 t .. 8 t + 7 of tokens g and g + 8
+  const T* b = static_cast<const T*>(p.b) + (int64_t)tile.l * N * p.rank;
+  const T* base = static_cast<const T*>(p.base);
+  T* out = static_cast<T*>(p.out);
+  uint4 w[4][RC], y[2];
+  auto load = [&](int strip) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int n = strip * 32 + (g >> 1) * 8 + j * 2 + (g & 1);
@@ -236,106 +389,291 @@ __global__ void __launch_bounds__(kThreads) lora16_expand_kernel(const Lora16Pro
     }
     const int n = strip * 32 + t * 8;
 #pragma unroll
-    for (int m = 0; m < TM; ++m) {
-      if (m >= tiles) break;
-      int64_t at[2];
-      uint4 y[2];
-      bool in[2];
+    for (int h = 0; h < 2; ++h)
+      y[h] = tok[h] >= 0 && n < N ? __ldcg(reinterpret_cast<const uint4*>(base + (int64_t)tok[h] * N + n)) : zero;
+  };
+  int strip = share * per_n + warp;
+  if (strip < last) load(strip);
+  const float scale = p.scales ? __ldcg(p.scales + tile.l) : 1.0f;
+  __syncthreads();
+  // element q of lane (g, t): rank 16 m + g + 8 (q / 2), token 8 j + 2 t + q % 2
+  for (int i = threadIdx.x; i < MR * TN * 128; i += kThreads) {
+    float s = 0.0f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int tok = s_tok[m * 16 + g + 8 * h];
-        in[h] = tok >= 0 && n < N;
-        at[h] = (int64_t)tok * N + n;
-        y[h] = in[h] ? __ldcg(reinterpret_cast<const uint4*>(base + at[h])) : zero;
-      }
-      float c[4][4] = {};
+    for (int u = 0; u < kWarps; ++u) s += s_part[u * MR * TN * 128 + i];
+    const int l = i & 31, q = (i >> 5) & 3, j = (i >> 7) % TN, m = (i >> 7) / TN;
+    s_sum[j * 8 + 2 * (l & 3) + (q & 1)][m * 16 + (l >> 2) + 8 * (q >> 1)] = s;
+  }
+  __syncwarp();
+  cluster_sync_all();
 #pragma unroll
-      for (int q = 0; q < RC; ++q) {
-        const int s = (m * 16 + g) * kPitch + q * 32 + t * 8;
-        const uint4 h0 = *reinterpret_cast<const uint4*>(s_hi + s), h1 = *reinterpret_cast<const uint4*>(s_hi + s + 8 * kPitch);
-        const uint4 l0 = *reinterpret_cast<const uint4*>(s_lo + s), l1 = *reinterpret_cast<const uint4*>(s_lo + s + 8 * kPitch);
+  for (int k = 0; k < kFewTokens / kWarps; ++k) {
+    const int i = warp + k * kWarps;
+    float v[RC];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          mma32<T>(c[j], l0, l1, w[j][q]);
-          mma32<T>(c[j], h0, h1, w[j][q]);
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        if (in[h]) {
-          const float f = s_pow[m * 16 + g + 8 * h];
-          const T* yt = reinterpret_cast<const T*>(&y[h]);
-          uint4 o;
-          T* ot = reinterpret_cast<T*>(&o);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            from_f32x2<T>(fmaf(scale, c[j][2 * h] * f, to_f32<T>(yt[2 * j])),
-                          fmaf(scale, c[j][2 * h + 1] * f, to_f32<T>(yt[2 * j + 1])), ot + 2 * j);
-          *reinterpret_cast<uint4*>(out + at[h]) = o;
-        }
+    for (int q = 0; q < RC; ++q) {
+      v[q] = 0.0f;
+      if (q * 32 + lane < MR * 16)
+        for (int u = 0; u < ctas; ++u) v[q] += ld_cluster(cluster_addr(&s_sum[i][q * 32 + lane], u));
+      v[q] *= scale;
     }
+    const float f = split_ranks<T, RC>(v, s_hi + i * kPitch, s_lo + i * kPitch, lane);
+    if (lane == 0) s_pow[i] = f;
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");  // done with the other CTAs' sums
+  __syncthreads();
+  while (strip < last) {
+    const int n = strip * 32 + t * 8;
+    float c[4][4] = {};
+#pragma unroll
+    for (int q = 0; q < RC; ++q) {
+      const int s = g * kPitch + q * 32 + t * 8;
+      const uint4 h0 = *reinterpret_cast<const uint4*>(s_hi + s), h1 = *reinterpret_cast<const uint4*>(s_hi + s + 8 * kPitch);
+      const uint4 l0 = *reinterpret_cast<const uint4*>(s_lo + s), l1 = *reinterpret_cast<const uint4*>(s_lo + s + 8 * kPitch);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        mma32<T>(c[j], l0, l1, w[j][q]);
+        mma32<T>(c[j], h0, h1, w[j][q]);
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (tok[h] >= 0 && n < N)
+        *reinterpret_cast<uint4*>(out + (int64_t)tok[h] * N + n) = add_base<T>(y[h], c, h, s_pow[g + 8 * h]);
+    strip += kWarps;
+    if (strip < last) load(strip);
+  }
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");  // no CTA leaves before the others have read its sums
+}
+
+// Many tokens to an adapter: 64, 16 to each of four groups of two warps, which keep their rank values in
+// registers; the adapter's rows of b pass through a ring in shared memory, 64 channels a stage, 32 to
+// a warp.  The rows lie there in the order of the MMAs' columns (a row of eight MMA columns after the
+// other, 16 bytes past a multiple of 32).
+template <typename T, int RK>  // RK x 16 ranks
+__global__ void __launch_bounds__(kThreads) lora16_expand_many_kernel(const Lora16Problem p, int splits, int shares) {
+  constexpr int RC = (RK + 1) / 2, kPitch = RC * 32 + 8, kRow = RK * 32 + 16, kStage = 64 * kRow;
+  extern __shared__ __align__(128) uint8_t s_mem[];  // the ring, then hi and lo of the rank values
+  __shared__ float s_pow[kManyTokens];
+  __shared__ int s_tok[kManyTokens];
+  T* s_hi = reinterpret_cast<T*>(s_mem + kStages * kStage);
+  T* s_lo = s_hi + kManyTokens * kPitch;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int share = blockIdx.x % shares, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const Tile tile = find_tile<kManyTokens, kThreads>(blockIdx.x / shares, p.cumsum, p.L, p.M);
+  const int N = p.N, strips = (N + 63) / 64, per = (strips + shares - 1) / shares;
+  const int first = share * per, n = max(0, min(strips - first, per));
+  if (threadIdx.x < kManyTokens) {
+    const int tok = (int)threadIdx.x < tile.rows ? __ldcg(p.route + tile.start + threadIdx.x) : -1;
+    s_tok[threadIdx.x] = (unsigned)tok < (unsigned)p.M ? tok : -1;
+  }
+  __syncthreads();
+  if (tile.rows == 0 || tile.l < 0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (tile.rows && p.base != p.out)
+      copy_base<T, kThreads>(p, s_tok, tile.rows, first * 64, min(N, (first + n) * 64));
+    return;
+  }
+  const float scale = p.scales ? __ldcg(p.scales + tile.l) : 1.0f;
+  const T* b = static_cast<const T*>(p.b) + (int64_t)tile.l * N * p.rank;
+  const T* base = static_cast<const T*>(p.base);
+  T* out = static_cast<T*>(p.out);
+  const uint32_t ring = smem_u32(s_mem);
+  auto load = [&](int i, int stage) {
+#pragma unroll
+    for (int k = 0; k < RK * 128; k += kThreads) {
+      const int at = k + threadIdx.x, ch = at / (RK * 2), piece = at % (RK * 2), c = (first + i) * 64 + ch;
+      // channel 8 (c / 2) + 2 j + c % 2 of 32: column c of MMA j
+      const int row = (ch & 32) + ((ch >> 1) & 3) * 8 + ((ch >> 3) & 3) * 2 + (ch & 1);
+      const bool in = c < N && piece * 8 < p.rank;
+      if (RK > 1 || at < 128) copy16(ring + stage * kStage + row * kRow + piece * 16, in ? b + (int64_t)c * p.rank + piece * 8 : b, in);
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) {
+    if (s < n) load(s, s);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  const int tg = warp >> 1, half = warp & 1;
+  const uint4 zero = make_uint4(0, 0, 0, 0);
+  const int tok[2] = {s_tok[tg * 16 + g], s_tok[tg * 16 + g + 8]};
+  const T* rows[2] = {base + (int64_t)tok[0] * N, base + (int64_t)tok[1] * N};  // read and written where tok >= 0
+  T* outs[2] = {out + (int64_t)tok[0] * N, out + (int64_t)tok[1] * N};
+  uint4 y[2][2];  // two strips
+  auto load_base = [&](int i, uint4 (&o)[2]) {
+    const int c = (first + i) * 64 + half * 32 + t * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) o[h] = i < n && tok[h] >= 0 && c < N ? __ldcg(reinterpret_cast<const uint4*>(rows[h] + c)) : zero;
+  };
+  load_base(0, y[0]);
+  load_base(1, y[1]);
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  for (int i0 = warp; i0 < kManyTokens; i0 += 4 * kWarps) {
+    float v[4][RC];
+    load_ranks<RC, 4, kWarps>(p, splits, tile, i0, scale, lane, v);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = i0 + k * kWarps;
+      const float f = split_ranks<T, RC>(v[k], s_hi + i * kPitch, s_lo + i * kPitch, lane);
+      if (lane == 0) s_pow[i] = f;
+    }
+  }
+  __syncthreads();
+  uint32_t hi[RK][4], lo[RK][4];
+  {
+    const int at = (tg * 16 + (lane & 15)) * kPitch + (lane >> 4) * 8;
+#pragma unroll
+    for (int k = 0; k < RK; ++k) {
+      ldmatrix4(hi[k], smem_u32(s_hi + at + k * 16));
+      ldmatrix4(lo[k], smem_u32(s_lo + at + k * 16));
+    }
+  }
+  const float f[2] = {s_pow[tg * 16 + g], s_pow[tg * 16 + g + 8]};
+  const uint32_t brow = (half * 32 + (lane >> 4) * 8 + (lane & 7)) * kRow + ((lane >> 3) & 1) * 16;
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncthreads();  // the stage has landed for all, and all are done with the one that is filled next
+    if (i + kStages - 1 < n) load(i + kStages - 1, (i + kStages - 1) % kStages);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    const uint32_t st = ring + (i % kStages) * kStage + brow;
+    float c[4][4] = {};
+#pragma unroll
+    for (int k = 0; k < RK; ++k)
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {
+        uint32_t w[4];
+        ldmatrix4(w, st + j * 8 * kRow + k * 32);
+        mma16<T>(c[j], lo[k], w[0], w[1]);
+        mma16<T>(c[j + 1], lo[k], w[2], w[3]);
+        mma16<T>(c[j], hi[k], w[0], w[1]);
+        mma16<T>(c[j + 1], hi[k], w[2], w[3]);
+      }
+    const int ch = (first + i) * 64 + half * 32 + t * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+      if (tok[h] >= 0 && ch < N) *reinterpret_cast<uint4*>(outs[h] + ch) = add_base<T>(y[i & 1][h], c, h, f[h]);
+    load_base(i + 2, y[i & 1]);
   }
 }
 
-// Shares of D: enough blocks for the device, at most what the workspace holds: max(M, kPartRows)
-// rows of fp32 rank values in all.
-constexpr int kMaxSplits = 16, kPartRows = 4096;
+// Shares of D: enough blocks for the device, at most what the workspace holds, part_rows(M) rows of
+// fp32 rank values in all: for four shares up to 8192 tokens, and for more with fewer than 1024.
+constexpr int kMaxSplits = 16;
+inline int part_rows(int M) {
+  const int many = M < 8192 ? 4 * M : 32768;
+  return M > many ? M : many < 4096 ? 4096 : many;
+}
 
 inline int tiles_of(int M, int groups, int tokens) { return M / tokens + (M < groups ? M : groups); }
 
-template <typename T, int MR, int TN>
-cudaError_t shrink(const Lora16Problem& p, int& splits, cudaStream_t stream) {
-  const int tiles = tiles_of(p.M, p.L, TN * 8), chunks = (p.D + 31) / 32;
-  splits = (2 * sm_count() + tiles - 1) / tiles;
+inline int shrink_splits(const Lora16Problem& p, int tiles, int blocks, int slices) {
+  int splits = (blocks + tiles - 1) / tiles;
   if (splits > kMaxSplits) splits = kMaxSplits;
-  if (splits > kPartRows / p.M) splits = kPartRows / p.M;
-  if (splits > chunks / kWarps) splits = chunks / kWarps;
-  if (splits < 1) splits = 1;
-  const size_t smem = (size_t)kWarps * MR * TN * 128 * 4;
+  if (splits > part_rows(p.M) / p.M) splits = part_rows(p.M) / p.M;
+  if (splits > slices) splits = slices;
+  return splits < 1 ? 1 : splits;
+}
+
+// CTAs to a cluster: as many as the device takes about at once, at most eight.
+template <typename T, int MR, int DEEP>
+cudaError_t few(const Lora16Problem& p, cudaStream_t stream) {
+  const int tiles = tiles_of(p.M, p.L + 1, kFewTokens);
+  int ctas = 8;
+  while (ctas > 1 && tiles * ctas > 4 * sm_count()) ctas /= 2;
+  const size_t smem = (size_t)kWarps * MR * 2 * 128 * 4;
+  static PerContextOnce set;
+  const int dev = current_device();
+  if (smem > 16 * 1024 && set.needed(dev)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(lora16_few_kernel<T, MR, DEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    set.done(dev);
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(tiles * ctas));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attrs[2];
+  attrs[0].id = cudaLaunchAttributeClusterDimension;
+  attrs[0].val.clusterDim.x = (unsigned)ctas;
+  attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
+  attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attrs[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attrs;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, lora16_few_kernel<T, MR, DEEP>, p, ctas);
+}
+
+template <typename T, int MR>
+cudaError_t shrink_many(const Lora16Problem& p, int& splits, cudaStream_t stream) {
+  const int tiles = tiles_of(p.M, p.L, kManyTokens);
+  splits = shrink_splits(p, tiles, 3 * sm_count(), (p.D + 255) / 256);
+  const size_t smem = (size_t)kStages * (kManyTokens + MR * 16) * 128;
+  static PerContextOnce set;
+  const int dev = current_device();
+  if (set.needed(dev)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(lora16_shrink_many_kernel<T, MR>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    set.done(dev);
+  }
+  return launch_dependent(lora16_shrink_many_kernel<T, MR>, (unsigned)(tiles * splits), kThreads, smem, stream, p, splits);
+}
+
+template <typename T, int RK>
+cudaError_t expand_many(const Lora16Problem& p, int splits, cudaStream_t stream) {
+  constexpr int RC = (RK + 1) / 2;
+  const int tiles = tiles_of(p.M, p.L + 1, kManyTokens), strips = (p.N + 63) / 64;
+  // two blocks fit an SM; as many as fill one wave, with adapters' last tiles half full
+  const int likely = p.M / kManyTokens + (p.M < p.L ? p.M : p.L) / 2 + 1;
+  int shares = 2 * sm_count() / likely;
+  if (shares > (strips + 3) / 4) shares = (strips + 3) / 4;
+  if (shares < 1) shares = 1;
+  const int smem = kStages * 64 * (RK * 32 + 16) + 2 * kManyTokens * (RC * 32 + 8) * 2;
   static PerContextOnce set;
   const int dev = current_device();
   if (smem > 48 * 1024 && set.needed(dev)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(lora16_shrink_kernel<T, MR, TN>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(lora16_expand_many_kernel<T, RK>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     set.done(dev);
   }
-  return launch_dependent(lora16_shrink_kernel<T, MR, TN>, (unsigned)(tiles * splits), kThreads, smem, stream, p, splits);
-}
-
-template <typename T, int RC, int TM>
-cudaError_t expand(const Lora16Problem& p, int splits, cudaStream_t stream) {
-  const int tiles = tiles_of(p.M, p.L + 1, TM * 16), strips = (p.N + 31) / 32;
-  int shares = (4 * sm_count() + tiles - 1) / tiles;
-  if (shares > (strips + kWarps - 1) / kWarps) shares = (strips + kWarps - 1) / kWarps;
-  return launch_dependent(lora16_expand_kernel<T, RC, TM>, (unsigned)(tiles * shares), kThreads, 0, stream, p, splits,
-                          shares);
+  return launch_dependent(lora16_expand_many_kernel<T, RK>, (unsigned)(tiles * shares), kThreads, (size_t)smem, stream, p,
+                          splits, shares);
 }
 
 template <typename T>
 cudaError_t launch(const Lora16Problem& p, cudaStream_t stream) {
-  // tiles of 64 tokens (32 above rank 64, whose sums would not fit the registers) or, for few tokens
-  // an adapter, of 16
-  const bool few = p.M <= 16 * p.L;
+  if (p.M <= 16 * p.L)  // few tokens to an adapter
+    return p.rank <= 16   ? few<T, 1, 4>(p, stream)
+           : p.rank <= 32 ? few<T, 2, 4>(p, stream)
+           : p.rank <= 64 ? few<T, 4, 2>(p, stream)
+                          : few<T, 8, 1>(p, stream);
   int splits = 1;
   cudaError_t e;
-  if (p.rank <= 16)
-    e = few ? shrink<T, 1, 2>(p, splits, stream) : shrink<T, 1, 8>(p, splits, stream);
-  else if (p.rank <= 32)
-    e = few ? shrink<T, 2, 2>(p, splits, stream) : shrink<T, 2, 8>(p, splits, stream);
-  else if (p.rank <= 64)
-    e = few ? shrink<T, 4, 2>(p, splits, stream) : shrink<T, 4, 8>(p, splits, stream);
-  else
-    e = few ? shrink<T, 8, 2>(p, splits, stream) : shrink<T, 8, 4>(p, splits, stream);
-  if (e != cudaSuccess) return e;
-  if (p.rank <= 32) return few ? expand<T, 1, 1>(p, splits, stream) : expand<T, 1, 4>(p, splits, stream);
-  if (p.rank <= 64) return few ? expand<T, 2, 1>(p, splits, stream) : expand<T, 2, 4>(p, splits, stream);
-  return few ? expand<T, 4, 1>(p, splits, stream) : expand<T, 4, 4>(p, splits, stream);
+  if (p.rank <= 16) {
+    e = shrink_many<T, 1>(p, splits, stream);
+    return e != cudaSuccess ? e : expand_many<T, 1>(p, splits, stream);
+  }
+  if (p.rank <= 32) {
+    e = shrink_many<T, 2>(p, splits, stream);
+    return e != cudaSuccess ? e : expand_many<T, 2>(p, splits, stream);
+  }
+  if (p.rank <= 64) {
+    e = shrink_many<T, 4>(p, splits, stream);
+    return e != cudaSuccess ? e : expand_many<T, 4>(p, splits, stream);
+  }
+  e = shrink_many<T, 8>(p, splits, stream);
+  return e != cudaSuccess ? e : expand_many<T, 8>(p, splits, stream);
 }
 
 }  // namespace
 
-size_t lora16_workspace_bytes(int M, int rank) { return (size_t)(M > kPartRows ? M : kPartRows) * rank * 4; }
+size_t lora16_workspace_bytes(int M, int rank) { return (size_t)part_rows(M) * rank * 4; }
 
 cudaError_t launch_lora16(const Lora16Problem& p, cudaStream_t stream) {
   return p.bf16 ? launch<__nv_bfloat16>(p, stream) : launch<__half>(p, stream);

@@ -105,55 +105,70 @@ __global__ void __launch_bounds__(kThreads) swiglu16_grad_kernel(int R, int E, i
   }
 }
 
-// One thread per eight channels of a token, to each of its rows.
-__global__ void __launch_bounds__(kThreads) dispatch16_kernel(int M, int D, int copies, int rows, const uint4* x,
+// Dispatch and combine: a block takes a token, or with few tokens a share of its channels, eight
+// channels to a thread; the token's rows are looked up once and all read or written together.
+constexpr int kRoutes = 8;  // at a time
+struct Routes {
+  int row[kRoutes];
+  __device__ __forceinline__ Routes(const int32_t* map, int j, int copies, int rows) {
+#pragma unroll
+    for (int q = 0; q < kRoutes; ++q) {
+      row[q] = j + q < copies ? __ldcg(map + j + q) : -1;
+      if ((unsigned)row[q] >= (unsigned)rows) row[q] = -1;
+    }
+  }
+};
+
+__global__ void __launch_bounds__(kThreads) dispatch16_kernel(int D, int copies, int rows, int shares, const uint4* x,
                                                               const int32_t* row_map, uint4* out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int per = D / 8;
-  const int64_t n = (int64_t)M * per, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-    const int64_t t = i / per, c = i - t * per;
-    const uint4 v = __ldcg(x + i);
-    for (int j = 0; j < copies; ++j) {
-      const int d = __ldcg(row_map + t * copies + j);
-      if ((unsigned)d < (unsigned)rows) out[(int64_t)d * per + c] = v;
+  const int t = blockIdx.x / shares, share = blockIdx.x - t * shares, per = D / 8;
+  for (int j = 0; j < copies; j += kRoutes) {
+    const Routes r(row_map + (int64_t)t * copies, j, copies, rows);
+    for (int c = share * kThreads + threadIdx.x; c < per; c += shares * kThreads) {
+      const uint4 v = __ldcg(x + (int64_t)t * per + c);
+#pragma unroll
+      for (int q = 0; q < kRoutes; ++q)
+        if (r.row[q] >= 0) out[(int64_t)r.row[q] * per + c] = v;
     }
   }
 }
 
-// One thread per eight channels of a token: four rows read at a time, then the sums in order.
+// The sums in order of the routes, in fp32; past eight routes a thread goes on with the next eight.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) combine16_kernel(int M, int D, int copies, int rows, const T* y,
+__global__ void __launch_bounds__(kThreads) combine16_kernel(int D, int copies, int rows, int shares, const T* y,
                                                              const int32_t* row_map, const float* probs, T* out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int per = D / 8;
-  const int64_t n = (int64_t)M * per, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
-    const int64_t t = i / per, c = i - t * per;
+  const int t = blockIdx.x / shares, share = blockIdx.x - t * shares, per = D / 8;
+  const int32_t* map = row_map + (int64_t)t * copies;
+  const Routes first(map, 0, copies, rows);
+  float p[kRoutes];
+#pragma unroll
+  for (int q = 0; q < kRoutes; ++q) p[q] = first.row[q] >= 0 && probs ? __ldcg(probs + (int64_t)t * copies + q) : 1.0f;
+  for (int c = share * kThreads + threadIdx.x; c < per; c += shares * kThreads) {
     float acc[8] = {};
-    for (int j = 0; j < copies; j += 4) {
-      Eight<T> v[4];
-      float w[4];
-      bool in[4];
+    Eight<T> v[kRoutes];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int d = j + q < copies ? __ldcg(row_map + t * copies + j + q) : -1;
-        in[q] = (unsigned)d < (unsigned)rows;
-        if (in[q]) {
-          load8(y + (int64_t)d * D + c * 8, v[q]);
-          w[q] = probs ? __ldcg(probs + t * copies + j + q) : 1.0f;
-        }
+    for (int q = 0; q < kRoutes; ++q)
+      if (first.row[q] >= 0) load8(y + (int64_t)first.row[q] * D + c * 8, v[q]);
+#pragma unroll
+    for (int q = 0; q < kRoutes; ++q)
+      if (first.row[q] >= 0) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = fmaf(p[q], to_f32<T>(v[q].t[k]), acc[k]);
       }
+    for (int j = kRoutes; j < copies; ++j) {
+      const int d = __ldcg(map + j);
+      if ((unsigned)d >= (unsigned)rows) continue;
+      const float w = probs ? __ldcg(probs + (int64_t)t * copies + j) : 1.0f;
+      Eight<T> u;
+      load8(y + (int64_t)d * D + c * 8, u);
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        if (in[q]) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] = fmaf(w[q], to_f32<T>(v[q].t[k]), acc[k]);
-        }
+      for (int k = 0; k < 8; ++k) acc[k] = fmaf(w, to_f32<T>(u.t[k]), acc[k]);
     }
-    store8(out + i * 8, acc);
+    store8(out + (int64_t)t * D + c * 8, acc);
   }
 }
 
@@ -217,11 +232,18 @@ inline unsigned grid_of(int64_t items, int per_sm = 8) {
   return (unsigned)(b < most ? b : most);
 }
 
-template <typename T>
+// Blocks to a token: one, or with few tokens enough for eight blocks on every SM, at most one for each
+// 256 threads' channels.
+inline int shares_of(int M, int D) {
+  const int most = (D / 8 + kThreads - 1) / kThreads, want = (8 * sm_count() + M - 1) / M;
+  return want < most ? want : most;
+}
+
+template <typename T, int G>
 cudaError_t combine_grad(int M, int D, int copies, int rows, const void* dout, const void* y, const int32_t* row_map,
                          const float* probs, void* dy, float* dprobs, cudaStream_t stream) {
-  const unsigned groups = (unsigned)(copies + 7) / 8;
-  return launch_dependent(combine16_grad_kernel<T, 8>, (unsigned)M * groups, kThreads, 0, stream, M, D, copies, rows,
+  const unsigned groups = (unsigned)(copies + G - 1) / G;
+  return launch_dependent(combine16_grad_kernel<T, G>, (unsigned)M * groups, kThreads, 0, stream, M, D, copies, rows,
                           static_cast<const T*>(dout), static_cast<const T*>(y), row_map, probs, static_cast<T*>(dy),
                           dprobs);
 }
@@ -252,25 +274,30 @@ cudaError_t launch_swiglu16_grad(int R, int E, int I, bool bf16, const void* dh,
 
 cudaError_t launch_dispatch16(int M, int D, int copies, int rows, const void* x, const int32_t* row_map, void* out,
                               cudaStream_t stream) {
-  return launch_dependent(dispatch16_kernel, grid_of((int64_t)M * (D / 8)), kThreads, 0, stream, M, D, copies, rows,
+  const int shares = shares_of(M, D);
+  return launch_dependent(dispatch16_kernel, (unsigned)(M * shares), kThreads, 0, stream, D, copies, rows, shares,
                           static_cast<const uint4*>(x), row_map, static_cast<uint4*>(out));
 }
 
 cudaError_t launch_combine16(int M, int D, int copies, int rows, bool bf16, const void* y, const int32_t* row_map,
                              const float* probs, void* out, cudaStream_t stream) {
-  const unsigned grid = grid_of((int64_t)M * (D / 8));
+  const int shares = shares_of(M, D);
   if (bf16)
-    return launch_dependent(combine16_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, M, D, copies, rows,
-                            static_cast<const __nv_bfloat16*>(y), row_map, probs, static_cast<__nv_bfloat16*>(out));
-  return launch_dependent(combine16_kernel<__half>, grid, kThreads, 0, stream, M, D, copies, rows,
+    return launch_dependent(combine16_kernel<__nv_bfloat16>, (unsigned)(M * shares), kThreads, 0, stream, D, copies, rows,
+                            shares, static_cast<const __nv_bfloat16*>(y), row_map, probs, static_cast<__nv_bfloat16*>(out));
+  return launch_dependent(combine16_kernel<__half>, (unsigned)(M * shares), kThreads, 0, stream, D, copies, rows, shares,
                           static_cast<const __half*>(y), row_map, probs, static_cast<__half*>(out));
 }
 
 cudaError_t launch_combine16_grad(int M, int D, int copies, int rows, bool bf16, const void* dout, const void* y,
                                   const int32_t* row_map, const float* probs, void* dy, float* dprobs,
                                   cudaStream_t stream) {
-  return bf16 ? combine_grad<__nv_bfloat16>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
-              : combine_grad<__half>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
+  // two routes to a block where there are few tokens: 61 tokens of 8 routes x 7168 TODO
+  if (M < 4 * sm_count())
+    return bf16 ? combine_grad<__nv_bfloat16, 2>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
+                : combine_grad<__half, 2>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
+  return bf16 ? combine_grad<__nv_bfloat16, 8>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
+              : combine_grad<__half, 8>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
 }
 
 }  // namespace moe
