@@ -23,6 +23,10 @@
 // which stream the weights past few rows; and CTA pairs (cta_group::2) of 256 channels and tiles of
 // up to 256 rows, of which each CTA loads half.
 //
+// Where there are too few items for the device, a cluster of single CTAs divides the reduction of each: every
+// CTA leaves its sums in its shared memory, and behind a barrier of the cluster each adds a share of
+// the tile's elements over the CTAs, in order, and stores it.
+//
 // Roles: warp 0 loads operand A and warp 2 operand B, 64 steps of the reduction a stage, into a ring
 // in shared memory; warp 3 (pairs) tells the leading CTA that a stage has landed; warp 1 of the
 // leading CTA issues the MMAs; warps 4-11, two groups, round the sums of one accumulator and store them
@@ -41,17 +45,23 @@ constexpr int kMaxExperts = 1024;
 constexpr int kABytes = 128 * 128;  // 128 channels x 64 steps
 constexpr int kOutRows = 32;        // of an epilogue group's store, x 128 channels
 constexpr int kBoxes = 3, kBoxRows = 64;
+constexpr int kMaxSplit = 4;
 
 template <Gmm16 KIND, int NT, bool PAIR>
 struct Cfg {
   static constexpr bool kWeight = KIND == Gmm16::kWeight;
   static constexpr int kStep = PAIR ? 32 : 16;
   static constexpr int kCtaCols = PAIR ? NT / 2 : NT;
-  static constexpr int kStageBytes = kABytes + kCtaCols * 128;
-  static constexpr int kStages = PAIR ? 6 : 10;
-  // kWeight: 4 KB a warp (32 channels x 128 bytes); else 8 KB a group
+  // 64-deep parts of a stage: two where few columns make the MMAs so short that a stage's commit counts
+  static constexpr int kParts = !PAIR && NT <= 32 ? 2 : 1, kDeep = 64 * kParts;
+  static constexpr int kBBytes = kCtaCols * 128;  // of a part
+  static constexpr int kStageBytes = kParts * (kABytes + kBBytes);  // the parts of A, then those of B
+  static constexpr int kStages = PAIR || NT > 32 ? 6 : 5;
+  // kWeight: 4 KB a warp (32 channels x 128 bytes); else 8 KB a group, or a tile of 32 rows' sums in fp32
+  static constexpr bool kSplits = !PAIR && NT <= 32;
   static constexpr int kEpiBytes = kWeight ? 8 * 4096 : 2 * kOutRows * 256;
-  static constexpr int kTmemCols = 2 * NT <= 64 ? 64 : 512;
+  static constexpr int kTmemCols = 2 * NT <= 64 ? 64 : 2 * NT <= 256 ? 256 : 512;
+  static_assert(!kSplits || kEpiBytes >= NT * 512, "a tile's sums");
   static constexpr int kSmem = kStages * kStageBytes + kEpiBytes;
   static_assert(kStageBytes % 1024 == 0 && 2 * NT <= kTmemCols, "swizzled rows, tensor memory");
   static_assert(kSmem + (kWeight ? 1024 : 9 * 1024) <= 227 * 1024, "shared memory");
@@ -63,6 +73,7 @@ struct Args {
   void* out;
   int32_t* status;
   bool bf16, out_f32, accumulate;
+  int split;
 };
 
 // a: operand A; b: operand B in boxes of 64, 32 and 16 rows (kWeight: b[0] alone); out.
@@ -141,7 +152,8 @@ __device__ __forceinline__ uint32_t pack16(bool bf16, uint32_t lo, uint32_t hi) 
 }
 
 // An arrival on the leading CTA's barrier that publishes what this thread has stored itself, to the
-// whole cluster; and the wait for it.  Only stages with overwritten rows pay for these.
+// whole cluster; and the wait for it.  Only stages with overwritten rows pay for these, and never the
+// warp that issues MMAs (a wait of cluster scope there took 6% of the weights' gradient).
 __device__ __forceinline__ void mbar_arrive_remote_release(uint32_t caddr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(caddr) : "memory");
 }
@@ -151,6 +163,15 @@ __device__ __forceinline__ void mbar_acquire_cluster(uint64_t* bar, uint32_t par
       "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(smem_u32(bar)),
       "r"(parity)
       : "memory");
+}
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
 }
 
 struct Item {
@@ -238,7 +259,8 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   constexpr int S = C::kStages;
   constexpr bool W = C::kWeight, A_MN = KIND != Gmm16::kForward, RELAY = PAIR || W;
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // swizzled rows: 1024-byte groups
-  __shared__ __align__(8) uint64_t full_bar[S], ready_bar[S], empty_bar[S], accfull_bar[2], accempty_bar[2], final_bar;
+  __shared__ __align__(8) uint64_t full_bar[S], peer_bar[S], ready_bar[S], empty_bar[S], accfull_bar[2], accempty_bar[2], final_bar;
+  __shared__ __align__(8) uint64_t sums_bar, read_bar;  // of a cluster that divides the reduction
   __shared__ int s_pref[W ? 1 : kMaxExperts + 1], s_end[W ? 1 : kMaxExperts], s_wsum[kThreads / 32];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_issued[2];
@@ -246,7 +268,8 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   const int out_rows = KIND == Gmm16::kInput ? a.D : a.N;  // the MMA's rows in all
   const int NB = (out_rows + 127) / 128, CB = PAIR ? (NB + 1) / 2 : NB;
   const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-  const int first = PAIR ? blockIdx.x >> 1 : blockIdx.x, stride = PAIR ? gridDim.x >> 1 : gridDim.x;
+  const int split = C::kSplits ? a.split : 1, share = C::kSplits ? (int)cluster_ctarank() : 0;  // of the reduction
+  const int ctas = PAIR ? 2 : split, first = blockIdx.x / ctas, stride = gridDim.x / ctas;
   volatile int* abort_flag = &s_abort;
 
   // ---- work list, barriers, tensor memory; what the kernels before this one wrote is read behind
@@ -259,14 +282,17 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       prefetch_tmap(&maps.out);
       for (int s = 0; s < S; ++s) {
         mbar_init(&full_bar[s], 2);
-        mbar_init(&ready_bar[s], PAIR ? 2 : 1);
+        mbar_init(&peer_bar[s], 1);
+        mbar_init(&ready_bar[s], 1);
         mbar_init(&empty_bar[s], 1);
       }
       for (int s = 0; s < 2; ++s) {
         mbar_init(&accfull_bar[s], 1);
-        mbar_init(&accempty_bar[s], PAIR ? 16 : 8);
+        mbar_init(&accempty_bar[s], (PAIR ? 2 : 1) * (W ? 4 : 8));
       }
       mbar_init(&final_bar, 1);
+      mbar_init(&sums_bar, 8 * split);
+      mbar_init(&read_bar, 8 * split);
       fence_barrier_init();
     }
     tc_fence_before();
@@ -308,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
     total = s_pref[E];
   }
   __syncwarp();
-  if (PAIR) cluster_sync_all();  // the peer's barriers and tensor memory are ready
+  if (ctas > 1) cluster_sync_all();  // the other CTAs' barriers and tensor memory are ready
   tc_fence_after();
   const WorkList wl{s_pref, s_end, CB, a.E};
   const uint32_t tmem = s_tmem;
@@ -320,6 +346,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
     else return tile_item<NT, C::kStep>(j, wl, e_hint);
   };
   auto steps = [&](const Item& it) { return W ? it.rows : depth; };  // of the reduction
+  // stages of an item that are this CTA's: [kb0, kb1) of KB (each of a cluster has one at least)
+  auto stage0 = [&](int KB) { return split == 1 ? 0 : share * KB / split; };
+  auto stage1 = [&](int KB) { return split == 1 ? KB : (share + 1) * KB / split; };
 
   if (warp == kAWarp || warp == kBWarp) {
     const uint32_t elected = elect_one();
@@ -329,35 +358,47 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
     for (int j = first; ok && j < total; j += stride) {
       const Item it = item(j, e_hint);
       const int m0 = (PAIR ? 2 * it.cb + (int)rank : it.cb) * 128;  // past the last: the copies bring zeros
-      const int cta_cols = PAIR ? it.n / 2 : it.n, KB = (steps(it) + 63) / 64;
+      const int cta_cols = PAIR ? it.n / 2 : it.n, deep = steps(it), KB = (deep + C::kDeep - 1) / C::kDeep;
       const int c0 = (W ? it.col0 : it.row0) + (int)rank * cta_cols;
-      for (int kb = 0; kb < KB; ++kb, ++n, at.next(S)) {
+      for (int kb = stage0(KB), kb1 = stage1(KB); kb < kb1; ++kb, ++n, at.next(S)) {
         if (!(ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status))) break;
         const uint32_t st = ring + at.slot * C::kStageBytes, bar = smem_u32(&full_bar[at.slot]);
+        const int k0 = kb * C::kDeep, parts = C::kParts == 2 && k0 + 64 < deep ? 2 : 1;
         if (warp == kAWarp) {
-          expect_tx_elect(elected, bar, kABytes);
-          if (KIND == Gmm16::kForward) {
-            tma_load_3d_elect(elected, st, &maps.a, kb * 64, m0, it.e, bar);
-          } else if (KIND == Gmm16::kInput) {
-            tma_load_3d_elect(elected, st, &maps.a, m0, kb * 64, it.e, bar);
-            tma_load_3d_elect(elected, st + 8192, &maps.a, m0 + 64, kb * 64, it.e, bar);
-          } else {
-            tma_load_2d_elect(elected, st, &maps.a, m0, it.row0 + kb * 64, bar);
-            tma_load_2d_elect(elected, st + 8192, &maps.a, m0 + 64, it.row0 + kb * 64, bar);
+          expect_tx_elect(elected, bar, (uint32_t)parts * kABytes);
+#pragma unroll
+          for (int q = 0; q < C::kParts; ++q) {
+            if (q >= parts) break;
+            const uint32_t to = st + q * kABytes;
+            const int k = k0 + q * 64;
+            if (KIND == Gmm16::kForward) {
+              tma_load_3d_elect(elected, to, &maps.a, k, m0, it.e, bar);
+            } else if (KIND == Gmm16::kInput) {
+              tma_load_3d_elect(elected, to, &maps.a, m0, k, it.e, bar);
+              tma_load_3d_elect(elected, to + 8192, &maps.a, m0 + 64, k, it.e, bar);
+            } else {
+              tma_load_2d_elect(elected, to, &maps.a, m0, it.row0 + k, bar);
+              tma_load_2d_elect(elected, to + 8192, &maps.a, m0 + 64, it.row0 + k, bar);
+            }
           }
         } else if (W) {
           const int boxes = (cta_cols + 63) / 64;
           expect_tx_elect(elected, bar, (uint32_t)boxes * 8192);
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d_elect(elected, st + kABytes + b * 8192, &maps.b[0], c0 + b * 64, it.row0 + kb * 64, bar);
+            tma_load_2d_elect(elected, st + kABytes + b * 8192, &maps.b[0], c0 + b * 64, it.row0 + k0, bar);
         } else {
-          expect_tx_elect(elected, bar, (uint32_t)cta_cols * 128);
-          int r = 0;
+          expect_tx_elect(elected, bar, (uint32_t)(parts * cta_cols) * 128);
 #pragma unroll
-          for (int b = 0; b < kBoxes; ++b) {
-            const int rows = kBoxRows >> b;
-            for (; cta_cols - r >= rows; r += rows)
-              tma_load_2d_elect(elected, st + kABytes + r * 128, &maps.b[b], kb * 64, c0 + r, bar);
+          for (int q = 0; q < C::kParts; ++q) {
+            if (q >= parts) break;
+            int r = 0;
+#pragma unroll
+            for (int b = 0; b < kBoxes; ++b) {
+              const int rows = kBoxRows >> b;
+              for (; cta_cols - r >= rows; r += rows)
+                tma_load_2d_elect(elected, st + C::kParts * kABytes + q * C::kBBytes + r * 128, &maps.b[b], k0 + q * 64,
+                                  c0 + r, bar);
+            }
           }
         }
       }
@@ -377,17 +418,27 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       const int n = steps(it), KB = (n + 63) / 64;
       for (int kb = 0; kb < KB; ++kb, at.next(S)) {
         if (!(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status))) break;
-        const uint32_t to = PAIR ? cluster_addr(&ready_bar[at.slot], 0) : smem_u32(&ready_bar[at.slot]);
         const int left = n - kb * 64, upto = (left + 15) & ~15;
-        if (W && left < 64 && left < upto) {
+        const bool tail = W && left < 64 && left < upto;
+        if (tail) {
           // rows of the next expert, in the four boxes of both operands (a row is 128 bytes of each)
           uint8_t* box = smem_raw + at.slot * C::kStageBytes + (lane >> 3) * 8192 + (lane & 7) * 16;
           for (int r = left; r < upto; ++r) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive_remote_release(to);
-        } else if (lane == 0) {
-          mbar_arrive_remote(to);
+        }
+        if (rank == 1) {
+          const uint32_t to = cluster_addr(&peer_bar[at.slot], 0);
+          if (lane == 0) {
+            if (tail) mbar_arrive_remote_release(to); else mbar_arrive_remote(to);
+          }
+        } else {
+          if (PAIR) {
+            if (!(ok = warp_wait(&peer_bar[at.slot], at.phase, abort_flag, a.status))) break;
+            if (tail) mbar_acquire_cluster(&peer_bar[at.slot], at.phase);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ready_bar[at.slot]);
         }
       }
     }
@@ -403,27 +454,28 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       uint32_t there = mbar_test(&there_bar[0], 0);
       for (int j = first; ok && j < total; j += stride, ++u) {
         const Item it = item(j, e_hint);
-        const int buf = u & 1, n = steps(it), KB = (n + 63) / 64;
+        const int buf = u & 1, n = steps(it), KB = (n + C::kDeep - 1) / C::kDeep;
         if (!(ok = warp_wait(&accempty_bar[buf], ((u >> 1) & 1) ^ 1, abort_flag, a.status))) break;
         tc_fence_after();
         const uint32_t idesc = f16_idesc(a.bf16, A_MN, W, PAIR ? 256 : 128, it.n), d = t0 + buf * NT;
-        for (int kb = 0; kb < KB; ++kb) {
+        const int kb0 = stage0(KB), kb1 = stage1(KB);
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!__all_sync(0xffffffffu, there) &&
               !(ok = warp_wait(&there_bar[at.slot], at.phase, abort_flag, a.status)))
             break;
-          if (W && PAIR && kb == KB - 1) mbar_acquire_cluster(&there_bar[at.slot], at.phase);
           tc_fence_after();
           const uint32_t st = ring + at.slot * C::kStageBytes;
           const uint64_t da = A_MN ? sw128_mn_desc(st) : sw128_desc(st);
-          const uint64_t db = W ? sw128_mn_desc(st + kABytes) : sw128_desc(st + kABytes);
+          const uint64_t db = W ? sw128_mn_desc(st + kABytes) : sw128_desc(st + C::kParts * kABytes);
           const uint32_t done = smem_u32(&empty_bar[at.slot]);
           at.next(S);
           there = mbar_test(&there_bar[at.slot], at.phase);
-          const int last = kb < KB - 1 ? 4 : (n - kb * 64 + 15) >> 4;  // 16 steps an MMA
+          const int last = min(4 * C::kParts, (n - kb * C::kDeep + 15) >> 4);  // 16 steps an MMA
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 4 * C::kParts; ++k)
             if (k < last)
-              f16_mma<PAIR>(elected, d, da + k * (A_MN ? 128 : 2), db + k * (W ? 128 : 2), idesc, kb || k ? 1u : 0u);
+              f16_mma<PAIR>(elected, d, da + (k >> 2) * (kABytes >> 4) + (k & 3) * (A_MN ? 128 : 2),
+                            db + (k >> 2) * (C::kBBytes >> 4) + (k & 3) * (W ? 128 : 2), idesc, kb > kb0 || k ? 1u : 0u);
           mx_commit<PAIR>(elected, done);
         }
         if (ok) mx_commit<PAIR>(elected, smem_u32(&accfull_bar[buf]));
@@ -432,11 +484,14 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       mbar_wait_sleep_bounded(&final_bar, 0);
     }
   } else if (warp >= kEpiWarp0) {
-    // both groups take part in every item: while they drain one accumulator the MMAs fill the other
+    // kWeight: the groups take turns, an accumulator each (together at every item, their bursts of stores
+    // slowed the loads: both gradients' largest case took 905 us for 880); else both take part in every
+    // item, and drain one accumulator while the MMAs fill the other
+    constexpr int kTurns = W ? 2 : 1;
     const int group = (warp - kEpiWarp0) >> 2, quarter = warp & 3;
     const uint32_t lanes = (uint32_t)quarter << 21;  // 32 * quarter in the lane field
     int e_hint = 0;
-    for (int u = 0, j = first; j < total; j += stride, ++u) {
+    for (int u = W ? group : 0, j = first + u * stride; j < total; j += kTurns * stride, u += kTurns) {
       const Item it = item(j, e_hint);
       const int buf = u & 1;
       bool ok = warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status);
@@ -451,7 +506,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         uint4* row = reinterpret_cast<uint4*>(own + lane * 128);
         const int cols = a.out_f32 ? 32 : 64, n = min(NT, a.D - it.col0), y = m0 + quarter * 32;
         if (y < a.N && !(it.rows == 0 && a.accumulate)) {
-          for (int c0 = group * cols; c0 < n; c0 += 2 * cols) {
+          for (int c0 = 0; c0 < n; c0 += cols) {
             uint32_t v[4][16];
             __syncwarp();
             if (it.rows) {
@@ -491,6 +546,56 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
             }
           }
         }
+      } else if (C::kSplits && split > 1) {
+        float* sums = reinterpret_cast<float*>(smem_raw + S * C::kStageBytes);  // [rows][128]
+        const int wg = warp - kEpiWarp0, th = wg * 32 + lane;
+        // everybody has read the item before
+        if (u > 0 && !warp_wait(&read_bar, (u - 1) & 1, abort_flag, a.status)) break;
+        for (int c0 = group * 16; c0 < it.n; c0 += 32) {
+          uint32_t v[16];
+          __syncwarp();
+          tmem_ld16(t + c0, v);
+          tmem_wait_ld();
+          float* o = sums + c0 * 128 + quarter * 32 + lane;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) o[i * 128] = __uint_as_float(v[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane < split) mbar_arrive_remote_release(cluster_addr(&sums_bar, lane));
+        if (lane == 0) mbar_arrive(&accempty_bar[buf]);
+        if (!warp_wait(&sums_bar, u & 1, abort_flag, a.status)) break;
+        mbar_acquire_cluster(&sums_bar, u & 1);
+        // eight channels of a row to a thread, the tile's pieces dealt out over the cluster
+        const int width = min(128, out_rows - m0);
+        for (int i = share * 256 + th; i < it.rows * 16; i += split * 256) {
+          const int r = i >> 4, c = (i & 15) * 8;
+          float4 y[kMaxSplit][2];
+#pragma unroll
+          for (int q = 0; q < kMaxSplit; ++q)
+            if (q < split) {
+              const uint32_t from = cluster_addr(sums + r * 128 + c, q);
+              y[q][0] = ld_cluster4(from);
+              y[q][1] = ld_cluster4(from + 16);
+            }
+          float x[8] = {};
+#pragma unroll
+          for (int q = 0; q < kMaxSplit; ++q)
+            if (q < split)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) x[k] += reinterpret_cast<const float*>(y[q])[k];
+          if (c < width) {
+            uint4 o;
+            o.x = pack16(a.bf16, __float_as_uint(x[0]), __float_as_uint(x[1]));
+            o.y = pack16(a.bf16, __float_as_uint(x[2]), __float_as_uint(x[3]));
+            o.z = pack16(a.bf16, __float_as_uint(x[4]), __float_as_uint(x[5]));
+            o.w = pack16(a.bf16, __float_as_uint(x[6]), __float_as_uint(x[7]));
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + (size_t)(it.row0 + r) * out_rows + m0 + c) = o;
+          }
+        }
+        __syncwarp();  // what was read has been used: nothing to publish
+        if (lane < split) mbar_arrive_remote(cluster_addr(&read_bar, lane));
+        continue;
       } else {
         // 32 rows x 128 channels gathered in shared memory and stored from there by one tensor copy,
         // or, where the tile's last rows are not its own, row by row
@@ -548,7 +653,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   tc_fence_before();
   __syncthreads();
   __syncwarp();
-  if (PAIR) cluster_sync_all();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
+  if (ctas > 1) cluster_sync_all();  // no CTA leaves while the others' MMAs, arrivals or reads may touch it
   if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc<PAIR, C::kTmemCols>(tmem);
@@ -569,8 +674,12 @@ bool encode_tensor_map_3d(CUtensorMap* m, CUtensorMapDataType dt, size_t elem, c
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Clusters of this many CTAs, one to an SM, that the device holds at once (GB300: 152, 76 and 36 of 1, 2
+// and 4: a cluster of four needs four SMs of one GPC).
+inline int resident_clusters(int ctas) { return ctas <= 2 ? sm_count() / ctas : sm_count() / 19 * 18 / ctas; }
+
 template <Gmm16 KIND, int NT, bool PAIR>
-cudaError_t launch(const Gmm16Problem& p, cudaStream_t stream) {
+cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
   using C = Cfg<KIND, NT, PAIR>;
   const CUtensorMapDataType t = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const uint64_t R = p.R, E = p.E, N = p.N, D = p.D;
@@ -597,15 +706,16 @@ cudaError_t launch(const Gmm16Problem& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     set.done(dev);
   }
-  Args a{p.R, p.E, p.N, p.D, p.cumsum, p.out, p.status, p.bf16, p.out_f32, p.accumulate};
+  Args a{p.R, p.E, p.N, p.D, p.cumsum, p.out, p.status, p.bf16, p.out_f32, p.accumulate, split};
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(PAIR ? sm_count() & ~1 : sm_count()));
+  const int ctas = PAIR ? 2 : split;
+  cfg.gridDim = dim3((unsigned)(resident_clusters(ctas) * ctas));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = stream;
   cudaLaunchAttribute attrs[2];
   attrs[0].id = cudaLaunchAttributeClusterDimension;
-  attrs[0].val.clusterDim.x = PAIR ? 2 : 1;
+  attrs[0].val.clusterDim.x = (unsigned)ctas;
   attrs[0].val.clusterDim.y = attrs[0].val.clusterDim.z = 1;
   attrs[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attrs[1].val.programmaticStreamSerializationAllowed = 1;
@@ -616,12 +726,45 @@ cudaError_t launch(const Gmm16Problem& p, cudaStream_t stream) {
 
 }  // namespace
 
+namespace {
+
+// What a form takes, in clocks: rounds of its items over the units that work at once, each the item's stages
+// and what an item costs besides.  The host knows the rows per expert on average only.
+struct Form {
+  int nt, split;  // columns of a tile; 256: pairs
+  double clocks;
+};
+Form choose(const Gmm16Problem& p) {
+  const int outs = p.kind == Gmm16::kForward ? p.N : p.D, depth = p.kind == Gmm16::kForward ? p.D : p.N;
+  const int experts = p.R < p.E ? p.R : p.E, KB = (depth + 63) / 64;
+  const double rows = (double)p.R / experts;
+  Form best{0, 1, 0.0};
+  for (const int nt : {32, 128, 256}) {
+    const int tiles = (int)((rows + nt - 1) / nt), blocks = (outs + (nt == 256 ? 255 : 127)) / (nt == 256 ? 256 : 128);
+    const double stage = nt == 32 ? 290 : nt == 128 ? 420 : 520;
+    for (int split = 1; split <= (nt > 32 || KB < 16 ? 1 : 4); split *= 2) {
+      const double items = (double)experts * tiles * blocks, units = resident_clusters(nt == 256 ? 2 : split);
+      const double rounds = (double)(int64_t)((items + units - 1) / units);
+      const double clocks = rounds * ((KB + split - 1) / split * stage + (split > 1 ? 3000 : 800));
+      if (!best.nt || clocks < best.clocks) best = Form{nt, split, clocks};
+    }
+  }
+  return best;
+}
+
+template <Gmm16 KIND>
+cudaError_t launch_rows(const Gmm16Problem& p, cudaStream_t stream) {
+  const Form f = choose(p);
+  return f.nt == 32    ? launch<KIND, 32, false>(p, f.split, stream)
+         : f.nt == 128 ? launch<KIND, 128, false>(p, f.split, stream)
+                       : launch<KIND, 256, true>(p, 1, stream);
+}
+
+}  // namespace
+
 cudaError_t launch_gmm16(const Gmm16Problem& p, cudaStream_t stream) {
-  if (p.kind == Gmm16::kWeight) return launch<Gmm16::kWeight, 256, true>(p, stream);
-  const bool few = (double)p.R / p.E <= 32.0;
-  if (p.kind == Gmm16::kForward)
-    return few ? launch<Gmm16::kForward, 32, false>(p, stream) : launch<Gmm16::kForward, 256, true>(p, stream);
-  return few ? launch<Gmm16::kInput, 32, false>(p, stream) : launch<Gmm16::kInput, 256, true>(p, stream);
+  if (p.kind == Gmm16::kWeight) return launch<Gmm16::kWeight, 256, true>(p, 1, stream);
+  return p.kind == Gmm16::kForward ? launch_rows<Gmm16::kForward>(p, stream) : launch_rows<Gmm16::kInput>(p, stream);
 }
 
 }  // namespace moe

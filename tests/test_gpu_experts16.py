@@ -49,6 +49,9 @@ CASES = [
     ([1], 0, 8, 8), ([1], 0, 4096, 1024), ([0], 3, 64, 64), ([0, 5, 0], 1, 136, 72), ([3, 0, 0, 1, 7], 0, 64, 200),
     ([16] * 3, 2, 128, 64), ([17, 15, 33], 0, 264, 72), ([31, 32, 1, 0], 5, 120, 1000), ([64], 0, 512, 4096),
     ([255, 256, 257], 1, 256, 264), ([100, 0, 129, 500], 0, 520, 136), ([1000], 24, 1416, 520), ([2049, 3], 0, 248, 256),
+    # few items, whose reduction a cluster divides: one round of them, several, odd depths, many rows
+    ([2], 0, 136, 4104), ([3, 0, 5, 1, 2, 40, 1, 4, 7, 2], 3, 2568, 4104), ([30] * 4, 1, 2048, 2056), ([100, 90, 128, 1, 129] * 2, 0, 2824, 2312),
+    ([250], 6, 1032, 4096), ([70, 3], 0, 4096, 1024),
     ([1, 2, 3] * 30, 0, 200, 128), ([0] * 60 + [40], 9, 1032, 640), ([511, 1], 0, 16, 2056), ([192, 193, 191, 224], 0, 384, 64),
 ]
 
