@@ -224,20 +224,71 @@ __device__ __forceinline__ int end_of(const Args& a, int e) {
   return e < 0 ? 0 : min(max(__ldcg(a.cumsum + e), 0), a.R);
 }
 
-// kWeight: blocks of 256 x 256, columns innermost.
+// The items that a role of a CTA goes through: the current one, `look` behind its first stage, `next` at its
+// end.
 template <int NT, int STEP>
-__device__ __forceinline__ Item block_item(int j, int CB, const Args& a) {
-  const int cols = (a.D + NT - 1) / NT, per = CB * cols;
+struct TileItems {
+  WorkList wl;
+  int total, stride, j, e_hint = 0;
   Item it;
-  it.e = j / per;
-  const int local = j - it.e * per;
-  it.cb = local / cols;
-  it.col0 = (local - it.cb * cols) * NT;
-  it.row0 = end_of(a, it.e - 1);
-  it.rows = max(end_of(a, it.e) - it.row0, 0);
-  it.n = (min(NT, a.D - it.col0) + STEP - 1) & -STEP;
-  return it;
-}
+  __device__ __forceinline__ TileItems(const WorkList& wl_, int total_, int first, int stride_)
+      : wl(wl_), total(total_), stride(stride_), j(first) {
+    if (j < total) it = tile_item<NT, STEP>(j, wl, e_hint);
+  }
+  __device__ __forceinline__ bool more() const { return j < total; }
+  __device__ __forceinline__ void look() {}
+  __device__ __forceinline__ void next() {
+    j += stride;
+    if (j < total) it = tile_item<NT, STEP>(j, wl, e_hint);
+  }
+};
+
+// kWeight: blocks of 256 x 256, columns innermost.  There is no room for the prefix in shared memory, and
+// its latency in global memory between items left the tensor cores idle (12288 rows x 2816 x 4096 on 16
+// experts 192 us, looked up ahead 183).
+template <int NT, int STEP>
+struct BlockItems {
+  const Args& a;
+  int total, stride, j, cols, per, de, dl, e, local, lo, hi;  // local: the item within its expert
+  Item it;
+  __device__ __forceinline__ BlockItems(const Args& a_, int CB, int total_, int first, int stride_)
+      : a(a_), total(total_), stride(stride_), j(first) {
+    cols = (a.D + NT - 1) / NT;
+    per = CB * cols;
+    e = j / per;
+    local = j - e * per;
+    de = stride / per;
+    dl = stride - de * per;
+    fetch();
+    set();
+  }
+  __device__ __forceinline__ bool more() const { return j < total; }
+  __device__ __forceinline__ void fetch() {
+    lo = e > 0 && e < a.E ? __ldcg(a.cumsum + e - 1) : 0;
+    hi = e < a.E ? __ldcg(a.cumsum + e) : 0;
+  }
+  __device__ __forceinline__ void look() {
+    e += de;
+    local += dl;
+    if (local >= per) {
+      local -= per;
+      ++e;
+    }
+    fetch();
+  }
+  __device__ __forceinline__ void set() {
+    it.e = e;
+    it.cb = local / cols;
+    it.col0 = (local - it.cb * cols) * NT;
+    it.row0 = min(max(lo, 0), a.R);
+    it.rows = max(min(max(hi, 0), a.R) - it.row0, 0);
+    it.n = (min(NT, a.D - it.col0) + STEP - 1) & -STEP;
+  }
+  __device__ __forceinline__ void next() {
+    j += stride;
+    set();
+  }
+};
 
 // Whether `ok` holds in all four warps of a group (named barrier `id`).
 __device__ __forceinline__ bool group_all(int id, bool ok) {
@@ -341,9 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   const uint32_t ring = smem_u32(smem_raw);
   // kForward, kInput: stages of every item
   const int depth = KIND == Gmm16::kForward ? a.D : a.N;
-  auto item = [&](int j, int& e_hint) -> Item {
-    if constexpr (W) return block_item<NT, C::kStep>(j, CB, a);
-    else return tile_item<NT, C::kStep>(j, wl, e_hint);
+  auto items = [&](int from, int by) {
+    if constexpr (W) return BlockItems<NT, C::kStep>(a, CB, total, from, by);
+    else return TileItems<NT, C::kStep>(wl, total, from, by);
   };
   auto steps = [&](const Item& it) { return W ? it.rows : depth; };  // of the reduction
   // stages of an item that are this CTA's: [kb0, kb1) of KB (each of a cluster has one at least)
@@ -353,10 +404,11 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   if (warp == kAWarp || warp == kBWarp) {
     const uint32_t elected = elect_one();
     RingPos at;
-    int n = 0, e_hint = 0;
+    int n = 0;
     bool ok = true;
-    for (int j = first; ok && j < total; j += stride) {
-      const Item it = item(j, e_hint);
+    for (auto list = items(first, stride); ok && list.more(); list.next()) {
+      const Item it = list.it;
+      list.look();
       const int m0 = (PAIR ? 2 * it.cb + (int)rank : it.cb) * 128;  // past the last: the copies bring zeros
       const int cta_cols = PAIR ? it.n / 2 : it.n, deep = steps(it), KB = (deep + C::kDeep - 1) / C::kDeep;
       const int c0 = (W ? it.col0 : it.row0) + (int)rank * cta_cols;
@@ -411,10 +463,10 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
     if (lane == 0) s_issued[warp == kBWarp] = n;
   } else if (RELAY && warp == kRelayWarp) {
     RingPos at;
-    int e_hint = 0;
     bool ok = true;
-    for (int j = first; ok && j < total; j += stride) {
-      const Item it = item(j, e_hint);
+    for (auto list = items(first, stride); ok && list.more(); list.next()) {
+      const Item it = list.it;
+      list.look();
       const int n = steps(it), KB = (n + 63) / 64;
       for (int kb = 0; kb < KB; ++kb, at.next(S)) {
         if (!(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status))) break;
@@ -447,13 +499,13 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       const uint32_t elected = elect_one(), t0 = __shfl_sync(0xffffffffu, tmem, 0);
       uint64_t* there_bar = RELAY ? ready_bar : full_bar;
       RingPos at;
-      int e_hint = 0, u = 0;
+      int u = 0;
       bool ok = true;
       // a barrier's answer takes as long as issuing several MMAs: the next stage's is asked for
       // before this one's are issued
       uint32_t there = mbar_test(&there_bar[0], 0);
-      for (int j = first; ok && j < total; j += stride, ++u) {
-        const Item it = item(j, e_hint);
+      for (auto list = items(first, stride); ok && list.more(); list.next(), ++u) {
+        const Item it = list.it;
         const int buf = u & 1, n = steps(it), KB = (n + C::kDeep - 1) / C::kDeep;
         if (!(ok = warp_wait(&accempty_bar[buf], ((u >> 1) & 1) ^ 1, abort_flag, a.status))) break;
         tc_fence_after();
@@ -477,7 +529,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
               f16_mma<PAIR>(elected, d, da + (k >> 2) * (kABytes >> 4) + (k & 3) * (A_MN ? 128 : 2),
                             db + (k >> 2) * (C::kBBytes >> 4) + (k & 3) * (W ? 128 : 2), idesc, kb > kb0 || k ? 1u : 0u);
           mx_commit<PAIR>(elected, done);
+          if (kb == kb0) list.look();
         }
+        if (kb0 == kb1) list.look();
         if (ok) mx_commit<PAIR>(elected, smem_u32(&accfull_bar[buf]));
       }
       mx_commit_local<PAIR>(elected, smem_u32(&final_bar));  // every MMA done before tensor memory is freed
@@ -490,9 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
     constexpr int kTurns = W ? 2 : 1;
     const int group = (warp - kEpiWarp0) >> 2, quarter = warp & 3;
     const uint32_t lanes = (uint32_t)quarter << 21;  // 32 * quarter in the lane field
-    int e_hint = 0;
-    for (int u = W ? group : 0, j = first + u * stride; j < total; j += kTurns * stride, u += kTurns) {
-      const Item it = item(j, e_hint);
+    int u = W ? group : 0;
+    for (auto list = items(first + u * stride, kTurns * stride); list.more(); list.next(), u += kTurns) {
+      const Item it = list.it;
+      list.look();
       const int buf = u & 1;
       bool ok = warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status);
       ok = group_all(9 + group, ok);  // the group's warps wait for one another below
