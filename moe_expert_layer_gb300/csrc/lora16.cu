@@ -307,11 +307,13 @@ __device__ __forceinline__ void copy_base(const Lora16Problem& p, const int* tok
 // takes a share of D: its warps take 32-deep slices straight from memory, DEEP of them under way, and
 // add up over its shared memory (MMA rows: ranks, MR x 16; columns: tokens).  Behind the cluster's barrier
 // every CTA adds the CTAs' sums, in order, and takes a share of N (MMA rows: tokens; columns: channels, 32 in
-// four MMAs); what its first strip needs is on the way meanwhile.
+// four MMAs); what its first strip needs is on the way meanwhile.  Past 64 ranks two halves of the warps
+// divide them, so that two CTAs still fit an SM.
 constexpr int kFewTokens = 16;
-template <typename T, int MR, int DEEP>
+template <typename T, int MR, int DEEP, int HALVES>
 __global__ void __launch_bounds__(kThreads) lora16_few_kernel(const Lora16Problem p, int ctas) {
-  constexpr int TN = 2, RC = (MR + 1) / 2, kRanks = RC * 32, kPitch = kRanks + 8;  // elements
+  constexpr int TN = 2, RC = (MR * HALVES + 1) / 2, kRanks = RC * 32, kPitch = kRanks + 8;  // elements
+  constexpr int kSlices = kWarps / HALVES;  // taken at once
   extern __shared__ __align__(16) float s_part[];  // [kWarps][MR][TN][4][32]
   __shared__ float s_sum[kFewTokens][kRanks];
   __shared__ __align__(16) T s_hi[kFewTokens * kPitch], s_lo[kFewTokens * kPitch];
@@ -337,22 +339,23 @@ __global__ void __launch_bounds__(kThreads) lora16_few_kernel(const Lora16Proble
   const uint4 zero = make_uint4(0, 0, 0, 0);
   {
     const int chunks = (D + 31) / 32, per = (chunks + ctas - 1) / ctas, c1 = min(chunks, (share + 1) * per);
-    const T* a = static_cast<const T*>(p.a) + (int64_t)tile.l * p.rank * D;
+    const int rank0 = warp % HALVES * MR * 16, ranks = p.rank - rank0;
+    const T* a = static_cast<const T*>(p.a) + ((int64_t)tile.l * p.rank + rank0) * D;
     const T* x[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) x[j] = tok[j] >= 0 ? static_cast<const T*>(p.x) + (int64_t)tok[j] * D : nullptr;
     float c[MR][TN][4] = {};
-    for (int chunk = share * per + warp; chunk < c1; chunk += kWarps * DEEP) {
+    for (int chunk = share * per + warp / HALVES; chunk < c1; chunk += kSlices * DEEP) {
       uint4 b[DEEP][TN], lo[DEEP][MR], hi[DEEP][MR];
 #pragma unroll
       for (int d = 0; d < DEEP; ++d) {
-        const int k = (chunk + d * kWarps) * 32 + t * 8;
-        const bool in = k < D && chunk + d * kWarps < c1;
+        const int k = (chunk + d * kSlices) * 32 + t * 8;
+        const bool in = k < D && chunk + d * kSlices < c1;
 #pragma unroll
         for (int m = 0; m < MR; ++m) {
           const int r = m * 16 + g;
-          lo[d][m] = in && r < p.rank ? __ldcg(reinterpret_cast<const uint4*>(a + (int64_t)r * D + k)) : zero;
-          hi[d][m] = in && r + 8 < p.rank ? __ldcg(reinterpret_cast<const uint4*>(a + (int64_t)(r + 8) * D + k)) : zero;
+          lo[d][m] = in && r < ranks ? __ldcg(reinterpret_cast<const uint4*>(a + (int64_t)r * D + k)) : zero;
+          hi[d][m] = in && r + 8 < ranks ? __ldcg(reinterpret_cast<const uint4*>(a + (int64_t)(r + 8) * D + k)) : zero;
         }
 #pragma unroll
         for (int j = 0; j < TN; ++j) b[d][j] = in && x[j] ? __ldcg(reinterpret_cast<const uint4*>(x[j] + k)) : zero;
@@ -397,10 +400,10 @@ __global__ void __launch_bounds__(kThreads) lora16_few_kernel(const Lora16Proble
   const float scale = p.scales ? __ldcg(p.scales + tile.l) : 1.0f;
   __syncthreads();
   // element q of lane (g, t): rank 16 m + g + 8 (q / 2), token 8 j + 2 t + q % 2
-  for (int i = threadIdx.x; i < MR * TN * 128; i += kThreads) {
+  for (int i = threadIdx.x; i < HALVES * MR * TN * 128; i += kThreads) {
     float s = 0.0f;
 #pragma unroll
-    for (int u = 0; u < kWarps; ++u) s += s_part[u * MR * TN * 128 + i];
+    for (int u = 0; u < kSlices; ++u) s += s_part[u * HALVES * MR * TN * 128 + i];
     const int l = i & 31, q = (i >> 5) & 3, j = (i >> 7) % TN, m = (i >> 7) / TN;
     s_sum[j * 8 + 2 * (l & 3) + (q & 1)][m * 16 + (l >> 2) + 8 * (q >> 1)] = s;
   }
@@ -413,7 +416,7 @@ __global__ void __launch_bounds__(kThreads) lora16_few_kernel(const Lora16Proble
 #pragma unroll
     for (int q = 0; q < RC; ++q) {
       v[q] = 0.0f;
-      if (q * 32 + lane < MR * 16)
+      if (q * 32 + lane < HALVES * MR * 16)
         for (int u = 0; u < ctas; ++u) v[q] += ld_cluster(cluster_addr(&s_sum[i][q * 32 + lane], u));
       v[q] *= scale;
     }
@@ -577,18 +580,21 @@ inline int shrink_splits(const Lora16Problem& p, int tiles, int blocks, int slic
   return splits < 1 ? 1 : splits;
 }
 
-// CTAs to a cluster: as many as the device takes about at once, at most eight.
-template <typename T, int MR, int DEEP>
+// CTAs to a cluster: at most eight, as many as have work for their warps in one of the products, and as the
+// device takes at once, about: half of the tiles counted on are there, and two CTAs fit
+// an SM (128 tokens on 100 adapters of rank 16: eight CTAs to a tile 15.1 us, four 10.9, two 16.8).
+template <typename T, int MR, int DEEP, int HALVES>
 cudaError_t few(const Lora16Problem& p, cudaStream_t stream) {
   const int tiles = tiles_of(p.M, p.L + 1, kFewTokens);
+  const int work = (p.D > p.N ? p.D : p.N) / (32 * kWarps) + 1;
   int ctas = 8;
-  while (ctas > 1 && tiles * ctas > 4 * sm_count()) ctas /= 2;
+  while (ctas > 1 && (tiles * ctas > 4 * sm_count() || ctas >= 2 * work)) ctas /= 2;
   const size_t smem = (size_t)kWarps * MR * 2 * 128 * 4;
   static PerContextOnce set;
   const int dev = current_device();
   if (smem > 16 * 1024 && set.needed(dev)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(lora16_few_kernel<T, MR, DEEP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        cudaFuncSetAttribute(lora16_few_kernel<T, MR, DEEP, HALVES>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     set.done(dev);
   }
@@ -605,7 +611,7 @@ cudaError_t few(const Lora16Problem& p, cudaStream_t stream) {
   attrs[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, lora16_few_kernel<T, MR, DEEP>, p, ctas);
+  return cudaLaunchKernelEx(&cfg, lora16_few_kernel<T, MR, DEEP, HALVES>, p, ctas);
 }
 
 template <typename T, int MR>
@@ -649,10 +655,10 @@ cudaError_t expand_many(const Lora16Problem& p, int splits, cudaStream_t stream)
 template <typename T>
 cudaError_t launch(const Lora16Problem& p, cudaStream_t stream) {
   if (p.M <= 16 * p.L)  // few tokens to an adapter
-    return p.rank <= 16   ? few<T, 1, 4>(p, stream)
-           : p.rank <= 32 ? few<T, 2, 4>(p, stream)
-           : p.rank <= 64 ? few<T, 4, 2>(p, stream)
-                          : few<T, 8, 1>(p, stream);
+    return p.rank <= 16   ? few<T, 1, 4, 1>(p, stream)
+           : p.rank <= 32 ? few<T, 2, 4, 1>(p, stream)
+           : p.rank <= 64 ? few<T, 4, 2, 1>(p, stream)
+                          : few<T, 4, 2, 2>(p, stream);
   int splits = 1;
   cudaError_t e;
   if (p.rank <= 16) {

@@ -105,8 +105,9 @@ __global__ void __launch_bounds__(kThreads) swiglu16_grad_kernel(int R, int E, i
   }
 }
 
-// Dispatch and combine: a block takes a token, or with few tokens a share of its channels, eight
-// channels to a thread; the token's rows are looked up once and all read or written together.
+// Dispatch and combine: `tpt` threads (a power of two from 32) take a token, or with few tokens a share of
+// its channels, eight channels to a thread; the token's rows are looked up once and all read or written
+// together.
 constexpr int kRoutes = 8;  // at a time
 struct Routes {
   int row[kRoutes];
@@ -119,14 +120,16 @@ struct Routes {
   }
 };
 
-__global__ void __launch_bounds__(kThreads) dispatch16_kernel(int D, int copies, int rows, int shares, const uint4* x,
-                                                              const int32_t* row_map, uint4* out) {
+__global__ void __launch_bounds__(kThreads) dispatch16_kernel(int M, int D, int copies, int rows, int tpt, int shares,
+                                                              const uint4* x, const int32_t* row_map, uint4* out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = blockIdx.x / shares, share = blockIdx.x - t * shares, per = D / 8;
+  const int group = blockIdx.x / shares, share = blockIdx.x - group * shares, per = D / 8;
+  const int t = group * (kThreads / tpt) + threadIdx.x / tpt, lane = threadIdx.x & (tpt - 1);
+  if (t >= M) return;
   for (int j = 0; j < copies; j += kRoutes) {
     const Routes r(row_map + (int64_t)t * copies, j, copies, rows);
-    for (int c = share * kThreads + threadIdx.x; c < per; c += shares * kThreads) {
+    for (int c = share * tpt + lane; c < per; c += shares * tpt) {
       const uint4 v = __ldcg(x + (int64_t)t * per + c);
 #pragma unroll
       for (int q = 0; q < kRoutes; ++q)
@@ -135,19 +138,22 @@ __global__ void __launch_bounds__(kThreads) dispatch16_kernel(int D, int copies,
   }
 }
 
-// The sums in order of the routes, in fp32; past eight routes a thread goes on with the next eight.
+// The sums in order of the routes, in fp32; past eight routes a thread goes on one by one.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) combine16_kernel(int D, int copies, int rows, int shares, const T* y,
-                                                             const int32_t* row_map, const float* probs, T* out) {
+__global__ void __launch_bounds__(kThreads) combine16_kernel(int M, int D, int copies, int rows, int tpt, int shares,
+                                                             const T* y, const int32_t* row_map, const float* probs,
+                                                             T* out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int t = blockIdx.x / shares, share = blockIdx.x - t * shares, per = D / 8;
+  const int group = blockIdx.x / shares, share = blockIdx.x - group * shares, per = D / 8;
+  const int t = group * (kThreads / tpt) + threadIdx.x / tpt, lane = threadIdx.x & (tpt - 1);
+  if (t >= M) return;
   const int32_t* map = row_map + (int64_t)t * copies;
   const Routes first(map, 0, copies, rows);
   float p[kRoutes];
 #pragma unroll
   for (int q = 0; q < kRoutes; ++q) p[q] = first.row[q] >= 0 && probs ? __ldcg(probs + (int64_t)t * copies + q) : 1.0f;
-  for (int c = share * kThreads + threadIdx.x; c < per; c += shares * kThreads) {
+  for (int c = share * tpt + lane; c < per; c += shares * tpt) {
     float acc[8] = {};
     Eight<T> v[kRoutes];
 #pragma unroll
@@ -172,28 +178,30 @@ __global__ void __launch_bounds__(kThreads) combine16_kernel(int D, int copies, 
   }
 }
 
-// A block per token and group of G of its routes: dout is read once for the group, each y row once,
-// each dy row written, and the products with y summed over the block in a fixed order.
+// `tpt` threads per token and group of G of its routes: dout is read once for the group, each y row once,
+// each dy row written, and the products with y summed over the threads in a fixed order.
 template <typename T, int G>
-__global__ void __launch_bounds__(kThreads) combine16_grad_kernel(int M, int D, int copies, int rows, const T* dout,
-                                                                  const T* y, const int32_t* row_map,
+__global__ void __launch_bounds__(kThreads) combine16_grad_kernel(int M, int D, int copies, int rows, int tpt,
+                                                                  const T* dout, const T* y, const int32_t* row_map,
                                                                   const float* probs, T* dy, float* dprobs) {
-  __shared__ float part[G][kThreads / 32];
+  __shared__ float part[kThreads / 32][G];
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int groups = (copies + G - 1) / G, t = blockIdx.x / groups, j0 = (blockIdx.x - t * groups) * G;
-  const int per = D / 8, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int groups = (copies + G - 1) / G, tokens = kThreads / tpt;
+  const int t0 = blockIdx.x / groups * tokens, j0 = (blockIdx.x % groups) * G;
+  const int t = t0 + threadIdx.x / tpt, lane = threadIdx.x & (tpt - 1);
+  const int per = D / 8;
   int row[G];
   float p[G], sum[G];
 #pragma unroll
   for (int q = 0; q < G; ++q) {
     const int64_t at = (int64_t)t * copies + j0 + q;
-    row[q] = j0 + q < copies ? __ldcg(row_map + at) : -1;
+    row[q] = t < M && j0 + q < copies ? __ldcg(row_map + at) : -1;
     if ((unsigned)row[q] >= (unsigned)rows) row[q] = -1;
     p[q] = row[q] >= 0 ? __ldcg(probs + at) : 0.0f;
     sum[q] = 0.0f;
   }
-  for (int c = threadIdx.x; c < per; c += kThreads) {
+  for (int c = lane; t < M && c < per; c += tpt) {
     Eight<T> g, v[G];
     load8(dout + (int64_t)t * D + c * 8, g);
 #pragma unroll
@@ -216,14 +224,14 @@ __global__ void __launch_bounds__(kThreads) combine16_grad_kernel(int M, int D, 
   for (int q = 0; q < G; ++q) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum[q] += __shfl_xor_sync(0xffffffffu, sum[q], o);
-    if (lane == 0) part[q][warp] = sum[q];
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5][q] = sum[q];
   }
   __syncthreads();
-  if (threadIdx.x < G && j0 + (int)threadIdx.x < copies) {
+  const int u = threadIdx.x / G, q = threadIdx.x % G;  // token of the block, route
+  if (u < tokens && t0 + u < M && j0 + q < copies) {
     float s = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) s += part[threadIdx.x][w];
-    dprobs[(int64_t)t * copies + j0 + threadIdx.x] = s;
+    for (int w = 0; w < tpt / 32; ++w) s += part[u * (tpt / 32) + w][q];
+    dprobs[(int64_t)(t0 + u) * copies + j0 + q] = s;
   }
 }
 
@@ -232,18 +240,27 @@ inline unsigned grid_of(int64_t items, int per_sm = 8) {
   return (unsigned)(b < most ? b : most);
 }
 
-// Blocks to a token: one, or with few tokens enough for eight blocks on every SM, at most one for each
-// 256 threads' channels.
-inline int shares_of(int M, int D) {
-  const int most = (D / 8 + kThreads - 1) / kThreads, want = (8 * sm_count() + M - 1) / M;
+// Threads to a token: two pieces of eight channels to each at least, where it has as many.
+inline int threads_of(int D) {
+  int tpt = kThreads;
+  while (tpt > 32 && D / 8 < 2 * tpt) tpt /= 2;
+  return tpt;
+}
+// Blocks to `kThreads / tpt` tokens: one, or with few tokens enough for eight blocks on every SM, at most one
+// for each piece that their threads take.
+inline int shares_of(int groups, int D, int tpt) {
+  const int most = (D / 8 + tpt - 1) / tpt, want = (8 * sm_count() + groups - 1) / groups;
   return want < most ? want : most;
 }
+inline int groups_of(int M, int tpt) { return (M + kThreads / tpt - 1) / (kThreads / tpt); }
 
 template <typename T, int G>
 cudaError_t combine_grad(int M, int D, int copies, int rows, const void* dout, const void* y, const int32_t* row_map,
                          const float* probs, void* dy, float* dprobs, cudaStream_t stream) {
+  const int tpt = threads_of(D);
   const unsigned groups = (unsigned)(copies + G - 1) / G;
-  return launch_dependent(combine16_grad_kernel<T, G>, (unsigned)M * groups, kThreads, 0, stream, M, D, copies, rows,
+  return launch_dependent(combine16_grad_kernel<T, G>, (unsigned)groups_of(M, tpt) * groups, kThreads, 0, stream, M, D,
+                          copies, rows, tpt,
                           static_cast<const T*>(dout), static_cast<const T*>(y), row_map, probs, static_cast<T*>(dy),
                           dprobs);
 }
@@ -274,18 +291,19 @@ cudaError_t launch_swiglu16_grad(int R, int E, int I, bool bf16, const void* dh,
 
 cudaError_t launch_dispatch16(int M, int D, int copies, int rows, const void* x, const int32_t* row_map, void* out,
                               cudaStream_t stream) {
-  const int shares = shares_of(M, D);
-  return launch_dependent(dispatch16_kernel, (unsigned)(M * shares), kThreads, 0, stream, D, copies, rows, shares,
-                          static_cast<const uint4*>(x), row_map, static_cast<uint4*>(out));
+  const int tpt = threads_of(D), groups = groups_of(M, tpt), shares = shares_of(groups, D, tpt);
+  return launch_dependent(dispatch16_kernel, (unsigned)(groups * shares), kThreads, 0, stream, M, D, copies, rows, tpt,
+                          shares, static_cast<const uint4*>(x), row_map, static_cast<uint4*>(out));
 }
 
 cudaError_t launch_combine16(int M, int D, int copies, int rows, bool bf16, const void* y, const int32_t* row_map,
                              const float* probs, void* out, cudaStream_t stream) {
-  const int shares = shares_of(M, D);
+  const int tpt = threads_of(D), groups = groups_of(M, tpt), shares = shares_of(groups, D, tpt);
+  const unsigned grid = (unsigned)(groups * shares);
   if (bf16)
-    return launch_dependent(combine16_kernel<__nv_bfloat16>, (unsigned)(M * shares), kThreads, 0, stream, D, copies, rows,
-                            shares, static_cast<const __nv_bfloat16*>(y), row_map, probs, static_cast<__nv_bfloat16*>(out));
-  return launch_dependent(combine16_kernel<__half>, (unsigned)(M * shares), kThreads, 0, stream, D, copies, rows, shares,
+    return launch_dependent(combine16_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, M, D, copies, rows, tpt, shares,
+                            static_cast<const __nv_bfloat16*>(y), row_map, probs, static_cast<__nv_bfloat16*>(out));
+  return launch_dependent(combine16_kernel<__half>, grid, kThreads, 0, stream, M, D, copies, rows, tpt, shares,
                           static_cast<const __half*>(y), row_map, probs, static_cast<__half*>(out));
 }
 
