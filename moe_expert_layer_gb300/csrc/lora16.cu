@@ -123,10 +123,12 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
 // Many tokens to an adapter.  MMA rows: tokens, 16 to each of four groups of two warps; columns:
 // ranks, MR x 8 to a warp.  A stage is 64 deep: rows of 128 bytes, their 16-byte pieces c at
 // c ^ (row % 8).
-constexpr int kManyTokens = 64, kStages = 4;
+constexpr int kManyTokens = 64;
+template <int MR>  // about 64 KB to a block: more copies under way at low ranks
+constexpr int kStagesOf = MR <= 2 ? 6 : 4;
 template <typename T, int MR>
 __global__ void __launch_bounds__(kThreads) lora16_shrink_many_kernel(const Lora16Problem p, int splits) {
-  constexpr int kXBytes = kManyTokens * 128, kStage = kXBytes + MR * 16 * 128;
+  constexpr int kXBytes = kManyTokens * 128, kStage = kXBytes + MR * 16 * 128, kStages = kStagesOf<MR>;
   extern __shared__ __align__(128) uint8_t s_ring[];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -452,12 +454,13 @@ __global__ void __launch_bounds__(kThreads) lora16_few_kernel(const Lora16Proble
 }
 
 // Many tokens to an adapter: 64, 16 to each of four groups of two warps, which keep their rank values in
-// registers; the adapter's rows of b pass through a ring in shared memory, 64 channels a stage, 32 to
-// a warp.  The rows lie there in the order of the MMAs' columns (a row of eight MMA columns after the
+// registers; base and the adapter's rows of b pass through a ring in shared memory, 64 channels a stage,
+// 32 to a warp.  The rows of b lie there in the order of the MMAs' columns (a row of eight MMA columns after the
 // other, 16 bytes past a multiple of 32).
 template <typename T, int RK>  // RK x 16 ranks
 __global__ void __launch_bounds__(kThreads) lora16_expand_many_kernel(const Lora16Problem p, int splits, int shares) {
-  constexpr int RC = (RK + 1) / 2, kPitch = RC * 32 + 8, kRow = RK * 32 + 16, kStage = 64 * kRow;
+  constexpr int RC = (RK + 1) / 2, kPitch = RC * 32 + 8, kRow = RK * 32 + 16;
+  constexpr int kBase = kManyTokens * 128, kStage = kBase + 64 * kRow, kStages = kStagesOf<RK>;
   extern __shared__ __align__(128) uint8_t s_mem[];  // the ring, then hi and lo of the rank values
   __shared__ float s_pow[kManyTokens];
   __shared__ int s_tok[kManyTokens];
@@ -484,14 +487,28 @@ __global__ void __launch_bounds__(kThreads) lora16_expand_many_kernel(const Lora
   const T* base = static_cast<const T*>(p.base);
   T* out = static_cast<T*>(p.out);
   const uint32_t ring = smem_u32(s_mem);
+  const int row = threadIdx.x >> 3, piece = threadIdx.x & 7;  // of base, rows 32 apart, pieces c at c ^ (row % 8)
+  const T* from[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int tok = s_tok[row + 32 * k];
+    from[k] = tok >= 0 ? base + (int64_t)tok * N + piece * 8 : nullptr;
+  }
   auto load = [&](int i, int stage) {
+    const uint32_t st = ring + stage * kStage;
+    const int c0 = (first + i) * 64;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const bool in = from[k] && c0 + piece * 8 < N;
+      copy16(st + (row + 32 * k) * 128 + ((piece ^ (row & 7)) << 4), in ? from[k] + c0 : base, in);
+    }
 #pragma unroll
     for (int k = 0; k < RK * 128; k += kThreads) {
-      const int at = k + threadIdx.x, ch = at / (RK * 2), piece = at % (RK * 2), c = (first + i) * 64 + ch;
+      const int at = k + threadIdx.x, ch = at / (RK * 2), q = at % (RK * 2), c = c0 + ch;
       // channel 8 (c / 2) + 2 j + c % 2 of 32: column c of MMA j
-      const int row = (ch & 32) + ((ch >> 1) & 3) * 8 + ((ch >> 3) & 3) * 2 + (ch & 1);
-      const bool in = c < N && piece * 8 < p.rank;
-      if (RK > 1 || at < 128) copy16(ring + stage * kStage + row * kRow + piece * 16, in ? b + (int64_t)c * p.rank + piece * 8 : b, in);
+      const int r = (ch & 32) + ((ch >> 1) & 3) * 8 + ((ch >> 3) & 3) * 2 + (ch & 1);
+      const bool in = c < N && q * 8 < p.rank;
+      if (RK > 1 || at < 128) copy16(st + kBase + r * kRow + q * 16, in ? b + (int64_t)c * p.rank + q * 8 : b, in);
     }
   };
 #pragma unroll
@@ -500,18 +517,8 @@ __global__ void __launch_bounds__(kThreads) lora16_expand_many_kernel(const Lora
     asm volatile("cp.async.commit_group;" ::: "memory");
   }
   const int tg = warp >> 1, half = warp & 1;
-  const uint4 zero = make_uint4(0, 0, 0, 0);
   const int tok[2] = {s_tok[tg * 16 + g], s_tok[tg * 16 + g + 8]};
-  const T* rows[2] = {base + (int64_t)tok[0] * N, base + (int64_t)tok[1] * N};  // read and written where tok >= 0
-  T* outs[2] = {out + (int64_t)tok[0] * N, out + (int64_t)tok[1] * N};
-  uint4 y[2][2];  // two strips
-  auto load_base = [&](int i, uint4 (&o)[2]) {
-    const int c = (first + i) * 64 + half * 32 + t * 8;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) o[h] = i < n && tok[h] >= 0 && c < N ? __ldcg(reinterpret_cast<const uint4*>(rows[h] + c)) : zero;
-  };
-  load_base(0, y[0]);
-  load_base(1, y[1]);
+  T* outs[2] = {out + (int64_t)tok[0] * N, out + (int64_t)tok[1] * N};  // written where tok >= 0
   asm volatile("griddepcontrol.wait;" ::: "memory");
   for (int i0 = warp; i0 < kManyTokens; i0 += 4 * kWarps) {
     float v[4][RC];
@@ -535,13 +542,13 @@ __global__ void __launch_bounds__(kThreads) lora16_expand_many_kernel(const Lora
   }
   const float f[2] = {s_pow[tg * 16 + g], s_pow[tg * 16 + g + 8]};
   const uint32_t brow = (half * 32 + (lane >> 4) * 8 + (lane & 7)) * kRow + ((lane >> 3) & 1) * 16;
-#pragma unroll 2
   for (int i = 0; i < n; ++i) {
     asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
     __syncthreads();  // the stage has landed for all, and all are done with the one that is filled next
     if (i + kStages - 1 < n) load(i + kStages - 1, (i + kStages - 1) % kStages);
     asm volatile("cp.async.commit_group;" ::: "memory");
-    const uint32_t st = ring + (i % kStages) * kStage + brow;
+    const uint32_t st = ring + (i % kStages) * kStage + kBase + brow;
+    const uint8_t* ys = s_mem + (i % kStages) * kStage;
     float c[4][4] = {};
 #pragma unroll
     for (int k = 0; k < RK; ++k)
@@ -557,17 +564,19 @@ __global__ void __launch_bounds__(kThreads) lora16_expand_many_kernel(const Lora
     const int ch = (first + i) * 64 + half * 32 + t * 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-      if (tok[h] >= 0 && ch < N) *reinterpret_cast<uint4*>(outs[h] + ch) = add_base<T>(y[i & 1][h], c, h, f[h]);
-    load_base(i + 2, y[i & 1]);
+      if (tok[h] >= 0 && ch < N) {
+        const uint4 y = *reinterpret_cast<const uint4*>(ys + (tg * 16 + g + 8 * h) * 128 + (((half * 4 + t) ^ g) << 4));
+        *reinterpret_cast<uint4*>(outs[h] + ch) = add_base<T>(y, c, h, f[h]);
+      }
   }
 }
 
 // Shares of D: enough blocks for the device, at most what the workspace holds, part_rows(M) rows of
-// fp32 rank values in all: for four shares up to 8192 tokens, and for more with fewer than 1024.
-constexpr int kMaxSplits = 16;
+// fp32 rank values in all: eight shares up to 4096 tokens, fewer above.
+constexpr int kMaxSplits = 8;
 inline int part_rows(int M) {
-  const int many = M < 8192 ? 4 * M : 32768;
-  return M > many ? M : many < 4096 ? 4096 : many;
+  const int many = M < 4096 ? kMaxSplits * M : kMaxSplits * 4096;
+  return M > many ? M : many;
 }
 
 inline int tiles_of(int M, int groups, int tokens) { return M / tokens + (M < groups ? M : groups); }
@@ -618,7 +627,7 @@ template <typename T, int MR>
 cudaError_t shrink_many(const Lora16Problem& p, int& splits, cudaStream_t stream) {
   const int tiles = tiles_of(p.M, p.L, kManyTokens);
   splits = shrink_splits(p, tiles, 3 * sm_count(), (p.D + 255) / 256);
-  const size_t smem = (size_t)kStages * (kManyTokens + MR * 16) * 128;
+  const size_t smem = (size_t)kStagesOf<MR> * (kManyTokens + MR * 16) * 128;
   static PerContextOnce set;
   const int dev = current_device();
   if (set.needed(dev)) {
@@ -639,7 +648,7 @@ cudaError_t expand_many(const Lora16Problem& p, int splits, cudaStream_t stream)
   int shares = 2 * sm_count() / likely;
   if (shares > (strips + 3) / 4) shares = (strips + 3) / 4;
   if (shares < 1) shares = 1;
-  const int smem = kStages * 64 * (RK * 32 + 16) + 2 * kManyTokens * (RC * 32 + 8) * 2;
+  const int smem = kStagesOf<RK> * (kManyTokens * 128 + 64 * (RK * 32 + 16)) + 2 * kManyTokens * (RC * 32 + 8) * 2;
   static PerContextOnce set;
   const int dev = current_device();
   if (smem > 48 * 1024 && set.needed(dev)) {
