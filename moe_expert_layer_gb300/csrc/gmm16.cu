@@ -191,8 +191,8 @@ __device__ __forceinline__ int tiles_of(int start, int end) {
   return end > start ? (end - start + NT - 1) / NT : 0;
 }
 
-// With t tiles of `size` rows (a multiple of the step, at most NT) none is empty: (t - 1) * size is
-// less than the rows, since size < rows / t + STEP and t > 1 only where rows > (t - 1) * NT.
+// An expert's rows are cut into t tiles of two sizes, multiples of the step that differ by it, the larger ones
+// first and as few as cover the rows (tiles of one size, 800 rows as four of 224, were TODO slower).
 template <int NT, int STEP>
 __device__ __forceinline__ Item tile_item(int j, const WorkList& wl, int& e_hint) {
   // pref[lo] <= j < pref[hi]: mostly the same expert as the item before, or one of the next
@@ -208,14 +208,14 @@ __device__ __forceinline__ Item tile_item(int j, const WorkList& wl, int& e_hint
   }
   e_hint = lo;
   const int start = lo ? wl.end[lo - 1] : 0, end = wl.end[lo];
-  const int t = tiles_of<NT>(start, end), size = ((end - start + t - 1) / t + STEP - 1) & -STEP;
+  const int t = tiles_of<NT>(start, end), steps = (end - start + STEP - 1) / STEP, less = steps / t, more = steps - less * t;
   const int local = j - wl.pref[lo], rt = local / wl.CB;
   Item it;
   it.e = lo;
   it.cb = local - rt * wl.CB;
-  it.row0 = start + rt * size;
-  it.rows = min(size, end - it.row0);
-  it.n = (it.rows + STEP - 1) & -STEP;
+  it.row0 = start + (rt * less + min(rt, more)) * STEP;
+  it.n = (less + (rt < more ? 1 : 0)) * STEP;
+  it.rows = min(it.n, end - it.row0);
   it.col0 = 0;
   return it;
 }

@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kThreads) swiglu16_kernel(int R, int E, int I,
 
 // dgu may be gu and h may be dh: a thread reads its elements before it writes them.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) swiglu16_grad_kernel(int R, int E, int I, const T* dh, const T* gu,
+__global__ void __launch_bounds__(kThreads, 4) swiglu16_grad_kernel(int R, int E, int I, const T* dh, const T* gu,
                                                                  const int32_t* cumsum, T* dgu, T* h) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
