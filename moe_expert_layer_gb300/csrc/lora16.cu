@@ -487,28 +487,37 @@ __global__ void __launch_bounds__(kThreads) lora16_expand_many_kernel(const Lora
   const T* base = static_cast<const T*>(p.base);
   T* out = static_cast<T*>(p.out);
   const uint32_t ring = smem_u32(s_mem);
-  const int row = threadIdx.x >> 3, piece = threadIdx.x & 7;  // of base, rows 32 apart, pieces c at c ^ (row % 8)
-  const T* from[2];
+  // this thread's pieces of a stage: two of base (rows 32 apart, piece c of a row at c ^ (row % 8)) and
+  // kB of b, whose channel 8 (c / 2) + 2 j + c % 2 of 32 is column c of MMA j
+  constexpr int kB = (RK * 128 + kThreads - 1) / kThreads;
+  const int row = threadIdx.x >> 3, piece = threadIdx.x & 7;
+  const T *from[2], *bfrom[kB];
+  uint32_t to[2], bto[kB];
+  int ch[kB];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int tok = s_tok[row + 32 * k];
-    from[k] = tok >= 0 ? base + (int64_t)tok * N + piece * 8 : nullptr;
+    from[k] = tok >= 0 ? base + (int64_t)tok * N + first * 64 + piece * 8 : nullptr;
+    to[k] = ring + (row + 32 * k) * 128 + ((piece ^ (row & 7)) << 4);
+  }
+#pragma unroll
+  for (int k = 0; k < kB; ++k) {
+    const int at = k * kThreads + threadIdx.x, c = at / (RK * 2), q = at % (RK * 2);
+    const int r = (c & 32) + ((c >> 1) & 3) * 8 + ((c >> 3) & 3) * 2 + (c & 1);
+    ch[k] = at < RK * 128 && q * 8 < p.rank ? first * 64 + c : N;  // N and past it: zeros
+    bfrom[k] = b + (int64_t)(first * 64 + c) * p.rank + q * 8;
+    bto[k] = ring + kBase + r * kRow + q * 16;
   }
   auto load = [&](int i, int stage) {
-    const uint32_t st = ring + stage * kStage;
-    const int c0 = (first + i) * 64;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const bool in = from[k] && c0 + piece * 8 < N;
-      copy16(st + (row + 32 * k) * 128 + ((piece ^ (row & 7)) << 4), in ? from[k] + c0 : base, in);
+      const bool in = from[k] && (first + i) * 64 + piece * 8 < N;
+      copy16(to[k] + stage * kStage, in ? from[k] + i * 64 : base, in);
     }
 #pragma unroll
-    for (int k = 0; k < RK * 128; k += kThreads) {
-      const int at = k + threadIdx.x, ch = at / (RK * 2), q = at % (RK * 2), c = c0 + ch;
-      // channel 8 (c / 2) + 2 j + c % 2 of 32: column c of MMA j
-      const int r = (ch & 32) + ((ch >> 1) & 3) * 8 + ((ch >> 3) & 3) * 2 + (ch & 1);
-      const bool in = c < N && q * 8 < p.rank;
-      if (RK > 1 || at < 128) copy16(st + kBase + r * kRow + q * 16, in ? b + (int64_t)c * p.rank + q * 8 : b, in);
+    for (int k = 0; k < kB; ++k) {
+      const bool in = ch[k] + i * 64 < N;
+      if (RK > 1 || threadIdx.x < 128) copy16(bto[k] + stage * kStage, in ? bfrom[k] + (int64_t)i * 64 * p.rank : b, in);
     }
   };
 #pragma unroll
@@ -551,16 +560,15 @@ __global__ void __launch_bounds__(kThreads) lora16_expand_many_kernel(const Lora
     const uint8_t* ys = s_mem + (i % kStages) * kStage;
     float c[4][4] = {};
 #pragma unroll
-    for (int k = 0; k < RK; ++k)
+    for (int k = 0; k < RK; ++k) {
+      uint32_t w[2][4];
+      ldmatrix4(w[0], st + k * 32);
+      ldmatrix4(w[1], st + 16 * kRow + k * 32);
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {
-        uint32_t w[4];
-        ldmatrix4(w, st + j * 8 * kRow + k * 32);
-        mma16<T>(c[j], lo[k], w[0], w[1]);
-        mma16<T>(c[j + 1], lo[k], w[2], w[3]);
-        mma16<T>(c[j], hi[k], w[0], w[1]);
-        mma16<T>(c[j + 1], hi[k], w[2], w[3]);
-      }
+      for (int j = 0; j < 4; ++j) mma16<T>(c[j], lo[k], w[j >> 1][2 * (j & 1)], w[j >> 1][2 * (j & 1) + 1]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mma16<T>(c[j], hi[k], w[j >> 1][2 * (j & 1)], w[j >> 1][2 * (j & 1) + 1]);
+    }
     const int ch = (first + i) * 64 + half * 32 + t * 8;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
