@@ -6,7 +6,8 @@
  * The conventions of moe_layer.h hold: device pointers owned by the caller and 16-byte
  * aligned (workspaces 256-byte aligned), dense row-major arrays, nothing allocated, work
  * enqueued on `stream`, arguments checked on the host before anything is launched, its
- * status codes and its route tables.  `type` is MOE_TYPE_F16 or MOE_TYPE_BF16 and is the
+ * status codes and its route tables.  Calls that may overlap on the device (on streams of
+ * their own, or as graphs replayed at once) need workspaces of their own.  `type` is MOE_TYPE_F16 or MOE_TYPE_BF16 and is the
  * type of every array whose type is not named.  Sums are held in fp32 and rounded to
  * nearest even where they are stored, once; binary16 saturates at +-65504 (a NaN stays a
  * NaN), bfloat16 overflows to infinity.
@@ -136,8 +137,8 @@ size_t moe_lora16_workspace_size(int32_t M, int32_t N, int32_t D, int32_t rank);
  *   x [M][D]; base [M][N], what the projection gave; out [M][N], which may be base itself
  *   route [M], cumsum [L]: the tokens sorted by adapter, sorted_src_route and cumsum of
  *       moe_route_sort on the tokens' adapters (topK = 1, E = L; an id outside [0, L) is no
- *       adapter).  Made once, they serve every projection of a batch.  Entries outside
- *       [0, M) are skipped.
+ *       adapter).  Made once, they serve every projection of a batch.  Entries of route
+ *       outside [0, M) are skipped; no token may be there twice.
  *   a [L][rank][D], b [L][N][rank]; scales [L] fp32 or NULL (all 1)
  * The rank values of a token between the two products keep 16 significant bits.
  */

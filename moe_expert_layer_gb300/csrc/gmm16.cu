@@ -13,25 +13,39 @@
 //
 // kForward and kInput: the ragged side, an expert's rows, is the one whose size the instruction
 // takes in steps of 16 (32 for a pair): an expert of cnt rows is cut into ceil(cnt / NT) tiles of
-// equal size rounded up to that step.  Items (expert, row tile, channel block) are dealt out
-// expert-major, channel blocks innermost, so that CTAs working at the same time share an expert's
-// rows and its weights through L2.  kWeight: items are 256 x 256 blocks of dw[e]; the last stage of
-// an expert's rows also brings rows of the next expert, which are overwritten with zeros in shared
-// memory (up to the 16 rows that an MMA takes) before the MMAs see them.
+// multiples of that step.  Items (expert, row tile, channel block) are dealt out expert-major, channel
+// blocks innermost, so that CTAs working at the same time share an expert's rows and its weights
+// through L2.  kWeight: items are 256 x 256 blocks of dw[e]; the last stage of an expert's rows also
+// brings rows of the next expert, which are overwritten with zeros in shared memory (up to the 16 rows
+// that an MMA takes) before the MMAs see them: 0 times what they hold could be NaN.
 //
-// Persistent CTAs, one per SM, in two forms: single CTAs of 128 channels and tiles of up to 32 rows,
-// which stream the weights past few rows; and CTA pairs (cta_group::2) of 256 channels and tiles of
-// up to 256 rows, of which each CTA loads half.
+// Persistent CTAs, one per SM, in three forms (`choose`, at the end, with what each takes):
+//   - single CTAs of 128 channels and tiles of up to 32 rows: the weights stream past few rows.  Where
+//     there are too few items for the device, a cluster divides the reduction of each: every CTA leaves
+//     its sums in its shared memory, and behind a barrier of the cluster each adds a share of the
+//     tile's elements over the CTAs, in order, and stores it.
+//   - single CTAs and tiles of up to 128 rows;
+//   - CTA pairs (cta_group::2) of 256 channels and tiles of up to 256 rows, of which each CTA loads half.
 //
-// Where there are too few items for the device, a cluster of single CTAs divides the reduction of each: every
-// CTA leaves its sums in its shared memory, and behind a barrier of the cluster each adds a share of
-// the tile's elements over the CTAs, in order, and stores it.
+// Measured (bfloat16, GB300; of MEASURED rates 6672 GB/s and 1920 TFLOP/s; weights not in L2):
+//   8 experts x 1 row, 7168 -> 4096       70 us   6.7 TB/s: the weights' stream, all there is
+//   256 experts x 4, 7168 -> 4096       2030 us   7.4 TB/s (reads alone run faster than a copy)
+//   1 expert x 1 row, 4096 -> 4096      10.7 us   3.1 TB/s: launch 3.7, then the stream of a round
+//   1 expert x 8192, 4096 -> 4096        138 us   1990 TFLOP/s (the library's product: 142)
+//   64 experts x 768, 4096 -> 2816   670-740 us   1530-1690 TFLOP/s alone, tensor pipe 89% busy; back to
+//       back for seconds 787, where the power limit holds the clock at 1.45 GHz.  What is left: experts a
+//       little past 768 rows take a fourth tile, and 34.2 rounds of items are 35.
+// L2 gives the SMs about 13.5 TB/s, which a pair's 64 KB a stage of 512 clocks nearly takes at 1.9 GHz.
+// Two pairs to a cluster that share their rows by multicast were slower all the same (180 us for 144 at
+// 8192 x 4096 x 4096): a slot is free only when both pairs are done, and 36 such clusters leave 8 SMs idle.
 //
 // Roles: warp 0 loads operand A and warp 2 operand B, 64 steps of the reduction a stage, into a ring
 // in shared memory; warp 3 (pairs) tells the leading CTA that a stage has landed; warp 1 of the
 // leading CTA issues the MMAs; warps 4-11, two groups, round the sums of one accumulator and store them
 // while the MMAs fill the other.  Every wait is bounded: one that gives up records MOE_ERR_TIMEOUT
 // and the CTA winds down.
+#include <cmath>
+
 #include "experts16.h"
 #include "mx_tc.cuh"
 #include "tensor_map.h"
@@ -192,7 +206,8 @@ __device__ __forceinline__ int tiles_of(int start, int end) {
 }
 
 // An expert's rows are cut into t tiles of two sizes, multiples of the step that differ by it, the larger ones
-// first and as few as cover the rows (tiles of one size, 800 rows as four of 224, were TODO slower).
+// first and as few as cover the rows (of one size, 800 rows would be four
+// of 224: 16 experts of 800 x 4096 x 2816 198 us for 192).
 template <int NT, int STEP>
 __device__ __forceinline__ Item tile_item(int j, const WorkList& wl, int& e_hint) {
   // pref[lo] <= j < pref[hi]: mostly the same expert as the item before, or one of the next
@@ -731,7 +746,10 @@ bool encode_tensor_map_3d(CUtensorMap* m, CUtensorMapDataType dt, size_t elem, c
 
 // Clusters of this many CTAs, one to an SM, that the device holds at once (GB300: 152, 76 and 36 of 1, 2
 // and 4: a cluster of four needs four SMs of one GPC).
-inline int resident_clusters(int ctas) { return ctas <= 2 ? sm_count() / ctas : sm_count() / 19 * 18 / ctas; }
+inline int resident_clusters(int ctas) {
+  const int n = ctas <= 2 ? sm_count() / ctas : sm_count() / 19 * 18 / ctas;
+  return n < 1 ? 1 : n;
+}
 
 template <Gmm16 KIND, int NT, bool PAIR>
 cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
@@ -779,29 +797,38 @@ cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, gmm16_kernel<KIND, NT, PAIR>, maps, a);
 }
 
-}  // namespace
-
-namespace {
-
-// What a form takes, in clocks: rounds of its items over the units that work at once, each the item's stages
-// and what an item costs besides.  The host knows the rows per expert on average only.
+// What a form takes, in clocks: rounds of its items over the clusters that work at once, each the item's stages
+// and what an item costs besides.  The host knows the rows per expert on average only.  Both sides, us
+// (forward / gradient for the rows; `32 x 4` is the first form divided by four):
+//                                          32      32 x 2     32 x 4      128        pairs
+//   1 expert x 1, 4096 -> 4096            13.1      11.3       10.8       15.9        18.4
+//   1 expert x 128                        13.7      17.1       22.1       18.1        20.3
+//   1 expert x 512                                                        18.8        24.9
+//   1 expert x 1024                                                       32.0        25.8
+//   8 experts x 40, 4096 -> 2816       41 / 39   39 / 40    48 / 54    41 / 34     44 / 36
+//   8 experts x 128                    51 / 50   55 / 59    81 / 101   44 / 36     46 / 37
+//   64 experts x 64                   267 / 238 252 / 265  337 / 397  232 / 224   240 / 228
+//   32 experts x 200, 2048 -> 1024     60 / 65   79 / 123  143 / 261   40 / 37     35 / 34
 struct Form {
   int nt, split;  // columns of a tile; 256: pairs
-  double clocks;
+  double stage;   // clocks of 64 steps of the reduction
 };
 Form choose(const Gmm16Problem& p) {
+  const Form forms[] = {{32, 1, 290}, {32, 2, 290}, {32, kMaxSplit, 290}, {128, 1, 420}, {256, 1, 520}};
   const int outs = p.kind == Gmm16::kForward ? p.N : p.D, depth = p.kind == Gmm16::kForward ? p.D : p.N;
   const int experts = p.R < p.E ? p.R : p.E, KB = (depth + 63) / 64;
   const double rows = (double)p.R / experts;
-  Form best{0, 1, 0.0};
-  for (const int nt : {32, 128, 256}) {
-    const int tiles = (int)((rows + nt - 1) / nt), blocks = (outs + (nt == 256 ? 255 : 127)) / (nt == 256 ? 256 : 128);
-    const double stage = nt == 32 ? 290 : nt == 128 ? 420 : 520;
-    for (int split = 1; split <= (nt > 32 || KB < 16 ? 1 : 4); split *= 2) {
-      const double items = (double)experts * tiles * blocks, units = resident_clusters(nt == 256 ? 2 : split);
-      const double rounds = (double)(int64_t)((items + units - 1) / units);
-      const double clocks = rounds * ((KB + split - 1) / split * stage + (split > 1 ? 3000 : 800));
-      if (!best.nt || clocks < best.clocks) best = Form{nt, split, clocks};
+  Form best{};
+  double least = 0.0;
+  for (const Form& f : forms) {
+    if (f.split > 1 && KB < 4 * kMaxSplit) continue;  // each CTA of a cluster has a stage at least
+    const int ctas = f.nt == 256 ? 2 : f.split, width = f.nt == 256 ? 256 : 128;
+    const double items = experts * ceil(rows / f.nt) * ((outs + width - 1) / width);
+    const double clocks =
+        ceil(items / resident_clusters(ctas)) * ((KB + f.split - 1) / f.split * f.stage + (f.split > 1 ? 3000 : 800));
+    if (!best.nt || clocks < least) {
+      best = f;
+      least = clocks;
     }
   }
   return best;

@@ -10,6 +10,7 @@ pytestmark = pytest.mark.gpu
 if torch.cuda.is_available():
     import moe_expert_layer_gb300 as moe
     from test_gpu_experts16 import F32, ints, normal, prefix, rng, space
+    from test_gpu_mxfp4_waits import narrow_stream  # noqa: F401  (a fixture)
 
 F16, BF16 = torch.float16, torch.bfloat16
 
@@ -290,3 +291,27 @@ def test_tensors_elsewhere_are_refused():
         args[bad] = args[bad].cpu()
         with pytest.raises(ValueError, match="device"):
             moe.moe_gmm16(**args)
+
+
+@pytest.mark.parametrize("rows,E,N,D", [(3, 2, 4096, 4096), (60, 8, 512, 512), (600, 3, 1024, 512)])
+def test_on_a_part_of_the_device(narrow_stream, rows, E, N, D):  # noqa: F811
+    """On a stream that may use fewer SMs than the device has, products and adapters give what they give on all of it."""
+    g, R = rng(8), rows * E
+    a, dc, w = ints((R, D), BF16, g, 2), ints((R, N), BF16, g, 1), ints((E, N, D), BF16, g, 1)
+    cumsum, ws = prefix([rows] * E), space(R, E, N, D)
+    la, lb = ints((E, 8, D), BF16, g, 1), ints((E, N, 8), BF16, g, 1)
+    route = torch.arange(R, device="cuda").int()
+    lws = torch.empty(moe.moe_lora16_workspace_size(R, N, D, 8), dtype=torch.uint8, device="cuda")
+    got = []
+    for stream in (None, narrow_stream):
+        c, da, out = (torch.zeros(s, dtype=BF16, device="cuda") for s in ((R, N), (R, D), (R, N)))
+        dw = torch.zeros((E, N, D), device="cuda")
+        torch.cuda.synchronize()
+        moe.moe_gmm16(a, cumsum, w, c, ws, stream=stream)
+        moe.moe_gmm16_input_grad(dc, cumsum, w, da, ws, stream=stream)
+        moe.moe_gmm16_weight_grad(dc, a, cumsum, dw, ws, stream=stream)
+        moe.moe_lora16(a, route, cumsum, la, lb, c, out, lws, stream=stream)
+        torch.cuda.synchronize()
+        assert moe.moe_workspace_status(ws) == 0
+        got.append([c, da, dw, out])
+    assert same(*got)
