@@ -40,8 +40,8 @@
 // 8192 x 4096 x 4096): a slot is free only when both pairs are done, and 36 such clusters leave 8 SMs idle.
 //
 // Roles: warp 0 loads operand A and warp 2 operand B, 64 steps of the reduction a stage, into a ring
-// in shared memory; warp 3 (pairs) tells the leading CTA that a stage has landed; warp 1 of the
-// leading CTA issues the MMAs; warps 4-11, two groups, round the sums of one accumulator and store them
+// in shared memory (a pair's copies complete the leading CTA's barriers); warp 3 overwrites rows
+// (kWeight); warp 1 of the leading CTA issues the MMAs; warps 4-11, two groups, round the sums of one accumulator and store them
 // while the MMAs fill the other.  Every wait is bounded: one that gives up records MOE_ERR_TIMEOUT
 // and the CTA winds down.
 #include <cmath>
@@ -54,7 +54,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kAWarp = 0, kMmaWarp = 1, kBWarp = 2, kRelayWarp = 3, kEpiWarp0 = 4;
+constexpr int kAWarp = 0, kMmaWarp = 1, kBWarp = 2, kFixWarp = 3, kEpiWarp0 = 4;
 constexpr int kMaxExperts = 1024;
 constexpr int kABytes = 128 * 128;  // 128 channels x 64 steps
 constexpr int kOutRows = 32;        // of an epilogue group's store, x 128 channels
@@ -130,15 +130,40 @@ __device__ __forceinline__ void f16_mma(uint32_t elected, uint32_t d, uint64_t a
         : "memory");
 }
 
-__device__ __forceinline__ void tma_load_3d_elect(uint32_t elected, uint32_t dst, const void* tmap, int32_t x, int32_t y,
-                                                  int32_t z, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "setp.ne.u32 e, %6, 0;\n\t"
-      "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(elected)
-      : "memory");
+// Boxes of a tensor map to this CTA's shared memory, completing `bar`: of this CTA or, in a pair, of either.
+template <bool PAIR>
+__device__ __forceinline__ void load_2d(uint32_t elected, uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                        uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.u32 e, %5, 0;\n\t"
+        "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(bar), "r"(elected)
+        : "memory");
+  else
+    tma_load_2d_elect(elected, dst, tmap, x, y, bar);
+}
+template <bool PAIR>
+__device__ __forceinline__ void load_3d(uint32_t elected, uint32_t dst, const void* tmap, int32_t x, int32_t y,
+                                        int32_t z, uint32_t bar) {
+  if (PAIR)
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.u32 e, %6, 0;\n\t"
+        "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(elected)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "setp.ne.u32 e, %6, 0;\n\t"
+        "@e cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];\n\t}" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(bar), "r"(elected)
+        : "memory");
 }
 // Tiled store of a 3-D map's box, or its addition (fp32) to what is there.
 __device__ __forceinline__ void tma_store_3d(const void* tmap, int32_t x, int32_t y, int32_t z, const void* src) {
@@ -187,6 +212,13 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
                : "memory");
   return v;
 }
+
+__device__ __forceinline__ void mbar_arrive_twice(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], 2;" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// kWeight: whether a stage of which `left` rows are the expert's is overwritten behind them: an MMA takes 16.
+__device__ __forceinline__ bool fixed(int left) { return left < 64 && (left & 15) != 0; }
 
 struct Item {
   int e, cb;          // expert, block of the MMA's rows (of a CTA or a pair)
@@ -323,9 +355,9 @@ template <Gmm16 KIND, int NT, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constant__ Maps maps, const Args a) {
   using C = Cfg<KIND, NT, PAIR>;
   constexpr int S = C::kStages;
-  constexpr bool W = C::kWeight, A_MN = KIND != Gmm16::kForward, RELAY = PAIR || W;
+  constexpr bool W = C::kWeight, A_MN = KIND != Gmm16::kForward, FIX = W;
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // swizzled rows: 1024-byte groups
-  __shared__ __align__(8) uint64_t full_bar[S], peer_bar[S], ready_bar[S], empty_bar[S], accfull_bar[2], accempty_bar[2], final_bar;
+  __shared__ __align__(8) uint64_t full_bar[S], tail_bar[W ? S : 1], peer_bar[W ? S : 1], empty_bar[S], accfull_bar[2], accempty_bar[2], final_bar;
   __shared__ __align__(8) uint64_t sums_bar, read_bar;  // of a cluster that divides the reduction
   __shared__ int s_pref[W ? 1 : kMaxExperts + 1], s_end[W ? 1 : kMaxExperts], s_wsum[kThreads / 32];
   __shared__ uint32_t s_tmem;
@@ -348,8 +380,10 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       prefetch_tmap(&maps.out);
       for (int s = 0; s < S; ++s) {
         mbar_init(&full_bar[s], 2);
-        mbar_init(&peer_bar[s], 1);
-        mbar_init(&ready_bar[s], 1);
+        if (W) {
+          mbar_init(&tail_bar[s], 2);
+          mbar_init(&peer_bar[s], 1);
+        }
         mbar_init(&empty_bar[s], 1);
       }
       for (int s = 0; s < 2; ++s) {
@@ -418,6 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
 
   if (warp == kAWarp || warp == kBWarp) {
     const uint32_t elected = elect_one();
+    const uint32_t full0 = PAIR ? cluster_addr(&full_bar[0], 0) : smem_u32(&full_bar[0]);
     RingPos at;
     int n = 0;
     bool ok = true;
@@ -429,32 +464,38 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       const int c0 = (W ? it.col0 : it.row0) + (int)rank * cta_cols;
       for (int kb = stage0(KB), kb1 = stage1(KB); kb < kb1; ++kb, ++n, at.next(S)) {
         if (!(ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status))) break;
-        const uint32_t st = ring + at.slot * C::kStageBytes, bar = smem_u32(&full_bar[at.slot]);
+        const uint32_t st = ring + at.slot * C::kStageBytes;
         const int k0 = kb * C::kDeep, parts = C::kParts == 2 && k0 + 64 < deep ? 2 : 1;
+        // The copies of both CTAs of a pair complete the leading one's barrier, which expects the bytes of both;
+        // those of a stage whose last rows are overwritten complete each CTA's own.
+        const bool fix = W && fixed(deep - k0);
+        const uint32_t bar = fix ? smem_u32(&tail_bar[W ? at.slot : 0]) : full0 + at.slot * 8;
+        const uint32_t expecting = PAIR && !fix ? (rank == 0 ? elected : 0u) : elected, times = PAIR && !fix ? 2 : 1;
+        const uint32_t expected = fix ? bar : smem_u32(&full_bar[at.slot]);
         if (warp == kAWarp) {
-          expect_tx_elect(elected, bar, (uint32_t)parts * kABytes);
+          expect_tx_elect(expecting, expected, times * (uint32_t)parts * kABytes);
 #pragma unroll
           for (int q = 0; q < C::kParts; ++q) {
             if (q >= parts) break;
             const uint32_t to = st + q * kABytes;
             const int k = k0 + q * 64;
             if (KIND == Gmm16::kForward) {
-              tma_load_3d_elect(elected, to, &maps.a, k, m0, it.e, bar);
+              load_3d<PAIR>(elected, to, &maps.a, k, m0, it.e, bar);
             } else if (KIND == Gmm16::kInput) {
-              tma_load_3d_elect(elected, to, &maps.a, m0, k, it.e, bar);
-              tma_load_3d_elect(elected, to + 8192, &maps.a, m0 + 64, k, it.e, bar);
+              load_3d<PAIR>(elected, to, &maps.a, m0, k, it.e, bar);
+              load_3d<PAIR>(elected, to + 8192, &maps.a, m0 + 64, k, it.e, bar);
             } else {
-              tma_load_2d_elect(elected, to, &maps.a, m0, it.row0 + k, bar);
-              tma_load_2d_elect(elected, to + 8192, &maps.a, m0 + 64, it.row0 + k, bar);
+              load_2d<PAIR>(elected, to, &maps.a, m0, it.row0 + k, bar);
+              load_2d<PAIR>(elected, to + 8192, &maps.a, m0 + 64, it.row0 + k, bar);
             }
           }
         } else if (W) {
           const int boxes = (cta_cols + 63) / 64;
-          expect_tx_elect(elected, bar, (uint32_t)boxes * 8192);
+          expect_tx_elect(expecting, expected, times * (uint32_t)boxes * 8192);
           for (int b = 0; b < boxes; ++b)
-            tma_load_2d_elect(elected, st + kABytes + b * 8192, &maps.b[0], c0 + b * 64, it.row0 + k0, bar);
+            load_2d<PAIR>(elected, st + kABytes + b * 8192, &maps.b[0], c0 + b * 64, it.row0 + k0, bar);
         } else {
-          expect_tx_elect(elected, bar, (uint32_t)(parts * cta_cols) * 128);
+          expect_tx_elect(expecting, expected, times * (uint32_t)(parts * cta_cols) * 128);
 #pragma unroll
           for (int q = 0; q < C::kParts; ++q) {
             if (q >= parts) break;
@@ -463,8 +504,8 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
             for (int b = 0; b < kBoxes; ++b) {
               const int rows = kBoxRows >> b;
               for (; cta_cols - r >= rows; r += rows)
-                tma_load_2d_elect(elected, st + C::kParts * kABytes + q * C::kBBytes + r * 128, &maps.b[b], k0 + q * 64,
-                                  c0 + r, bar);
+                load_2d<PAIR>(elected, st + C::kParts * kABytes + q * C::kBBytes + r * 128, &maps.b[b], k0 + q * 64, c0 + r,
+                              bar);
             }
           }
         }
@@ -476,49 +517,44 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
     // before an arrival that is still on its way to it
     for (int s = 0; ok && s < S; ++s, at.next(S)) ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status);
     if (lane == 0) s_issued[warp == kBWarp] = n;
-  } else if (RELAY && warp == kRelayWarp) {
-    RingPos at;
-    bool ok = true;
-    for (auto list = items(first, stride); ok && list.more(); list.next()) {
-      const Item it = list.it;
-      list.look();
-      const int n = steps(it), KB = (n + 63) / 64;
-      for (int kb = 0; kb < KB; ++kb, at.next(S)) {
-        if (!(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status))) break;
-        const int left = n - kb * 64, upto = (left + 15) & ~15;
-        const bool tail = W && left < 64 && left < upto;
-        if (tail) {
+  } else if (FIX && warp == kFixWarp) {
+    if constexpr (FIX) {
+      RingPos at;
+      uint32_t turn = 0;  // parity of each slot's next use of tail_bar and peer_bar
+      bool ok = true;
+      for (auto list = items(first, stride); ok && list.more(); list.next()) {
+        const Item it = list.it;
+        list.look();
+        for (int left = it.rows; ok && left > 0; left -= 64, at.next(S)) {
+          if (!fixed(left)) continue;
+          const uint32_t parity = turn >> at.slot & 1u;
+          turn ^= 1u << at.slot;
+          if (!(ok = warp_wait(&tail_bar[at.slot], parity, abort_flag, a.status))) break;
           // rows of the next expert, in the four boxes of both operands (a row is 128 bytes of each)
           uint8_t* box = smem_raw + at.slot * C::kStageBytes + (lane >> 3) * 8192 + (lane & 7) * 16;
-          for (int r = left; r < upto; ++r) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0, 0, 0, 0);
+          for (int r = left; r < ((left + 15) & ~15); ++r) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
           __syncwarp();
-        }
-        if (rank == 1) {
-          const uint32_t to = cluster_addr(&peer_bar[at.slot], 0);
-          if (lane == 0) {
-            if (tail) mbar_arrive_remote_release(to); else mbar_arrive_remote(to);
+          if (rank == 1) {
+            if (lane == 0) mbar_arrive_remote_release(cluster_addr(&peer_bar[at.slot], 0));
+          } else {
+            if (!(ok = warp_wait(&peer_bar[at.slot], parity, abort_flag, a.status))) break;
+            mbar_acquire_cluster(&peer_bar[at.slot], parity);
+            __syncwarp();
+            if (lane == 0) mbar_arrive_twice(&full_bar[at.slot]);  // in place of the loaders
           }
-        } else {
-          if (PAIR) {
-            if (!(ok = warp_wait(&peer_bar[at.slot], at.phase, abort_flag, a.status))) break;
-            if (tail) mbar_acquire_cluster(&peer_bar[at.slot], at.phase);
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ready_bar[at.slot]);
         }
       }
     }
   } else if (warp == kMmaWarp) {
     if (rank == 0) {
       const uint32_t elected = elect_one(), t0 = __shfl_sync(0xffffffffu, tmem, 0);
-      uint64_t* there_bar = RELAY ? ready_bar : full_bar;
       RingPos at;
       int u = 0;
       bool ok = true;
       // a barrier's answer takes as long as issuing several MMAs: the next stage's is asked for
       // before this one's are issued
-      uint32_t there = mbar_test(&there_bar[0], 0);
+      uint32_t there = mbar_test(&full_bar[0], 0);
       for (auto list = items(first, stride); ok && list.more(); list.next(), ++u) {
         const Item it = list.it;
         const int buf = u & 1, n = steps(it), KB = (n + C::kDeep - 1) / C::kDeep;
@@ -528,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         const int kb0 = stage0(KB), kb1 = stage1(KB);
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!__all_sync(0xffffffffu, there) &&
-              !(ok = warp_wait(&there_bar[at.slot], at.phase, abort_flag, a.status)))
+              !(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status)))
             break;
           tc_fence_after();
           const uint32_t st = ring + at.slot * C::kStageBytes;
@@ -536,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
           const uint64_t db = W ? sw128_mn_desc(st + kABytes) : sw128_desc(st + C::kParts * kABytes);
           const uint32_t done = smem_u32(&empty_bar[at.slot]);
           at.next(S);
-          there = mbar_test(&there_bar[at.slot], at.phase);
+          there = mbar_test(&full_bar[at.slot], at.phase);
           const int last = min(4 * C::kParts, (n - kb * C::kDeep + 15) >> 4);  // 16 steps an MMA
 #pragma unroll
           for (int k = 0; k < 4 * C::kParts; ++k)
@@ -715,7 +751,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   }
 
   __syncthreads();
-  if (threadIdx.x == 0) {  // copies still in flight (only after an abort) land before shared memory is released
+  // copies still in flight (only after an abort) land before shared memory is released; those of a pair
+  // complete the leading CTA's barriers, and the other waits for it below
+  if (threadIdx.x == 0 && rank == 0) {
     const int n0 = min(s_issued[0], s_issued[1]), n1 = max(s_issued[0], s_issued[1]);
     for (int n = n0; n < n1; ++n) mbar_arrive(&full_bar[n % S]);  // stages that one of the two loaders never began
     for (int n = max(0, n1 - S); n < n1; ++n) mbar_wait_bounded(&full_bar[n % S], (n / S) & 1);
