@@ -35,9 +35,13 @@
 //   64 experts x 768, 4096 -> 2816   670-740 us   1530-1690 TFLOP/s alone, tensor pipe 89% busy; back to
 //       back for seconds 787, where the power limit holds the clock at 1.45 GHz.  What is left: experts a
 //       little past 768 rows take a fourth tile, and 34.2 rounds of items are 35.
-// L2 gives the SMs about 13.5 TB/s, which a pair's 64 KB a stage of 512 clocks nearly takes at 1.9 GHz.
-// Two pairs to a cluster that share their rows by multicast were slower all the same (180 us for 144 at
-// 8192 x 4096 x 4096): a slot is free only when both pairs are done, and 36 such clusters leave 8 SMs idle.
+//   64 experts x 768, kWeight, 4096 x 1408  487 us   1160 TFLOP/s, 1.48 GB written in fp32 (in 16 bits 365)
+// At 1.9 GHz a stage of a pair takes its 512 clocks, for every kind; that is 18.4 TB/s from L2, about what
+// it has: kWeight's stores and their way on to memory come on top (12 stages and 20 MB of fp32 sums from
+// all pairs: 3.24 us without stores, 3.9 while L2 holds them, 5.5 when it writes them back; the same
+// stored from registers, or 4 KB contiguous, or with other L2 policies: no faster).  Two pairs to a
+// cluster that share their rows by multicast were slower all the same (180 us for 144 at 8192 x 4096 x
+// 4096, kWeight 525 for 505): a slot is free only when both are done, and 36 such clusters leave 8 SMs idle.
 //
 // Roles: warp 0 loads operand A and warp 2 operand B, 64 steps of the reduction a stage, into a ring
 // in shared memory (a pair's copies complete the leading CTA's barriers); warp 3 overwrites rows
