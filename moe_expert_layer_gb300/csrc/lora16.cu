@@ -19,7 +19,7 @@
 // Measured (us; GB/s over the bytes of the definition): 128 tokens 7168 -> 4096 on 100 adapters of rank 16
 // 10.9 (launch, two chains of loads and the cluster's barrier; 26 MB are 3.9); 8192 tokens 4096 -> 4096,
 // 24 adapters, of rank 16 40 (5000), of rank 64 54 (3900): 21 in the first kernel, and there the warp-level
-// tensor path is 45% busy.  Above that it bounds: rank 128 105.
+// tensor path is 45% busy.  Above that it bounds: rank 128 93.
 //
 // v goes into the second MMA as two 16-bit numbers, s v 2^-e = hi + lo with e the exponent of the token's
 // largest: 16 significant bits or more, and no rank value leaves binary16's range.  The columns of
@@ -129,8 +129,10 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
 // ranks, MR x 8 to a warp.  A stage is 64 deep: rows of 128 bytes, their 16-byte pieces c at
 // c ^ (row % 8).
 constexpr int kManyTokens = 64;
-template <int MR>  // about 64 KB to a block: more copies under way at low ranks
-constexpr int kStagesOf = MR <= 2 ? 6 : 4;
+// Stages of the rings: more copies under way at low ranks, two blocks of the second kernel to an SM at high ones
+// (rank 128, 8192 tokens: four stages 105 us, three 93).
+template <int MR>
+constexpr int kStagesOf = MR <= 2 ? 6 : MR <= 4 ? 4 : 3;
 template <typename T, int MR>
 __global__ void __launch_bounds__(kThreads) lora16_shrink_many_kernel(const Lora16Problem p, int splits) {
   constexpr int kXBytes = kManyTokens * 128, kStage = kXBytes + MR * 16 * 128, kStages = kStagesOf<MR>;
