@@ -35,7 +35,7 @@
 //   64 experts x 768, 4096 -> 2816   670-740 us   1530-1690 TFLOP/s alone, tensor pipe 89% busy; back to
 //       back for seconds 787, where the power limit holds the clock at 1.45 GHz.  What is left: experts a
 //       little past 768 rows take a fourth tile, and 34.2 rounds of items are 35.
-//   64 experts x 768, kWeight, 4096 x 1408  487 us   1160 TFLOP/s, 1.48 GB written in fp32 (in 16 bits 365)
+//   64 experts x 768, kWeight, 4096 x 1408  493 us   1150 TFLOP/s, 1.48 GB written in fp32 (in 16 bits 365)
 // At 1.9 GHz a stage of a pair takes its 512 clocks, for every kind; that is 18.4 TB/s from L2, about what
 // it has: kWeight's stores and their way on to memory come on top (12 stages and 20 MB of fp32 sums from
 // all pairs: 3.24 us without stores, 3.9 while L2 holds them, 5.5 when it writes them back; the same
@@ -45,9 +45,10 @@
 //
 // Roles: warp 0 loads operand A and warp 2 operand B, 64 steps of the reduction a stage, into a ring
 // in shared memory (a pair's copies complete the leading CTA's barriers); warp 3 overwrites rows
-// (kWeight); warp 1 of the leading CTA issues the MMAs; warps 4-11, two groups, round the sums of one accumulator and store them
-// while the MMAs fill the other.  Every wait is bounded: one that gives up records MOE_ERR_TIMEOUT
-// and the CTA winds down.
+// (kWeight); warp 1 of the leading CTA issues the MMAs; warps 4-11, two groups, round the
+// sums of one accumulator and store them while the MMAs fill the other; an fp32 gradient of more rows than
+// a part has is added up in their registers, which they get from the other warps.  Every wait
+// is bounded: one that gives up records MOE_ERR_TIMEOUT and the CTA winds down.
 #include <cmath>
 
 #include "experts16.h"
@@ -64,6 +65,15 @@ constexpr int kABytes = 128 * 128;  // 128 channels x 64 steps
 constexpr int kOutRows = 32;        // of an epilogue group's store, x 128 channels
 constexpr int kBoxes = 3, kBoxRows = 64;
 constexpr int kMaxSplit = 4;
+// kWeight, sums in parts: the stages of a part at most, and the registers a thread is launched with and goes on
+// with: roles, epilogue.
+constexpr int kPart = 12, kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
+static_assert(128 * kRoleRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "an increase past the launch's registers never ends");
+
+template <uint32_t kRegs>
+__device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
+template <uint32_t kRegs>
+__device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
 template <Gmm16 KIND, int NT, bool PAIR>
 struct Cfg {
@@ -355,13 +365,14 @@ __device__ __forceinline__ bool group_all(int id, bool ok) {
   return r != 0;
 }
 
-template <Gmm16 KIND, int NT, bool PAIR>
+template <Gmm16 KIND, int NT, bool PAIR, bool PARTS>
 __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constant__ Maps maps, const Args a) {
   using C = Cfg<KIND, NT, PAIR>;
   constexpr int S = C::kStages;
   constexpr bool W = C::kWeight, A_MN = KIND != Gmm16::kForward, FIX = W;
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // swizzled rows: 1024-byte groups
-  __shared__ __align__(8) uint64_t full_bar[S], tail_bar[W ? S : 1], peer_bar[W ? S : 1], empty_bar[S], accfull_bar[2], accempty_bar[2], final_bar;
+  __shared__ __align__(8) uint64_t full_bar[S], tail_bar[W ? S : 1], peer_bar[W ? S : 1], empty_bar[S];
+  __shared__ __align__(8) uint64_t accfull_bar[W ? 4 : 2], accempty_bar[W ? 4 : 2], stored_bar[2], final_bar;
   __shared__ __align__(8) uint64_t sums_bar, read_bar;  // of a cluster that divides the reduction
   __shared__ int s_pref[W ? 1 : kMaxExperts + 1], s_end[W ? 1 : kMaxExperts], s_wsum[kThreads / 32];
   __shared__ uint32_t s_tmem;
@@ -390,10 +401,11 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         }
         mbar_init(&empty_bar[s], 1);
       }
-      for (int s = 0; s < 2; ++s) {
+      for (int s = 0; s < (W ? 4 : 2); ++s) {  // kWeight: by 2 * group + accumulator
         mbar_init(&accfull_bar[s], 1);
         mbar_init(&accempty_bar[s], (PAIR ? 2 : 1) * (W ? 4 : 8));
       }
+      for (int s = 0; s < 2; ++s) mbar_init(&stored_bar[s], 4);
       mbar_init(&final_bar, 1);
       mbar_init(&sums_bar, 8 * split);
       mbar_init(&read_bar, 8 * split);
@@ -454,208 +466,314 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   auto stage0 = [&](int KB) { return split == 1 ? 0 : share * KB / split; };
   auto stage1 = [&](int KB) { return split == 1 ? KB : (share + 1) * KB / split; };
 
-  if (warp == kAWarp || warp == kBWarp) {
-    const uint32_t elected = elect_one();
-    const uint32_t full0 = PAIR ? cluster_addr(&full_bar[0], 0) : smem_u32(&full_bar[0]);
-    RingPos at;
-    int n = 0;
-    bool ok = true;
-    for (auto list = items(first, stride); ok && list.more(); list.next()) {
-      const Item it = list.it;
-      list.look();
-      const int m0 = (PAIR ? 2 * it.cb + (int)rank : it.cb) * 128;  // past the last: the copies bring zeros
-      const int cta_cols = PAIR ? it.n / 2 : it.n, deep = steps(it), KB = (deep + C::kDeep - 1) / C::kDeep;
-      const int c0 = (W ? it.col0 : it.row0) + (int)rank * cta_cols;
-      for (int kb = stage0(KB), kb1 = stage1(KB); kb < kb1; ++kb, ++n, at.next(S)) {
-        if (!(ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status))) break;
-        const uint32_t st = ring + at.slot * C::kStageBytes;
-        const int k0 = kb * C::kDeep, parts = C::kParts == 2 && k0 + 64 < deep ? 2 : 1;
-        // The copies of both CTAs of a pair complete the leading one's barrier, which expects the bytes of both;
-        // those of a stage whose last rows are overwritten complete each CTA's own.
-        const bool fix = W && fixed(deep - k0);
-        const uint32_t bar = fix ? smem_u32(&tail_bar[W ? at.slot : 0]) : full0 + at.slot * 8;
-        const uint32_t expecting = PAIR && !fix ? (rank == 0 ? elected : 0u) : elected, times = PAIR && !fix ? 2 : 1;
-        const uint32_t expected = fix ? bar : smem_u32(&full_bar[at.slot]);
-        if (warp == kAWarp) {
-          expect_tx_elect(expecting, expected, times * (uint32_t)parts * kABytes);
-#pragma unroll
-          for (int q = 0; q < C::kParts; ++q) {
-            if (q >= parts) break;
-            const uint32_t to = st + q * kABytes;
-            const int k = k0 + q * 64;
-            if (KIND == Gmm16::kForward) {
-              load_3d<PAIR>(elected, to, &maps.a, k, m0, it.e, bar);
-            } else if (KIND == Gmm16::kInput) {
-              load_3d<PAIR>(elected, to, &maps.a, m0, k, it.e, bar);
-              load_3d<PAIR>(elected, to + 8192, &maps.a, m0 + 64, k, it.e, bar);
-            } else {
-              load_2d<PAIR>(elected, to, &maps.a, m0, it.row0 + k, bar);
-              load_2d<PAIR>(elected, to + 8192, &maps.a, m0 + 64, it.row0 + k, bar);
-            }
-          }
-        } else if (W) {
-          const int boxes = (cta_cols + 63) / 64;
-          expect_tx_elect(expecting, expected, times * (uint32_t)boxes * 8192);
-          for (int b = 0; b < boxes; ++b)
-            load_2d<PAIR>(elected, st + kABytes + b * 8192, &maps.b[0], c0 + b * 64, it.row0 + k0, bar);
-        } else {
-          expect_tx_elect(expecting, expected, times * (uint32_t)(parts * cta_cols) * 128);
-#pragma unroll
-          for (int q = 0; q < C::kParts; ++q) {
-            if (q >= parts) break;
-            int r = 0;
-#pragma unroll
-            for (int b = 0; b < kBoxes; ++b) {
-              const int rows = kBoxRows >> b;
-              for (; cta_cols - r >= rows; r += rows)
-                load_2d<PAIR>(elected, st + C::kParts * kABytes + q * C::kBBytes + r * 128, &maps.b[b], k0 + q * 64, c0 + r,
-                              bar);
-            }
-          }
-        }
-      }
-    }
-    // the next kernel's setup beside the last items
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    // the last stages' releases: commits arrive in both CTAs of a pair, and neither may leave
-    // before an arrival that is still on its way to it
-    for (int s = 0; ok && s < S; ++s, at.next(S)) ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status);
-    if (lane == 0) s_issued[warp == kBWarp] = n;
-  } else if (FIX && warp == kFixWarp) {
-    if constexpr (FIX) {
+  // An accumulator takes an item's whole sum, but with PARTS: the tensor cores drop bits where they add (a sum
+  // of n products loses about 1e-9 n of itself, always towards zero), which a gradient of thousands of rows
+  // would show in fp32 (4096 rows: 4.4e-6 of its norm). Such a sum is made in parts of up to kPart stages, added in
+  // registers: 6e-7 to 9e-7 for any number of rows; parts of 8 stages 4.7e-7 to 6.5e-7, but half of the experts
+  // around 768 rows would then be in two, which costs 4% instead of 2.
+  auto whole_sum = [&](int n) { return !PARTS || n <= kPart * 64; };
+  if (warp < kEpiWarp0) {
+    if (PARTS) regs_dec<kRoleRegs>();
+    if (warp == kAWarp || warp == kBWarp) {
+      const uint32_t elected = elect_one();
+      const uint32_t full0 = PAIR ? cluster_addr(&full_bar[0], 0) : smem_u32(&full_bar[0]);
       RingPos at;
-      uint32_t turn = 0;  // parity of each slot's next use of tail_bar and peer_bar
+      int n = 0;
       bool ok = true;
       for (auto list = items(first, stride); ok && list.more(); list.next()) {
         const Item it = list.it;
         list.look();
-        for (int left = it.rows; ok && left > 0; left -= 64, at.next(S)) {
-          if (!fixed(left)) continue;
-          const uint32_t parity = turn >> at.slot & 1u;
-          turn ^= 1u << at.slot;
-          if (!(ok = warp_wait(&tail_bar[at.slot], parity, abort_flag, a.status))) break;
-          // rows of the next expert, in the four boxes of both operands (a row is 128 bytes of each)
-          uint8_t* box = smem_raw + at.slot * C::kStageBytes + (lane >> 3) * 8192 + (lane & 7) * 16;
-          for (int r = left; r < ((left + 15) & ~15); ++r) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (rank == 1) {
-            if (lane == 0) mbar_arrive_remote_release(cluster_addr(&peer_bar[at.slot], 0));
+        const int m0 = (PAIR ? 2 * it.cb + (int)rank : it.cb) * 128;  // past the last: the copies bring zeros
+        const int cta_cols = PAIR ? it.n / 2 : it.n, deep = steps(it), KB = (deep + C::kDeep - 1) / C::kDeep;
+        const int c0 = (W ? it.col0 : it.row0) + (int)rank * cta_cols;
+        for (int kb = stage0(KB), kb1 = stage1(KB); kb < kb1; ++kb, ++n, at.next(S)) {
+          if (!(ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status))) break;
+          const uint32_t st = ring + at.slot * C::kStageBytes;
+          const int k0 = kb * C::kDeep, parts = C::kParts == 2 && k0 + 64 < deep ? 2 : 1;
+          // The copies of both CTAs of a pair complete the leading one's barrier, which expects the bytes of both;
+          // those of a stage whose last rows are overwritten complete each CTA's own.
+          const bool fix = W && fixed(deep - k0);
+          const uint32_t bar = fix ? smem_u32(&tail_bar[W ? at.slot : 0]) : full0 + at.slot * 8;
+          const uint32_t expecting = PAIR && !fix ? (rank == 0 ? elected : 0u) : elected, times = PAIR && !fix ? 2 : 1;
+          const uint32_t expected = fix ? bar : smem_u32(&full_bar[at.slot]);
+          if (warp == kAWarp) {
+            expect_tx_elect(expecting, expected, times * (uint32_t)parts * kABytes);
+#pragma unroll
+            for (int q = 0; q < C::kParts; ++q) {
+              if (q >= parts) break;
+              const uint32_t to = st + q * kABytes;
+              const int k = k0 + q * 64;
+              if (KIND == Gmm16::kForward) {
+                load_3d<PAIR>(elected, to, &maps.a, k, m0, it.e, bar);
+              } else if (KIND == Gmm16::kInput) {
+                load_3d<PAIR>(elected, to, &maps.a, m0, k, it.e, bar);
+                load_3d<PAIR>(elected, to + 8192, &maps.a, m0 + 64, k, it.e, bar);
+              } else {
+                load_2d<PAIR>(elected, to, &maps.a, m0, it.row0 + k, bar);
+                load_2d<PAIR>(elected, to + 8192, &maps.a, m0 + 64, it.row0 + k, bar);
+              }
+            }
+          } else if (W) {
+            const int boxes = (cta_cols + 63) / 64;
+            expect_tx_elect(expecting, expected, times * (uint32_t)boxes * 8192);
+            for (int b = 0; b < boxes; ++b)
+              load_2d<PAIR>(elected, st + kABytes + b * 8192, &maps.b[0], c0 + b * 64, it.row0 + k0, bar);
           } else {
-            if (!(ok = warp_wait(&peer_bar[at.slot], parity, abort_flag, a.status))) break;
-            mbar_acquire_cluster(&peer_bar[at.slot], parity);
-            __syncwarp();
-            if (lane == 0) mbar_arrive_twice(&full_bar[at.slot]);  // in place of the loaders
+            expect_tx_elect(expecting, expected, times * (uint32_t)(parts * cta_cols) * 128);
+#pragma unroll
+            for (int q = 0; q < C::kParts; ++q) {
+              if (q >= parts) break;
+              int r = 0;
+#pragma unroll
+              for (int b = 0; b < kBoxes; ++b) {
+                const int rows = kBoxRows >> b;
+                for (; cta_cols - r >= rows; r += rows)
+                  load_2d<PAIR>(elected, st + C::kParts * kABytes + q * C::kBBytes + r * 128, &maps.b[b], k0 + q * 64, c0 + r,
+                                bar);
+              }
+            }
           }
         }
       }
-    }
-  } else if (warp == kMmaWarp) {
-    if (rank == 0) {
-      const uint32_t elected = elect_one(), t0 = __shfl_sync(0xffffffffu, tmem, 0);
-      RingPos at;
-      int u = 0;
-      bool ok = true;
-      // a barrier's answer takes as long as issuing several MMAs: the next stage's is asked for
-      // before this one's are issued
-      uint32_t there = mbar_test(&full_bar[0], 0);
-      for (auto list = items(first, stride); ok && list.more(); list.next(), ++u) {
-        const Item it = list.it;
-        const int buf = u & 1, n = steps(it), KB = (n + C::kDeep - 1) / C::kDeep;
-        if (!(ok = warp_wait(&accempty_bar[buf], ((u >> 1) & 1) ^ 1, abort_flag, a.status))) break;
-        tc_fence_after();
-        const uint32_t idesc = f16_idesc(a.bf16, A_MN, W, PAIR ? 256 : 128, it.n), d = t0 + buf * NT;
-        const int kb0 = stage0(KB), kb1 = stage1(KB);
-        for (int kb = kb0; kb < kb1; ++kb) {
-          if (!__all_sync(0xffffffffu, there) &&
-              !(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status)))
-            break;
-          tc_fence_after();
-          const uint32_t st = ring + at.slot * C::kStageBytes;
-          const uint64_t da = A_MN ? sw128_mn_desc(st) : sw128_desc(st);
-          const uint64_t db = W ? sw128_mn_desc(st + kABytes) : sw128_desc(st + C::kParts * kABytes);
-          const uint32_t done = smem_u32(&empty_bar[at.slot]);
-          at.next(S);
-          there = mbar_test(&full_bar[at.slot], at.phase);
-          const int last = min(4 * C::kParts, (n - kb * C::kDeep + 15) >> 4);  // 16 steps an MMA
-#pragma unroll
-          for (int k = 0; k < 4 * C::kParts; ++k)
-            if (k < last)
-              f16_mma<PAIR>(elected, d, da + (k >> 2) * (kABytes >> 4) + (k & 3) * (A_MN ? 128 : 2),
-                            db + (k >> 2) * (C::kBBytes >> 4) + (k & 3) * (W ? 128 : 2), idesc, kb > kb0 || k ? 1u : 0u);
-          mx_commit<PAIR>(elected, done);
-          if (kb == kb0) list.look();
+      // the next kernel's setup beside the last items
+      asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+      // the last stages' releases: commits arrive in both CTAs of a pair, and neither may leave
+      // before an arrival that is still on its way to it
+      for (int s = 0; ok && s < S; ++s, at.next(S)) ok = warp_wait(&empty_bar[at.slot], at.phase ^ 1u, abort_flag, a.status);
+      if (lane == 0) s_issued[warp == kBWarp] = n;
+    } else if (FIX && warp == kFixWarp) {
+      if constexpr (FIX) {
+        RingPos at;
+        uint32_t turn = 0;  // parity of each slot's next use of tail_bar and peer_bar
+        bool ok = true;
+        for (auto list = items(first, stride); ok && list.more(); list.next()) {
+          const Item it = list.it;
+          list.look();
+          for (int left = it.rows; ok && left > 0; left -= 64, at.next(S)) {
+            if (!fixed(left)) continue;
+            const uint32_t parity = turn >> at.slot & 1u;
+            turn ^= 1u << at.slot;
+            if (!(ok = warp_wait(&tail_bar[at.slot], parity, abort_flag, a.status))) break;
+            // rows of the next expert, in the four boxes of both operands (a row is 128 bytes of each)
+            uint8_t* box = smem_raw + at.slot * C::kStageBytes + (lane >> 3) * 8192 + (lane & 7) * 16;
+            for (int r = left; r < ((left + 15) & ~15); ++r) *reinterpret_cast<uint4*>(box + r * 128) = make_uint4(0, 0, 0, 0);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (rank == 1) {
+              if (lane == 0) mbar_arrive_remote_release(cluster_addr(&peer_bar[at.slot], 0));
+            } else {
+              if (!(ok = warp_wait(&peer_bar[at.slot], parity, abort_flag, a.status))) break;
+              mbar_acquire_cluster(&peer_bar[at.slot], parity);
+              __syncwarp();
+              if (lane == 0) mbar_arrive_twice(&full_bar[at.slot]);  // in place of the loaders
+            }
+          }
         }
-        if (kb0 == kb1) list.look();
-        if (ok) mx_commit<PAIR>(elected, smem_u32(&accfull_bar[buf]));
       }
-      mx_commit_local<PAIR>(elected, smem_u32(&final_bar));  // every MMA done before tensor memory is freed
-      mbar_wait_sleep_bounded(&final_bar, 0);
+    } else if (warp == kMmaWarp) {
+      if (rank == 0) {
+        const uint32_t elected = elect_one(), t0 = __shfl_sync(0xffffffffu, tmem, 0);
+        RingPos at;
+        int u = 0;
+        uint32_t held = 0, back = 0;  // kWeight: by 2 * group + accumulator, handed over, and its return's parity
+        bool ok = true;
+        // a barrier's answer takes as long as issuing several MMAs: the next stage's is asked for
+        // before this one's are issued
+        uint32_t there = mbar_test(&full_bar[0], 0);
+        for (auto list = items(first, stride); ok && list.more(); list.next()) {
+          const Item it = list.it;
+          const int n = steps(it), KB = (n + C::kDeep - 1) / C::kDeep, kb0 = stage0(KB), kb1 = stage1(KB);
+          const bool whole = whole_sum(n);
+          const uint32_t idesc = f16_idesc(a.bf16, A_MN, W, PAIR ? 256 : 128, it.n);
+          int from = kb0;
+          do {
+            const int buf = u & 1;
+            int to = kb1;
+            if (!whole && to - from > kPart) to = to - from > 2 * kPart ? from + kPart : (from + to + 1) >> 1;
+            if constexpr (W) {  // from those that have it
+              for (int i = buf; ok && i < 4; i += 2)
+                if (held >> i & 1u) {
+                  ok = warp_wait(&accempty_bar[i], back >> i & 1u, abort_flag, a.status);
+                  held ^= 1u << i, back ^= 1u << i;
+                }
+            } else {
+              ok = warp_wait(&accempty_bar[buf], ((u >> 1) & 1) ^ 1, abort_flag, a.status);
+            }
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = t0 + buf * NT;
+            for (int kb = from; kb < to; ++kb) {
+              if (!__all_sync(0xffffffffu, there) &&
+                  !(ok = warp_wait(&full_bar[at.slot], at.phase, abort_flag, a.status)))
+                break;
+              tc_fence_after();
+              const uint32_t st = ring + at.slot * C::kStageBytes;
+              const uint64_t da = A_MN ? sw128_mn_desc(st) : sw128_desc(st);
+              const uint64_t db = W ? sw128_mn_desc(st + kABytes) : sw128_desc(st + C::kParts * kABytes);
+              const uint32_t done = smem_u32(&empty_bar[at.slot]);
+              at.next(S);
+              there = mbar_test(&full_bar[at.slot], at.phase);
+              const int last = min(4 * C::kParts, (n - kb * C::kDeep + 15) >> 4);  // 16 steps an MMA
+#pragma unroll
+              for (int k = 0; k < 4 * C::kParts; ++k)
+                if (k < last)
+                  f16_mma<PAIR>(elected, d, da + (k >> 2) * (kABytes >> 4) + (k & 3) * (A_MN ? 128 : 2),
+                                db + (k >> 2) * (C::kBBytes >> 4) + (k & 3) * (W ? 128 : 2), idesc, kb > from || k ? 1u : 0u);
+              mx_commit<PAIR>(elected, done);
+              if (kb == kb0) list.look();
+            }
+            if (!ok) break;
+            if constexpr (W) {
+              const uint32_t who = whole ? 1u << (3 * buf) : 5u << buf;  // the accumulator's group, or both
+              for (int i = buf; i < 4; i += 2)
+                if (who >> i & 1u) mx_commit<PAIR>(elected, smem_u32(&accfull_bar[i]));
+              held |= who;
+            } else {
+              mx_commit<PAIR>(elected, smem_u32(&accfull_bar[buf]));
+            }
+            from = to;
+            ++u;
+          } while (from < kb1);
+          if (kb0 == kb1) list.look();
+        }
+        mx_commit_local<PAIR>(elected, smem_u32(&final_bar));  // every MMA done before tensor memory is freed
+        mbar_wait_sleep_bounded(&final_bar, 0);
+      }
     }
-  } else if (warp >= kEpiWarp0) {
-    // kWeight: the groups take turns, an accumulator each (together at every item, their bursts of stores
-    // slowed the loads: both gradients' largest case took 905 us for 880); else both take part in every
-    // item, and drain one accumulator while the MMAs fill the other
-    constexpr int kTurns = W ? 2 : 1;
+  } else {
+    if (PARTS) regs_inc<kEpiRegs>();
+    // Both groups take part in every item, and drain one accumulator while the MMAs fill the other. But
+    // those of kWeight take turns at items of one part, an accumulator each: together, their bursts of
+    // stores slowed the loads (64 experts x 64 rows, 2816 x 4096: 302 us for 276). Each hears of, and hands
+    // back, only what it takes.
     const int group = (warp - kEpiWarp0) >> 2, quarter = warp & 3;
     const uint32_t lanes = (uint32_t)quarter << 21;  // 32 * quarter in the lane field
-    int u = W ? group : 0;
-    for (auto list = items(first + u * stride, kTurns * stride); list.more(); list.next(), u += kTurns) {
+    constexpr int by = W && !PARTS ? 2 : 1;
+    int u = by == 2 ? group : 0;
+    uint32_t turn = 0;  // kWeight: parity of this group's next turn at each accumulator; from bit 2 on: items in parts
+    auto heard = [&](int buf) {
+      turn ^= 1u << buf;
+      return warp_wait(&accfull_bar[W ? 2 * group + buf : 0], ~turn >> buf & 1u, abort_flag, a.status);
+    };
+    for (auto list = items(first + u * stride, by * stride); list.more(); list.next(), u += by) {
       const Item it = list.it;
       list.look();
       const int buf = u & 1;
-      bool ok = warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status);
-      ok = group_all(9 + group, ok);  // the group's warps wait for one another below
+      const bool whole = whole_sum(it.rows);
+      if (W && whole && buf != group) continue;
+      bool ok = W ? heard(buf) : warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status);
+      // warps that wait for one another below give up together
+      if (!W && split == 1) ok = group_all(9 + group, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t t = tmem + lanes + buf * NT;
       const int m0 = (PAIR ? 2 * it.cb + (int)rank : it.cb) * 128;
       if constexpr (W) {
-        // a warp's 32 channels, 128 bytes of columns at a time, in the 128-byte swizzle of the output's map
+        // 32 channels of a warp, 128 bytes of columns at a time, in the 128-byte swizzle of the output's map
         uint8_t* own = smem_raw + S * C::kStageBytes + (warp - kEpiWarp0) * 4096;
         uint4* row = reinterpret_cast<uint4*>(own + lane * 128);
-        const int cols = a.out_f32 ? 32 : 64, n = min(NT, a.D - it.col0), y = m0 + quarter * 32;
-        if (y < a.N && !(it.rows == 0 && a.accumulate)) {
-          for (int c0 = 0; c0 < n; c0 += cols) {
-            uint32_t v[4][16];
-            __syncwarp();
-            if (it.rows) {
-              tmem_ld16(t + c0, v[0]);
-              if (c0 + 16 < it.n) tmem_ld16(t + c0 + 16, v[1]);
-              if (!a.out_f32) {
-                if (c0 + 32 < it.n) tmem_ld16(t + c0 + 32, v[2]);
-                if (c0 + 48 < it.n) tmem_ld16(t + c0 + 48, v[3]);
-              }
-              tmem_wait_ld();
-            } else {
+        const int y = m0 + quarter * 32;
+        const bool stored = y < a.N && (it.rows || !a.accumulate);
+        auto put = [&](int c) {  // the rows are in shared memory
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (a.accumulate) tma_add_3d(&maps.out, it.col0 + c, y, it.e, own);
+            else tma_store_3d(&maps.out, it.col0 + c, y, it.e, own);
+            bulk_commit_group();
+          }
+        };
+        auto release = [&](int n) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(cluster_addr(&accempty_bar[2 * group + n], 0));
+        };
+        if (whole) {
+          const int cols = a.out_f32 ? 32 : 64;
+          if (stored) {
+            for (int c = 0; c < it.n; c += cols) {
+              uint32_t v[4][16];
+              __syncwarp();
+              if (it.rows) {
+                tmem_ld16(t + c, v[0]);
+                tmem_ld16(t + c + 16, v[1]);  // a pair's columns come in steps of 32
+                if (!a.out_f32 && c + 32 < it.n) {
+                  tmem_ld16(t + c + 32, v[2]);
+                  tmem_ld16(t + c + 48, v[3]);
+                }
+                tmem_wait_ld();
+              } else {
 #pragma unroll
-              for (int i = 0; i < 64; ++i) v[i >> 4][i & 15] = 0;
+                for (int i = 0; i < 64; ++i) v[i >> 4][i & 15] = 0;
+              }
+              bulk_wait_read_all();
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint4 o;
+                if (a.out_f32) {
+                  const int k = (i & 3) * 4;
+                  o = make_uint4(v[i >> 2][k], v[i >> 2][k + 1], v[i >> 2][k + 2], v[i >> 2][k + 3]);
+                } else {
+                  const int k = (i & 1) * 8;
+                  const uint32_t(&x)[16] = v[i >> 1];
+                  o = make_uint4(pack16(a.bf16, x[k], x[k + 1]), pack16(a.bf16, x[k + 2], x[k + 3]),
+                                 pack16(a.bf16, x[k + 4], x[k + 5]), pack16(a.bf16, x[k + 6], x[k + 7]));
+                }
+                row[i ^ (lane & 7)] = o;
+              }
+              put(c);
             }
+          }
+          release(buf);
+          continue;
+        }
+        // A lane's channel, 128 columns of it to a group: drained into registers, where the parts are added,
+        // and the accumulators free again before anything is stored.
+        float sum[128] = {};
+        const int from = group * 128, parts = (it.rows + kPart * 64 - 1) / (kPart * 64);
+        for (int part = 0; part < parts; ++part) {
+          if (part) {
+            ++u;
+            if (!(ok = heard(u & 1))) break;
+            tc_fence_after();
+          }
+#pragma unroll
+          for (int c = 0; c < 128; c += 32)
+            if (from + c < it.n) {
+              uint32_t v[2][16];
+              __syncwarp();
+              tmem_ld16(tmem + lanes + (u & 1) * NT + from + c, v[0]);
+              tmem_ld16(tmem + lanes + (u & 1) * NT + from + c + 16, v[1]);
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) sum[c + i] += __uint_as_float(v[i >> 4][i & 15]);
+            }
+          release(u & 1);
+        }
+        if (!ok) break;
+        // The second group stores behind the first (16 experts x 1536 rows, 2816 x 4096: 373 us for 383). The
+        // first is never two items ahead: their parts take the accumulators that the second still has.
+        uint64_t* before = &stored_bar[turn >> 2 & 1u];
+        const uint32_t parity = turn >> 3 & 1u;
+        turn += 4;
+        if (group == 1 && !warp_wait(before, parity, abort_flag, a.status)) break;
+#pragma unroll
+        for (int c = 0; c < 128; c += 32)
+          if (stored && from + c < it.n) {
             bulk_wait_read_all();
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint4 o;
-              if (a.out_f32) {
-                o = make_uint4(v[i >> 2][(i * 4) & 15], v[i >> 2][(i * 4 + 1) & 15], v[i >> 2][(i * 4 + 2) & 15],
-                               v[i >> 2][(i * 4 + 3) & 15]);
-              } else {
-                const uint32_t(&x)[16] = v[i >> 1];
-                const int k = (i & 1) * 8;
-                o = make_uint4(pack16(a.bf16, x[k], x[k + 1]), pack16(a.bf16, x[k + 2], x[k + 3]),
-                               pack16(a.bf16, x[k + 4], x[k + 5]), pack16(a.bf16, x[k + 6], x[k + 7]));
-              }
-              row[i ^ (lane & 7)] = o;
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (a.accumulate) tma_add_3d(&maps.out, it.col0 + c0, y, it.e, own);
-              else tma_store_3d(&maps.out, it.col0 + c0, y, it.e, own);
-              bulk_commit_group();
-            }
+            for (int i = 0; i < 8; ++i)
+              row[i ^ (lane & 7)] = make_uint4(__float_as_uint(sum[c + 4 * i]), __float_as_uint(sum[c + 4 * i + 1]),
+                                               __float_as_uint(sum[c + 4 * i + 2]), __float_as_uint(sum[c + 4 * i + 3]));
+            put(from + c);
           }
+        if (group == 0) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(before);
         }
+        continue;
       } else if (C::kSplits && split > 1) {
         float* sums = reinterpret_cast<float*>(smem_raw + S * C::kStageBytes);  // [rows][128]
         const int wg = warp - kEpiWarp0, th = wg * 32 + lane;
@@ -793,7 +911,7 @@ inline int resident_clusters(int ctas) {
   return n < 1 ? 1 : n;
 }
 
-template <Gmm16 KIND, int NT, bool PAIR>
+template <Gmm16 KIND, int NT, bool PAIR, bool PARTS = false>
 cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
   using C = Cfg<KIND, NT, PAIR>;
   const CUtensorMapDataType t = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -817,8 +935,16 @@ cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
   const int dev = current_device();
   if (set.needed(dev)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(gmm16_kernel<KIND, NT, PAIR>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        cudaFuncSetAttribute(gmm16_kernel<KIND, NT, PAIR, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
+    if (PARTS) {
+      // launched with other registers than its split counts on, it would wait for them: a build that
+      // does is refused
+      cudaFuncAttributes fa;
+      const cudaError_t q = cudaFuncGetAttributes(&fa, gmm16_kernel<KIND, NT, PAIR, PARTS>);
+      if (q != cudaSuccess) return q;
+      if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
+    }
     set.done(dev);
   }
   Args a{p.R, p.E, p.N, p.D, p.cumsum, p.out, p.status, p.bf16, p.out_f32, p.accumulate, split};
@@ -836,7 +962,7 @@ cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
   attrs[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gmm16_kernel<KIND, NT, PAIR>, maps, a);
+  return cudaLaunchKernelEx(&cfg, gmm16_kernel<KIND, NT, PAIR, PARTS>, maps, a);
 }
 
 // What a form takes, in clocks: rounds of its items over the clusters that work at once, each the item's stages
@@ -887,7 +1013,9 @@ cudaError_t launch_rows(const Gmm16Problem& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_gmm16(const Gmm16Problem& p, cudaStream_t stream) {
-  if (p.kind == Gmm16::kWeight) return launch<Gmm16::kWeight, 256, true>(p, 1, stream);
+  if (p.kind == Gmm16::kWeight)
+    return p.out_f32 && p.R > kPart * 64 ? launch<Gmm16::kWeight, 256, true, true>(p, 1, stream)
+                                          : launch<Gmm16::kWeight, 256, true>(p, 1, stream);
   return p.kind == Gmm16::kForward ? launch_rows<Gmm16::kForward>(p, stream) : launch_rows<Gmm16::kInput>(p, stream);
 }
 

@@ -118,6 +118,44 @@ def test_products_of_real_values(counts, N, D, t):
 
 
 @TYPES
+@pytest.mark.parametrize(
+    "counts,behind,N,D",
+    [([0, 769, 1537, 3, 2304, 768, 1600, 0, 833], 5, 264, 328), ([769], 0, 8, 8), ([64 * 300 + 1, 50], 0, 136, 96),
+     # several items of several parts to every pair of the device, short ones between them
+     ([800, 20, 1700, 768] * 15, 3, 512, 512), ([900] * 80, 0, 512, 256)],
+)
+def test_weight_gradients_of_many_rows_are_exact(counts, behind, N, D, t):
+    """Sums in several parts (in fp32, of experts with more than 768 rows), written and added."""
+    g, R, E = rng(N + D), sum(counts) + behind, len(counts)
+    cumsum, n = prefix(counts), sum(counts)
+    a, dc, ws = ints((R, D), t, g), ints((R, N), t, g, 2), space(R, E, N, D)
+    a[n:], dc[n:] = float("nan"), float("nan")
+    want = ref.weight_grad(dc, a, cumsum.tolist())
+    for out in (t, F32):
+        dw = marked((E, N, D), out)
+        moe.moe_gmm16_weight_grad(dc, a, cumsum, dw, ws)
+        assert torch.equal(dw, ref.rounded(want, out))
+    start = ints((E, N, D), F32, g, 1000)
+    dw = start.clone()
+    moe.moe_gmm16_weight_grad(dc, a, cumsum, dw, ws, accumulate=True)
+    assert torch.equal(dw, (start.double() + want).float())
+    assert moe.moe_workspace_status(ws) == 0
+
+
+@TYPES
+def test_long_weight_gradients_keep_fp32(t):
+    """Sums of 70000 positive products, where bits dropped one way would add up: an fp32 gradient is made of
+    parts of up to 768 rows (n 2^-23 each, as above), added at half a step of the sum so far each."""
+    g, counts, N, D = rng(3), [100, 70000], 72, 136
+    cumsum, R = prefix(counts), sum(counts)
+    a, dc = (torch.rand((R, k), device="cuda", generator=g).add(0.5).to(t) for k in (D, N))
+    dw = marked((2, N, D), F32)
+    moe.moe_gmm16_weight_grad(dc, a, cumsum, dw, space(R, 2, N, D))
+    want = ref.weight_grad(dc, a, cumsum.tolist())
+    close(dw, want, want, 768 + (70000 // 768 + 1) / 2, F32)
+
+
+@TYPES
 @pytest.mark.parametrize("E", [2, 40])
 def test_gradients_against_differences(t, E):
     """The gradients of <dc, c(a, w)>: c is linear in a and in w, so the definition's differences along
