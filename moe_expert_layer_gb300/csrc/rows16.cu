@@ -184,6 +184,90 @@ __global__ void __launch_bounds__(kThreads) combine16_kernel(int M, int D, int c
   }
 }
 
+// The same for many tokens of up to eight routes: a block goes over its tokens, and while a thread adds up a
+// piece, eight channels of a token, copies of its next one are on their way to its own places in shared memory.
+// No thread reads what another has copied, so there is nothing to wait for but a thread's own copies.  Two
+// blocks to an SM and one piece ahead are as much on the way as the memory likes (8192 x 4096 of six rows:
+// 76 us; three blocks 92, two pieces ahead 84, three 129).
+constexpr int kCombineBlocks = 2;
+constexpr int kCombineSmem = 2 * kRoutes * kThreads * 16;
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kCombineBlocks)
+    combine16_stream_kernel(int M, int D, int copies, int rows, int tpt, const T* y, const int32_t* row_map,
+                            const float* probs, T* out) {
+  extern __shared__ __align__(16) uint4 ring[];  // [2][kRoutes][kThreads]
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  struct Token {
+    int row[kRoutes];
+    float p[kRoutes];
+  };
+  auto look = [&](int t) {
+    Token r;
+#pragma unroll
+    for (int q = 0; q < kRoutes; ++q) {
+      const int64_t at = (int64_t)t * copies + q;
+      const bool in = t < M && q < copies;
+      r.row[q] = in ? __ldcg(row_map + at) : -1;
+      r.p[q] = in && probs ? __ldcg(probs + at) : 1.0f;
+      if ((unsigned)r.row[q] >= (unsigned)rows) r.row[q] = -1;
+    }
+    return r;
+  };
+  const int tokens = kThreads / tpt, per = D / 8, lane = threadIdx.x & (tpt - 1), stride = gridDim.x * tokens;
+  int t = blockIdx.x * tokens + threadIdx.x / tpt, c = lane;  // of the next piece to be copied
+  if (c >= per) return;
+  Token now = look(t), later = look(t + stride);  // its token, and the one behind it
+  struct Piece {
+    int t, c;
+    uint32_t there;
+    float p[kRoutes];
+  };
+  auto copy = [&](uint32_t half) {
+    Piece x;
+    x.t = t;
+    x.c = c;
+    x.there = 0;
+    const uint32_t to = smem_u32(ring + half * kRoutes * kThreads + threadIdx.x);
+#pragma unroll
+    for (int q = 0; q < kRoutes; ++q) {
+      x.p[q] = now.p[q];
+      if (now.row[q] >= 0) {
+        x.there |= 1u << q;
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + q * (kThreads * 16)),
+                     "l"(y + (int64_t)now.row[q] * D + c * 8)
+                     : "memory");
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    c += tpt;
+    if (c >= per) {
+      c = lane;
+      t += stride;
+      now = later;
+      later = look(t + stride);
+    }
+    return x;
+  };
+  Piece next = copy(0);
+  for (uint32_t half = 0; next.t < M; half ^= 1u) {
+    const Piece x = next;
+    next = copy(half ^ 1u);
+    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    const uint4* from = ring + half * kRoutes * kThreads + threadIdx.x;
+    float acc[8] = {};
+#pragma unroll
+    for (int q = 0; q < kRoutes; ++q)
+      if (x.there >> q & 1u) {
+        Eight<T> v;
+        v.u = from[q * kThreads];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = fmaf(x.p[q], to_f32<T>(v.t[k]), acc[k]);
+      }
+    store8(out + (int64_t)x.t * D + x.c * 8, acc);
+  }
+}
+
 // `tpt` threads per token and group of G of its routes: dout is read once for the group, each y row once,
 // each dy row written, and the products with y summed over the threads in a fixed order.
 template <typename T, int G>
@@ -260,6 +344,21 @@ inline int shares_of(int groups, int D, int tpt) {
 }
 inline int groups_of(int M, int tpt) { return (M + kThreads / tpt - 1) / (kThreads / tpt); }
 
+template <typename T>
+cudaError_t combine_stream(unsigned blocks, int M, int D, int copies, int rows, int tpt, const void* y,
+                           const int32_t* row_map, const float* probs, void* out, cudaStream_t stream) {
+  static PerContextOnce set;
+  const int dev = current_device();
+  if (set.needed(dev)) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(combine16_stream_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCombineSmem);
+    if (e != cudaSuccess) return e;
+    set.done(dev);
+  }
+  return launch_dependent(combine16_stream_kernel<T>, blocks, kThreads, kCombineSmem, stream, M, D, copies, rows, tpt,
+                          static_cast<const T*>(y), row_map, probs, static_cast<T*>(out));
+}
+
 template <typename T, int G>
 cudaError_t combine_grad(int M, int D, int copies, int rows, const void* dout, const void* y, const int32_t* row_map,
                          const float* probs, void* dy, float* dprobs, cudaStream_t stream) {
@@ -306,6 +405,15 @@ cudaError_t launch_combine16(int M, int D, int copies, int rows, bool bf16, cons
                              const float* probs, void* out, cudaStream_t stream) {
   const int tpt = threads_of(D), groups = groups_of(M, tpt), shares = shares_of(groups, D, tpt);
   const unsigned grid = (unsigned)(groups * shares);
+  // Pieces of eight channels, as multiples of the threads of a block on every SM (us, streamed and not):
+  // 3.4: 4.0 and 4.5 (256 x 4096, six rows), 5.6 and 6.8 (2048 x 512); 2.9: 6.4 and 5.6 (128 x 7168, eight rows);
+  // 1.7: 3.8 and 3.0 (128 x 4096).
+  if (copies <= kRoutes && (int64_t)M * (D / 8) > 3 * (int64_t)sm_count() * kThreads) {
+    const int most = sm_count() * kCombineBlocks;
+    const unsigned blocks = (unsigned)(groups < most ? groups : most);
+    return bf16 ? combine_stream<__nv_bfloat16>(blocks, M, D, copies, rows, tpt, y, row_map, probs, out, stream)
+                : combine_stream<__half>(blocks, M, D, copies, rows, tpt, y, row_map, probs, out, stream);
+  }
   if (bf16)
     return launch_dependent(combine16_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, M, D, copies, rows, tpt, shares,
                             static_cast<const __nv_bfloat16*>(y), row_map, probs, static_cast<__nv_bfloat16*>(out));
