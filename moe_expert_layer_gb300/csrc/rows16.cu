@@ -3,12 +3,9 @@
 //
 // All are bound by bytes: eight elements (16 bytes) to a lane, arithmetic in fp32, one rounding at
 // the store.  Measured (bfloat16; GB/s over the bytes that each call reads and writes):
-//   SwiGLU, 48169 rows x 1408           64 us  6360      its gradient                      113 us  6000
-//   dispatch, 8192 x 4096 to six rows   72 us  6420      combine                            88 us  5270
+//   SwiGLU, 48169 rows x 1408           64 us  6360      its gradient                      102 us  6650
+//   dispatch, 8192 x 4096 to six rows   72 us  6420      combine                            75 us  6260
 //   combine's gradient                 138 us  6230
-// The combine's loads are what is left: six rows to a token fill the registers of three blocks to an SM
-// (four blocks 83 us and 4.5 for 3.7 with 61 tokens; routes in two halves and six blocks 92; rows looked
-// up a token ahead 87).
 #include "mxfp4.cuh"
 #include "experts16.h"
 #include "tensor_map.h"
@@ -81,20 +78,64 @@ __global__ void __launch_bounds__(kThreads) swiglu16_kernel(int R, int E, int I,
   }
 }
 
-// dgu may be gu and h may be dh: a thread reads its elements before it writes them.
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) swiglu16_grad_kernel(int R, int E, int I, const T* dh, const T* gu,
-                                                                 const int32_t* cumsum, T* dgu, T* h) {
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// dgu may be gu and h may be dh: a thread writes no element but those of a piece that it has read.  AHEAD: where a
+// thread has several pieces, copies of its next ones are on their way to its own places in shared memory (no
+// thread reads what another has copied) while it is at one.  Two ahead and three blocks to an SM, which is as
+// much as the memory likes (48169 x 1408: 102 us; one ahead 105, three 106; two blocks 108, four 113; loads
+// to registers by four blocks 113).
+constexpr int kGradAhead = 2, kGradBlocks = 3;
+constexpr int kGradSmem = (kGradAhead + 1) * 3 * kThreads * 16;
+template <typename T, bool AHEAD>
+__global__ void __launch_bounds__(kThreads, AHEAD ? kGradBlocks : 4)
+    swiglu16_grad_kernel(int R, int E, int I, const T* dh, const T* gu, const int32_t* cumsum, T* dgu, T* h) {
+  extern __shared__ __align__(16) uint4 ring[];  // AHEAD: [kGradAhead + 1][g, u, dh][kThreads]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int per = I / 8;
   const int64_t n = (int64_t)valid_rows(cumsum, E, R) * per, step = (int64_t)gridDim.x * kThreads;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < n; i += step) {
+  const int64_t first = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+  int64_t coming = first;
+  int to = 0, from = 0;
+  auto copy = [&] {
+    if (coming < n) {
+      const int64_t d = coming / per;
+      const T* g = gu + d * 2 * I + (coming - d * per) * 8;
+      const uint32_t at = smem_u32(ring + to * 3 * kThreads + threadIdx.x);
+      copy16(at, g);
+      copy16(at + kThreads * 16, g + I);
+      copy16(at + kThreads * 32, dh + coming * 8);
+    }
+    copies_commit();
+    coming += step;
+    to = to == kGradAhead ? 0 : to + 1;
+  };
+  if (AHEAD)
+    for (int i = 0; i < kGradAhead; ++i) copy();
+  for (int64_t i = first; i < n; i += step) {
     const int64_t d = i / per, at = d * 2 * I + (i - d * per) * 8;
     Eight<T> g8, u8, dh8;
-    load8(gu + at, g8);
-    load8(gu + at + I, u8);
-    load8(dh + i * 8, dh8);
+    if (AHEAD) {
+      copy();
+      copies_wait<kGradAhead>();
+      const uint4* x = ring + from * 3 * kThreads + threadIdx.x;
+      g8.u = x[0];
+      u8.u = x[kThreads];
+      dh8.u = x[2 * kThreads];
+      from = from == kGradAhead ? 0 : from + 1;
+    } else {
+      load8(gu + at, g8);
+      load8(gu + at + I, u8);
+      load8(dh + i * 8, dh8);
+    }
     float dg[8], du[8], o[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -234,12 +275,10 @@ __global__ void __launch_bounds__(kThreads, kCombineBlocks)
       x.p[q] = now.p[q];
       if (now.row[q] >= 0) {
         x.there |= 1u << q;
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + q * (kThreads * 16)),
-                     "l"(y + (int64_t)now.row[q] * D + c * 8)
-                     : "memory");
+        copy16(to + q * (kThreads * 16), y + (int64_t)now.row[q] * D + c * 8);
       }
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
+    copies_commit();
     c += tpt;
     if (c >= per) {
       c = lane;
@@ -253,7 +292,7 @@ __global__ void __launch_bounds__(kThreads, kCombineBlocks)
   for (uint32_t half = 0; next.t < M; half ^= 1u) {
     const Piece x = next;
     next = copy(half ^ 1u);
-    asm volatile("cp.async.wait_group 1;" ::: "memory");
+    copies_wait<1>();
     const uint4* from = ring + half * kRoutes * kThreads + threadIdx.x;
     float acc[8] = {};
 #pragma unroll
@@ -344,6 +383,15 @@ inline int shares_of(int groups, int D, int tpt) {
 }
 inline int groups_of(int M, int tpt) { return (M + kThreads / tpt - 1) / (kThreads / tpt); }
 
+template <typename T, bool AHEAD>
+cudaError_t swiglu_grad(int R, int E, int I, const void* dh, const void* gu, const int32_t* cumsum, void* dgu, void* h,
+                        cudaStream_t stream) {
+  const unsigned grid = grid_of((int64_t)R * (I / 8), AHEAD ? kGradBlocks : 8);
+  return launch_dependent(swiglu16_grad_kernel<T, AHEAD>, grid, kThreads, AHEAD ? kGradSmem : 0, stream, R, E, I,
+                          static_cast<const T*>(dh), static_cast<const T*>(gu), cumsum, static_cast<T*>(dgu),
+                          static_cast<T*>(h));
+}
+
 template <typename T>
 cudaError_t combine_stream(unsigned blocks, int M, int D, int copies, int rows, int tpt, const void* y,
                            const int32_t* row_map, const float* probs, void* out, cudaStream_t stream) {
@@ -384,14 +432,14 @@ cudaError_t launch_swiglu16(int R, int E, int I, bool bf16, const void* gu, cons
 
 cudaError_t launch_swiglu16_grad(int R, int E, int I, bool bf16, const void* dh, const void* gu, const int32_t* cumsum,
                                  void* dgu, void* h, cudaStream_t stream) {
-  const unsigned grid = grid_of((int64_t)R * (I / 8));
+  // ahead where eight blocks to an SM would have a second round (1024 x 2048, 3.4 blocks: 4.9 us, ahead 5.1,
+  // and 0.6 more behind kernels that leave the memory to L1)
+  const bool ahead = (int64_t)R * (I / 8) > 8 * (int64_t)sm_count() * kThreads;
   if (bf16)
-    return launch_dependent(swiglu16_grad_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, R, E, I,
-                            static_cast<const __nv_bfloat16*>(dh), static_cast<const __nv_bfloat16*>(gu), cumsum,
-                            static_cast<__nv_bfloat16*>(dgu), static_cast<__nv_bfloat16*>(h));
-  return launch_dependent(swiglu16_grad_kernel<__half>, grid, kThreads, 0, stream, R, E, I,
-                          static_cast<const __half*>(dh), static_cast<const __half*>(gu), cumsum,
-                          static_cast<__half*>(dgu), static_cast<__half*>(h));
+    return ahead ? swiglu_grad<__nv_bfloat16, true>(R, E, I, dh, gu, cumsum, dgu, h, stream)
+                 : swiglu_grad<__nv_bfloat16, false>(R, E, I, dh, gu, cumsum, dgu, h, stream);
+  return ahead ? swiglu_grad<__half, true>(R, E, I, dh, gu, cumsum, dgu, h, stream)
+               : swiglu_grad<__half, false>(R, E, I, dh, gu, cumsum, dgu, h, stream);
 }
 
 cudaError_t launch_dispatch16(int M, int D, int copies, int rows, const void* x, const int32_t* row_map, void* out,
