@@ -243,7 +243,8 @@ def gate_values(R, I, t, g):
 
 
 @TYPES
-@pytest.mark.parametrize("R,I,behind", [(1, 8, 0), (5, 200, 2), (300, 1408, 7), (1025, 64, 0), (4, 32768, 1)])
+@pytest.mark.parametrize("R,I,behind", [(1, 8, 0), (5, 200, 2), (300, 1408, 7), (1025, 64, 0), (4, 32768, 1),
+                                        (3000, 1000, 5), (40000, 64, 9), (77, 32768, 2)])
 def test_swiglu_and_gradient(R, I, behind, t):
     """exp's relative error is 2^-22 |g| + 2^-22, a division's and each product's 2^-22: 2^-15 covers |g| up
     to 120; the slope 1 + g (1 - s) is off by 2^-22 (1 + |g|) absolutely, where it passes through zero."""
@@ -296,7 +297,10 @@ def maps(M, copies, rows, g, dropped=0.2):
 
 
 MAPS = pytest.mark.parametrize("M,copies,rows,D", [(1, 1, 1, 8), (1, 8, 8, 7168), (3, 2, 9, 200), (61, 8, 488, 1032),
-                                                   (300, 6, 1700, 264), (7, 33, 300, 72), (2, 300, 600, 16), (1000, 1, 1000, 65536 // 64)])
+                                                   (300, 6, 1700, 264), (7, 33, 300, 72), (2, 300, 600, 16), (1000, 1, 1000, 65536 // 64),
+                                                   # many tokens: whole and partial pieces, more threads than pieces, ninth routes
+                                                   (2000, 3, 5000, 520), (230, 8, 1840, 4104), (20000, 2, 30000, 64), (130, 5, 600, 65536),
+                                                   (9000, 1, 9000, 136), (2000, 9, 17000, 520)])
 
 
 @TYPES
