@@ -71,7 +71,8 @@ def w1_shape(E, I, K):
     return (E, 2 * I, K)
 
 
-SIZES = [(1, 256, 64, 4, 2), (40, 384, 128, 8, 3), (700, 512, 256, 6, 2)]
+# the last: weight gradients in parts, rows and pieces of many tokens
+SIZES = [(1, 256, 64, 4, 2), (40, 384, 128, 8, 3), (700, 512, 256, 6, 2), (3000, 512, 512, 2, 2)]
 
 
 def same(a, b):
@@ -130,11 +131,11 @@ def test_captured_and_replayed(sizes):
 
 def test_on_several_streams_at_once():
     """Steps of different sizes on streams of two priorities, none ordered with another."""
-    steps = [Step(i, *SIZES[i % 3]) for i in range(4)]
+    steps = [Step(i, *SIZES[i % 4]) for i in range(5)]
     for s in steps:
         s.run(wait=True)
     want = [s.results() for s in steps]
-    streams = [torch.cuda.Stream(priority=p) for p in (0, -1, 0, -1)]
+    streams = [torch.cuda.Stream(priority=p) for p in (0, -1, 0, -1, 0)]
     torch.cuda.synchronize()
     for _ in range(15):
         for s, stream in zip(steps, streams):
@@ -293,7 +294,7 @@ def test_tensors_elsewhere_are_refused():
             moe.moe_gmm16(**args)
 
 
-@pytest.mark.parametrize("rows,E,N,D", [(3, 2, 4096, 4096), (60, 8, 512, 512), (600, 3, 1024, 512)])
+@pytest.mark.parametrize("rows,E,N,D", [(3, 2, 4096, 4096), (60, 8, 512, 512), (600, 3, 1024, 512), (2000, 4, 1024, 512)])
 def test_on_a_part_of_the_device(narrow_stream, rows, E, N, D):  # noqa: F811
     """On a stream that may use fewer SMs than the device has, products and adapters give what they give on all of it."""
     g, R = rng(8), rows * E
