@@ -1,5 +1,9 @@
 """The operators of 16-bit experts as programs call them: captured and replayed, on several streams at
 once, one right behind the other, repeatedly, and past 32-bit offsets."""
+import os
+import subprocess
+import sys
+
 import pytest
 
 import experts16_reference as ref
@@ -316,3 +320,25 @@ def test_on_a_part_of_the_device(narrow_stream, rows, E, N, D):  # noqa: F811
         assert moe.moe_workspace_status(ws) == 0
         got.append([c, da, dw, out])
     assert same(*got)
+
+
+def test_first_calls_may_be_captured():
+    """In a process of its own: nothing has run before the capture, whose replay gives what the calls give."""
+    code = """
+import torch
+from test_gpu_experts16_use import Step, same
+s = Step(1, 3000, 512, 512, 2, 2)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    s.run()
+g.replay()
+torch.cuda.synchronize()
+got = s.results()
+s.run(wait=True)
+assert same(got, s.results())
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([here, os.path.dirname(here)]))
+    r = subprocess.run([sys.executable, "-c", code], env=env, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0, r.stdout[-2000:] + r.stderr[-2000:]
