@@ -70,12 +70,19 @@ constexpr int kMaxSplit = 4;
 constexpr int kPart = 12, kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
 static_assert(128 * kRoleRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "an increase past the launch's registers never ends");
 
+template <int kLeft>
+__device__ __forceinline__ void bulk_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
 template <uint32_t kRegs>
 __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 template <uint32_t kRegs>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
-template <Gmm16 KIND, int NT, bool PAIR>
+// kWeight: items of few stages, of many, or in parts (`launch_gmm16`).
+enum class Sums { kFew, kMany, kParts };
+
+template <Gmm16 KIND, int NT, bool PAIR, Sums SUMS>
 struct Cfg {
   static constexpr bool kWeight = KIND == Gmm16::kWeight;
   static constexpr int kStep = PAIR ? 32 : 16;
@@ -84,10 +91,11 @@ struct Cfg {
   static constexpr int kParts = !PAIR && NT <= 32 ? 2 : 1, kDeep = 64 * kParts;
   static constexpr int kBBytes = kCtaCols * 128;  // of a part
   static constexpr int kStageBytes = kParts * (kABytes + kBBytes);  // the parts of A, then those of B
-  static constexpr int kStages = PAIR || NT > 32 ? 6 : 5;
-  // kWeight: 4 KB a warp (32 channels x 128 bytes); else 8 KB a group, or a tile of 32 rows' sums in fp32
+  static constexpr int kStages = kWeight && SUMS == Sums::kFew ? 5 : PAIR || NT > 32 ? 6 : 5;
+  // kWeight: pieces of 4 KB a warp (32 channels x 128 bytes); else 8 KB a group, or a tile of 32 rows' sums in fp32
   static constexpr bool kSplits = !PAIR && NT <= 32;
-  static constexpr int kEpiBytes = kWeight ? 8 * 4096 : 2 * kOutRows * 256;
+  static constexpr int kPieces = SUMS == Sums::kFew ? 2 : 1;
+  static constexpr int kEpiBytes = kWeight ? 8 * kPieces * 4096 : 2 * kOutRows * 256;
   static constexpr int kTmemCols = 2 * NT <= 64 ? 64 : 2 * NT <= 256 ? 256 : 512;
   static_assert(!kSplits || kEpiBytes >= NT * 512, "a tile's sums");
   static constexpr int kSmem = kStages * kStageBytes + kEpiBytes;
@@ -365,9 +373,10 @@ __device__ __forceinline__ bool group_all(int id, bool ok) {
   return r != 0;
 }
 
-template <Gmm16 KIND, int NT, bool PAIR, bool PARTS>
+template <Gmm16 KIND, int NT, bool PAIR, Sums SUMS>
 __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constant__ Maps maps, const Args a) {
-  using C = Cfg<KIND, NT, PAIR>;
+  using C = Cfg<KIND, NT, PAIR, SUMS>;
+  constexpr bool PARTS = SUMS == Sums::kParts;
   constexpr int S = C::kStages;
   constexpr bool W = C::kWeight, A_MN = KIND != Gmm16::kForward, FIX = W;
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // swizzled rows: 1024-byte groups
@@ -650,6 +659,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
     const uint32_t lanes = (uint32_t)quarter << 21;  // 32 * quarter in the lane field
     constexpr int by = W && !PARTS ? 2 : 1;
     int u = by == 2 ? group : 0;
+    uint32_t at = 0;  // kWeight: the next piece's place
     uint32_t turn = 0;  // kWeight: parity of this group's next turn at each accumulator; from bit 2 on: items in parts
     auto heard = [&](int buf) {
       turn ^= 1u << buf;
@@ -670,19 +680,20 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       const int m0 = (PAIR ? 2 * it.cb + (int)rank : it.cb) * 128;
       if constexpr (W) {
         // 32 channels of a warp, 128 bytes of columns at a time, in the 128-byte swizzle of the output's map
-        uint8_t* own = smem_raw + S * C::kStageBytes + (warp - kEpiWarp0) * 4096;
-        uint4* row = reinterpret_cast<uint4*>(own + lane * 128);
+        uint8_t* own = smem_raw + S * C::kStageBytes + (warp - kEpiWarp0) * C::kPieces * 4096;
         const int y = m0 + quarter * 32;
         const bool stored = y < a.N && (it.rows || !a.accumulate);
         auto put = [&](int c) {  // the rows are in shared memory
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (a.accumulate) tma_add_3d(&maps.out, it.col0 + c, y, it.e, own);
-            else tma_store_3d(&maps.out, it.col0 + c, y, it.e, own);
+            if (a.accumulate) tma_add_3d(&maps.out, it.col0 + c, y, it.e, own + at);
+            else tma_store_3d(&maps.out, it.col0 + c, y, it.e, own + at);
             bulk_commit_group();
           }
+          if (C::kPieces == 2) at ^= 4096;
         };
+        auto row = [&](int i) -> uint4& { return reinterpret_cast<uint4*>(own + at + lane * 128)[i ^ (lane & 7)]; };
         auto release = [&](int n) {
           tc_fence_before();
           __syncwarp();
@@ -706,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
 #pragma unroll
                 for (int i = 0; i < 64; ++i) v[i >> 4][i & 15] = 0;
               }
-              bulk_wait_read_all();
+              bulk_wait_read<C::kPieces - 1>();
               __syncwarp();
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
@@ -720,7 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
                   o = make_uint4(pack16(a.bf16, x[k], x[k + 1]), pack16(a.bf16, x[k + 2], x[k + 3]),
                                  pack16(a.bf16, x[k + 4], x[k + 5]), pack16(a.bf16, x[k + 6], x[k + 7]));
                 }
-                row[i ^ (lane & 7)] = o;
+                row(i) = o;
               }
               put(c);
             }
@@ -761,11 +772,11 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
 #pragma unroll
         for (int c = 0; c < 128; c += 32)
           if (stored && from + c < it.n) {
-            bulk_wait_read_all();
+            bulk_wait_read<C::kPieces - 1>();
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              row[i ^ (lane & 7)] = make_uint4(__float_as_uint(sum[c + 4 * i]), __float_as_uint(sum[c + 4 * i + 1]),
+              row(i) = make_uint4(__float_as_uint(sum[c + 4 * i]), __float_as_uint(sum[c + 4 * i + 1]),
                                                __float_as_uint(sum[c + 4 * i + 2]), __float_as_uint(sum[c + 4 * i + 3]));
             put(from + c);
           }
@@ -911,9 +922,9 @@ inline int resident_clusters(int ctas) {
   return n < 1 ? 1 : n;
 }
 
-template <Gmm16 KIND, int NT, bool PAIR, bool PARTS = false>
+template <Gmm16 KIND, int NT, bool PAIR, Sums SUMS = Sums::kMany>
 cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
-  using C = Cfg<KIND, NT, PAIR>;
+  using C = Cfg<KIND, NT, PAIR, SUMS>;
   const CUtensorMapDataType t = p.bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const uint64_t R = p.R, E = p.E, N = p.N, D = p.D;
   Maps maps;
@@ -935,13 +946,13 @@ cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
   const int dev = current_device();
   if (set.needed(dev)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(gmm16_kernel<KIND, NT, PAIR, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        cudaFuncSetAttribute(gmm16_kernel<KIND, NT, PAIR, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    if (PARTS) {
+    if (SUMS == Sums::kParts) {
       // launched with other registers than its split counts on, it would wait for them: a build that
       // does is refused
       cudaFuncAttributes fa;
-      const cudaError_t q = cudaFuncGetAttributes(&fa, gmm16_kernel<KIND, NT, PAIR, PARTS>);
+      const cudaError_t q = cudaFuncGetAttributes(&fa, gmm16_kernel<KIND, NT, PAIR, SUMS>);
       if (q != cudaSuccess) return q;
       if (fa.numRegs != kLaunchRegs) return cudaErrorInvalidKernelImage;
     }
@@ -962,7 +973,7 @@ cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
   attrs[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attrs;
   cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, gmm16_kernel<KIND, NT, PAIR, PARTS>, maps, a);
+  return cudaLaunchKernelEx(&cfg, gmm16_kernel<KIND, NT, PAIR, SUMS>, maps, a);
 }
 
 // What a form takes, in clocks: rounds of its items over the clusters that work at once, each the item's stages
@@ -1013,9 +1024,15 @@ cudaError_t launch_rows(const Gmm16Problem& p, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_gmm16(const Gmm16Problem& p, cudaStream_t stream) {
-  if (p.kind == Gmm16::kWeight)
-    return p.out_f32 && p.R > kPart * 64 ? launch<Gmm16::kWeight, 256, true, true>(p, 1, stream)
-                                          : launch<Gmm16::kWeight, 256, true>(p, 1, stream);
+  if (p.kind == Gmm16::kWeight) {
+    if (p.out_f32 && p.R > kPart * 64) return launch<Gmm16::kWeight, 256, true, Sums::kParts>(p, 1, stream);
+    // Shared memory of one of six stages for a second piece of a warp's sums, where an item has about as few stages
+    // as pieces (us, with and without; 16 bits): 1 expert x 128 rows, 4096 x 4096 10.8 and 11.4, 8 x 75, 1416 x
+    // 1024 10.3 and 10.7 (fp32 13.7 and 14.5), 8 x 256, 2816 x 4096 44.6 and 43.8, 16 x 768 93.7 and 90.6.
+    const int experts = p.R < p.E ? p.R : p.E;
+    return p.R <= 192 * (int64_t)experts ? launch<Gmm16::kWeight, 256, true, Sums::kFew>(p, 1, stream)
+                                         : launch<Gmm16::kWeight, 256, true, Sums::kMany>(p, 1, stream);
+  }
   return p.kind == Gmm16::kForward ? launch_rows<Gmm16::kForward>(p, stream) : launch_rows<Gmm16::kInput>(p, stream);
 }
 
