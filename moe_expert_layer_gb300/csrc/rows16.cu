@@ -225,28 +225,33 @@ __global__ void __launch_bounds__(kThreads) combine16_kernel(int M, int D, int c
   }
 }
 
-// The same for many tokens of up to eight routes: a block goes over its tokens, and while a thread adds up a
+// The same for many tokens of up to ROUTES routes: a block goes over its tokens, and while a thread adds up a
 // piece, eight channels of a token, copies of its next one are on their way to its own places in shared memory.
 // No thread reads what another has copied, so there is nothing to wait for but a thread's own copies.  Two
 // blocks to an SM and one piece ahead are as much on the way as the memory likes (8192 x 4096 of six rows:
-// 76 us; three blocks 92, two pieces ahead 84, three 129).
-constexpr int kCombineBlocks = 2;
-constexpr int kCombineSmem = 2 * kRoutes * kThreads * 16;
-template <typename T>
-__global__ void __launch_bounds__(kThreads, kCombineBlocks)
+// 75 us; three blocks 92, two pieces ahead 84, three 129), or three of half the threads for up to sixteen routes
+// (4096 x 4096 of ten rows: 63 us; two blocks 87, unstreamed 80).
+template <int ROUTES>
+struct Stream {
+  static constexpr int kThreads = ROUTES <= 8 ? 256 : 128, kBlocks = ROUTES <= 8 ? 2 : 3;
+  static constexpr int kSmem = 2 * ROUTES * kThreads * 16;
+};
+template <typename T, int ROUTES>
+__global__ void __launch_bounds__(Stream<ROUTES>::kThreads, Stream<ROUTES>::kBlocks)
     combine16_stream_kernel(int M, int D, int copies, int rows, int tpt, const T* y, const int32_t* row_map,
                             const float* probs, T* out) {
-  extern __shared__ __align__(16) uint4 ring[];  // [2][kRoutes][kThreads]
+  constexpr int kThreads = Stream<ROUTES>::kThreads;
+  extern __shared__ __align__(16) uint4 ring[];  // [2][ROUTES][kThreads]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   struct Token {
-    int row[kRoutes];
-    float p[kRoutes];
+    int row[ROUTES];
+    float p[ROUTES];
   };
   auto look = [&](int t) {
     Token r;
 #pragma unroll
-    for (int q = 0; q < kRoutes; ++q) {
+    for (int q = 0; q < ROUTES; ++q) {
       const int64_t at = (int64_t)t * copies + q;
       const bool in = t < M && q < copies;
       r.row[q] = in ? __ldcg(row_map + at) : -1;
@@ -262,16 +267,16 @@ __global__ void __launch_bounds__(kThreads, kCombineBlocks)
   struct Piece {
     int t, c;
     uint32_t there;
-    float p[kRoutes];
+    float p[ROUTES];
   };
   auto copy = [&](uint32_t half) {
     Piece x;
     x.t = t;
     x.c = c;
     x.there = 0;
-    const uint32_t to = smem_u32(ring + half * kRoutes * kThreads + threadIdx.x);
+    const uint32_t to = smem_u32(ring + half * ROUTES * kThreads + threadIdx.x);
 #pragma unroll
-    for (int q = 0; q < kRoutes; ++q) {
+    for (int q = 0; q < ROUTES; ++q) {
       x.p[q] = now.p[q];
       if (now.row[q] >= 0) {
         x.there |= 1u << q;
@@ -293,10 +298,10 @@ __global__ void __launch_bounds__(kThreads, kCombineBlocks)
     const Piece x = next;
     next = copy(half ^ 1u);
     copies_wait<1>();
-    const uint4* from = ring + half * kRoutes * kThreads + threadIdx.x;
+    const uint4* from = ring + half * ROUTES * kThreads + threadIdx.x;
     float acc[8] = {};
 #pragma unroll
-    for (int q = 0; q < kRoutes; ++q)
+    for (int q = 0; q < ROUTES; ++q)
       if (x.there >> q & 1u) {
         Eight<T> v;
         v.u = from[q * kThreads];
@@ -392,19 +397,23 @@ cudaError_t swiglu_grad(int R, int E, int I, const void* dh, const void* gu, con
                           static_cast<T*>(h));
 }
 
-template <typename T>
-cudaError_t combine_stream(unsigned blocks, int M, int D, int copies, int rows, int tpt, const void* y,
-                           const int32_t* row_map, const float* probs, void* out, cudaStream_t stream) {
+template <typename T, int ROUTES>
+cudaError_t combine_stream(int M, int D, int copies, int rows, const void* y, const int32_t* row_map,
+                           const float* probs, void* out, cudaStream_t stream) {
+  using S = Stream<ROUTES>;
   static PerContextOnce set;
   const int dev = current_device();
   if (set.needed(dev)) {
     const cudaError_t e =
-        cudaFuncSetAttribute(combine16_stream_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, kCombineSmem);
+        cudaFuncSetAttribute(combine16_stream_kernel<T, ROUTES>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess) return e;
     set.done(dev);
   }
-  return launch_dependent(combine16_stream_kernel<T>, blocks, kThreads, kCombineSmem, stream, M, D, copies, rows, tpt,
-                          static_cast<const T*>(y), row_map, probs, static_cast<T*>(out));
+  const int tpt = threads_of(D) < S::kThreads ? threads_of(D) : S::kThreads, tokens = S::kThreads / tpt;
+  const int blocks = (M + tokens - 1) / tokens, most = sm_count() * S::kBlocks;
+  return launch_dependent(combine16_stream_kernel<T, ROUTES>, (unsigned)(blocks < most ? blocks : most), S::kThreads,
+                          S::kSmem, stream, M, D, copies, rows, tpt, static_cast<const T*>(y), row_map, probs,
+                          static_cast<T*>(out));
 }
 
 template <typename T, int G>
@@ -456,11 +465,12 @@ cudaError_t launch_combine16(int M, int D, int copies, int rows, bool bf16, cons
   // Pieces of eight channels, as multiples of the threads of a block on every SM (us, streamed and not):
   // 3.4: 4.0 and 4.5 (256 x 4096, six rows), 5.6 and 6.8 (2048 x 512); 2.9: 6.4 and 5.6 (128 x 7168, eight rows);
   // 1.7: 3.8 and 3.0 (128 x 4096).
-  if (copies <= kRoutes && (int64_t)M * (D / 8) > 3 * (int64_t)sm_count() * kThreads) {
-    const int most = sm_count() * kCombineBlocks;
-    const unsigned blocks = (unsigned)(groups < most ? groups : most);
-    return bf16 ? combine_stream<__nv_bfloat16>(blocks, M, D, copies, rows, tpt, y, row_map, probs, out, stream)
-                : combine_stream<__half>(blocks, M, D, copies, rows, tpt, y, row_map, probs, out, stream);
+  if (copies <= 16 && (int64_t)M * (D / 8) > 3 * (int64_t)sm_count() * kThreads) {
+    if (copies <= 8)
+      return bf16 ? combine_stream<__nv_bfloat16, 8>(M, D, copies, rows, y, row_map, probs, out, stream)
+                  : combine_stream<__half, 8>(M, D, copies, rows, y, row_map, probs, out, stream);
+    return bf16 ? combine_stream<__nv_bfloat16, 16>(M, D, copies, rows, y, row_map, probs, out, stream)
+                : combine_stream<__half, 16>(M, D, copies, rows, y, row_map, probs, out, stream);
   }
   if (bf16)
     return launch_dependent(combine16_kernel<__nv_bfloat16>, grid, kThreads, 0, stream, M, D, copies, rows, tpt, shares,

@@ -300,7 +300,7 @@ MAPS = pytest.mark.parametrize("M,copies,rows,D", [(1, 1, 1, 8), (1, 8, 8, 7168)
                                                    (300, 6, 1700, 264), (7, 33, 300, 72), (2, 300, 600, 16), (1000, 1, 1000, 65536 // 64),
                                                    # many tokens: whole and partial pieces, more threads than pieces, ninth routes
                                                    (2000, 3, 5000, 520), (230, 8, 1840, 4104), (20000, 2, 30000, 64), (130, 5, 600, 65536),
-                                                   (9000, 1, 9000, 136), (2000, 9, 17000, 520)])
+                                                   (9000, 1, 9000, 136), (2000, 9, 17000, 520), (700, 16, 9000, 2056), (2000, 17, 30000, 520)])
 
 
 @TYPES
