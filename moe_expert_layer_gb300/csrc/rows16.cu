@@ -167,6 +167,7 @@ struct Routes {
   }
 };
 
+template <int DEEP>
 __global__ void __launch_bounds__(kThreads) dispatch16_kernel(int M, int D, int copies, int rows, int tpt, int shares,
                                                               const uint4* x, const int32_t* row_map, uint4* out) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -176,11 +177,20 @@ __global__ void __launch_bounds__(kThreads) dispatch16_kernel(int M, int D, int 
   if (t >= M) return;
   for (int j = 0; j < copies; j += kRoutes) {
     const Routes r(row_map + (int64_t)t * copies, j, copies, rows);
-    for (int c = share * tpt + lane; c < per; c += shares * tpt) {
-      const uint4 v = __ldcg(x + (int64_t)t * per + c);
+    for (int c0 = share * tpt + lane; c0 < per; c0 += DEEP * shares * tpt) {
+      uint4 v[DEEP];
 #pragma unroll
-      for (int q = 0; q < kRoutes; ++q)
-        if (r.row[q] >= 0) out[(int64_t)r.row[q] * per + c] = v;
+      for (int d = 0; d < DEEP; ++d) {
+        const int c = c0 + d * shares * tpt;
+        if (c < per) v[d] = __ldcg(x + (int64_t)t * per + c);
+      }
+#pragma unroll
+      for (int d = 0; d < DEEP; ++d) {
+        const int c = c0 + d * shares * tpt;
+#pragma unroll
+        for (int q = 0; q < kRoutes; ++q)
+          if (r.row[q] >= 0 && c < per) out[(int64_t)r.row[q] * per + c] = v[d];
+      }
     }
   }
 }
@@ -227,21 +237,25 @@ __global__ void __launch_bounds__(kThreads) combine16_kernel(int M, int D, int c
 
 // The same for many tokens of up to ROUTES routes: a block goes over its tokens, and while a thread adds up a
 // piece, eight channels of a token, copies of its next one are on their way to its own places in shared memory.
-// No thread reads what another has copied, so there is nothing to wait for but a thread's own copies.  Two
-// blocks to an SM and one piece ahead are as much on the way as the memory likes (8192 x 4096 of six rows:
-// 75 us; three blocks 92, two pieces ahead 84, three 129), or three of half the threads for up to sixteen routes
-// (4096 x 4096 of ten rows: 63 us; two blocks 87, unstreamed 80).
+// No thread reads what another has copied, so there is nothing to wait for but a thread's own copies.  What is on
+// the way at once is what counts, as much as the memory likes and no more (us, of 8192 x 4096, from registers as the
+// kernel above: one row 47, two 52, three 57, four 62, six 88; 4096 x 4096 of ten 80):
+//   one row, two    four blocks to an SM, three pieces ahead 24, 32; three and four 29, 36; two and six 36, 43
+//   three, four     four blocks, one ahead 43, 53; three, one 45, 56; two, two 47, 55; two, three 52, 59
+//   six             two blocks, one ahead 75; three blocks 92; two ahead 84, three 129
+//   ten             three blocks of half the threads, one ahead 63; two 87
 template <int ROUTES>
 struct Stream {
-  static constexpr int kThreads = ROUTES <= 8 ? 256 : 128, kBlocks = ROUTES <= 8 ? 2 : 3;
-  static constexpr int kSmem = 2 * ROUTES * kThreads * 16;
+  static constexpr int kThreads = ROUTES <= 8 ? 256 : 128, kBlocks = ROUTES <= 4 ? 4 : ROUTES <= 8 ? 2 : 3;
+  static constexpr int kAhead = ROUTES <= 2 ? 3 : 1;
+  static constexpr int kSmem = (kAhead + 1) * ROUTES * kThreads * 16;
 };
 template <typename T, int ROUTES>
 __global__ void __launch_bounds__(Stream<ROUTES>::kThreads, Stream<ROUTES>::kBlocks)
     combine16_stream_kernel(int M, int D, int copies, int rows, int tpt, const T* y, const int32_t* row_map,
                             const float* probs, T* out) {
-  constexpr int kThreads = Stream<ROUTES>::kThreads;
-  extern __shared__ __align__(16) uint4 ring[];  // [2][ROUTES][kThreads]
+  constexpr int kThreads = Stream<ROUTES>::kThreads, kAhead = Stream<ROUTES>::kAhead;
+  extern __shared__ __align__(16) uint4 ring[];  // [kAhead + 1][ROUTES][kThreads]
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
   struct Token {
@@ -269,12 +283,14 @@ __global__ void __launch_bounds__(Stream<ROUTES>::kThreads, Stream<ROUTES>::kBlo
     uint32_t there;
     float p[ROUTES];
   };
-  auto copy = [&](uint32_t half) {
+  int to_slot = 0, slot = 0;
+  auto copy = [&] {
     Piece x;
     x.t = t;
     x.c = c;
     x.there = 0;
-    const uint32_t to = smem_u32(ring + half * ROUTES * kThreads + threadIdx.x);
+    const uint32_t to = smem_u32(ring + to_slot * ROUTES * kThreads + threadIdx.x);
+    to_slot = to_slot == kAhead ? 0 : to_slot + 1;
 #pragma unroll
     for (int q = 0; q < ROUTES; ++q) {
       x.p[q] = now.p[q];
@@ -293,12 +309,17 @@ __global__ void __launch_bounds__(Stream<ROUTES>::kThreads, Stream<ROUTES>::kBlo
     }
     return x;
   };
-  Piece next = copy(0);
-  for (uint32_t half = 0; next.t < M; half ^= 1u) {
-    const Piece x = next;
-    next = copy(half ^ 1u);
-    copies_wait<1>();
-    const uint4* from = ring + half * ROUTES * kThreads + threadIdx.x;
+  Piece coming[kAhead];
+#pragma unroll
+  for (int i = 0; i < kAhead; ++i) coming[i] = copy();
+  while (coming[0].t < M) {
+    const Piece x = coming[0];
+#pragma unroll
+    for (int i = 0; i + 1 < kAhead; ++i) coming[i] = coming[i + 1];
+    coming[kAhead - 1] = copy();
+    copies_wait<kAhead>();
+    const uint4* from = ring + slot * ROUTES * kThreads + threadIdx.x;
+    slot = slot == kAhead ? 0 : slot + 1;
     float acc[8] = {};
 #pragma unroll
     for (int q = 0; q < ROUTES; ++q)
@@ -312,9 +333,9 @@ __global__ void __launch_bounds__(Stream<ROUTES>::kThreads, Stream<ROUTES>::kBlo
   }
 }
 
-// `tpt` threads per token and group of G of its routes: dout is read once for the group, each y row once,
-// each dy row written, and the products with y summed over the threads in a fixed order.
-template <typename T, int G>
+// `tpt` threads per token and group of G of its routes, DEEP pieces at a time: dout is read once for the group,
+// each y row once, each dy row written, and the products with y summed over the threads in a fixed order.
+template <typename T, int G, int DEEP>
 __global__ void __launch_bounds__(kThreads) combine16_grad_kernel(int M, int D, int copies, int rows, int tpt,
                                                                   const T* dout, const T* y, const int32_t* row_map,
                                                                   const float* probs, T* dy, float* dprobs) {
@@ -335,24 +356,34 @@ __global__ void __launch_bounds__(kThreads) combine16_grad_kernel(int M, int D, 
     p[q] = row[q] >= 0 ? __ldcg(probs + at) : 0.0f;
     sum[q] = 0.0f;
   }
-  for (int c = lane; t < M && c < per; c += tpt) {
-    Eight<T> g, v[G];
-    load8(dout + (int64_t)t * D + c * 8, g);
+  for (int c0 = lane; t < M && c0 < per; c0 += DEEP * tpt) {
+    Eight<T> g[DEEP], v[DEEP][G];
 #pragma unroll
-    for (int q = 0; q < G; ++q)
-      if (row[q] >= 0) load8(y + (int64_t)row[q] * D + c * 8, v[q]);
+    for (int d = 0; d < DEEP; ++d) {
+      const int c = c0 + d * tpt;
+      if (d && c >= per) continue;
+      load8(dout + (int64_t)t * D + c * 8, g[d]);
 #pragma unroll
-    for (int q = 0; q < G; ++q)
-      if (row[q] >= 0) {
-        float o[8];
+      for (int q = 0; q < G; ++q)
+        if (row[q] >= 0) load8(y + (int64_t)row[q] * D + c * 8, v[d][q]);
+    }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float x = to_f32<T>(g.t[k]);
-          sum[q] = fmaf(x, to_f32<T>(v[q].t[k]), sum[q]);
-          o[k] = p[q] * x;
+    for (int d = 0; d < DEEP; ++d) {
+      const int c = c0 + d * tpt;
+      if (d && c >= per) continue;
+#pragma unroll
+      for (int q = 0; q < G; ++q)
+        if (row[q] >= 0) {
+          float o[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float x = to_f32<T>(g[d].t[k]);
+            sum[q] = fmaf(x, to_f32<T>(v[d][q].t[k]), sum[q]);
+            o[k] = p[q] * x;
+          }
+          store8(dy + (int64_t)row[q] * D + c * 8, o);
         }
-        store8(dy + (int64_t)row[q] * D + c * 8, o);
-      }
+    }
   }
 #pragma unroll
   for (int q = 0; q < G; ++q) {
@@ -416,15 +447,14 @@ cudaError_t combine_stream(int M, int D, int copies, int rows, const void* y, co
                           static_cast<T*>(out));
 }
 
-template <typename T, int G>
+template <typename T, int G, int DEEP>
 cudaError_t combine_grad(int M, int D, int copies, int rows, const void* dout, const void* y, const int32_t* row_map,
                          const float* probs, void* dy, float* dprobs, cudaStream_t stream) {
   const int tpt = threads_of(D);
   const unsigned groups = (unsigned)(copies + G - 1) / G;
-  return launch_dependent(combine16_grad_kernel<T, G>, (unsigned)groups_of(M, tpt) * groups, kThreads, 0, stream, M, D,
-                          copies, rows, tpt,
-                          static_cast<const T*>(dout), static_cast<const T*>(y), row_map, probs, static_cast<T*>(dy),
-                          dprobs);
+  return launch_dependent(combine16_grad_kernel<T, G, DEEP>, (unsigned)groups_of(M, tpt) * groups, kThreads, 0, stream,
+                          M, D, copies, rows, tpt, static_cast<const T*>(dout), static_cast<const T*>(y), row_map, probs,
+                          static_cast<T*>(dy), dprobs);
 }
 
 }  // namespace
@@ -454,8 +484,11 @@ cudaError_t launch_swiglu16_grad(int R, int E, int I, bool bf16, const void* dh,
 cudaError_t launch_dispatch16(int M, int D, int copies, int rows, const void* x, const int32_t* row_map, void* out,
                               cudaStream_t stream) {
   const int tpt = threads_of(D), groups = groups_of(M, tpt), shares = shares_of(groups, D, tpt);
-  return launch_dependent(dispatch16_kernel, (unsigned)(groups * shares), kThreads, 0, stream, M, D, copies, rows, tpt,
-                          shares, static_cast<const uint4*>(x), row_map, static_cast<uint4*>(out));
+  // a thread that has a token's channels to itself reads two pieces at once (8192 x 4096 to one row: 25.1 and 28.5
+  // us, to six 73.0 and 73.8; where they are shared there is one for each: 300 x 4096 to two rows 3.3 and 2.8)
+  return launch_dependent(shares == 1 ? dispatch16_kernel<2> : dispatch16_kernel<1>, (unsigned)(groups * shares),
+                          kThreads, 0, stream, M, D, copies, rows, tpt, shares, static_cast<const uint4*>(x), row_map,
+                          static_cast<uint4*>(out));
 }
 
 cudaError_t launch_combine16(int M, int D, int copies, int rows, bool bf16, const void* y, const int32_t* row_map,
@@ -466,6 +499,12 @@ cudaError_t launch_combine16(int M, int D, int copies, int rows, bool bf16, cons
   // 3.4: 4.0 and 4.5 (256 x 4096, six rows), 5.6 and 6.8 (2048 x 512); 2.9: 6.4 and 5.6 (128 x 7168, eight rows);
   // 1.7: 3.8 and 3.0 (128 x 4096).
   if (copies <= 16 && (int64_t)M * (D / 8) > 3 * (int64_t)sm_count() * kThreads) {
+    if (copies <= 2)
+      return bf16 ? combine_stream<__nv_bfloat16, 2>(M, D, copies, rows, y, row_map, probs, out, stream)
+                  : combine_stream<__half, 2>(M, D, copies, rows, y, row_map, probs, out, stream);
+    if (copies <= 4)
+      return bf16 ? combine_stream<__nv_bfloat16, 4>(M, D, copies, rows, y, row_map, probs, out, stream)
+                  : combine_stream<__half, 4>(M, D, copies, rows, y, row_map, probs, out, stream);
     if (copies <= 8)
       return bf16 ? combine_stream<__nv_bfloat16, 8>(M, D, copies, rows, y, row_map, probs, out, stream)
                   : combine_stream<__half, 8>(M, D, copies, rows, y, row_map, probs, out, stream);
@@ -482,13 +521,21 @@ cudaError_t launch_combine16(int M, int D, int copies, int rows, bool bf16, cons
 cudaError_t launch_combine16_grad(int M, int D, int copies, int rows, bool bf16, const void* dout, const void* y,
                                   const int32_t* row_map, const float* probs, void* dy, float* dprobs,
                                   cudaStream_t stream) {
-  // two routes to a group where there are few tokens (61 tokens of eight routes x 7168: 4.6 us, with eight
-  // routes to a group 6.5), eight where dout should be read once (8192 x 4096 of six rows: 138 us)
+  // Routes to a group, and pieces read at once.  Few tokens: two and four (61 tokens of eight routes x 7168: 3.4 us;
+  // one piece 4.6, eight routes to a group 6.5).  Many: all up to eight, so that dout is read once, as registers
+  // for no more leave room for more blocks (8192 x 4096, of one row 44 us, in groups of eight 68; of three 81 and 95;
+  // of six 138).
   if (M < 4 * sm_count())
-    return bf16 ? combine_grad<__nv_bfloat16, 2>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
-                : combine_grad<__half, 2>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
-  return bf16 ? combine_grad<__nv_bfloat16, 8>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
-              : combine_grad<__half, 8>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
+    return bf16 ? combine_grad<__nv_bfloat16, 2, 4>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
+                : combine_grad<__half, 2, 4>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
+  if (copies <= 2)
+    return bf16 ? combine_grad<__nv_bfloat16, 2, 2>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
+                : combine_grad<__half, 2, 2>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
+  if (copies <= 4)
+    return bf16 ? combine_grad<__nv_bfloat16, 4, 1>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
+                : combine_grad<__half, 4, 1>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
+  return bf16 ? combine_grad<__nv_bfloat16, 8, 1>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream)
+              : combine_grad<__half, 8, 1>(M, D, copies, rows, dout, y, row_map, probs, dy, dprobs, stream);
 }
 
 }  // namespace moe
