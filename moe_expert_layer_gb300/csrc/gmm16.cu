@@ -91,11 +91,11 @@ struct Cfg {
   static constexpr int kParts = !PAIR && NT <= 32 ? 2 : 1, kDeep = 64 * kParts;
   static constexpr int kBBytes = kCtaCols * 128;  // of a part
   static constexpr int kStageBytes = kParts * (kABytes + kBBytes);  // the parts of A, then those of B
-  static constexpr int kStages = kWeight && SUMS == Sums::kFew ? 5 : PAIR || NT > 32 ? 6 : 5;
+  static constexpr int kStages = kWeight && (SUMS == Sums::kFew || !PAIR) ? 5 : PAIR || NT > 32 ? 6 : 5;
   // kWeight: pieces of 4 KB a warp (32 channels x 128 bytes); else 8 KB a group, or a tile of 32 rows' sums in fp32
-  static constexpr bool kSplits = !PAIR && NT <= 32;
+  static constexpr bool kSplits = !PAIR && (kWeight || NT <= 32);
   static constexpr int kPieces = SUMS == Sums::kFew ? 2 : 1;
-  static constexpr int kEpiBytes = kWeight ? 8 * kPieces * 4096 : 2 * kOutRows * 256;
+  static constexpr int kEpiBytes = kWeight ? (PAIR ? 8 * kPieces * 4096 : NT * 512) : 2 * kOutRows * 256;
   static constexpr int kTmemCols = 2 * NT <= 64 ? 64 : 2 * NT <= 256 ? 256 : 512;
   static_assert(!kSplits || kEpiBytes >= NT * 512, "a tile's sums");
   static constexpr int kSmem = kStages * kStageBytes + kEpiBytes;
@@ -226,6 +226,11 @@ __device__ __forceinline__ void mbar_acquire_cluster(uint64_t* bar, uint32_t par
       : "memory");
 }
 
+__device__ __forceinline__ float ld_cluster1(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -379,9 +384,10 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   constexpr bool PARTS = SUMS == Sums::kParts;
   constexpr int S = C::kStages;
   constexpr bool W = C::kWeight, A_MN = KIND != Gmm16::kForward, FIX = W;
+  constexpr bool TURNS = W && PAIR;  // the epilogue's groups have accumulators of their own
   extern __shared__ __align__(1024) uint8_t smem_raw[];  // swizzled rows: 1024-byte groups
   __shared__ __align__(8) uint64_t full_bar[S], tail_bar[W ? S : 1], peer_bar[W ? S : 1], empty_bar[S];
-  __shared__ __align__(8) uint64_t accfull_bar[W ? 4 : 2], accempty_bar[W ? 4 : 2], stored_bar[2], final_bar;
+  __shared__ __align__(8) uint64_t accfull_bar[TURNS ? 4 : 2], accempty_bar[TURNS ? 4 : 2], stored_bar[2], final_bar;
   __shared__ __align__(8) uint64_t sums_bar, read_bar;  // of a cluster that divides the reduction
   __shared__ int s_pref[W ? 1 : kMaxExperts + 1], s_end[W ? 1 : kMaxExperts], s_wsum[kThreads / 32];
   __shared__ uint32_t s_tmem;
@@ -410,9 +416,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         }
         mbar_init(&empty_bar[s], 1);
       }
-      for (int s = 0; s < (W ? 4 : 2); ++s) {  // kWeight: by 2 * group + accumulator
+      for (int s = 0; s < (TURNS ? 4 : 2); ++s) {  // by 2 * group + accumulator
         mbar_init(&accfull_bar[s], 1);
-        mbar_init(&accempty_bar[s], (PAIR ? 2 : 1) * (W ? 4 : 8));
+        mbar_init(&accempty_bar[s], (PAIR ? 2 : 1) * (TURNS ? 4 : 8));
       }
       for (int s = 0; s < 2; ++s) mbar_init(&stored_bar[s], 4);
       mbar_init(&final_bar, 1);
@@ -558,7 +564,9 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         for (auto list = items(first, stride); ok && list.more(); list.next()) {
           const Item it = list.it;
           list.look();
-          for (int left = it.rows; ok && left > 0; left -= 64, at.next(S)) {
+          const int KB = (it.rows + 63) / 64;
+          for (int kb = stage0(KB), kb1 = stage1(KB); ok && kb < kb1; ++kb, at.next(S)) {
+            const int left = it.rows - kb * 64;
             if (!fixed(left)) continue;
             const uint32_t parity = turn >> at.slot & 1u;
             turn ^= 1u << at.slot;
@@ -571,9 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
             if (rank == 1) {
               if (lane == 0) mbar_arrive_remote_release(cluster_addr(&peer_bar[at.slot], 0));
             } else {
-              if (!(ok = warp_wait(&peer_bar[at.slot], parity, abort_flag, a.status))) break;
-              mbar_acquire_cluster(&peer_bar[at.slot], parity);
-              __syncwarp();
+              if (PAIR) {
+                if (!(ok = warp_wait(&peer_bar[at.slot], parity, abort_flag, a.status))) break;
+                mbar_acquire_cluster(&peer_bar[at.slot], parity);
+                __syncwarp();
+              }
               if (lane == 0) mbar_arrive_twice(&full_bar[at.slot]);  // in place of the loaders
             }
           }
@@ -599,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
             const int buf = u & 1;
             int to = kb1;
             if (!whole && to - from > kPart) to = to - from > 2 * kPart ? from + kPart : (from + to + 1) >> 1;
-            if constexpr (W) {  // from those that have it
+            if constexpr (TURNS) {  // from those that have it
               for (int i = buf; ok && i < 4; i += 2)
                 if (held >> i & 1u) {
                   ok = warp_wait(&accempty_bar[i], back >> i & 1u, abort_flag, a.status);
@@ -632,7 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
               if (kb == kb0) list.look();
             }
             if (!ok) break;
-            if constexpr (W) {
+            if constexpr (TURNS) {
               const uint32_t who = whole ? 1u << (3 * buf) : 5u << buf;  // the accumulator's group, or both
               for (int i = buf; i < 4; i += 2)
                 if (who >> i & 1u) mx_commit<PAIR>(elected, smem_u32(&accfull_bar[i]));
@@ -657,28 +667,29 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
     // back, only what it takes.
     const int group = (warp - kEpiWarp0) >> 2, quarter = warp & 3;
     const uint32_t lanes = (uint32_t)quarter << 21;  // 32 * quarter in the lane field
-    constexpr int by = W && !PARTS ? 2 : 1;
+    constexpr int by = TURNS && !PARTS ? 2 : 1;
     int u = by == 2 ? group : 0;
     uint32_t at = 0;  // kWeight: the next piece's place
     uint32_t turn = 0;  // kWeight: parity of this group's next turn at each accumulator; from bit 2 on: items in parts
     auto heard = [&](int buf) {
       turn ^= 1u << buf;
-      return warp_wait(&accfull_bar[W ? 2 * group + buf : 0], ~turn >> buf & 1u, abort_flag, a.status);
+      return warp_wait(&accfull_bar[TURNS ? 2 * group + buf : 0], ~turn >> buf & 1u, abort_flag, a.status);
     };
     for (auto list = items(first + u * stride, by * stride); list.more(); list.next(), u += by) {
       const Item it = list.it;
       list.look();
       const int buf = u & 1;
       const bool whole = whole_sum(it.rows);
-      if (W && whole && buf != group) continue;
-      bool ok = W ? heard(buf) : warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status);
+      if (TURNS && whole && buf != group) continue;
+      bool ok = TURNS ? heard(buf) : warp_wait(&accfull_bar[buf], (u >> 1) & 1, abort_flag, a.status);
       // warps that wait for one another below give up together
-      if (!W && split == 1) ok = group_all(9 + group, ok);
+      if (!C::kSplits || split == 1)
+        if (!TURNS) ok = group_all(9 + group, ok);
       if (!ok) break;
       tc_fence_after();
       const uint32_t t = tmem + lanes + buf * NT;
       const int m0 = (PAIR ? 2 * it.cb + (int)rank : it.cb) * 128;
-      if constexpr (W) {
+      if constexpr (TURNS) {
         // 32 channels of a warp, 128 bytes of columns at a time, in the 128-byte swizzle of the output's map
         uint8_t* own = smem_raw + S * C::kStageBytes + (warp - kEpiWarp0) * C::kPieces * 4096;
         const int y = m0 + quarter * 32;
@@ -785,16 +796,19 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
           if (lane == 0) mbar_arrive(before);
         }
         continue;
-      } else if (C::kSplits && split > 1) {
+      } else if (C::kSplits && (W || split > 1)) {
         float* sums = reinterpret_cast<float*>(smem_raw + S * C::kStageBytes);  // [rows][128]
-        const int wg = warp - kEpiWarp0, th = wg * 32 + lane;
+        const int wg = warp - kEpiWarp0, th = wg * 32 + lane, KB = (steps(it) + C::kDeep - 1) / C::kDeep;
+        const bool some = stage0(KB) < stage1(KB);  // the others' share is 0
         // everybody has read the item before
         if (u > 0 && !warp_wait(&read_bar, (u - 1) & 1, abort_flag, a.status)) break;
         for (int c0 = group * 16; c0 < it.n; c0 += 32) {
-          uint32_t v[16];
+          uint32_t v[16] = {};
           __syncwarp();
-          tmem_ld16(t + c0, v);
-          tmem_wait_ld();
+          if (!W || some) {
+            tmem_ld16(t + c0, v);
+            tmem_wait_ld();
+          }
           float* o = sums + c0 * 128 + quarter * 32 + lane;
 #pragma unroll
           for (int i = 0; i < 16; ++i) o[i * 128] = __uint_as_float(v[i]);
@@ -807,7 +821,44 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         mbar_acquire_cluster(&sums_bar, u & 1);
         // eight channels of a row to a thread, the tile's pieces dealt out over the cluster
         const int width = min(128, out_rows - m0);
-        for (int i = share * 256 + th; i < it.rows * 16; i += split * 256) {
+        if constexpr (W) {  // eight columns of a channel
+          const int n = it.rows || !a.accumulate ? min(NT, a.D - it.col0) / 8 * 128 : 0;
+          for (int i = share * 256 + th; i < n; i += split * 256) {
+            const int ch = i & 127, c = (i >> 7) * 8;
+            float y[kMaxSplit][8], x[8] = {};
+#pragma unroll
+            for (int q = 0; q < kMaxSplit; ++q)
+              if (q < split)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[q][k] = ld_cluster1(cluster_addr(sums + (c + k) * 128 + ch, q));
+#pragma unroll
+            for (int q = 0; q < kMaxSplit; ++q)
+              if (q < split)
+#pragma unroll
+                for (int k = 0; k < 8; ++k) x[k] += y[q][k];
+            if (ch >= width) continue;
+            const size_t at = ((size_t)it.e * a.N + m0 + ch) * a.D + it.col0 + c;
+            if (a.out_f32) {
+              float4* o = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+              float4 lo = make_float4(x[0], x[1], x[2], x[3]), hi = make_float4(x[4], x[5], x[6], x[7]);
+              if (a.accumulate) {
+                const float4 l = o[0], h = o[1];
+                lo = make_float4(l.x + lo.x, l.y + lo.y, l.z + lo.z, l.w + lo.w);
+                hi = make_float4(h.x + hi.x, h.y + hi.y, h.z + hi.z, h.w + hi.w);
+              }
+              o[0] = lo;
+              o[1] = hi;
+            } else {
+              uint4 o;
+              o.x = pack16(a.bf16, __float_as_uint(x[0]), __float_as_uint(x[1]));
+              o.y = pack16(a.bf16, __float_as_uint(x[2]), __float_as_uint(x[3]));
+              o.z = pack16(a.bf16, __float_as_uint(x[4]), __float_as_uint(x[5]));
+              o.w = pack16(a.bf16, __float_as_uint(x[6]), __float_as_uint(x[7]));
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = o;
+            }
+          }
+        }
+        for (int i = share * 256 + th; !W && i < it.rows * 16; i += split * 256) {
           const int r = i >> 4, c = (i & 15) * 8;
           float4 y[kMaxSplit][2];
 #pragma unroll
@@ -1013,6 +1064,23 @@ Form choose(const Gmm16Problem& p) {
   return best;
 }
 
+// kWeight of few blocks and many rows: CTAs whose clusters divide the rows (0: pairs after all).
+int divide_rows(const Gmm16Problem& p) {
+  const int experts = p.R < p.E ? p.R : p.E, KB = (p.R / experts + 63) / 64;
+  auto blocks = [&](int m, int n) { return (double)experts * ((p.N + m - 1) / m) * ((p.D + n - 1) / n); };
+  double least = ceil(blocks(256, 256) / resident_clusters(2)) * (KB * 520.0 + 1500);
+  int best = 0;
+  for (int split = 2; split <= kMaxSplit; split *= 2) {
+    if (p.out_f32 && p.R > split * kPart * 64) continue;  // parts
+    const double clocks = ceil(blocks(128, 128) / resident_clusters(split)) * ((KB + split - 1) / split * 420.0 + 3000);
+    if (clocks < least) {
+      best = split;
+      least = clocks;
+    }
+  }
+  return best;
+}
+
 template <Gmm16 KIND>
 cudaError_t launch_rows(const Gmm16Problem& p, cudaStream_t stream) {
   const Form f = choose(p);
@@ -1025,6 +1093,7 @@ cudaError_t launch_rows(const Gmm16Problem& p, cudaStream_t stream) {
 
 cudaError_t launch_gmm16(const Gmm16Problem& p, cudaStream_t stream) {
   if (p.kind == Gmm16::kWeight) {
+    if (const int split = divide_rows(p)) return launch<Gmm16::kWeight, 128, false>(p, split, stream);
     if (p.out_f32 && p.R > kPart * 64) return launch<Gmm16::kWeight, 256, true, Sums::kParts>(p, 1, stream);
     // Shared memory of one of six stages for a second piece of a warp's sums, where an item has about as few stages
     // as pieces (us, with and without; 16 bits): 1 expert x 128 rows, 4096 x 4096 10.8 and 11.4, 8 x 75, 1416 x
