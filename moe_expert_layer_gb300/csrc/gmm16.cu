@@ -15,7 +15,8 @@
 // takes in steps of 16 (32 for a pair): an expert of cnt rows is cut into ceil(cnt / NT) tiles of
 // multiples of that step.  Items (expert, row tile, channel block) are dealt out expert-major, channel
 // blocks innermost, so that CTAs working at the same time share an expert's rows and its weights
-// through L2.  kWeight: items are 256 x 256 blocks of dw[e]; the last stage of an expert's rows also
+// through L2.  kWeight: items are 256 x 256 blocks of dw[e] (128 x 128 where clusters divide the rows, as below:
+// `divide_rows`); the last stage of an expert's rows also
 // brings rows of the next expert, which are overwritten with zeros in shared memory (up to the 16 rows
 // that an MMA takes) before the MMAs see them: 0 times what they hold could be NaN.
 //
@@ -92,12 +93,12 @@ struct Cfg {
   static constexpr int kBBytes = kCtaCols * 128;  // of a part
   static constexpr int kStageBytes = kParts * (kABytes + kBBytes);  // the parts of A, then those of B
   static constexpr int kStages = kWeight && (SUMS == Sums::kFew || !PAIR) ? 5 : PAIR || NT > 32 ? 6 : 5;
-  // kWeight: pieces of 4 KB a warp (32 channels x 128 bytes); else 8 KB a group, or a tile of 32 rows' sums in fp32
+  // kWeight: pairs' pieces of 4 KB a warp (32 channels x 128 bytes), a block's sums in fp32; else 8 KB a group, or a tile of 32 rows' sums in fp32
   static constexpr bool kSplits = !PAIR && (kWeight || NT <= 32);
   static constexpr int kPieces = SUMS == Sums::kFew ? 2 : 1;
   static constexpr int kEpiBytes = kWeight ? (PAIR ? 8 * kPieces * 4096 : NT * 512) : 2 * kOutRows * 256;
   static constexpr int kTmemCols = 2 * NT <= 64 ? 64 : 2 * NT <= 256 ? 256 : 512;
-  static_assert(!kSplits || kEpiBytes >= NT * 512, "a tile's sums");
+  static_assert(!kSplits || kEpiBytes >= NT * 512, "an item's sums");
   static constexpr int kSmem = kStages * kStageBytes + kEpiBytes;
   static_assert(kStageBytes % 1024 == 0 && 2 * NT <= kTmemCols, "swizzled rows, tensor memory");
   static_assert(kSmem + (kWeight ? 1024 : 9 * 1024) <= 227 * 1024, "shared memory");
@@ -486,7 +487,8 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   // would show in fp32 (4096 rows: 4.4e-6 of its norm). Such a sum is made in parts of up to kPart stages, added in
   // registers: 6e-7 to 9e-7 for any number of rows; parts of 8 stages 4.7e-7 to 6.5e-7, but half of the experts
   // around 768 rows would then be in two, which costs 4% instead of 2.
-  auto whole_sum = [&](int n) { return !PARTS || n <= kPart * 64; };
+  // (CTAs that divide the rows add them in shared memory.)
+  auto whole_sum = [&](int n) { return W && !PAIR ? !a.out_f32 || n <= kPart * 64 : !PARTS || n <= kPart * 64; };
   if (warp < kEpiWarp0) {
     if (PARTS) regs_dec<kRoleRegs>();
     if (warp == kAWarp || warp == kBWarp) {
@@ -602,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         for (auto list = items(first, stride); ok && list.more(); list.next()) {
           const Item it = list.it;
           const int n = steps(it), KB = (n + C::kDeep - 1) / C::kDeep, kb0 = stage0(KB), kb1 = stage1(KB);
-          const bool whole = whole_sum(n);
+          const bool whole = whole_sum(W && !PAIR ? (kb1 - kb0) * 64 : n);
           const uint32_t idesc = f16_idesc(a.bf16, A_MN, W, PAIR ? 256 : 128, it.n);
           int from = kb0;
           do {
@@ -669,6 +671,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
     const uint32_t lanes = (uint32_t)quarter << 21;  // 32 * quarter in the lane field
     constexpr int by = TURNS && !PARTS ? 2 : 1;
     int u = by == 2 ? group : 0;
+    int done = 0;     // items of a cluster's sums
     uint32_t at = 0;  // kWeight: the next piece's place
     uint32_t turn = 0;  // kWeight: parity of this group's next turn at each accumulator; from bit 2 on: items in parts
     auto heard = [&](int buf) {
@@ -799,26 +802,36 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
       } else if (C::kSplits && (W || split > 1)) {
         float* sums = reinterpret_cast<float*>(smem_raw + S * C::kStageBytes);  // [rows][128]
         const int wg = warp - kEpiWarp0, th = wg * 32 + lane, KB = (steps(it) + C::kDeep - 1) / C::kDeep;
-        const bool some = stage0(KB) < stage1(KB);  // the others' share is 0
+        const int own = stage1(KB) - stage0(KB);  // 0: so are its sums
+        const int parts = !W || whole_sum(own * 64) ? 1 : (own + kPart - 1) / kPart;
         // everybody has read the item before
-        if (u > 0 && !warp_wait(&read_bar, (u - 1) & 1, abort_flag, a.status)) break;
-        for (int c0 = group * 16; c0 < it.n; c0 += 32) {
-          uint32_t v[16] = {};
-          __syncwarp();
-          if (!W || some) {
-            tmem_ld16(t + c0, v);
-            tmem_wait_ld();
+        if (done > 0 && !warp_wait(&read_bar, (done - 1) & 1, abort_flag, a.status)) break;
+        for (int part = 0; part < parts; ++part) {
+          if (part) {
+            ++u;
+            if (!(ok = warp_wait(&accfull_bar[u & 1], (u >> 1) & 1, abort_flag, a.status))) break;
+            tc_fence_after();
           }
-          float* o = sums + c0 * 128 + quarter * 32 + lane;
+          for (int c0 = group * 16; c0 < it.n; c0 += 32) {
+            uint32_t v[16] = {};
+            __syncwarp();
+            if (!W || own) {
+              tmem_ld16(tmem + lanes + (u & 1) * NT + c0, v);
+              tmem_wait_ld();
+            }
+            float* o = sums + c0 * 128 + quarter * 32 + lane;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) o[i * 128] = __uint_as_float(v[i]);
+            for (int i = 0; i < 16; ++i) o[i * 128] = part ? o[i * 128] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&accempty_bar[u & 1]);
         }
-        tc_fence_before();
-        __syncwarp();
+        if (!ok) break;
         if (lane < split) mbar_arrive_remote_release(cluster_addr(&sums_bar, lane));
-        if (lane == 0) mbar_arrive(&accempty_bar[buf]);
-        if (!warp_wait(&sums_bar, u & 1, abort_flag, a.status)) break;
-        mbar_acquire_cluster(&sums_bar, u & 1);
+        if (!warp_wait(&sums_bar, done & 1, abort_flag, a.status)) break;
+        mbar_acquire_cluster(&sums_bar, done & 1);
+        ++done;
         // eight channels of a row to a thread, the tile's pieces dealt out over the cluster
         const int width = min(128, out_rows - m0);
         if constexpr (W) {  // eight columns of a channel
@@ -1064,14 +1077,19 @@ Form choose(const Gmm16Problem& p) {
   return best;
 }
 
-// kWeight of few blocks and many rows: CTAs whose clusters divide the rows (0: pairs after all).
+// kWeight of few blocks and many rows: blocks of 128 x 128, clusters of CTAs that divide the rows of each (0: pairs
+// after all), by the same count.  Both sides, us (16 bits / fp32):            pairs      divided
+//   1 expert x 16384 rows, 512 x 512                                      73 / 75      22 / 22
+//   1 x 8192, 1024 x 1024                                                 40 / 41      22 / 23
+//   4 x 2868, 72 x 928                                                    19 / 21      13 / 13
+//   3 x 1400, 408 x 152                                                   14 / 15      10 / 10
+//   2 x 653, 448 x 632                                                   9.3 / 10.7   8.7 / 9.2
 int divide_rows(const Gmm16Problem& p) {
   const int experts = p.R < p.E ? p.R : p.E, KB = (p.R / experts + 63) / 64;
   auto blocks = [&](int m, int n) { return (double)experts * ((p.N + m - 1) / m) * ((p.D + n - 1) / n); };
   double least = ceil(blocks(256, 256) / resident_clusters(2)) * (KB * 520.0 + 1500);
   int best = 0;
   for (int split = 2; split <= kMaxSplit; split *= 2) {
-    if (p.out_f32 && p.R > split * kPart * 64) continue;  // parts
     const double clocks = ceil(blocks(128, 128) / resident_clusters(split)) * ((KB + split - 1) / split * 420.0 + 3000);
     if (clocks < least) {
       best = split;
