@@ -15,9 +15,8 @@
 // takes in steps of 16 (32 for a pair): an expert of cnt rows is cut into ceil(cnt / NT) tiles of
 // multiples of that step.  Items (expert, row tile, channel block) are dealt out expert-major, channel
 // blocks innermost, so that CTAs working at the same time share an expert's rows and its weights
-// through L2.  kWeight: items are 256 x 256 blocks of dw[e] (128 x 128 where clusters divide the rows, as below:
-// `divide_rows`); the last stage of an expert's rows also
-// brings rows of the next expert, which are overwritten with zeros in shared memory (up to the 16 rows
+// through L2.  kWeight: items are 256 x 256 blocks of dw[e] (128 x 128 where clusters divide the rows:
+// `divide_rows`); the last stage of an expert's rows also brings rows of the next expert, which are overwritten with zeros in shared memory (up to the 16 rows
 // that an MMA takes) before the MMAs see them: 0 times what they hold could be NaN.
 //
 // Persistent CTAs, one per SM, in three forms (`choose`, at the end, with what each takes):
@@ -66,9 +65,12 @@ constexpr int kABytes = 128 * 128;  // 128 channels x 64 steps
 constexpr int kOutRows = 32;        // of an epilogue group's store, x 128 channels
 constexpr int kBoxes = 3, kBoxRows = 64;
 constexpr int kMaxSplit = 4;
-// kWeight, sums in parts: the stages of a part at most, and the registers a thread is launched with and goes on
-// with: roles, epilogue.
-constexpr int kPart = 12, kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
+// kWeight, sums in parts: the stages of a part at most (see there), and the registers a thread is launched with and
+// goes on with: roles, epilogue.
+__host__ __device__ constexpr int part_of(bool bf16) { return bf16 ? 12 : 8; }
+template <bool BF16>
+__device__ __forceinline__ int parts_of(int rows) { return (rows + part_of(BF16) * 64 - 1) / (part_of(BF16) * 64); }
+constexpr int kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
 static_assert(128 * kRoleRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "an increase past the launch's registers never ends");
 
 template <int kLeft>
@@ -93,7 +95,8 @@ struct Cfg {
   static constexpr int kBBytes = kCtaCols * 128;  // of a part
   static constexpr int kStageBytes = kParts * (kABytes + kBBytes);  // the parts of A, then those of B
   static constexpr int kStages = kWeight && (SUMS == Sums::kFew || !PAIR) ? 5 : PAIR || NT > 32 ? 6 : 5;
-  // kWeight: pairs' pieces of 4 KB a warp (32 channels x 128 bytes), a block's sums in fp32; else 8 KB a group, or a tile of 32 rows' sums in fp32
+  // kWeight: pairs' pieces of 4 KB a warp (32 channels x 128 bytes), or a block's sums in fp32; else 8 KB a
+  // group, or the sums of a tile of 32 rows
   static constexpr bool kSplits = !PAIR && (kWeight || NT <= 32);
   static constexpr int kPieces = SUMS == Sums::kFew ? 2 : 1;
   static constexpr int kEpiBytes = kWeight ? (PAIR ? 8 * kPieces * 4096 : NT * 512) : 2 * kOutRows * 256;
@@ -482,13 +485,14 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   auto stage0 = [&](int KB) { return split == 1 ? 0 : share * KB / split; };
   auto stage1 = [&](int KB) { return split == 1 ? KB : (share + 1) * KB / split; };
 
-  // An accumulator takes an item's whole sum, but with PARTS: the tensor cores drop bits where they add (a sum
-  // of n products loses about 1e-9 n of itself, always towards zero), which a gradient of thousands of rows
-  // would show in fp32 (4096 rows: 4.4e-6 of its norm). Such a sum is made in parts of up to kPart stages, added in
-  // registers: 6e-7 to 9e-7 for any number of rows; parts of 8 stages 4.7e-7 to 6.5e-7, but half of the experts
-  // around 768 rows would then be in two, which costs 4% instead of 2.
-  // (CTAs that divide the rows add them in shared memory.)
-  auto whole_sum = [&](int n) { return W && !PAIR ? !a.out_f32 || n <= kPart * 64 : !PARTS || n <= kPart * 64; };
+  // An accumulator takes an item's whole sum, but with PARTS: the tensor cores drop bits where they add, always
+  // towards zero (of its norm, a sum of n bfloat16 products loses about 1e-9 n, of binary16 ones, which have more bits
+  // to lose, 1.3e-9 n), which a gradient of thousands of rows would show in fp32.  Such a sum is made in parts,
+  // added in registers (in shared memory, where CTAs divide the rows): 12 stages of bfloat16 7e-7, 8 of
+  // binary16 6.5e-7 for any number of rows.  With 8 for bfloat16 too (4.7e-7) experts of 768 rows would be in two
+  // parts: 64 of them, 4096 x 1408, took 4% more instead of 2.
+  const int most = part_of(a.bf16);
+  auto whole_sum = [&](int n) { return W && !PAIR ? !a.out_f32 || n <= most * 64 : !PARTS || n <= most * 64; };
   if (warp < kEpiWarp0) {
     if (PARTS) regs_dec<kRoleRegs>();
     if (warp == kAWarp || warp == kBWarp) {
@@ -610,7 +614,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
           do {
             const int buf = u & 1;
             int to = kb1;
-            if (!whole && to - from > kPart) to = to - from > 2 * kPart ? from + kPart : (from + to + 1) >> 1;
+            if (!whole && to - from > most) to = to - from > 2 * most ? from + most : (from + to + 1) >> 1;
             if constexpr (TURNS) {  // from those that have it
               for (int i = buf; ok && i < 4; i += 2)
                 if (held >> i & 1u) {
@@ -756,7 +760,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         // A lane's channel, 128 columns of it to a group: drained into registers, where the parts are added,
         // and the accumulators free again before anything is stored.
         float sum[128] = {};
-        const int from = group * 128, parts = (it.rows + kPart * 64 - 1) / (kPart * 64);
+        const int from = group * 128, parts = a.bf16 ? parts_of<true>(it.rows) : parts_of<false>(it.rows);
         for (int part = 0; part < parts; ++part) {
           if (part) {
             ++u;
@@ -803,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         float* sums = reinterpret_cast<float*>(smem_raw + S * C::kStageBytes);  // [rows][128]
         const int wg = warp - kEpiWarp0, th = wg * 32 + lane, KB = (steps(it) + C::kDeep - 1) / C::kDeep;
         const int own = stage1(KB) - stage0(KB);  // 0: so are its sums
-        const int parts = !W || whole_sum(own * 64) ? 1 : (own + kPart - 1) / kPart;
+        const int parts = !W || whole_sum(own * 64) ? 1 : a.bf16 ? parts_of<true>(own * 64) : parts_of<false>(own * 64);
         // everybody has read the item before
         if (done > 0 && !warp_wait(&read_bar, (done - 1) & 1, abort_flag, a.status)) break;
         for (int part = 0; part < parts; ++part) {
@@ -1112,7 +1116,7 @@ cudaError_t launch_rows(const Gmm16Problem& p, cudaStream_t stream) {
 cudaError_t launch_gmm16(const Gmm16Problem& p, cudaStream_t stream) {
   if (p.kind == Gmm16::kWeight) {
     if (const int split = divide_rows(p)) return launch<Gmm16::kWeight, 128, false>(p, split, stream);
-    if (p.out_f32 && p.R > kPart * 64) return launch<Gmm16::kWeight, 256, true, Sums::kParts>(p, 1, stream);
+    if (p.out_f32 && p.R > part_of(p.bf16) * 64) return launch<Gmm16::kWeight, 256, true, Sums::kParts>(p, 1, stream);
     // Shared memory of one of six stages for a second piece of a warp's sums, where an item has about as few stages
     // as pieces (us, with and without; 16 bits): 1 expert x 128 rows, 4096 x 4096 10.8 and 11.4, 8 x 75, 1416 x
     // 1024 10.3 and 10.7 (fp32 13.7 and 14.5), 8 x 256, 2816 x 4096 44.6 and 43.8, 16 x 768 93.7 and 90.6.

@@ -125,7 +125,7 @@ def test_products_of_real_values(counts, N, D, t):
      ([800, 20, 1700, 768] * 15, 3, 512, 512), ([900] * 80, 0, 512, 256)],
 )
 def test_weight_gradients_of_many_rows_are_exact(counts, behind, N, D, t):
-    """Sums in several parts (in fp32, of experts with more than 768 rows), written and added."""
+    """Sums in several parts (in fp32, of experts with more than 768 or 512 rows), written and added."""
     g, R, E = rng(N + D), sum(counts) + behind, len(counts)
     cumsum, n = prefix(counts), sum(counts)
     a, dc, ws = ints((R, D), t, g), ints((R, N), t, g, 2), space(R, E, N, D)
@@ -145,14 +145,15 @@ def test_weight_gradients_of_many_rows_are_exact(counts, behind, N, D, t):
 @TYPES
 def test_long_weight_gradients_keep_fp32(t):
     """Sums of 70000 positive products, where bits dropped one way would add up: an fp32 gradient is made of
-    parts of up to 768 rows (n 2^-23 each, as above), added at half a step of the sum so far each."""
+    parts of up to 768 rows (binary16: 512; n 2^-23 each, as above), added at half a step of the sum so far each."""
     g, counts, N, D = rng(3), [100, 70000], 72, 136
     cumsum, R = prefix(counts), sum(counts)
     a, dc = (torch.rand((R, k), device="cuda", generator=g).add(0.5).to(t) for k in (D, N))
     dw = marked((2, N, D), F32)
     moe.moe_gmm16_weight_grad(dc, a, cumsum, dw, space(R, 2, N, D))
     want = ref.weight_grad(dc, a, cumsum.tolist())
-    close(dw, want, want, 768 + (70000 // 768 + 1) / 2, F32)
+    part = 768 if t == BF16 else 512
+    close(dw, want, want, part + (70000 // part + 1) / 2, F32)
 
 
 @TYPES
