@@ -16,8 +16,9 @@
 // multiples of that step.  Items (expert, row tile, channel block) are dealt out expert-major, channel
 // blocks innermost, so that CTAs working at the same time share an expert's rows and its weights
 // through L2.  kWeight: items are 256 x 256 blocks of dw[e] (128 x 128 where clusters divide the rows:
-// `divide_rows`); the last stage of an expert's rows also brings rows of the next expert, which are overwritten with zeros in shared memory (up to the 16 rows
-// that an MMA takes) before the MMAs see them: 0 times what they hold could be NaN.
+// `divide_rows`); the last stage of an expert's rows also brings rows of the next expert, which are
+// overwritten with zeros in shared memory (up to the 16 rows that an MMA takes) before the MMAs see
+// them: 0 times what they hold could be NaN.
 //
 // Persistent CTAs, one per SM, in three forms (`choose`, at the end, with what each takes):
 //   - single CTAs of 128 channels and tiles of up to 32 rows: the weights stream past few rows.  Where
