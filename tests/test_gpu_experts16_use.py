@@ -75,8 +75,8 @@ def w1_shape(E, I, K):
     return (E, 2 * I, K)
 
 
-# the last: weight gradients in parts, rows and pieces of many tokens
-SIZES = [(1, 256, 64, 4, 2), (40, 384, 128, 8, 3), (700, 512, 256, 6, 2), (3000, 512, 512, 2, 2)]
+# the last two: rows and pieces of many tokens, and weight gradients whose rows are divided, or in parts
+SIZES = [(1, 256, 64, 4, 2), (40, 384, 128, 8, 3), (700, 512, 256, 6, 2), (3000, 512, 512, 2, 2), (4000, 1024, 512, 8, 2)]
 
 
 def same(a, b):
@@ -135,11 +135,11 @@ def test_captured_and_replayed(sizes):
 
 def test_on_several_streams_at_once():
     """Steps of different sizes on streams of two priorities, none ordered with another."""
-    steps = [Step(i, *SIZES[i % 4]) for i in range(5)]
+    steps = [Step(i, *SIZES[i % 5]) for i in range(6)]
     for s in steps:
         s.run(wait=True)
     want = [s.results() for s in steps]
-    streams = [torch.cuda.Stream(priority=p) for p in (0, -1, 0, -1, 0)]
+    streams = [torch.cuda.Stream(priority=p) for p in (0, -1, 0, -1, 0, -1)]
     torch.cuda.synchronize()
     for _ in range(15):
         for s, stream in zip(steps, streams):
@@ -162,6 +162,20 @@ def test_products_repeat_to_the_bit(rows, E, N, D):
     for _ in range(20):
         again = torch.zeros_like(first)
         moe.moe_gmm16(a, cumsum, w, again, ws)
+        assert torch.equal(again, first)
+
+
+@pytest.mark.parametrize("rows,E,N,D", [(3000, 1, 512, 520), (2000, 3, 200, 264), (1500, 16, 1024, 512), (100, 8, 512, 512)])
+def test_weight_gradients_repeat_to_the_bit(rows, E, N, D):
+    """Sums over parts, and over a cluster that divides the rows, are added in the same order every time."""
+    g, R = rng(6), rows * E
+    a, dc = normal((R, D), BF16, g), normal((R, N), BF16, g)
+    cumsum, ws = prefix([rows] * E), space(R, E, N, D)
+    first = torch.empty((E, N, D), device="cuda")
+    moe.moe_gmm16_weight_grad(dc, a, cumsum, first, ws)
+    for _ in range(20):
+        again = torch.zeros_like(first)
+        moe.moe_gmm16_weight_grad(dc, a, cumsum, again, ws)
         assert torch.equal(again, first)
 
 
@@ -298,7 +312,7 @@ def test_tensors_elsewhere_are_refused():
             moe.moe_gmm16(**args)
 
 
-@pytest.mark.parametrize("rows,E,N,D", [(3, 2, 4096, 4096), (60, 8, 512, 512), (600, 3, 1024, 512), (2000, 4, 1024, 512)])
+@pytest.mark.parametrize("rows,E,N,D", [(3, 2, 4096, 4096), (60, 8, 512, 512), (600, 3, 1024, 512), (2000, 4, 1024, 512), (3000, 1, 512, 512)])
 def test_on_a_part_of_the_device(narrow_stream, rows, E, N, D):  # noqa: F811
     """On a stream that may use fewer SMs than the device has, products and adapters give what they give on all of it."""
     g, R = rng(8), rows * E
