@@ -10,7 +10,12 @@
  * their own, or as graphs replayed at once) need workspaces of their own.  `type` is MOE_TYPE_F16 or MOE_TYPE_BF16 and is the
  * type of every array whose type is not named.  Sums are held in fp32 and rounded to
  * nearest even where they are stored, once; binary16 saturates at +-65504 (a NaN stays a
- * NaN), bfloat16 overflows to infinity.
+ * NaN), bfloat16 overflows to infinity.  The tensor cores' fp32 sums drop bits towards
+ * zero: of n products 2^-27 n of their magnitudes at most.  n is the depth of a product
+ * or of a gradient for the rows (that is half a step of binary16 at the deepest, 65536, a
+ * sixteenth of it at 4096; bfloat16 an eighth of those), and for a weight gradient of any
+ * number of rows at most 4096 (binary16) or 32768 (bfloat16), in fp32 512 or 768: longer
+ * sums are made of such parts, added in fp32.
  *
  * Expert-major rows: those of expert e are cumsum[e - 1] .. cumsum[e] - 1 (from 0 for
  * e = 0) of R rows; cumsum [E] is the inclusive prefix that moe_route_sort writes (entries

@@ -68,9 +68,16 @@ constexpr int kBoxes = 3, kBoxRows = 64;
 constexpr int kMaxSplit = 4;
 // kWeight, sums in parts: the stages of a part at most (see there), and the registers a thread is launched with and
 // goes on with: roles, epilogue.
-__host__ __device__ constexpr int part_of(bool bf16) { return bf16 ? 12 : 8; }
-template <bool BF16>
-__device__ __forceinline__ int parts_of(int rows) { return (rows + part_of(BF16) * 64 - 1) / (part_of(BF16) * 64); }
+__host__ __device__ constexpr int part_of(bool bf16, bool out_f32) { return out_f32 ? (bf16 ? 12 : 8) : bf16 ? 512 : 64; }
+template <bool BF16, bool OUT_F32>
+__device__ __forceinline__ int parts_of(int rows) {
+  constexpr int kRows = part_of(BF16, OUT_F32) * 64;
+  return (rows + kRows - 1) / kRows;
+}
+__device__ __forceinline__ int parts_of(bool bf16, bool out_f32, int rows) {  // divided by constants
+  if (out_f32) return bf16 ? parts_of<true, true>(rows) : parts_of<false, true>(rows);
+  return bf16 ? parts_of<true, false>(rows) : parts_of<false, false>(rows);
+}
 constexpr int kLaunchRegs = 168, kRoleRegs = 72, kEpiRegs = 216;
 static_assert(128 * kRoleRegs + 256 * kEpiRegs <= kThreads * kLaunchRegs, "an increase past the launch's registers never ends");
 
@@ -83,8 +90,8 @@ __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.a
 template <uint32_t kRegs>
 __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs)); }
 
-// kWeight: items of few stages, of many, or in parts (`launch_gmm16`).
-enum class Sums { kFew, kMany, kParts };
+// kWeight: items of few stages, or of many; or either, some of them in parts (`launch_gmm16`).
+enum class Sums { kFew, kMany, kFewParts, kParts };
 
 template <Gmm16 KIND, int NT, bool PAIR, Sums SUMS>
 struct Cfg {
@@ -95,11 +102,13 @@ struct Cfg {
   static constexpr int kParts = !PAIR && NT <= 32 ? 2 : 1, kDeep = 64 * kParts;
   static constexpr int kBBytes = kCtaCols * 128;  // of a part
   static constexpr int kStageBytes = kParts * (kABytes + kBBytes);  // the parts of A, then those of B
-  static constexpr int kStages = kWeight && (SUMS == Sums::kFew || !PAIR) ? 5 : PAIR || NT > 32 ? 6 : 5;
+  static constexpr bool kFew = SUMS == Sums::kFew || SUMS == Sums::kFewParts;
+  static constexpr bool kInParts = SUMS == Sums::kParts || SUMS == Sums::kFewParts;
+  static constexpr int kStages = kWeight && (kFew || !PAIR) ? 5 : PAIR || NT > 32 ? 6 : 5;
   // kWeight: pairs' pieces of 4 KB a warp (32 channels x 128 bytes), or a block's sums in fp32; else 8 KB a
   // group, or the sums of a tile of 32 rows
   static constexpr bool kSplits = !PAIR && (kWeight || NT <= 32);
-  static constexpr int kPieces = SUMS == Sums::kFew ? 2 : 1;
+  static constexpr int kPieces = kFew ? 2 : 1;
   static constexpr int kEpiBytes = kWeight ? (PAIR ? 8 * kPieces * 4096 : NT * 512) : 2 * kOutRows * 256;
   static constexpr int kTmemCols = 2 * NT <= 64 ? 64 : 2 * NT <= 256 ? 256 : 512;
   static_assert(!kSplits || kEpiBytes >= NT * 512, "an item's sums");
@@ -347,13 +356,14 @@ struct BlockItems {
     hi = e < a.E ? __ldcg(a.cumsum + e) : 0;
   }
   __device__ __forceinline__ void look() {
+    const int was = e;
     e += de;
     local += dl;
     if (local >= per) {
       local -= per;
       ++e;
     }
-    fetch();
+    if (e != was) fetch();  // a group that leaves an item to the other has nothing to hide it behind
   }
   __device__ __forceinline__ void set() {
     it.e = e;
@@ -386,7 +396,7 @@ __device__ __forceinline__ bool group_all(int id, bool ok) {
 template <Gmm16 KIND, int NT, bool PAIR, Sums SUMS>
 __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constant__ Maps maps, const Args a) {
   using C = Cfg<KIND, NT, PAIR, SUMS>;
-  constexpr bool PARTS = SUMS == Sums::kParts;
+  constexpr bool PARTS = C::kInParts;
   constexpr int S = C::kStages;
   constexpr bool W = C::kWeight, A_MN = KIND != Gmm16::kForward, FIX = W;
   constexpr bool TURNS = W && PAIR;  // the epilogue's groups have accumulators of their own
@@ -486,14 +496,18 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
   auto stage0 = [&](int KB) { return split == 1 ? 0 : share * KB / split; };
   auto stage1 = [&](int KB) { return split == 1 ? KB : (share + 1) * KB / split; };
 
-  // An accumulator takes an item's whole sum, but with PARTS: the tensor cores drop bits where they add, always
-  // towards zero (of its norm, a sum of n bfloat16 products loses about 1e-9 n, of binary16 ones, which have more bits
-  // to lose, 1.3e-9 n), which a gradient of thousands of rows would show in fp32.  Such a sum is made in parts,
-  // added in registers (in shared memory, where CTAs divide the rows): 12 stages of bfloat16 7e-7, 8 of
-  // binary16 6.5e-7 for any number of rows.  With 8 for bfloat16 too (4.7e-7) experts of 768 rows would be in two
-  // parts: 64 of them, 4096 x 1408, took 4% more instead of 2.
-  const int most = part_of(a.bf16);
-  auto whole_sum = [&](int n) { return W && !PAIR ? !a.out_f32 || n <= most * 64 : !PARTS || n <= most * 64; };
+  // An accumulator takes an item's whole sum; of a weight gradient, one of so many rows at most, where it could have
+  // more.  The tensor cores add 16 products a step and drop what lies below the sum's last place, always towards zero:
+  // two units of it at most, 2^-27 n of the magnitudes of n products.  (Measured, of the norm: n random products
+  // 1.3e-9 n in binary16, 1e-9 n in bfloat16; of one sign up to 6e-9 n.)  A longer sum is made in parts,
+  // added in registers, or in shared memory where CTAs divide the rows.
+  //   16-bit output: 64 stages of binary16, 512 of bfloat16; 2^-27 n is a sixteenth of half a step there.
+  //   fp32 output: 8 stages of binary16 (up to 65536 random products 6.7e-7 of the norm, of one sign 2.4e-6), 12 of
+  //   bfloat16 (7.4e-7, 6.2e-7).  With 8 for bfloat16 too (4.7e-7) experts of 768 rows would be in two parts: 64 of
+  //   them, 4096 x 1408, took 4% more instead of 2.  The additions of the parts round as well: 2^20 random products
+  //   8e-7, 2^24 1.7e-6.
+  const int most = part_of(a.bf16, a.out_f32);
+  auto whole_sum = [&](int n) { return W && (PARTS || !PAIR) ? n <= most * 64 : true; };
   if (warp < kEpiWarp0) {
     if (PARTS) regs_dec<kRoleRegs>();
     if (warp == kAWarp || warp == kBWarp) {
@@ -761,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         // A lane's channel, 128 columns of it to a group: drained into registers, where the parts are added,
         // and the accumulators free again before anything is stored.
         float sum[128] = {};
-        const int from = group * 128, parts = a.bf16 ? parts_of<true>(it.rows) : parts_of<false>(it.rows);
+        const int from = group * 128, parts = parts_of(a.bf16, a.out_f32, it.rows);
         for (int part = 0; part < parts; ++part) {
           if (part) {
             ++u;
@@ -788,17 +802,35 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         const uint32_t parity = turn >> 3 & 1u;
         turn += 4;
         if (group == 1 && !warp_wait(before, parity, abort_flag, a.status)) break;
+        if (a.out_f32) {
 #pragma unroll
-        for (int c = 0; c < 128; c += 32)
-          if (stored && from + c < it.n) {
-            bulk_wait_read<C::kPieces - 1>();
-            __syncwarp();
+          for (int c = 0; c < 128; c += 32)
+            if (stored && from + c < it.n) {
+              bulk_wait_read<C::kPieces - 1>();
+              __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              row(i) = make_uint4(__float_as_uint(sum[c + 4 * i]), __float_as_uint(sum[c + 4 * i + 1]),
-                                               __float_as_uint(sum[c + 4 * i + 2]), __float_as_uint(sum[c + 4 * i + 3]));
-            put(from + c);
-          }
+              for (int i = 0; i < 8; ++i)
+                row(i) = make_uint4(__float_as_uint(sum[c + 4 * i]), __float_as_uint(sum[c + 4 * i + 1]),
+                                    __float_as_uint(sum[c + 4 * i + 2]), __float_as_uint(sum[c + 4 * i + 3]));
+              put(from + c);
+            }
+        } else {
+#pragma unroll
+          for (int c = 0; c < 128; c += 64)
+            if (stored && from + c < it.n) {
+              bulk_wait_read<C::kPieces - 1>();
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                uint32_t x[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  x[k] = pack16(a.bf16, __float_as_uint(sum[c + 8 * i + 2 * k]), __float_as_uint(sum[c + 8 * i + 2 * k + 1]));
+                row(i) = make_uint4(x[0], x[1], x[2], x[3]);
+              }
+              put(from + c);
+            }
+        }
         if (group == 0) {
           __syncwarp();
           if (lane == 0) mbar_arrive(before);
@@ -808,7 +840,7 @@ __global__ void __launch_bounds__(kThreads, 1) gmm16_kernel(const __grid_constan
         float* sums = reinterpret_cast<float*>(smem_raw + S * C::kStageBytes);  // [rows][128]
         const int wg = warp - kEpiWarp0, th = wg * 32 + lane, KB = (steps(it) + C::kDeep - 1) / C::kDeep;
         const int own = stage1(KB) - stage0(KB);  // 0: so are its sums
-        const int parts = !W || whole_sum(own * 64) ? 1 : a.bf16 ? parts_of<true>(own * 64) : parts_of<false>(own * 64);
+        const int parts = whole_sum(own * 64) ? 1 : parts_of(a.bf16, a.out_f32, own * 64);
         // everybody has read the item before
         if (done > 0 && !warp_wait(&read_bar, (done - 1) & 1, abort_flag, a.status)) break;
         for (int part = 0; part < parts; ++part) {
@@ -1017,7 +1049,7 @@ cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
     const cudaError_t e =
         cudaFuncSetAttribute(gmm16_kernel<KIND, NT, PAIR, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
-    if (SUMS == Sums::kParts) {
+    if (C::kInParts) {
       // launched with other registers than its split counts on, it would wait for them: a build that
       // does is refused
       cudaFuncAttributes fa;
@@ -1117,13 +1149,18 @@ cudaError_t launch_rows(const Gmm16Problem& p, cudaStream_t stream) {
 cudaError_t launch_gmm16(const Gmm16Problem& p, cudaStream_t stream) {
   if (p.kind == Gmm16::kWeight) {
     if (const int split = divide_rows(p)) return launch<Gmm16::kWeight, 128, false>(p, split, stream);
-    if (p.out_f32 && p.R > part_of(p.bf16) * 64) return launch<Gmm16::kWeight, 256, true, Sums::kParts>(p, 1, stream);
     // Shared memory of one of six stages for a second piece of a warp's sums, where an item has about as few stages
     // as pieces (us, with and without; 16 bits): 1 expert x 128 rows, 4096 x 4096 10.8 and 11.4, 8 x 75, 1416 x
-    // 1024 10.3 and 10.7 (fp32 13.7 and 14.5), 8 x 256, 2816 x 4096 44.6 and 43.8, 16 x 768 93.7 and 90.6.
+    // 1024 10.3 and 10.7 (fp32 13.7 and 14.5; 64 x 75, 2816 x 4096 519 and 530), 8 x 256, 2816 x 4096 44.6 and 43.8,
+    // 16 x 768 93.7 and 90.6.  In parts, if an expert could have more rows than one: the host knows only how
+    // many there are in all.
     const int experts = p.R < p.E ? p.R : p.E;
-    return p.R <= 192 * (int64_t)experts ? launch<Gmm16::kWeight, 256, true, Sums::kFew>(p, 1, stream)
-                                         : launch<Gmm16::kWeight, 256, true, Sums::kMany>(p, 1, stream);
+    const bool few = p.R <= 192 * (int64_t)experts, parts = p.R > part_of(p.bf16, p.out_f32) * 64;
+    if (parts)
+      return few ? launch<Gmm16::kWeight, 256, true, Sums::kFewParts>(p, 1, stream)
+                 : launch<Gmm16::kWeight, 256, true, Sums::kParts>(p, 1, stream);
+    return few ? launch<Gmm16::kWeight, 256, true, Sums::kFew>(p, 1, stream)
+               : launch<Gmm16::kWeight, 256, true, Sums::kMany>(p, 1, stream);
   }
   return p.kind == Gmm16::kForward ? launch_rows<Gmm16::kForward>(p, stream) : launch_rows<Gmm16::kInput>(p, stream);
 }
