@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kThreads) lora16_few_kernel(const Lora16Proble
 #pragma unroll
     for (int q = 0; q < RC; ++q) {
       v[q] = 0.0f;
-      if (q * 32 + lane < HALVES * MR * 16)
+      if (q * 32 + lane < p.rank)  // those behind are 0 times x, NaN where x is not finite
         for (int u = 0; u < ctas; ++u) v[q] += ld_cluster(cluster_addr(&s_sum[i][q * 32 + lane], u));
       v[q] *= scale;
     }
