@@ -21,10 +21,12 @@
 // 24 adapters, of rank 16 40 (5000), of rank 64 54 (3900): 21 in the first kernel, and there the warp-level
 // tensor path is 45% busy.  Above that it bounds: rank 128 93.
 //
-// v goes into the second MMA as two 16-bit numbers, s v 2^-e = hi + lo with e the exponent of the token's
+// v goes into the second MMA as two 16-bit numbers, s v 2^-e = hi + lo with e set by the exponent of the token's
 // largest: 16 significant bits or more, and no rank value leaves binary16's range.  The columns of
 // four MMAs are dealt out so that a lane gets eight neighbouring channels of a token, 16 bytes of base
 // and out.
+#include <type_traits>
+
 #include "experts16.h"
 #include "mxfp4.cuh"
 #include "tc_common.cuh"
@@ -214,8 +216,9 @@ template <typename T> __device__ __forceinline__ T to16(float v);
 template <> __device__ __forceinline__ __half to16<__half>(float v) { return __float2half_rn(v); }
 template <> __device__ __forceinline__ __nv_bfloat16 to16<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// s v of a token as 2^e (hi + lo), e the exponent of its largest finite value; a warp enters, lane r
-// with ranks q * 32 + r.  Returns 2^e.
+// s v of a token as 2^e (hi + lo); a warp enters, lane r with ranks q * 32 + r.  Returns 2^e.  e is the exponent of the
+// token's largest finite value, and for bfloat16, whose b may be as large as fp32's numbers, 8 more (held at
+// the last one): 128 values below 2^-7 times b stay finite where their sum does.
 template <typename T, int RC>
 __device__ __forceinline__ float split_ranks(const float (&v)[RC], T* hi, T* lo, int lane) {
   uint32_t most = 0;
@@ -225,6 +228,7 @@ __device__ __forceinline__ float split_ranks(const float (&v)[RC], T* hi, T* lo,
     if (f != 255u) most = max(most, f);
   }
   most = max(__reduce_max_sync(0xffffffffu, most), 1u);  // 1 .. 254: 2^(most - 127)
+  if (!std::is_same<T, __half>::value) most = min(most + 8u, 254u);
   const float down = most == 254u ? __uint_as_float(0x00400000u) : __uint_as_float((254u - most) << 23);
 #pragma unroll
   for (int q = 0; q < RC; ++q) {

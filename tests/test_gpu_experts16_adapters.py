@@ -34,3 +34,20 @@ def test_infinite_tokens_give_infinities(M, r, t):
     assert (out[3] == most).all() and (out[8] == -most).all() and out[10].isnan().all()
     rest = [i for i in range(M) if i not in (3, 8, 10)]
     assert torch.equal(out[rest], ref.rounded(ref.lora(x[rest], adapter[rest], a, b, None, base[rest]), t))
+
+
+@pytest.mark.parametrize("rank_value,weight", [(-120, 127), (-30, 127), (0, 120), (120, -120), (127, -127), (100, -126), (-126, 100)])
+@pytest.mark.parametrize("r", [8, 64, 128])
+@pytest.mark.parametrize("M", [16, 40])
+def test_bfloat16_weights_and_rank_values_at_their_ends(M, r, rank_value, weight):
+    """Rank values and weights far apart, whose products are ordinary numbers: powers of two, exact (with signs that
+    leave r / 4 of the products, so that no sum on the way leaves fp32)."""
+    D, N = 64, 72
+    lo = rank_value // 2
+    x, a = torch.full((M, D), 2.0 ** lo, dtype=BF16, device="cuda"), torch.zeros((1, r, D), dtype=BF16, device="cuda")
+    a[..., 7] = 2.0 ** (rank_value - lo)
+    b = torch.full((1, N, r), 2.0 ** min(weight, 127), dtype=BF16, device="cuda")
+    b[..., 3::4], b[..., 2::4] = -b[..., 3::4], 0.0
+    base, out = torch.zeros((M, N), dtype=BF16, device="cuda"), marked((M, N), BF16)
+    lora_call(x, torch.zeros(M, dtype=torch.int32, device="cuda"), a, b, None, base, out)
+    assert (out.double() == r / 4 * 2.0 ** (rank_value + weight)).all()
