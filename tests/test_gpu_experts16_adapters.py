@@ -51,3 +51,73 @@ def test_bfloat16_weights_and_rank_values_at_their_ends(M, r, rank_value, weight
     base, out = torch.zeros((M, N), dtype=BF16, device="cuda"), marked((M, N), BF16)
     lora_call(x, torch.zeros(M, dtype=torch.int32, device="cuda"), a, b, None, base, out)
     assert (out.double() == r / 4 * 2.0 ** (rank_value + weight)).all()
+
+
+def sorted_by_library(adapter, L):
+    """Tables of moe_route_sort, one adapter to a token."""
+    M = adapter.numel()
+    d = moe.dims(M, 128, 64, L, 1)
+    route, row, count, cumsum = (torch.empty(n, dtype=torch.int32, device="cuda") for n in (M, M, L, L))
+    ws = torch.empty(max(1, moe.moe_route_sort_workspace_size(d)), dtype=torch.uint8, device="cuda")
+    moe.moe_route_sort(d, adapter, route, row, count, cumsum, ws)
+    return route, row, cumsum
+
+
+def adapters_of(M, L, g):
+    """Ids of adapters, and others that name none."""
+    adapter = torch.randint(0, L, (M,), device="cuda", generator=g).int()
+    other = torch.tensor([-1, L, L + 3, -(1 << 31), (1 << 31) - 1], device="cuda").int()
+    none = torch.rand(M, device="cuda", generator=g) < 0.2
+    return torch.where(none, other[torch.arange(M, device="cuda") % 5], adapter).contiguous()
+
+
+@TYPES
+@pytest.mark.parametrize("M,L", [(1, 1), (2, 3), (40, 1), (130, 100), (3000, 5), (20000, 1023), (70000, 24)])
+def test_adapters_on_the_tables_of_the_route_sort(M, L, t):
+    """The tables that moe_route_sort makes of the tokens' adapters give what tables made otherwise give, to the bit:
+    tokens whose id names no adapter are sorted behind the others and get their base."""
+    g = torch.Generator(device="cuda").manual_seed(M + L)
+    D, N, r = 136, 72, 24
+    adapter = adapters_of(M, L, g)
+    normal = lambda *s: torch.randn(s, device="cuda", generator=g).to(t)
+    x, a, b, base = normal(M, D), normal(L, r, D) * D ** -0.5, normal(L, N, r), normal(M, N)
+    scales = torch.rand(L, device="cuda", generator=g)
+    want, out = marked((M, N), t), marked((M, N), t)
+    lora_call(x, adapter, a, b, scales, base, want)
+    route, _, cumsum = sorted_by_library(adapter, L)
+    ws = torch.empty(moe.moe_lora16_workspace_size(M, N, D, r), dtype=torch.uint8, device="cuda")
+    moe.moe_lora16(x, route, cumsum, a, b, base, out, ws, scales=scales)
+    assert torch.equal(out, want)
+    bare = (adapter < 0) | (adapter >= L)
+    assert torch.equal(out[bare], base[bare]) and (M < 40 or not torch.equal(out, base))
+
+
+@TYPES
+@pytest.mark.parametrize("M,L", [(5, 2), (300, 4), (2500, 70)])
+def test_gradients_of_adapters_by_the_products(M, L, t):
+    """The gradients of a and b are those of two products grouped by adapter, on the rows sorted by it; against
+    autograd in 64 bits.  Rank values and their gradients round once each, and so do the results: within
+    four half steps of the norm."""
+    g = torch.Generator(device="cuda").manual_seed(M)
+    D, N, r = 264, 136, 16
+    adapter = adapters_of(M, L, g)
+    normal = lambda *s: torch.randn(s, device="cuda", generator=g).to(t)
+    x, a, b, dout = normal(M, D), normal(L, r, D) * D ** -0.5, normal(L, N, r), normal(M, N)
+    _, row, cumsum = sorted_by_library(adapter, L)
+    ws = torch.empty(moe.moe_gmm16_workspace_size(M, L, max(N, r), max(D, r)), dtype=torch.uint8, device="cuda")
+    new = lambda *s: marked(s, t)
+    xs, ds, v, dv, da, db = new(M, D), new(M, N), new(M, r), new(M, r), marked(a.shape, F32), marked(b.shape, F32)
+    moe.moe_dispatch16(x, row, xs)
+    moe.moe_dispatch16(dout, row, ds)
+    moe.moe_gmm16(xs, cumsum, a, v, ws)
+    moe.moe_gmm16_weight_grad(ds, v, cumsum, db, ws)
+    moe.moe_gmm16_input_grad(ds, cumsum, b, dv, ws)
+    moe.moe_gmm16_weight_grad(dv, xs, cumsum, da, ws)
+    a64, b64 = a.double().requires_grad_(), b.double().requires_grad_()
+    has = ((adapter >= 0) & (adapter < L)).nonzero()[:, 0]
+    l = adapter[has].long()
+    y = torch.einsum("tnr,tr->tn", b64[l], torch.einsum("trd,td->tr", a64[l], x[has].double()))
+    (y * dout[has].double()).sum().backward()
+    e = 4 * torch.finfo(t).eps / 2
+    for got, want in ((da, a64.grad), (db, b64.grad)):
+        assert (got.double() - want).norm() <= e * want.norm()

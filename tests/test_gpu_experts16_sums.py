@@ -101,3 +101,42 @@ def test_long_16_bit_weight_gradients_of_integers_are_exact(E, N, D, t):
     moe.moe_gmm16_weight_grad(dc, a, cumsum, dw, ws)
     assert moe.moe_workspace_status(ws) == 0
     assert torch.equal(dw, ref.rounded(ref.weight_grad(dc, a, cumsum.tolist()), t))
+
+
+@pytest.mark.parametrize("positive", [True, False], ids=["one sign", "normal"])
+@pytest.mark.parametrize("t", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("E,R,N,D", PAIRS + DIVIDED)
+def test_long_fp32_weight_gradients(E, R, N, D, t, positive):
+    """By the norm: what a part drops, and half an fp32 step for every second part.  One accumulator for all of
+    the rows (for a fourth of them where clusters divide them), off by 6e-9 (one sign) and 1e-9 (normal values) of the
+    sum to a product as measured, would be off by 20 times and 5 times as much at least."""
+    dw, dc, a = gradient(E, R, N, D, t, F32, positive)
+    n, d = min(N, 64), min(D, 64)
+    want = corner64(dc, a, n, d)
+    part = 512 if t == F16 else 768
+    share = R if (E, R, N, D) in PAIRS else R / 4
+    tol = part * 2.0 ** -27 + (share / part / 2 + 4) * 2.0 ** -24
+    assert tol <= share * (6e-9 / 20 if positive else 1e-9 / 5), "the test would not tell"
+    assert (dw[:n, :d].double() - want).norm() <= tol * want.norm()
+
+
+@pytest.mark.parametrize("t", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("R", [1, 16, 128, 2048])
+@pytest.mark.parametrize("depth", [8192, 65536])
+def test_deep_products_of_one_sign(R, depth, t):
+    """Products and gradients for the rows, whose sums are never in parts: half a step and 2^-27 of a sum's
+    magnitudes to a product."""
+    g, other = rng(R), 256
+    rows, ws = filled(R, depth, t, g, True), space(R, 1, other, depth)
+    cumsum = torch.tensor([R], dtype=torch.int32, device="cuda")
+    c = marked((R, other), t)
+    w = filled(other, depth, t, g, True)
+    moe.moe_gmm16(rows, cumsum, w[None], c, ws)
+    da = marked((R, other), t)
+    wt = w.T.contiguous()
+    moe.moe_gmm16_input_grad(rows, cumsum, wt[None], da, space(R, 1, depth, other))
+    want = rows.double() @ w.double().T
+    tol = ref.half_step(t, want) + want * depth * 2.0 ** -27
+    for got in (c, da):
+        err = (got.double() - want).abs()
+        assert (err <= tol).all(), (err / tol).max()
