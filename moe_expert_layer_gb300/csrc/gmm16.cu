@@ -1050,8 +1050,8 @@ cudaError_t launch(const Gmm16Problem& p, int split, cudaStream_t stream) {
         cudaFuncSetAttribute(gmm16_kernel<KIND, NT, PAIR, SUMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     if (C::kInParts) {
-      // launched with other registers than its split counts on, it would wait for them: a build that
-      // does is refused
+      // launched with other registers than its split counts on, it would wait for them: the build refuses such a
+      // kernel (build.py), and so does this
       cudaFuncAttributes fa;
       const cudaError_t q = cudaFuncGetAttributes(&fa, gmm16_kernel<KIND, NT, PAIR, SUMS>);
       if (q != cudaSuccess) return q;

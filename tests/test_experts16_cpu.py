@@ -141,3 +141,20 @@ def test_binding_refuses_other_types_shapes_and_strides(moe):
     args = arguments(moe)["moe_gmm16_weight_grad"]
     with pytest.raises(ValueError):
         moe.moe_gmm16_weight_grad(**{**args, "dw": args["dw"].to(torch.int16)}, stream=0)
+
+
+PTXAS = """ptxas info    : Compiling entry function '_ZN3moe12gmm16_kernelILNS_5Gmm16E2ELi256ELb1ELNS_4SumsE%dEEEvi' for 'sm_103a'
+ptxas info    : Function properties for _ZN3moe12gmm16_kernelILNS_5Gmm16E2ELi256ELb1ELNS_4SumsE%dEEEvi
+    0 bytes stack frame, 0 bytes spill stores, 0 bytes spill loads
+ptxas info    : Used %d registers, used 1 barriers, 1024 bytes smem
+"""
+
+
+def test_build_refuses_other_launch_registers():
+    """Kernels whose warps hand registers over are built with the registers that they count on, or not at all."""
+    from moe_expert_layer_gb300 import build
+    log = lambda *kernels: "".join(PTXAS % (i, i, n) for i, n in kernels)
+    build.check_registers("gmm16.cu", log((1, 116), (2, 168), (0, 117), (3, 168)))
+    for bad in (((1, 168), (2, 168), (0, 117), (3, 160)), ((2, 128), (3, 168)), ((2, 168),), ((0, 168), (1, 168)), ()):
+        with pytest.raises(RuntimeError, match="gmm16.cu"):
+            build.check_registers("gmm16.cu", log(*bad))
