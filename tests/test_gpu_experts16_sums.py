@@ -140,3 +140,28 @@ def test_deep_products_of_one_sign(R, depth, t):
     for got in (c, da):
         err = (got.double() - want).abs()
         assert (err <= tol).all(), (err / tol).max()
+
+
+@pytest.mark.parametrize("t", [F16, BF16], ids=["f16", "bf16"])
+@pytest.mark.parametrize("N,D", [(264, 520), (136, 72)])
+def test_long_experts_among_many_short_ones(N, D, t):
+    """Few rows to an expert on average, one or two with several parts all the same: exactly, written and added."""
+    g, E = rng(N), 200
+    counts = [(3 * i) % 7 for i in range(E)]
+    for i, n in ((7, 9000), (8, 0), (9, 4097)) if t == F16 else ((7, 33000), (8, 0), (9, 1537)):
+        counts[i] = n
+    cumsum, R = torch.tensor(counts, device="cuda").cumsum(0).int(), sum(counts) + 3
+    assert 4096 < R <= 192 * E
+    values = lambda k, m: torch.randint(-m, m + 1, (R, k), device="cuda", generator=g).to(t)
+    a, dc, ws = values(D, 2), values(N, 1), space(R, E, N, D)
+    a[R - 3:], dc[R - 3:] = float("nan"), float("nan")
+    want = ref.weight_grad(dc, a, cumsum.tolist())
+    for out in (t, F32):
+        dw = marked((E, N, D), out)
+        moe.moe_gmm16_weight_grad(dc, a, cumsum, dw, ws)
+        assert torch.equal(dw, ref.rounded(want, out))
+    start = torch.randint(-1000, 1000, (E, N, D), device="cuda", generator=g).float()
+    dw = start.clone()
+    moe.moe_gmm16_weight_grad(dc, a, cumsum, dw, ws, accumulate=True)
+    assert torch.equal(dw, (start.double() + want).float())
+    assert moe.moe_workspace_status(ws) == 0
