@@ -711,7 +711,7 @@ def moe_lora16_workspace_size(M, N, D, rank):
 def moe_lora16(x, route, cumsum, a, b, base, out, workspace, scales=None, stream=None):
     """out [M][N] (it may be base) = base + scales[l] b[l] (a[l] x[t]), a [L][rank][D], b [L][N][rank], l the adapter of
     token t; route [M], cumsum [L]: sorted_src_route and cumsum of moe_route_sort on the tokens' adapters."""
-    (M, D), (L, rank, _), N, t = x.shape, a.shape, b.shape[1], x.dtype
+    (M, D), (L, rank, _), (_, N, _), t = x.shape, a.shape, b.shape, x.dtype
     dev = _device() if _device else _find_device()
     _check("moe_lora16", load_library().moe_lora16(
         M, N, D, rank, L, _type16(x, "x"), _array(x, (M, D), t, dev, "x"), _list(route, M, _INT32, dev, "route"),

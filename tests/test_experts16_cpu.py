@@ -158,3 +158,14 @@ def test_build_refuses_other_launch_registers():
     for bad in (((1, 168), (2, 168), (0, 117), (3, 160)), ((2, 128), (3, 168)), ((2, 168),), ((0, 168), (1, 168)), ()):
         with pytest.raises(RuntimeError, match="gmm16.cu"):
             build.check_registers("gmm16.cu", log(*bad))
+
+
+def test_binding_refuses_other_numbers_of_dimensions(moe):
+    """Every matrix and stack of matrices of every call, flattened or with a dimension more: refused as other shapes are."""
+    for name, args in arguments(moe).items():
+        f = getattr(moe, name)
+        for k, v in args.items():
+            if v.dim() > 1:
+                for bad in (v.reshape(-1), v[None]):
+                    with pytest.raises(ValueError):
+                        f(**{**args, k: bad}, stream=0)
