@@ -17,6 +17,14 @@
  * number of rows at most 4096 (binary16) or 32768 (bfloat16), in fp32 512 or 768: longer
  * sums are made of such parts, added in fp32.
  *
+ * In binary16 an infinity that comes in is stored as +-65504 too, by the gradients as well: a
+ * loss scaler that looks for infinities finds none in da, dgu, dy or a 16-bit dw, and an fp32 dw
+ * made of those is finite.  It has to look at what it passes in, at dprobs and fp32 sums of
+ * its own, or take +-65504 for an overflow.  (bfloat16 keeps infinities.)
+ *
+ * A batch without rows (R, M or rows 0) is refused: MOE_ERR_SHAPE, nothing written.  The caller
+ * leaves the call out, and clears a dw that it does not accumulate into.
+ *
  * Expert-major rows: those of expert e are cumsum[e - 1] .. cumsum[e] - 1 (from 0 for
  * e = 0) of R rows; cumsum [E] is the inclusive prefix that moe_route_sort writes (entries
  * are held to 0 .. R).  Rows from cumsum[E - 1] on belong to no expert: outputs there are

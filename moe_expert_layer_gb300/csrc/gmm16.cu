@@ -36,7 +36,8 @@
 //   64 experts x 768, 4096 -> 2816   670-740 us   1530-1690 TFLOP/s alone, tensor pipe 89% busy; back to
 //       back for seconds 787, where the power limit holds the clock at 1.45 GHz.  What is left: experts a
 //       little past 768 rows take a fourth tile, and 34.2 rounds of items are 35.
-//   64 experts x 768, kWeight, 4096 x 1408  493 us   1150 TFLOP/s, 1.48 GB written in fp32 (in 16 bits 365)
+//   64 experts x 768, kWeight, 4096 x 1408  460-490 us   1160-1230 TFLOP/s, 1.48 GB written in fp32 (in 16 bits
+//       365-400; added to what is there 610)
 // At 1.9 GHz a stage of a pair takes its 512 clocks, for every kind; that is 18.4 TB/s from L2, about what
 // it has: kWeight's stores and their way on to memory come on top (12 stages and 20 MB of fp32 sums from
 // all pairs: 3.24 us without stores, 3.9 while L2 holds them, 5.5 when it writes them back; the same
@@ -47,7 +48,7 @@
 // Roles: warp 0 loads operand A and warp 2 operand B, 64 steps of the reduction a stage, into a ring
 // in shared memory (a pair's copies complete the leading CTA's barriers); warp 3 overwrites rows
 // (kWeight); warp 1 of the leading CTA issues the MMAs; warps 4-11, two groups, round the
-// sums of one accumulator and store them while the MMAs fill the other; an fp32 gradient of more rows than
+// sums of one accumulator and store them while the MMAs fill the other; a weight gradient of more rows than
 // a part has is added up in their registers, which they get from the other warps.  Every wait
 // is bounded: one that gives up records MOE_ERR_TIMEOUT and the CTA winds down.
 #include <cmath>
@@ -1017,7 +1018,8 @@ bool encode_tensor_map_3d(CUtensorMap* m, CUtensorMapDataType dt, size_t elem, c
 }
 
 // Clusters of this many CTAs, one to an SM, that the device holds at once (GB300: 152, 76 and 36 of 1, 2
-// and 4: a cluster of four needs four SMs of one GPC).
+// and 4: a cluster of four needs four SMs of one GPC).  CTAs take items whatever their number: where it is another,
+// forms are chosen by a wrong count and some CTAs begin when others are done.
 inline int resident_clusters(int ctas) {
   const int n = ctas <= 2 ? sm_count() / ctas : sm_count() / 19 * 18 / ctas;
   return n < 1 ? 1 : n;
@@ -1114,8 +1116,8 @@ Form choose(const Gmm16Problem& p) {
   return best;
 }
 
-// kWeight of few blocks and many rows: blocks of 128 x 128, clusters of CTAs that divide the rows of each (0: pairs
-// after all), by the same count.  Both sides, us (16 bits / fp32):            pairs      divided
+// kWeight of few blocks and many rows: blocks of 128 x 128, clusters of up to four CTAs that divide the rows of each
+// (0: pairs after all), by the same count; larger clusters have not been measured.  Both sides, us (16 bits / fp32):            pairs      divided
 //   1 expert x 16384 rows, 512 x 512                                      73 / 75      22 / 22
 //   1 x 8192, 1024 x 1024                                                 40 / 41      22 / 23
 //   4 x 2868, 72 x 928                                                    19 / 21      13 / 13
